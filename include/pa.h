@@ -396,6 +396,61 @@ int pa_prefill_varlen(void* out, const void* q, const void* k_cache, const void*
                       int head_dim, int dtype, int block_size, int64_t num_blocks, int causal,
                       float scale, int* dev_err, void* stream);
 
+/*
+ * Modified scores: the rules under which pa_decode_mod and pa_prefill_mod attend. A query at
+ * absolute position p of sequence s (p = context_lens[s] - 1 in the decode) scores key t
+ *   x = scale * q.k
+ *   x = softcap * tanh(x / softcap)            when softcap > 0
+ *   x = x - slopes[h] * |p - t|                when slopes is not NULL (h: the query head)
+ * and sees it when both hold:
+ *   t <= p, or the call is not causal, or t < prefix_lens[s]
+ *   window == 0, or t > p - window, or t < sink, or t < prefix_lens[s]
+ * out = softmax over the keys it sees, times V. prefix_lens is the bidirectional prefix of a
+ * prefix language model: its keys are seen by every query of the sequence, earlier ones
+ * included; window bounds how far back a query looks, and sink keeps the first keys in
+ * sight of every later query. (A mask by documents needs no rule here: each document of a
+ * packed batch is a sequence of its own.)
+ *
+ *   softcap         >= 0 and finite; 0 = no cap.
+ *   window, sink    >= 0; window 0 = no window (sink then changes nothing).
+ *   slopes          device, fp32 [num_heads], or NULL.
+ *   prefix_lens     device, int32 [num_seqs], or NULL (all 0); negative values count as 0,
+ *                   values beyond the sequence as its length.
+ *
+ * Keys that no query of the call sees need not exist: a block whose every position is hidden
+ * may have any id in the table (-1 for a block given back), and rows hidden from a decode
+ * query, or from a whole prefill work unit (up to 256 consecutive query rows of a KV head),
+ * may hold anything, NaN included. Rows that some query of such a unit sees must be finite.
+ *
+ * pa_decode_mod — pa_decode under these rules: arguments, workspace, launch and errors as
+ * there (every shape runs on the tensor cores). Key tiles that lie wholly outside the window
+ * are not read.
+ * pa_prefill_mod — pa_prefill_varlen under these rules: arguments, requirements and errors
+ * as there.
+ * Both: a softcap or window out of range is PA_ERR_SHAPE, mod == NULL is PA_ERR_NULL.
+ */
+typedef struct pa_score_mod {
+  float softcap;
+  int32_t window;
+  int32_t sink;
+  const float* slopes;
+  const int32_t* prefix_lens;
+} pa_score_mod;
+
+int pa_decode_mod(void* out, const void* q, const void* k_cache, const void* v_cache,
+                  const int32_t* block_tables, int max_blocks_per_seq,
+                  const int32_t* context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                  int head_dim, int dtype, int block_size, int64_t num_blocks, float scale,
+                  const pa_score_mod* mod, int grid_ctas, void* workspace,
+                  size_t workspace_bytes, int* dev_err, void* stream);
+
+int pa_prefill_mod(void* out, const void* q, const void* k_cache, const void* v_cache,
+                   const int32_t* block_tables, int max_blocks_per_seq,
+                   const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int num_seqs,
+                   int max_seqlen_q, int max_seqlen_k, int num_heads, int num_kv_heads,
+                   int head_dim, int dtype, int block_size, int64_t num_blocks, int causal,
+                   float scale, const pa_score_mod* mod, int* dev_err, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

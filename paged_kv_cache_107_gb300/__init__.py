@@ -9,6 +9,7 @@ is absent the calls raise.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 import math
 import os
 import threading
@@ -19,7 +20,8 @@ import torch
 from . import build as _build
 
 __all__ = ["pa_store_kvcache", "pa_decode", "pa_decode_step", "pa_decode_workspace_size",
-           "pa_prefill_varlen", "pa_decode_noalloc", "pa_staged_write_apply",
+           "pa_prefill_varlen", "pa_decode_noalloc", "pa_decode_mod", "pa_prefill_mod",
+           "ScoreMod", "pa_staged_write_apply",
            "pa_staged_pack", "pa_staged_pack_bound", "pa_staged_upload_apply",
            "PaStagedLayout", "pa_sample_workspace_size", "pa_gumbel_sample",
            "SampleWorkspace",
@@ -508,4 +510,149 @@ def pa_decode_noalloc(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
             float(scale) if scale is not None else 0.0, int(grid_ctas), _ptr(dev_err),
             _stream(stream))
     _check(rc, "pa_decode_noalloc")
+    return out
+
+
+# ---------------------------------------------------------------- modified scores
+class _PaScoreMod(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("sink", ctypes.c_int32), ("slopes", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
+
+
+@dataclasses.dataclass
+class ScoreMod:
+    """The rules of pa_decode_mod and pa_prefill_mod (pa_score_mod in pa.h): tanh cap, bias by
+    distance (slopes fp32 [H]), window, kept first positions, bidirectional prefix
+    (prefix_lens int32 [B])."""
+    softcap: float = 0.0
+    slopes: Optional[torch.Tensor] = None
+    window: int = 0
+    sink: int = 0
+    prefix_lens: Optional[torch.Tensor] = None
+
+    def _check(self, num_heads: int, num_seqs: int) -> _PaScoreMod:
+        for name, t, dt, n in (("slopes", self.slopes, torch.float32, num_heads),
+                               ("prefix_lens", self.prefix_lens, torch.int32, num_seqs)):
+            if t is None:
+                continue
+            _need(t, name, dt, 1)
+            if t.shape[0] != n or not t.is_contiguous():
+                raise PagedAttentionError(f"{name} must be contiguous with {n} entries")
+        if not (self.softcap >= 0.0 and math.isfinite(self.softcap)):
+            raise PagedAttentionError(f"softcap must be finite and >= 0, got {self.softcap}")
+        if not (0 <= self.window < 1 << 31 and 0 <= self.sink < 1 << 31):
+            raise PagedAttentionError("window and sink must be >= 0 (32-bit)")
+        return _PaScoreMod(self.softcap, self.window, self.sink,
+                           None if self.slopes is None else self.slopes.data_ptr(),
+                           None if self.prefix_lens is None else self.prefix_lens.data_ptr())
+
+
+_stream_ws = {}
+
+
+def _stream_workspace(key: tuple, make, fits, device, stream):
+    """The default workspace of a call: one for each (device, stream, key), made on the stream
+    it serves, replaced by a larger one when a call needs it. Calls on one stream follow each
+    other, so they never share it at the same time. A captured graph may be replayed beside
+    other work and outlives any cache, so a captured call has to bring its own."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        if torch.cuda.is_current_stream_capturing():
+            raise PagedAttentionError("pass a workspace when the call is captured into a graph")
+        key = (device.index, stream.cuda_stream) + key
+        ws = _stream_ws.get(key)
+        if ws is None or not fits(ws):
+            ws = _stream_ws[key] = make()
+    return ws
+
+
+def _typed(name: str, argtypes, restype=ctypes.c_int):
+    """The library's function `name` with its argument types set."""
+    fn = getattr(load_library(), name)
+    if not getattr(fn, "_pa_typed", False):
+        fn.argtypes = argtypes
+        fn.restype = restype
+        fn._pa_typed = True
+    return fn
+
+
+def pa_decode_mod(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                  v_cache: torch.Tensor, block_tables: torch.Tensor,
+                  context_lens: torch.Tensor, mod: ScoreMod, scale: Optional[float] = None,
+                  grid_ctas: int = 0, workspace: Optional[DecodeWorkspace] = None,
+                  dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_decode under the rules of `mod`: the same tensors and the same workspace."""
+    vp, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
+                             ctypes.c_size_t)
+    _need16(q, "q", 3)
+    for name, t, dt, nd in (("out", out, q.dtype, 3), ("q", q, q.dtype, 3),
+                            ("k_cache", k_cache, q.dtype, 4),
+                            ("v_cache", v_cache, q.dtype, 4),
+                            ("block_tables", block_tables, torch.int32, 2),
+                            ("context_lens", context_lens, torch.int32, 1)):
+        _need(t, name, dt, nd)
+        if not t.is_contiguous():
+            raise PagedAttentionError(f"{name} must be contiguous")
+    B, H, D = q.shape
+    nb, bs, hk, d2 = k_cache.shape
+    if out.shape != q.shape or d2 != D or v_cache.shape != k_cache.shape:
+        raise PagedAttentionError("shape mismatch")
+    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise PagedAttentionError("block_tables / context_lens batch mismatch")
+    rules = mod._check(H, B)
+    _one_device(out, q, k_cache, v_cache, block_tables, context_lens, mod.slopes,
+                mod.prefix_lens, None if workspace is None else workspace.buffer, dev_err,
+                stream=stream)
+    if workspace is None:
+        workspace = _stream_workspace(("decode", H, hk, D),
+                                      lambda: DecodeWorkspace(max(B, 1), H, hk, D, q.device),
+                                      lambda w: w.fits(B, H, hk, D), q.device, stream)
+    fn = _typed("pa_decode_mod", [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i64,
+                                  f32, vp, i32, vp, sz, vp, vp])
+    rc = fn(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+            block_tables.shape[1], _ptr(context_lens), B, H, hk, D, PA_DTYPE[q.dtype], bs, nb,
+            float(scale) if scale is not None else 0.0, ctypes.byref(rules), int(grid_ctas),
+            _ptr(workspace.buffer), workspace.nbytes, _ptr(dev_err), _stream(stream))
+    _check(rc, "pa_decode_mod")
+    return out
+
+
+def pa_prefill_mod(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, block_tables: torch.Tensor,
+                   cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor, max_seqlen_q: int,
+                   max_seqlen_k: int, mod: ScoreMod, causal: bool = True,
+                   scale: Optional[float] = None, dev_err: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """pa_prefill_varlen under the rules of `mod`: the same tensors."""
+    vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
+    _need16(q, "q", 3)
+    for name, t, dt, nd in (("out", out, q.dtype, 3), ("q", q, q.dtype, 3),
+                            ("k_cache", k_cache, q.dtype, 4),
+                            ("v_cache", v_cache, q.dtype, 4),
+                            ("block_tables", block_tables, torch.int32, 2),
+                            ("cu_seqlens_q", cu_seqlens_q, torch.int32, 1),
+                            ("cu_seqlens_k", cu_seqlens_k, torch.int32, 1)):
+        _need(t, name, dt, nd)
+        if not t.is_contiguous():
+            raise PagedAttentionError(f"{name} must be contiguous")
+    T, H, D = q.shape
+    nb, bs, hk, d2 = k_cache.shape
+    S = cu_seqlens_q.shape[0] - 1
+    if out.shape != q.shape or d2 != D or v_cache.shape != k_cache.shape:
+        raise PagedAttentionError("shape mismatch")
+    if cu_seqlens_k.shape[0] != S + 1 or block_tables.shape[0] != S:
+        raise PagedAttentionError("cu_seqlens / block_tables batch mismatch")
+    rules = mod._check(H, S)
+    _one_device(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, mod.slopes,
+                mod.prefix_lens, dev_err, stream=stream)
+    fn = _typed("pa_prefill_mod", [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
+                                   i32, i32, i64, i32, f32, vp, vp, vp])
+    rc = fn(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+            block_tables.shape[1], _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), S, int(max_seqlen_q),
+            int(max_seqlen_k), H, hk, D, PA_DTYPE[q.dtype], bs, nb, 1 if causal else 0,
+            float(scale) if scale is not None else 0.0, ctypes.byref(rules), _ptr(dev_err),
+            _stream(stream))
+    _check(rc, "pa_prefill_mod")
     return out

@@ -37,7 +37,10 @@
 #include <cuda.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "decode_kernel.cuh"
+#include "score_mod.cuh"
 #include "tensor_map.h"
 
 namespace pa {
@@ -45,7 +48,13 @@ namespace {
 
 constexpr int kTcGMax = 8;   // query heads per KV head on this path (rows of the 16-row tile)
 
-template <int S>
+// What a stage's tile needs beyond StageMeta with modified scores: key t of the sequence is
+// visible when t < keep or t >= low; the position of the query.
+struct __align__(16) ModMeta : StageMeta {
+  int keep, low, pos;
+};
+
+template <int S, typename Meta = StageMeta>
 struct TcCtrl {
   uint64_t full[S];
   uint64_t empty[S];
@@ -53,7 +62,7 @@ struct TcCtrl {
   uint64_t q_empty[2];
   uint64_t seg_bar;
   uint64_t merge_bar[8];
-  StageMeta meta[S];
+  Meta meta[S];
   int64_t nt;      // tiles in the stream
   int64_t x0, x1;  // this CTA's tile range
   int64_t pb0;     // first tile of the sequence holding x0
@@ -87,7 +96,7 @@ struct TcCfg {
   static constexpr size_t SMEM =
       1024 + (size_t)STAGES * STAGE_BYTES + (size_t)QS * Q_BYTES + CTRL_BYTES;
   static_assert(STAGES >= 2, "at least two stages");
-  static_assert(sizeof(TcCtrl<STAGES>) <= CTRL_BYTES, "control block");
+  static_assert(sizeof(TcCtrl<STAGES, ModMeta>) <= CTRL_BYTES, "control block");
   static_assert(HS * (WPH - 1) * MERGE_FLOATS * 4 <= 2 * KV_BYTES, "merge scratch");
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
@@ -148,18 +157,32 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-template <int HS, bool FUSED, int D, bool F16>
+// The kernel's forms: plain, or with modified scores (pa_decode_mod).
+enum TcForm { kTcPlain = 0, kTcMod = 1 };
+template <int FORM>
+struct TcArgs {
+  using type = DecodeArgs;
+};
+template <>
+struct TcArgs<kTcMod> {
+  using type = DecodeModArgs;
+};
+
+template <int HS, bool FUSED, int D, bool F16, int FORM = kTcPlain>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
-                           const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a,
-                           const int tb) {
+                           const __grid_constant__ CUtensorMap tm_v,
+                           const typename TcArgs<FORM>::type a, const int tb) {
+  static_assert(!FUSED || FORM == kTcPlain, "the fused store has no modified form");
   using TC = TcCfg<HS, D>;
   constexpr int S = TC::STAGES;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* qbuf = smem + (size_t)S * TC::STAGE_BYTES;
-  TcCtrl<S>& ctl = *reinterpret_cast<TcCtrl<S>*>(qbuf + (size_t)TC::QS * TC::Q_BYTES);
+  using Meta = std::conditional_t<FORM == kTcMod, ModMeta, StageMeta>;
+  using Ctrl = TcCtrl<S, Meta>;
+  Ctrl& ctl = *reinterpret_cast<Ctrl*>(qbuf + (size_t)TC::QS * TC::Q_BYTES);
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -172,6 +195,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int cap = a.max_blocks * a.block_size;
   const int B = a.num_seqs;
   constexpr int T = TC::T;
+  constexpr bool kHidden = FORM != kTcPlain;
+  // the keys of sequence b that count (every form but the modified one: all of them)
+  auto span_of = [&](int b) {
+    KeySpan<kHidden> k{load_ctx(a.context_lens, b, cap), 0, 0};
+    if constexpr (FORM == kTcMod) mod_span(k, a.mod, b, k.hi - 1);
+    return k;
+  };
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -206,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (FUSED && (raw <= 0 || raw > cap) && __ldg(a.slot_mapping + b) != -1) {
       if ((b % gridDim.x) == c && slab == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SLOT);
     }
-    local += (load_ctx(a.context_lens, b, cap) + T - 1) / T;
+    local += span_of(b).tiles(T);
   }
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) local += __shfl_xor_sync(0xffffffffu, local, m);
@@ -240,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int base = 0; base < B; base += kConsumerWarps * 32) {
       int n = 0;
       const int b = base + tid;
-      if (tid < kConsumerWarps * 32 && b < B) n = (load_ctx(a.context_lens, b, cap) + T - 1) / T;
+      if (tid < kConsumerWarps * 32 && b < B) n = span_of(b).tiles(T);
       int incl = n;
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) {
@@ -278,16 +308,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t x = x0 + (lane >> 1);
       int b = ctl.b0;
       int64_t pb = ctl.pb0;
-      int ctx_b = load_ctx(a.context_lens, b, cap);
-      int nb = (ctx_b + T - 1) / T;
+      KeySpan<kHidden> sp = span_of(b);
+      int nb = sp.tiles(T);
       while (x >= pb + nb && b + 1 < B) {
         pb += nb;
         ++b;
-        ctx_b = load_ctx(a.context_lens, b, cap);
-        nb = (ctx_b + T - 1) / T;
+        sp = span_of(b);
+        nb = sp.tiles(T);
       }
-      const int tok0 = (int)(x - pb) * T;
-      const int count = min(T, ctx_b - tok0);
+      const int tok0 = sp.first_key(T, (int)(x - pb));
+      const int count = min(T, sp.hi - tok0);
       if (count > 0 && tok0 / a.block_size == (tok0 + count - 1) / a.block_size) {
         const int blk = __ldg(a.block_tables + (int64_t)b * a.max_blocks + tok0 / a.block_size);
         if (blk >= 0 && (int64_t)blk < a.num_blocks) {
@@ -341,21 +371,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nbx = tb > 0 ? T / tb : 0;  // boxes per half
     int b = ctl.b0;
     int64_t pb = ctl.pb0;
-    int ctx_b = load_ctx(a.context_lens, b, cap);
-    int nb = (ctx_b + T - 1) / T;
+    KeySpan<kHidden> sp = span_of(b);
+    int nb = sp.tiles(T);
     int q_n = 0;  // segments whose Q has been issued
     for (int64_t it = 0; it < n_tiles; ++it) {
       const int64_t x = x0 + it;
       while (x >= pb + nb && b + 1 < B) {
         pb += nb;
         ++b;
-        ctx_b = load_ctx(a.context_lens, b, cap);
-        nb = (ctx_b + T - 1) / T;
+        sp = span_of(b);
+        nb = sp.tiles(T);
       }
       const int s = (int)(it % S);
       const int lt = (int)(x - pb);
-      const int tok0 = lt * T;
-      const int count = min(T, ctx_b - tok0);
+      const int tok0 = sp.first_key(T, lt);
+      const int count = min(T, sp.hi - tok0);
       int flags = 0;
       if (x == x0 || lt == 0) flags |= kFlagFirst;
       if (x == x1 - 1 || lt == nb - 1) flags |= kFlagLast;
@@ -363,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int new_row = -1;
       int64_t new_slot = -1;
       if (FUSED && lt == nb - 1 && count > 0) {
-        const int pos = ctx_b - 1;
+        const int pos = sp.hi - 1;
         const int32_t sl = __ldg(a.slot_mapping + b);
         if (sl != -1) {
           const int blk = __ldg(a.block_tables + (int64_t)b * a.max_blocks + pos / a.block_size);
@@ -381,7 +411,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this lane's box: tokens tok0 + lane*tb .. +tb-1, inside one block
       int blk = -1, off = 0;
       bool box_ok = false;
-      if (lane < nbx && lane * tb < count) {
+      // (a box without a visible key is not read: its block may be gone)
+      if (lane < nbx && lane * tb < count &&
+          sp.any_visible(tok0 + lane * tb, tb)) {
         const int pos = tok0 + lane * tb;
         blk = __ldg(a.block_tables + (int64_t)b * a.max_blocks + pos / a.block_size);
         off = pos % a.block_size;
@@ -400,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       unsigned char* st = smem + (size_t)s * TC::STAGE_BYTES;
       unsigned char* side = st + 2 * TC::KV_BYTES;
       if (lane == 0) {
-        StageMeta& m = ctl.meta[s];
+        Meta& m = ctl.meta[s];
         m.pb = pb;
         m.b = b;
         m.tok0 = tok0;
@@ -409,6 +441,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         m.flags = flags;
         m.new_row = new_row;
         m.new_slot = new_slot;
+        if constexpr (kHidden) {
+          m.keep = sp.keep;
+          m.low = sp.low;
+          m.pos = sp.hi - 1;
+        }
         if (tb > 0)
           mbar_arrive_expect_tx(&ctl.full[s], (uint32_t)(nbox * 2 * TC::NH * box_bytes +
                                                          (new_row >= 0 ? 2 * TC::SIDE_ROW : 0)));
@@ -449,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             cp_async16(side + kv * TC::SIDE_ROW + (jj * D + ch * 8) * 2, src);
           } else {
             const int pos = tok0 + t;
+            if (!sp.any_visible(pos, 1)) continue;
             const int bk = __ldg(a.block_tables + (int64_t)b * a.max_blocks + pos / a.block_size);
             if (bk < 0 || (int64_t)bk >= a.num_blocks) {
               if (kv == 0 && jj == 0 && ch == 0) set_dev_err(a.dev_err, PA_DEV_ERR_BLOCK_ID);
@@ -515,6 +553,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
   for (int n = 0; n < NO; ++n) o[n][0] = o[n][1] = 0.f;
   const float sl2 = a.scale_log2;
+  float slope2 = 0.f;  // this row's slope of the distance, in log2 units
+  if constexpr (FORM == kTcMod) {
+    if (a.mod.slopes && row_ok)
+      slope2 = __ldg(a.mod.slopes + kvh * G + gid) * 1.4426950408889634f;
+  }
 
   // shared-memory row of token t of head j within a half: boxes of tbl tokens, each
   // [head][token]; chunk c of the row sits at chunk c ^ (t % 8)
@@ -543,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         set_dev_err(a.dev_err, PA_DEV_ERR_TIMEOUT);
       }
     }
-    const StageMeta meta = ctl.meta[s];
+    const Meta meta = ctl.meta[s];
     unsigned char* Kst = smem + (size_t)s * TC::STAGE_BYTES;
     unsigned char* Vst = Kst + TC::KV_BYTES;
     unsigned char* side = Kst + 2 * TC::KV_BYTES;
@@ -584,11 +627,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t k_lane = (uint32_t)row_off(tK) + ((uint32_t)(k_hi ^ (sw & 1)) << 4);
       const uint32_t v_lane =
           (uint32_t)(TC::KV_BYTES + row_off(tV)) + ((uint32_t)(v_hi ^ (sw & 1)) << 4);
-      // rows of this warp's V past the tile's valid tokens: zero them (head j's rows)
-      if (tw0 + 16 > count) {
+      // rows of this warp's V past the tile's valid tokens, or hidden from the query: zero
+      // them (head j's rows)
+      bool part_hidden = false;
+      if constexpr (kHidden)
+        part_hidden = meta.tok0 + tw0 < meta.low && meta.tok0 + tw0 + 16 > meta.keep;
+      if (tw0 + 16 > count || part_hidden) {
         for (int i = lane; i < 16 * TC::NH * 8; i += 32) {
           const int t = tw0 + i / (TC::NH * 8);
-          if (t >= count)
+          bool drop = t >= count;
+          if constexpr (kHidden)
+            drop = drop || (meta.tok0 + t < meta.low && meta.tok0 + t >= meta.keep);
+          if (drop)
             *reinterpret_cast<uint4*>(Vst + ((i >> 3) % TC::NH) * TC::HALF + row_off(t) + (i & 7) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
         }
@@ -632,7 +682,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int t = tw0 + n * 8 + 2 * tig + e;
-          const float v = t < count ? sc[n][e] * sl2 : -INFINITY;
+          float v;
+          if constexpr (FORM == kTcMod) {
+            const int key = meta.tok0 + t;  // the query sits at the last position
+            v = a.mod.cap2 > 0.f ? a.mod.cap2 * cap_tanh(sc[n][e] * a.mod.cap_in) : sc[n][e] * sl2;
+            v = fmaf(-slope2, (float)(meta.pos - key), v);
+            v = t < count && (key >= meta.low || key < meta.keep) ? v : -INFINITY;
+          } else {
+            v = t < count ? sc[n][e] * sl2 : -INFINITY;
+          }
           sc[n][e] = v;
           tmax = fmaxf(tmax, v);
         }
@@ -782,14 +840,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int HS, bool FUSED, int D, bool F16>
-int launch_decode_tc_t(const DecodeArgs& a, const DeviceInfo& info, cudaStream_t stream) {
+template <int HS, bool FUSED, int D, bool F16, int FORM = kTcPlain>
+int launch_decode_tc_t(const typename TcArgs<FORM>::type& a, const DeviceInfo& info,
+                       cudaStream_t stream) {
   using TC = TcCfg<HS, D>;
   static std::atomic<bool> attr_done[64];  // zero-initialised: false
   const int dev = info.device;
   if (dev < 0 || dev >= 64) return PA_ERR_CUDA;
   if (!attr_done[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(paged_decode_tc_kernel<HS, FUSED, D, F16>,
+    if (cudaFuncSetAttribute(paged_decode_tc_kernel<HS, FUSED, D, F16, FORM>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TC::SMEM) != cudaSuccess)
       return PA_ERR_CUDA;
     attr_done[dev].store(true, std::memory_order_release);
@@ -809,20 +868,21 @@ int launch_decode_tc_t(const DecodeArgs& a, const DeviceInfo& info, cudaStream_t
     return PA_ERR_CUDA;
   const int slabs = a.num_kv_heads / HS;
   dim3 grid((unsigned)a.grid_ctas, (unsigned)slabs);
-  if (launch_dependent(paged_decode_tc_kernel<HS, FUSED, D, F16>, grid, dim3(kThreads), TC::SMEM,
-                       stream, mk, mv, a, tb) != cudaSuccess)
+  if (launch_dependent(paged_decode_tc_kernel<HS, FUSED, D, F16, FORM>, grid, dim3(kThreads),
+                       TC::SMEM, stream, mk, mv, a, tb) != cudaSuccess)
     return PA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// Every head slab of the tensor-core path for one (FUSED, D, element type) combination.
-template <bool FUSED, int D, bool F16>
-int dispatch_slab_tc(const DecodeArgs& a, const DeviceInfo& info, cudaStream_t stream) {
+// Every head slab of the tensor-core path for one (FUSED, D, element type, form) combination.
+template <bool FUSED, int D, bool F16, int FORM = kTcPlain>
+int dispatch_slab_tc(const typename TcArgs<FORM>::type& a, const DeviceInfo& info,
+                     cudaStream_t stream) {
   switch (decode_head_slab(a.num_kv_heads)) {
-    case 8: return launch_decode_tc_t<8, FUSED, D, F16>(a, info, stream);
-    case 4: return launch_decode_tc_t<4, FUSED, D, F16>(a, info, stream);
-    case 2: return launch_decode_tc_t<2, FUSED, D, F16>(a, info, stream);
-    default: return launch_decode_tc_t<1, FUSED, D, F16>(a, info, stream);
+    case 8: return launch_decode_tc_t<8, FUSED, D, F16, FORM>(a, info, stream);
+    case 4: return launch_decode_tc_t<4, FUSED, D, F16, FORM>(a, info, stream);
+    case 2: return launch_decode_tc_t<2, FUSED, D, F16, FORM>(a, info, stream);
+    default: return launch_decode_tc_t<1, FUSED, D, F16, FORM>(a, info, stream);
   }
 }
 

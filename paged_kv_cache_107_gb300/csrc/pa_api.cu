@@ -36,9 +36,30 @@ bool current_device_info(DeviceInfo* info) {
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-static float resolve_scale(float scale, int head_dim) {
+constexpr float kLog2e = 1.4426950408889634f;  // exp(x) = exp2(x * log2(e))
+
+static float natural_scale(float scale, int head_dim) {
   if (!(scale > 0.f) || isnan(scale)) scale = 1.0f / sqrtf((float)head_dim);
-  return scale * 1.4426950408889634f;  // exp(x) = exp2(x * log2(e))
+  return scale;
+}
+static float resolve_scale(float scale, int head_dim) {
+  return natural_scale(scale, head_dim) * kLog2e;
+}
+
+// Checks pa_score_mod and folds its factors (ScoreModArgs).
+static int resolve_mod(const pa_score_mod* mod, float scale, int head_dim, ScoreModArgs* m) {
+  if (!mod) return PA_ERR_NULL;
+  if (!(mod->softcap >= 0.f) || isinf(mod->softcap) || mod->window < 0 || mod->sink < 0)
+    return PA_ERR_SHAPE;
+  if (head_dim <= 0) return PA_ERR_UNSUPPORTED;
+  m->cap2 = mod->softcap * kLog2e;
+  m->cap_in = mod->softcap > 0.f ? natural_scale(scale, head_dim) / mod->softcap : 0.f;
+  if (isinf(m->cap2) || isinf(m->cap_in)) return PA_ERR_SHAPE;
+  m->slopes = mod->slopes;
+  m->window = mod->window;
+  m->sink = mod->sink;
+  m->prefix_lens = mod->prefix_lens;
+  return PA_OK;
 }
 
 }  // namespace pa
@@ -245,9 +266,18 @@ size_t decode_bind_workspace(DecodeArgs* a, unsigned char* ws, int layout_ctas) 
   return total;
 }
 
-// pa_decode and pa_decode_step: the caller's workspace, laid out for the largest grid the
-// device allows (so one workspace serves every grid_ctas); `step` is null for the plain
-// call.
+// Binds the caller's workspace, laid out for the largest grid the device allows (so one
+// workspace serves every grid_ctas).
+static int decode_check_workspace(DecodeArgs* a, const DeviceInfo& info, void* workspace,
+                                  size_t workspace_bytes) {
+  const size_t need =
+      decode_bind_workspace(a, static_cast<unsigned char*>(workspace), decode_max_ctas(info));
+  if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return PA_ERR_ALIGN;
+  return PA_OK;
+}
+
+// pa_decode and pa_decode_step; `step` is null for the plain call.
 static int decode_entry(void* out, const void* q, const void* k_cache, const void* v_cache,
                         const int32_t* block_tables, int max_blocks_per_seq,
                         const int32_t* context_lens, int num_seqs, int num_heads,
@@ -263,12 +293,67 @@ static int decode_entry(void* out, const void* q, const void* k_cache, const voi
                                 dtype, block_size, num_blocks, scale, grid_ctas, dev_err, step,
                                 &a, &info, &nothing);
   if (rc != PA_OK || nothing) return rc;
-  const size_t need =
-      decode_bind_workspace(&a, static_cast<unsigned char*>(workspace), decode_max_ctas(info));
-  if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE;
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return PA_ERR_ALIGN;
+  const int wrc = decode_check_workspace(&a, info, workspace, workspace_bytes);
+  if (wrc != PA_OK) return wrc;
   if (step) return launch_decode_step(a, info, static_cast<cudaStream_t>(stream));
   return launch_decode(a, info, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace pa
+
+namespace pa {
+
+// pa_prefill_varlen and pa_prefill_mod: argument validation and packing. On PA_OK, *nothing
+// is set when there is no query to launch for.
+static int prefill_prepare(void* out, const void* q, const void* k_cache, const void* v_cache,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                           int num_seqs, int max_seqlen_q, int max_seqlen_k, int num_heads,
+                           int num_kv_heads, int head_dim, int dtype, int block_size,
+                           int64_t num_blocks, int causal, float scale, int* dev_err,
+                           PrefillArgs* a, DeviceInfo* info, bool* nothing) {
+  *nothing = false;
+  if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || block_size <= 0 ||
+      num_blocks <= 0 || max_blocks_per_seq < 0 || max_seqlen_q < 0 || max_seqlen_k < 0)
+    return PA_ERR_SHAPE;
+  if (num_heads % num_kv_heads != 0) return PA_ERR_SHAPE;
+  if (!head_dim_supported(head_dim) ||
+      !prefill_supported(num_heads, num_kv_heads, block_size) ||
+      (dtype != PA_DTYPE_BF16 && dtype != PA_DTYPE_F16))
+    return PA_ERR_UNSUPPORTED;
+  if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (max_seqlen_k > (int64_t)max_blocks_per_seq * block_size) return PA_ERR_SHAPE;
+  if (num_seqs == 0 || max_seqlen_q == 0) {
+    *nothing = true;
+    return PA_OK;
+  }
+  if (!out || !q || !k_cache || !v_cache || !cu_seqlens_q || !cu_seqlens_k) return PA_ERR_NULL;
+  if (max_blocks_per_seq > 0 && !block_tables) return PA_ERR_NULL;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) ||
+      !aligned16(v_cache))
+    return PA_ERR_ALIGN;
+  if (!current_device_info(info)) return PA_ERR_CUDA;
+  a->out = out;
+  a->q = q;
+  a->k_cache = k_cache;
+  a->v_cache = v_cache;
+  a->block_tables = block_tables;
+  a->cu_seqlens_q = cu_seqlens_q;
+  a->cu_seqlens_k = cu_seqlens_k;
+  a->max_blocks = max_blocks_per_seq;
+  a->num_seqs = num_seqs;
+  a->max_seqlen_q = max_seqlen_q;
+  a->max_seqlen_k = max_seqlen_k;
+  a->num_heads = num_heads;
+  a->num_kv_heads = num_kv_heads;
+  a->block_size = block_size;
+  a->num_blocks = num_blocks;
+  a->causal = causal ? 1 : 0;
+  a->scale_log2 = resolve_scale(scale, head_dim);
+  a->head_dim = head_dim;
+  a->f16 = dtype == PA_DTYPE_F16;
+  a->dev_err = dev_err;
+  return PA_OK;
 }
 
 }  // namespace pa
@@ -306,46 +391,56 @@ int pa_prefill_varlen(void* out, const void* q, const void* k_cache, const void*
                       int max_seqlen_q, int max_seqlen_k, int num_heads, int num_kv_heads,
                       int head_dim, int dtype, int block_size, int64_t num_blocks, int causal,
                       float scale, int* dev_err, void* stream) {
-  if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || block_size <= 0 ||
-      num_blocks <= 0 || max_blocks_per_seq < 0 || max_seqlen_q < 0 || max_seqlen_k < 0)
-    return PA_ERR_SHAPE;
-  if (num_heads % num_kv_heads != 0) return PA_ERR_SHAPE;
-  if (!pa::head_dim_supported(head_dim) ||
-      !pa::prefill_supported(num_heads, num_kv_heads, block_size) ||
-      (dtype != PA_DTYPE_BF16 && dtype != PA_DTYPE_F16))
-    return PA_ERR_UNSUPPORTED;
-  if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX) return PA_ERR_UNSUPPORTED;
-  if (max_seqlen_k > (int64_t)max_blocks_per_seq * block_size) return PA_ERR_SHAPE;
-  if (num_seqs == 0 || max_seqlen_q == 0) return PA_OK;
-  if (!out || !q || !k_cache || !v_cache || !cu_seqlens_q || !cu_seqlens_k) return PA_ERR_NULL;
-  if (max_blocks_per_seq > 0 && !block_tables) return PA_ERR_NULL;
-  if (!pa::aligned16(out) || !pa::aligned16(q) || !pa::aligned16(k_cache) ||
-      !pa::aligned16(v_cache))
-    return PA_ERR_ALIGN;
-  pa::DeviceInfo info;
-  if (!pa::current_device_info(&info)) return PA_ERR_CUDA;
   pa::PrefillArgs a;
-  a.out = out;
-  a.q = q;
-  a.k_cache = k_cache;
-  a.v_cache = v_cache;
-  a.block_tables = block_tables;
-  a.cu_seqlens_q = cu_seqlens_q;
-  a.cu_seqlens_k = cu_seqlens_k;
-  a.max_blocks = max_blocks_per_seq;
-  a.num_seqs = num_seqs;
-  a.max_seqlen_q = max_seqlen_q;
-  a.max_seqlen_k = max_seqlen_k;
-  a.num_heads = num_heads;
-  a.num_kv_heads = num_kv_heads;
-  a.block_size = block_size;
-  a.num_blocks = num_blocks;
-  a.causal = causal ? 1 : 0;
-  a.scale_log2 = pa::resolve_scale(scale, head_dim);
-  a.head_dim = head_dim;
-  a.f16 = dtype == PA_DTYPE_F16;
-  a.dev_err = dev_err;
+  pa::DeviceInfo info;
+  bool nothing = false;
+  const int rc = pa::prefill_prepare(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                                     cu_seqlens_q, cu_seqlens_k, num_seqs, max_seqlen_q,
+                                     max_seqlen_k, num_heads, num_kv_heads, head_dim, dtype,
+                                     block_size, num_blocks, causal, scale, dev_err, &a, &info,
+                                     &nothing);
+  if (rc != PA_OK || nothing) return rc;
   return pa::launch_prefill(a, info, static_cast<cudaStream_t>(stream));
+}
+
+int pa_decode_mod(void* out, const void* q, const void* k_cache, const void* v_cache,
+                  const int32_t* block_tables, int max_blocks_per_seq,
+                  const int32_t* context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                  int head_dim, int dtype, int block_size, int64_t num_blocks, float scale,
+                  const pa_score_mod* mod, int grid_ctas, void* workspace,
+                  size_t workspace_bytes, int* dev_err, void* stream) {
+  pa::DecodeModArgs a;
+  pa::DeviceInfo info;
+  bool nothing = false;
+  int rc = pa::resolve_mod(mod, scale, head_dim, &a.mod);
+  if (rc != PA_OK) return rc;
+  rc = pa::decode_prepare(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                          context_lens, num_seqs, num_heads, num_kv_heads, head_dim, dtype,
+                          block_size, num_blocks, scale, grid_ctas, dev_err, nullptr, &a, &info,
+                          &nothing);
+  if (rc != PA_OK || nothing) return rc;
+  rc = pa::decode_check_workspace(&a, info, workspace, workspace_bytes);
+  if (rc != PA_OK) return rc;
+  return pa::launch_decode_mod(a, info, static_cast<cudaStream_t>(stream));
+}
+
+int pa_prefill_mod(void* out, const void* q, const void* k_cache, const void* v_cache,
+                   const int32_t* block_tables, int max_blocks_per_seq,
+                   const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int num_seqs,
+                   int max_seqlen_q, int max_seqlen_k, int num_heads, int num_kv_heads,
+                   int head_dim, int dtype, int block_size, int64_t num_blocks, int causal,
+                   float scale, const pa_score_mod* mod, int* dev_err, void* stream) {
+  pa::PrefillModArgs a;
+  pa::DeviceInfo info;
+  bool nothing = false;
+  int rc = pa::resolve_mod(mod, scale, head_dim, &a.mod);
+  if (rc != PA_OK) return rc;
+  rc = pa::prefill_prepare(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                           cu_seqlens_q, cu_seqlens_k, num_seqs, max_seqlen_q, max_seqlen_k,
+                           num_heads, num_kv_heads, head_dim, dtype, block_size, num_blocks,
+                           causal, scale, dev_err, &a, &info, &nothing);
+  if (rc != PA_OK || nothing) return rc;
+  return pa::launch_prefill_mod(a, info, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -77,6 +77,26 @@ struct DecodeArgs {
   int* dev_err;
 };
 
+// Modified scores (pa_score_mod with the factors folded to log2 units): for a query at
+// absolute position p, key t scores
+//   x = cap2 * tanh(q.k * cap_in) - slope_h * log2(e) * |p - t|   (cap2 > 0)
+//   x = q.k * scale_log2 - slope_h * log2(e) * |p - t|            (cap2 = 0)
+// and is visible when (t <= p or the call is not causal or t < prefix) and (window = 0 or
+// t > p - window or t < max(sink, prefix)).
+struct ScoreModArgs {
+  float cap2;                  // softcap * log2(e); 0 = no cap
+  float cap_in;                // scale / softcap
+  const float* slopes;         // [num_heads]; null = no bias
+  int window;                  // 0 = none
+  int sink;
+  const int32_t* prefix_lens;  // [num_seqs]; null = 0
+};
+
+// pa_decode_mod: the decode with modified scores.
+struct DecodeModArgs : DecodeArgs {
+  ScoreModArgs mod;
+};
+
 // The new tokens of pa_decode_step (null for pa_decode and pa_decode_noalloc).
 struct DecodeStepInput {
   const void* k_new;
@@ -123,6 +143,9 @@ int launch_decode_step_d128_f16(const DecodeArgs& a, const DeviceInfo& info, cud
 // The tensor-core path (decode_tc.cuh).
 int launch_decode_tc(const DecodeArgs& a, const DeviceInfo& info, cudaStream_t stream);
 int launch_decode_step_tc(const DecodeArgs& a, const DeviceInfo& info, cudaStream_t stream);
+// Modified scores: the tensor-core kernel, every shape.
+int launch_decode_mod(const DecodeModArgs& a, const DeviceInfo& info, cudaStream_t stream);
+int launch_decode_mod_d64(const DecodeModArgs& a, const DeviceInfo& info, cudaStream_t stream);
 // Shapes that take the tensor-core path: every group of 3..8 query heads per KV head, and
 // groups of 1 or 2 unless the head dimension is 128 and one slab holds all KV heads
 // (num_kv_heads 1, 2, 4 or 8), the case where a CUDA-core tile is one contiguous run of
@@ -162,8 +185,26 @@ struct PrefillArgs {
   int persistent;  // set by the launcher: 1 = one CTA per SM walking a sorted unit list
 };
 
+// pa_prefill_mod: the prefill with modified scores.
+struct PrefillModArgs : PrefillArgs {
+  ScoreModArgs mod;
+};
+
 bool prefill_supported(int num_heads, int num_kv_heads, int block_size);
 int launch_prefill(const PrefillArgs& a, const DeviceInfo& info, cudaStream_t stream);
+int launch_prefill_mod(const PrefillModArgs& a, const DeviceInfo& info, cudaStream_t stream);
+int launch_prefill_mod_d64_bf16(const PrefillModArgs& a, const DeviceInfo& info,
+                                cudaStream_t stream, const CUtensorMap& mk,
+                                const CUtensorMap& mv);
+int launch_prefill_mod_d64_f16(const PrefillModArgs& a, const DeviceInfo& info,
+                               cudaStream_t stream, const CUtensorMap& mk,
+                               const CUtensorMap& mv);
+int launch_prefill_mod_d128_bf16(const PrefillModArgs& a, const DeviceInfo& info,
+                                 cudaStream_t stream, const CUtensorMap& mk,
+                                 const CUtensorMap& mv);
+int launch_prefill_mod_d128_f16(const PrefillModArgs& a, const DeviceInfo& info,
+                                cudaStream_t stream, const CUtensorMap& mk,
+                                const CUtensorMap& mv);
 // The prefill instantiations other than head_dim 128 with bf16, one translation unit each.
 int launch_prefill_d64_bf16(const PrefillArgs& a, const DeviceInfo& info, cudaStream_t stream,
                             const CUtensorMap& mk, const CUtensorMap& mv);

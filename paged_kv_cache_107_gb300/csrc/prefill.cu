@@ -37,18 +37,35 @@ bool prefill_supported(int num_heads, int num_kv_heads, int block_size) {
   return block_size >= 8 && block_size % 8 == 0 && kKeys % block_size == 0;
 }
 
-int launch_prefill(const PrefillArgs& a, const DeviceInfo& info, cudaStream_t stream) {
+static int cache_maps(const PrefillArgs& a, CUtensorMap* mk, CUtensorMap* mv) {
   if (a.num_seqs > 65535 || a.max_seqlen_q <= 0) return PA_ERR_UNSUPPORTED;
-  CUtensorMap mk, mv;
-  if (!make_cache_map(&mk, a.k_cache, a.num_kv_heads, a.head_dim, a.f16, a.block_size,
+  if (!make_cache_map(mk, a.k_cache, a.num_kv_heads, a.head_dim, a.f16, a.block_size,
                       a.num_blocks) ||
-      !make_cache_map(&mv, a.v_cache, a.num_kv_heads, a.head_dim, a.f16, a.block_size,
+      !make_cache_map(mv, a.v_cache, a.num_kv_heads, a.head_dim, a.f16, a.block_size,
                       a.num_blocks))
     return PA_ERR_CUDA;
+  return PA_OK;
+}
+
+int launch_prefill(const PrefillArgs& a, const DeviceInfo& info, cudaStream_t stream) {
+  CUtensorMap mk, mv;
+  const int rc = cache_maps(a, &mk, &mv);
+  if (rc != PA_OK) return rc;
   if (a.head_dim == 128 && !a.f16) return dispatch_prefill<128, false>(a, info, stream, mk, mv);
   if (a.head_dim == 64) return a.f16 ? launch_prefill_d64_f16(a, info, stream, mk, mv)
                                      : launch_prefill_d64_bf16(a, info, stream, mk, mv);
   if (a.head_dim == 128) return launch_prefill_d128_f16(a, info, stream, mk, mv);
+  return PA_ERR_UNSUPPORTED;
+}
+
+int launch_prefill_mod(const PrefillModArgs& a, const DeviceInfo& info, cudaStream_t stream) {
+  CUtensorMap mk, mv;
+  const int rc = cache_maps(a, &mk, &mv);
+  if (rc != PA_OK) return rc;
+  if (a.head_dim == 128) return a.f16 ? launch_prefill_mod_d128_f16(a, info, stream, mk, mv)
+                                      : launch_prefill_mod_d128_bf16(a, info, stream, mk, mv);
+  if (a.head_dim == 64) return a.f16 ? launch_prefill_mod_d64_f16(a, info, stream, mk, mv)
+                                     : launch_prefill_mod_d64_bf16(a, info, stream, mk, mv);
   return PA_ERR_UNSUPPORTED;
 }
 

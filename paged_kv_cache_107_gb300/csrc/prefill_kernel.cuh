@@ -64,8 +64,11 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "pa_device.cuh"
 #include "pa_launch.h"
+#include "score_mod.cuh"
 #include "tensor_map.h"
 #include "umma.cuh"
 
@@ -112,6 +115,16 @@ struct UnitRec {
   int nt;      // key tiles of tile A (bits 0..15) and of tile B (bits 16..31; may be 0)
 };
 
+// With modified scores (MOD) a record also holds the unit's hidden range: the keys from keep
+// up to low are seen by none of its queries; keys below prefix are seen by all of them.
+struct UnitRecMod : UnitRec {
+  int prefix, keep, low;
+};
+template <bool MOD>
+using RecT = std::conditional_t<MOD, UnitRecMod, UnitRec>;
+template <bool MOD>
+using ArgsT = std::conditional_t<MOD, PrefillModArgs, PrefillArgs>;
+
 // Barriers and schedule state; first in shared memory, then the unit records, then the
 // tiles from the next 1024-byte boundary (128-byte swizzle atoms are 1024 bytes).
 struct PrefillCtl {
@@ -143,7 +156,8 @@ struct PrefillTiles {
 constexpr int kCtlBytes = 256;
 constexpr int kRecBytes = 1792;  // fills the opt-in limit at head_dim 128 with the slack below
 // (56 records)
-constexpr int kMaxUnitRecs = kRecBytes / (int)sizeof(UnitRec);
+template <bool MOD>
+constexpr int kMaxUnitRecs = kRecBytes / (int)sizeof(RecT<MOD>);
 static_assert(sizeof(PrefillCtl) <= kCtlBytes, "control block");
 
 template <int D>
@@ -204,20 +218,33 @@ __device__ __forceinline__ bool seq_ok(int n, int kv_len, int cap, int max_q) {
   return n >= 0 && kv_len >= n && kv_len <= cap && n <= max_q;
 }
 
+// The keys that the queries of tile g of a unit see: up to hi for the last of them, from low
+// on for the first of the unit's queries (every tile of a unit walks the same key tiles).
+template <int P, bool MOD>
+__device__ __forceinline__ KeySpan<MOD> tile_span(const ArgsT<MOD>& a, int s, int n, int kv_len,
+                                                  int i0, int g) {
+  const int c_len = kv_len - n;
+  const int rows = min(P, n - (i0 + g * P));
+  KeySpan<MOD> k{0, 0, 0};
+  if (rows <= 0) return k;
+  k.hi = a.causal ? c_len + i0 + g * P + rows : kv_len;
+  if constexpr (MOD) {
+    k.hi = max(k.hi, min(kv_len, mod_prefix(a.mod, s)));
+    mod_span(k, a.mod, s, c_len + i0);
+  }
+  return k;
+}
+
 // Estimated time of a unit (the longest-first order's key), given its first new token i0:
 // a key-tile step that both tiles take costs about 2.1 us on GB300, a step of one tile
 // alone about 1.8 us, and a unit's start and end about 5 us (measured per unit with clock
 // traces of this kernel on the chunked-prefill workload); in units of 0.1 us.
-template <int P>
-__device__ __forceinline__ uint32_t pair_cost(int n, int kv_len, int i0, bool causal) {
-  const int c_len = kv_len - n;
+template <int P, bool MOD>
+__device__ __forceinline__ uint32_t pair_cost(const ArgsT<MOD>& a, int s, int n, int kv_len,
+                                              int i0) {
   int nt[2];
 #pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const int rows = min(P, n - (i0 + g * P));
-    const int keys = rows <= 0 ? 0 : (causal ? c_len + i0 + g * P + rows : kv_len);
-    nt[g] = (keys + kKeys - 1) / kKeys;
-  }
+  for (int g = 0; g < 2; ++g) nt[g] = tile_span<P, MOD>(a, s, n, kv_len, i0, g).tiles(kKeys);
   const uint32_t both = (uint32_t)min(nt[0], nt[1]);
   const uint32_t single = (uint32_t)abs(nt[0] - nt[1]);
   return 21u * both + 18u * single + 50u;
@@ -225,16 +252,12 @@ __device__ __forceinline__ uint32_t pair_cost(int n, int kv_len, int i0, bool ca
 
 // Key tiles each tile of a unit multiplies (causal: up to its last position); tile B may
 // have none.
-template <int P>
-__device__ __forceinline__ int unit_tiles(int n, int kv_len, int i0, bool causal) {
-  const int c_len = kv_len - n;
+template <int P, bool MOD>
+__device__ __forceinline__ int unit_tiles(const ArgsT<MOD>& a, int s, int n, int kv_len, int i0) {
   int packed = 0;
 #pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const int rows = min(P, n - (i0 + g * P));
-    const int keys = rows <= 0 ? 0 : (causal ? c_len + i0 + g * P + rows : kv_len);
-    packed |= ((keys + kKeys - 1) / kKeys) << (16 * g);
-  }
+  for (int g = 0; g < 2; ++g)
+    packed |= tile_span<P, MOD>(a, s, n, kv_len, i0, g).tiles(kKeys) << (16 * g);
   return packed;
 }
 __device__ __forceinline__ int nt_of(int nt, int g) { return (nt >> (16 * g)) & 0xFFFF; }
@@ -242,12 +265,20 @@ __device__ __forceinline__ int nt_all(int nt) { return max(nt & 0xFFFF, nt >> 16
 
 // Completes this CTA's records (ring positions and tile counts; thread 0) and publishes the
 // count. Ends with a block-wide barrier.
-template <int P>
-__device__ void finish_records(PrefillCtl& ctl, UnitRec* recs, int count, bool causal) {
+template <int P, bool MOD>
+__device__ void finish_records(PrefillCtl& ctl, RecT<MOD>* recs, int count,
+                               const ArgsT<MOD>& a) {
   if (threadIdx.x == 0) {
     int v = 0;
     for (int k = 0; k < count; ++k) {
-      recs[k].nt = unit_tiles<P>(recs[k].n, recs[k].kv_len, recs[k].i0, causal);
+      recs[k].nt = unit_tiles<P, MOD>(a, recs[k].s, recs[k].n, recs[k].kv_len, recs[k].i0);
+      if constexpr (MOD) {
+        const KeySpan<true> sp =
+            tile_span<P, MOD>(a, recs[k].s, recs[k].n, recs[k].kv_len, recs[k].i0, 0);
+        recs[k].prefix = mod_prefix(a.mod, recs[k].s);
+        recs[k].keep = sp.keep;
+        recs[k].low = sp.low;
+      }
       recs[k].vbase = v;
       v += nt_all(recs[k].nt);
     }
@@ -257,8 +288,8 @@ __device__ void finish_records(PrefillCtl& ctl, UnitRec* recs, int count, bool c
 }
 
 // One unit per CTA: (KV head, sequence, pair) from the grid, latest pairs first.
-template <int P>
-__device__ void single_schedule(PrefillCtl& ctl, UnitRec* recs, const PrefillArgs& a) {
+template <int P, bool MOD>
+__device__ void single_schedule(PrefillCtl& ctl, RecT<MOD>* recs, const ArgsT<MOD>& a) {
   int count = 0;
   if (threadIdx.x == 0) {
     const int j = blockIdx.x, s = blockIdx.y;
@@ -269,22 +300,22 @@ __device__ void single_schedule(PrefillCtl& ctl, UnitRec* recs, const PrefillArg
     if (!seq_ok(n, kv, a.max_blocks * a.block_size, a.max_seqlen_q)) {
       if (qt == 0 && j == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SEQLENS);
     } else if (qt * 2 * P < n) {
-      recs[0] = UnitRec{q0, n, kv, s, qt * 2 * P, j, 0, 0};
+      static_cast<UnitRec&>(recs[0]) = UnitRec{q0, n, kv, s, qt * 2 * P, j, 0, 0};
       count = 1;
     }
     ctl.n_units = count;
   }
   __syncthreads();
-  finish_records<P>(ctl, recs, ctl.n_units, a.causal != 0);
+  finish_records<P, MOD>(ctl, recs, ctl.n_units, a);
 }
 
 // Builds the sorted schedule (all threads of the CTA take part; ends with a block-wide
 // barrier). The scratch (cu_seqlens copies, per-sequence pair offsets, sort keys) lives in
 // the K ring, which no copy has touched yet. The launcher takes this schedule only when
 // the batch's bounds (num_seqs, max_seqlen_q, KV heads) guarantee that it fits.
-template <int P>
-__device__ void build_schedule(PrefillCtl& ctl, UnitRec* recs, unsigned char* scratch,
-                               const PrefillArgs& a, int cu_q0, int cu_k0) {
+template <int P, bool MOD>
+__device__ void build_schedule(PrefillCtl& ctl, RecT<MOD>* recs, unsigned char* scratch,
+                               const ArgsT<MOD>& a, int cu_q0, int cu_k0) {
   const int tid = threadIdx.x;
   const int S = a.num_seqs, Hk = a.num_kv_heads;
   if (S > kMaxSortSeqs) {  // excluded by the launcher
@@ -344,7 +375,7 @@ __device__ void build_schedule(PrefillCtl& ctl, UnitRec* recs, unsigned char* sc
   const int npairs = carry;
   const int64_t nunits = (int64_t)npairs * Hk;
   const int64_t per_cta = (nunits + gridDim.x - 1) / gridDim.x + 1;
-  if (npairs > kMaxSortPairs || per_cta > kMaxUnitRecs) {  // excluded by the launcher
+  if (npairs > kMaxSortPairs || per_cta > kMaxUnitRecs<MOD>) {  // excluded by the launcher
     if (tid == 0) {
       ctl.n_units = 0;
       if (blockIdx.x == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SEQLENS);
@@ -370,7 +401,7 @@ __device__ void build_schedule(PrefillCtl& ctl, UnitRec* recs, unsigned char* sc
     const int n = cuq[s + 1] - cuq[s];
     const int kv = cuk[s + 1] - cuk[s];
     const uint32_t id = ((uint32_t)s << 12) | (uint32_t)qt;
-    const uint32_t cost = pair_cost<P>(n, kv, qt * 2 * P, a.causal != 0);
+    const uint32_t cost = pair_cost<P, MOD>(a, s, n, kv, qt * 2 * P);
     keys[p] = ((unsigned long long)cost << 32) | (unsigned long long)(0xFFFFFFFFu - id);
   }
   for (int i = npairs + tid; i < n2; i += kThreads) keys[i] = 0ull;
@@ -407,33 +438,51 @@ __device__ void build_schedule(PrefillCtl& ctl, UnitRec* recs, unsigned char* sc
   }
   // this CTA's units: the deal indices k with serp_index(k) < nunits form a prefix
   const int c = (int)blockIdx.x, G = (int)gridDim.x;
-  for (int k = tid; k < kMaxUnitRecs; k += kThreads) {
+  for (int k = tid; k < kMaxUnitRecs<MOD>; k += kThreads) {
     const int64_t idx = serp_index(k, c, G);
     if (idx >= nunits) continue;
     const unsigned long long key = keys[idx / Hk];
     const uint32_t id = 0xFFFFFFFFu - (uint32_t)(key & 0xFFFFFFFFull);
     const int s = (int)(id >> 12), qt = (int)(id & 4095u);
-    recs[k] = UnitRec{cuq[s], cuq[s + 1] - cuq[s], cuk[s + 1] - cuk[s], s, qt * 2 * P,
-                      (int)(idx % Hk), 0, 0};
+    static_cast<UnitRec&>(recs[k]) = UnitRec{cuq[s], cuq[s + 1] - cuq[s], cuk[s + 1] - cuk[s], s,
+                                             qt * 2 * P, (int)(idx % Hk), 0, 0};
   }
   int count = 0;
-  while (count < kMaxUnitRecs && serp_index(count, c, G) < nunits) ++count;
+  while (count < kMaxUnitRecs<MOD> && serp_index(count, c, G) < nunits) ++count;
   __syncthreads();
-  finish_records<P>(ctl, recs, count, a.causal != 0);
+  finish_records<P, MOD>(ctl, recs, count, a);
 }
 
-template <int G, int D, bool F16>
+// Raw products q.k of one row and tile to scores in log2 units (ScoreModArgs), in place; dist
+// is the row's position minus the tile's first key. Without a cap or slopes the products
+// stay as they are (the softmax scales them).
+__device__ __forceinline__ void mod_scores(float* sv, const ScoreModArgs& m, float scale_log2,
+                                           float slope2, int dist) {
+  if (m.cap2 > 0.f) {
+#pragma unroll
+    for (int c = 0; c < kKeys; ++c) sv[c] = m.cap2 * cap_tanh(sv[c] * m.cap_in);
+  }
+  if (m.slopes) {
+    const float pre = m.cap2 > 0.f ? 1.f : scale_log2;
+#pragma unroll
+    for (int c = 0; c < kKeys; ++c)
+      sv[c] = fmaf(sv[c], pre, -slope2 * fabsf((float)(dist - c)));
+  }
+}
+
+template <int G, int D, bool F16, bool MOD = false>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
-                         const __grid_constant__ CUtensorMap tm_q, const PrefillArgs a) {
+                         const __grid_constant__ CUtensorMap tm_q, const ArgsT<MOD> a) {
   constexpr int P = kRows / G;  // query positions per tile
   constexpr int NH = D / 64;    // 64-dim swizzled column blocks per row
   constexpr bool kSepP = D == 64;  // P in its own tensor-memory columns (see col_p)
   using Tiles = PrefillTiles<D>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   PrefillCtl& ctl = *reinterpret_cast<PrefillCtl*>(smem_raw);
-  UnitRec* recs = reinterpret_cast<UnitRec*>(smem_raw + kCtlBytes);
+  using Rec = RecT<MOD>;
+  Rec* recs = reinterpret_cast<Rec*>(smem_raw + kCtlBytes);
   Tiles& sm = *reinterpret_cast<Tiles*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + kCtlBytes + kRecBytes + 1023) & ~uintptr_t(1023));
 
@@ -479,8 +528,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     umma::tmem_relinquish();
   }
   __syncthreads();
-  if (a.persistent) build_schedule<P>(ctl, recs, &sm.k[0][0], a, cu_q0, cu_k0);
-  else single_schedule<P>(ctl, recs, a);
+  if (a.persistent) build_schedule<P, MOD>(ctl, recs, &sm.k[0][0], a, cu_q0, cu_k0);
+  else single_schedule<P, MOD>(ctl, recs, a);
+  // first key of the it-th key tile of a unit (MOD: the hidden tiles are left out)
+  auto tile_key0 = [&](const Rec& u, int it) {
+    if constexpr (MOD) return KeySpan<true>{u.kv_len, u.low, u.keep}.first_key(kKeys, it);
+    else return it * kKeys;
+  };
   // the schedule's scratch in the K ring was written through the generic proxy; TMA (the
   // async proxy) writes there next
   fence_proxy_async_smem();
@@ -513,9 +567,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -2 out of the pool
     auto read_id = [&](int k, int it) {
       if (k >= n_units || lane >= boxes) return -1;
-      const UnitRec& u = recs[k];
-      const int key0 = it * kKeys + lane * box_rows;
+      const Rec& u = recs[k];
+      const int key0 = tile_key0(u, it) + lane * box_rows;
       if (key0 >= u.kv_len) return -1;
+      if constexpr (MOD) {  // a box that no query of the unit sees is not read
+        if (key0 >= u.keep && key0 + box_rows <= u.low) return -1;
+      }
       const int id = __ldg(a.block_tables + (int64_t)u.s * a.max_blocks + key0 / bs);
       return (id >= 0 && (int64_t)id < a.num_blocks) ? id : -2;
     };
@@ -532,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k2 = k1, it2 = it1;
     advance(k2, it2);
     int id0 = read_id(0, 0), id1 = read_id(k1, it1), id2 = read_id(k2, it2);
-    auto load = [&](bool is_v, int hj, int it, int id) {
+    auto load = [&](bool is_v, int hj, int key0, int id) {
       const int stages = is_v ? kVStages : kKStages;
       const int cnt = is_v ? vl++ : kl++;
       const int st = cnt % stages;
@@ -548,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(full, (uint32_t)__popc(valid) * NH * box_rows * 128u);
       __syncwarp();  // the stage is free and its bytes are expected: each box's lane copies
       if (id >= 0) {
-        const int row0 = (bs > kKeys) ? ((it * kKeys) % bs) : 0;
+        const int row0 = (bs > kKeys) ? (key0 % bs) : 0;
         unsigned char* dst = (is_v ? sm.v[st] : sm.k[st]) + lane * box_rows * 128;
         const CUtensorMap* map = is_v ? &tm_v : &tm_k;
         for (int h2 = 0; h2 < NH; ++h2)
@@ -560,10 +617,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_all = nt_all(recs[k].nt);
       const int hj = recs[k].j;
       // K runs one tile ahead of V: S(i+1) is issued right after PV(i)
-      load(false, hj, 0, id0);
+      load(false, hj, tile_key0(recs[k], 0), id0);
       for (int it = 0; it < n_all; ++it) {
-        load(true, hj, it, id0);
-        if (it + 1 < n_all) load(false, hj, it + 1, id1);
+        load(true, hj, tile_key0(recs[k], it), id0);
+        if (it + 1 < n_all) load(false, hj, tile_key0(recs[k], it + 1), id1);
         // shift the window one tile along the stream
         id0 = id1;
         id1 = id2;
@@ -741,11 +798,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) umma::prefetch_tmap(&tm_q);
     uint32_t qep = 0, started = 0;  // per tile: parity of its next q_empty phase; first done
     int qn[2] = {0, 0};             // Q copies issued per tile (one q_full phase each)
-    auto box_ok = [&](const UnitRec& u, int g) {
+    auto box_ok = [&](const Rec& u, int g) {
       return (int64_t)u.q0 + u.i0 + g * P + P <= q_rows;
     };
     for (int k = 0; k < n_units; ++k) {
-      const UnitRec& u = recs[k];
+      const Rec& u = recs[k];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         if (nt_of(u.nt, g) == 0) continue;
@@ -820,13 +877,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (k < n_units) {
       const int kn = next_unit(k);
       int lim_row, kv_len, vbase, my_nt;
-      {
-        const UnitRec& u = recs[k];
-        const int qpos = (u.kv_len - u.n) + u.i0 + g * P + pos;  // absolute position of the row
+      int qpos;          // absolute position of the row
+      int low_row = 0;   // MOD: of the keys [0, lim_row) those below keep or from low_row on
+      {                  // count
+        const Rec& u = recs[k];
+        qpos = (u.kv_len - u.n) + u.i0 + g * P + pos;
         kv_len = u.kv_len;
         lim_row = causal ? min(kv_len, qpos + 1) : kv_len;  // keys [0, lim_row) count
         vbase = u.vbase;
         my_nt = nt_of(u.nt, g);
+        if constexpr (MOD) {
+          lim_row = max(lim_row, min(kv_len, u.prefix));
+          if (a.mod.window > 0) low_row = qpos - a.mod.window + 1;
+        }
+      }
+      float score_scale = a.scale_log2;  // of the values that the softmax below reads
+      float slope2 = 0.f;
+      if constexpr (MOD) {
+        if (a.mod.slopes)
+          slope2 = __ldg(a.mod.slopes + recs[k].j * G + hh) * 1.4426950408889634f;
+        if (a.mod.slopes || a.mod.cap2 > 0.f) score_scale = 1.f;
       }
       float m_run = -INFINITY, l_run = 0.f;
       for (int it = 0; it < my_nt; ++it) {
@@ -842,12 +912,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&ctl.s_free[g]);
         }
 
-        const int t0 = it * kKeys;
+        const int t0 = tile_key0(recs[k], it);
+        if constexpr (MOD) mod_scores(sv, a.mod, a.scale_log2, slope2, qpos - t0);
         // only tiles that reach past this row's last visible key need a mask
         if (__any_sync(0xffffffffu, t0 + kKeys > lim_row)) {
 #pragma unroll
           for (int c = 0; c < kKeys; ++c)
             if (t0 + c >= lim_row) sv[c] = -INFINITY;
+        }
+        if constexpr (MOD) {
+          // ... or that hold keys before its window
+          const int keep = recs[k].keep;
+          if (__any_sync(0xffffffffu, t0 < low_row && t0 + kKeys > keep)) {
+#pragma unroll
+            for (int c = 0; c < kKeys; ++c)
+              if (t0 + c < low_row && t0 + c >= keep) sv[c] = -INFINITY;
+          }
         }
         float mx[8];
 #pragma unroll
@@ -855,8 +935,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 8; c < kKeys; ++c) mx[c & 7] = fmaxf(mx[c & 7], sv[c]);
         // the scale is positive, so the max of the scaled scores is the scaled max
-        const float mt = a.scale_log2 * fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                              fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        const float mt = score_scale * fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
         float m_use, alpha;
         bool rescale = false;
         if (it == 0) {
@@ -873,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m_safe = (m_use == -INFINITY) ? 0.f : m_use;
         // p = 2^(s*scale - m): one packed fma per pair, then ex2; P packed as 16-bit pairs
         // over S, in the element type of V (the PV product takes both operands in one type)
-        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+        const float2 sc2 = make_float2(score_scale, score_scale);
         const float2 nm2 = make_float2(-m_safe, -m_safe);
         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                          make_float2(0.f, 0.f)};
@@ -914,14 +994,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma::tmem_st32(lane_addr + col_o(g) + 32 * c4, ob);
           }
         }
-        // rows of the last V tile beyond the sequence: zero them (never multiply a stale row)
-        if (t0 + kKeys > kv_len) {
+        // rows of the last V tile beyond the sequence (MOD: and rows that no query of the unit
+        // sees): zero them (never multiply a stale row)
+        bool v_hidden = false;
+        if constexpr (MOD) v_hidden = t0 < recs[k].low && t0 + kKeys > recs[k].keep;
+        if (t0 + kKeys > kv_len || v_hidden) {
           const int vi = vbase + it;
           const int st = vi % kVStages;
           if (!mbar_wait(&ctl.v_full[st], (uint32_t)((vi / kVStages) & 1), abort_flag))
             note_timeout(ctl, a.dev_err);
-          const int first_bad = kv_len - t0;
-          if (r >= first_bad) {
+          bool bad = t0 + r >= kv_len;
+          if constexpr (MOD) bad = bad || (t0 + r < recs[k].low && t0 + r >= recs[k].keep);
+          if (bad) {
 #pragma unroll
             for (int ch = 0; ch < D / 8; ++ch)
               *reinterpret_cast<uint4*>(sm.v[st] + (ch >> 3) * kHalf + r * 128 + (ch & 7) * 16) =
@@ -939,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++oc;
       umma::fence_after_sync();
       const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-      const UnitRec& u = recs[k];
+      const Rec& u = recs[k];
       const int qi = u.i0 + g * P + pos;
       const bool row_ok = qi < u.n;
       uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
@@ -983,8 +1067,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }
 
-template <int G, int D, bool F16>
-int launch_prefill_t(const PrefillArgs& a, const DeviceInfo& info, cudaStream_t stream,
+template <int G, int D, bool F16, bool MOD = false>
+int launch_prefill_t(const ArgsT<MOD>& a, const DeviceInfo& info, cudaStream_t stream,
                      const CUtensorMap& mk, const CUtensorMap& mv) {
   constexpr int P = kRows / G;
   constexpr size_t smem = prefill_smem_bytes<D>();
@@ -993,7 +1077,8 @@ int launch_prefill_t(const PrefillArgs& a, const DeviceInfo& info, cudaStream_t 
   if (info.device < 0 || info.device >= 64) return PA_ERR_CUDA;
   if ((size_t)info.max_smem_optin < smem) return PA_ERR_UNSUPPORTED;
   if (!attr_done[info.device].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(paged_prefill_kernel<G, D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(paged_prefill_kernel<G, D, F16, MOD>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem) != cudaSuccess)
       return PA_ERR_CUDA;
     attr_done[info.device].store(true, std::memory_order_release);
@@ -1001,33 +1086,33 @@ int launch_prefill_t(const PrefillArgs& a, const DeviceInfo& info, cudaStream_t 
   const int64_t qt_n = (a.max_seqlen_q + 2 * P - 1) / (2 * P);  // pairs per sequence at most
   const int64_t max_pairs = qt_n * a.num_seqs;
   const int64_t max_units = max_pairs * a.num_kv_heads;
-  PrefillArgs args = a;
+  ArgsT<MOD> args = a;
   CUtensorMap mq;
   if (!make_rows_map(&mq, a.q, q_map_rows(a), a.num_heads, D, F16, G, P)) return PA_ERR_CUDA;
   // persistent (one CTA per SM, fewer when the batch has fewer units) when the in-kernel
   // sort and every CTA's records are sure to hold the batch; else one unit per CTA
   const int grid1 = (int)(max_units < info.num_sms ? max_units : info.num_sms);
   args.persistent = a.num_seqs <= kMaxSortSeqs && max_pairs <= kMaxSortPairs && grid1 > 0 &&
-                    (max_units + grid1 - 1) / grid1 + 1 <= kMaxUnitRecs;
+                    (max_units + grid1 - 1) / grid1 + 1 <= kMaxUnitRecs<MOD>;
   if (args.persistent) {
-    paged_prefill_kernel<G, D, F16><<<grid1, kThreads, smem, stream>>>(mk, mv, mq, args);
+    paged_prefill_kernel<G, D, F16, MOD><<<grid1, kThreads, smem, stream>>>(mk, mv, mq, args);
   } else {
     if (qt_n > 65535) return PA_ERR_UNSUPPORTED;
     dim3 grid((unsigned)a.num_kv_heads, (unsigned)a.num_seqs, (unsigned)qt_n);
-    paged_prefill_kernel<G, D, F16><<<grid, kThreads, smem, stream>>>(mk, mv, mq, args);
+    paged_prefill_kernel<G, D, F16, MOD><<<grid, kThreads, smem, stream>>>(mk, mv, mq, args);
   }
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// Every GQA group size for one (head_dim, element type) combination.
-template <int D, bool F16>
-int dispatch_prefill(const PrefillArgs& a, const DeviceInfo& info, cudaStream_t stream,
+// Every GQA group size for one (head_dim, element type, form) combination.
+template <int D, bool F16, bool MOD = false>
+int dispatch_prefill(const ArgsT<MOD>& a, const DeviceInfo& info, cudaStream_t stream,
                      const CUtensorMap& mk, const CUtensorMap& mv) {
   switch (a.num_heads / a.num_kv_heads) {
-    case 1: return launch_prefill_t<1, D, F16>(a, info, stream, mk, mv);
-    case 2: return launch_prefill_t<2, D, F16>(a, info, stream, mk, mv);
-    case 4: return launch_prefill_t<4, D, F16>(a, info, stream, mk, mv);
-    case 8: return launch_prefill_t<8, D, F16>(a, info, stream, mk, mv);
+    case 1: return launch_prefill_t<1, D, F16, MOD>(a, info, stream, mk, mv);
+    case 2: return launch_prefill_t<2, D, F16, MOD>(a, info, stream, mk, mv);
+    case 4: return launch_prefill_t<4, D, F16, MOD>(a, info, stream, mk, mv);
+    case 8: return launch_prefill_t<8, D, F16, MOD>(a, info, stream, mk, mv);
     default: return PA_ERR_UNSUPPORTED;
   }
 }
