@@ -451,6 +451,55 @@ int pa_prefill_mod(void* out, const void* q, const void* k_cache, const void* v_
                    int head_dim, int dtype, int block_size, int64_t num_blocks, int causal,
                    float scale, const pa_score_mod* mod, int* dev_err, void* stream);
 
+/*
+ * pa_decode_shared_workspace_size — bytes of scratch that pa_decode_shared needs for num_seqs
+ * sequences on the CURRENT device. Returns 0 for invalid sizes.
+ *
+ * pa_decode_shared — pa_decode for a batch in groups of sequences that hold the same leading
+ * positions (a system prompt, a document): the shared part is read once for its group.
+ * Source: "nano-vllm解读", section "前缀缓存" (sequences with a common prefix hold the same
+ * blocks), and the sources of pa_decode. The result is pa_decode's on the same tensors, up
+ * to the rounding of probabilities and of the final combine.
+ *
+ *   group_starts    device, int32 [num_groups + 1], non-decreasing from 0 to num_seqs: group
+ *                   g is the sequences group_starts[g] .. group_starts[g+1] - 1. Groups may
+ *                   be empty (a captured graph's spare ones) or hold one sequence.
+ *   prefix_lens     device, int32 [num_groups], >= 0: the sequences of group g hold the same
+ *                   keys and values at their first prefix_lens[g] positions. They are read
+ *                   through the block table of the group's first sequence; the other tables'
+ *                   entries for blocks wholly inside the prefix are not read when the group
+ *                   is computed together. Any length is allowed, whole blocks or not.
+ *   num_groups      1 .. num_seqs (any value for an empty batch).
+ *   num_seqs        at most 8192, else PA_ERR_UNSUPPORTED.
+ *   workspace       device scratch of at least pa_decode_shared_workspace_size(...) bytes,
+ *                   256-byte aligned. Its contents before a call do not matter, and one sized
+ *                   for more sequences serves fewer. Calls that overlap in time must use
+ *                   different workspaces.
+ *   everything else as pa_decode.
+ *
+ * A sequence's context must reach at least to the end of its group's prefix; one of length 0
+ * (a padding row) writes a zero row, and must not be the first of a group that has a prefix
+ * and other members. A context that ends inside the prefix sets PA_DEV_ERR_CONTEXT. Arrays
+ * that do not describe groups of the batch (or a prefix above max_blocks_per_seq*block_size)
+ * set PA_DEV_ERR_SEQLENS; the sequences are then decoded as by pa_decode.
+ * Block sizes that no power of two from 8 up divides are accepted, without sharing.
+ *
+ * Two launches: the shared parts on the tcgen05 tensor cores, then the rest of every sequence
+ * and the combine. Both are programmatic dependents: the rule of pa_decode on context_lens
+ * and block_tables holds for group_starts and prefix_lens too. Graph-capturable: the arrays
+ * may change between replays. The result does not depend on the order in which CTAs finish.
+ */
+size_t pa_decode_shared_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                       int head_dim);
+
+int pa_decode_shared(void* out, const void* q, const void* k_cache, const void* v_cache,
+                     const int32_t* block_tables, int max_blocks_per_seq,
+                     const int32_t* context_lens, const int32_t* group_starts,
+                     const int32_t* prefix_lens, int num_seqs, int num_groups, int num_heads,
+                     int num_kv_heads, int head_dim, int dtype, int block_size,
+                     int64_t num_blocks, float scale, void* workspace, size_t workspace_bytes,
+                     int* dev_err, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,7 +21,8 @@ from . import build as _build
 
 __all__ = ["pa_store_kvcache", "pa_decode", "pa_decode_step", "pa_decode_workspace_size",
            "pa_prefill_varlen", "pa_decode_noalloc", "pa_decode_mod", "pa_prefill_mod",
-           "ScoreMod", "pa_staged_write_apply",
+           "ScoreMod", "pa_decode_shared", "pa_decode_shared_workspace_size",
+           "SharedDecodeWorkspace", "pa_staged_write_apply",
            "pa_staged_pack", "pa_staged_pack_bound", "pa_staged_upload_apply",
            "PaStagedLayout", "pa_sample_workspace_size", "pa_gumbel_sample",
            "SampleWorkspace",
@@ -655,4 +656,77 @@ def pa_prefill_mod(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
             float(scale) if scale is not None else 0.0, ctypes.byref(rules), _ptr(dev_err),
             _stream(stream))
     _check(rc, "pa_prefill_mod")
+    return out
+
+
+# ---------------------------------------------------------------- shared prefixes
+def pa_decode_shared_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int,
+                                    head_dim: int = 128) -> int:
+    i32 = ctypes.c_int
+    fn = _typed("pa_decode_shared_workspace_size", [i32, i32, i32, i32], ctypes.c_size_t)
+    return int(fn(num_seqs, num_heads, num_kv_heads, head_dim))
+
+
+class SharedDecodeWorkspace:
+    """Scratch of pa_decode_shared (its contents before a call do not matter). One workspace per
+    stream of concurrent calls."""
+
+    def __init__(self, num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int = 128,
+                 device=None):
+        n = pa_decode_shared_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim)
+        if n == 0:
+            raise PagedAttentionError("invalid decode workspace sizes")
+        self.nbytes = n
+        self.buffer = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+    def fits(self, num_seqs, num_heads, num_kv_heads, head_dim=128) -> bool:
+        return pa_decode_shared_workspace_size(num_seqs, num_heads, num_kv_heads,
+                                               head_dim) <= self.nbytes
+
+
+def pa_decode_shared(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, block_tables: torch.Tensor,
+                     context_lens: torch.Tensor, group_starts: torch.Tensor,
+                     prefix_lens: torch.Tensor, scale: Optional[float] = None,
+                     workspace: Optional[SharedDecodeWorkspace] = None,
+                     dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_decode for a batch in groups: sequences group_starts[g]..group_starts[g+1]-1 (int32
+    [groups + 1]) hold the same first prefix_lens[g] positions (int32 [groups]), which are read
+    once for the group."""
+    vp, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
+                             ctypes.c_size_t)
+    _need16(q, "q", 3)
+    for name, t, dt, nd in (("out", out, q.dtype, 3), ("q", q, q.dtype, 3),
+                            ("k_cache", k_cache, q.dtype, 4),
+                            ("v_cache", v_cache, q.dtype, 4),
+                            ("block_tables", block_tables, torch.int32, 2),
+                            ("context_lens", context_lens, torch.int32, 1),
+                            ("group_starts", group_starts, torch.int32, 1),
+                            ("prefix_lens", prefix_lens, torch.int32, 1)):
+        _need(t, name, dt, nd)
+        if not t.is_contiguous():
+            raise PagedAttentionError(f"{name} must be contiguous")
+    B, H, D = q.shape
+    nb, bs, hk, d2 = k_cache.shape
+    groups = prefix_lens.shape[0]
+    if out.shape != q.shape or d2 != D or v_cache.shape != k_cache.shape:
+        raise PagedAttentionError("shape mismatch")
+    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise PagedAttentionError("block_tables / context_lens batch mismatch")
+    if group_starts.shape[0] != groups + 1:
+        raise PagedAttentionError("group_starts must have one entry more than prefix_lens")
+    _one_device(out, q, k_cache, v_cache, block_tables, context_lens, group_starts, prefix_lens,
+                None if workspace is None else workspace.buffer, dev_err, stream=stream)
+    if workspace is None:
+        workspace = _stream_workspace(
+            ("shared", H, hk, D), lambda: SharedDecodeWorkspace(max(B, 1), H, hk, D, q.device),
+            lambda w: w.fits(B, H, hk, D), q.device, stream)
+    fn = _typed("pa_decode_shared", [vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32,
+                                     i32, i32, i64, f32, vp, sz, vp, vp])
+    rc = fn(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+            block_tables.shape[1], _ptr(context_lens), _ptr(group_starts), _ptr(prefix_lens), B,
+            groups, H, hk, D, PA_DTYPE[q.dtype], bs, nb,
+            float(scale) if scale is not None else 0.0, _ptr(workspace.buffer), workspace.nbytes,
+            _ptr(dev_err), _stream(stream))
+    _check(rc, "pa_decode_shared")
     return out

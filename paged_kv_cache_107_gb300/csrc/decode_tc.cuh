@@ -41,6 +41,7 @@
 
 #include "decode_kernel.cuh"
 #include "score_mod.cuh"
+#include "shared_groups.cuh"
 #include "tensor_map.h"
 
 namespace pa {
@@ -48,10 +49,10 @@ namespace {
 
 constexpr int kTcGMax = 8;   // query heads per KV head on this path (rows of the 16-row tile)
 
-// What a stage's tile needs beyond StageMeta with modified scores: key t of the sequence is
-// visible when t < keep or t >= low; the position of the query.
-struct __align__(16) ModMeta : StageMeta {
-  int keep, low, pos;
+// What a stage's tile needs beyond StageMeta where keys may be hidden: key t of the sequence
+// is visible when t < keep or t >= low; the position of the query; the sequence's group.
+struct __align__(16) SpanMeta : StageMeta {
+  int keep, low, pos, group;
 };
 
 template <int S, typename Meta = StageMeta>
@@ -96,7 +97,7 @@ struct TcCfg {
   static constexpr size_t SMEM =
       1024 + (size_t)STAGES * STAGE_BYTES + (size_t)QS * Q_BYTES + CTRL_BYTES;
   static_assert(STAGES >= 2, "at least two stages");
-  static_assert(sizeof(TcCtrl<STAGES, ModMeta>) <= CTRL_BYTES, "control block");
+  static_assert(sizeof(TcCtrl<STAGES, SpanMeta>) <= CTRL_BYTES, "control block");
   static_assert(HS * (WPH - 1) * MERGE_FLOATS * 4 <= 2 * KV_BYTES, "merge scratch");
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
@@ -157,8 +158,9 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// The kernel's forms: plain, or with modified scores (pa_decode_mod).
-enum TcForm { kTcPlain = 0, kTcMod = 1 };
+// The kernel's forms: plain; with modified scores (pa_decode_mod); the part of pa_decode_shared
+// behind the shared prefix, joined with the prefix kernel's partial results.
+enum TcForm { kTcPlain = 0, kTcMod = 1, kTcShared = 2 };
 template <int FORM>
 struct TcArgs {
   using type = DecodeArgs;
@@ -167,6 +169,124 @@ template <>
 struct TcArgs<kTcMod> {
   using type = DecodeModArgs;
 };
+
+template <>
+struct TcArgs<kTcShared> {
+  using type = DecodeSharedArgs;
+};
+
+// The partial results that the prefix kernel left for (sequence b of group grp, KV head kvh).
+struct PrefixParts {
+  int n;            // parts
+  int64_t c0;       // CTA of the first
+  int row;          // row of the sequence's first head within a CTA's 256
+  const float *first_o, *first_lse, *more_o, *more_lse;  // first_*: at (b, first head of kvh)
+  // log-sum-exp and row of head h in part i
+  __device__ __forceinline__ const float* lse(int i, int h) const {
+    return i == 0 ? first_lse + h : more_lse + (c0 + i) * 256 + row + h;
+  }
+  __device__ __forceinline__ const float* o(int i, int h, int D) const {
+    return i == 0 ? first_o + (int64_t)h * D : more_o + ((c0 + i) * 256 + row + h) * D;
+  }
+};
+
+__device__ __forceinline__ PrefixParts prefix_parts(const DecodeSharedArgs& a, int b, int grp,
+                                                    int kvh, int D) {
+  const SharedArgs& sh = a.sh;
+  const int H = a.num_heads, Hk = a.num_kv_heads, G = H / Hk, P = kPrefixRows / G;
+  const int first = __ldg(sh.group_starts + grp);
+  const GroupWork w(sh, __ldg(sh.group_starts + grp + 1) - first, __ldg(sh.prefix_lens + grp), P);
+  const int tile = (b - first) / P;
+  const int64_t nx = __ldcg(sh.plan);
+  const int64_t x = __ldcg(sh.plan + 1 + grp) + w.unit_first(Hk, tile >> 1, kvh);
+  const int ctas = prefix_ctas(nx, sh.prefix_grid);
+  PrefixParts p;
+  p.c0 = prefix_cta_of(x, nx, ctas);
+  p.n = (int)(prefix_cta_of(x + w.unit_steps(tile >> 1) - 1, nx, ctas) - p.c0) + 1;
+  p.row = (tile & 1) * kPrefixRows + ((b - first) % P) * G;
+  p.first_o = sh.first_o + ((int64_t)b * H + kvh * G) * D;
+  p.first_lse = sh.first_lse + (int64_t)b * H + kvh * G;
+  p.more_o = sh.more_o;
+  p.more_lse = sh.more_lse;
+  return p;
+}
+
+// combine_partials with the prefix's parts before the nseg segments of the rest (in that
+// order; nseg may be 0). One warp.
+template <int D, bool F16>
+__device__ __forceinline__ void combine_shared(const DecodeSharedArgs& a, int b, int grp, int kvh,
+                                               int G, int64_t c_lo, int nseg, int64_t NT,
+                                               int g_eff, int64_t pb, int lane) {
+  constexpr int CPL = D / 32;  // combined dims per lane
+  constexpr int SU = 4;        // parts whose loads are in flight together
+  const int H = a.num_heads;
+  const PrefixParts parts = prefix_parts(a, b, grp, kvh, D);
+  const int total = parts.n + nseg;
+  auto seg_at = [&](int i) {  // slot of segment i of the rest
+    const int64_t c = c_lo + i;
+    return c * 2 + (tile_begin(c, NT, g_eff) < pb ? 1 : 0);
+  };
+  const int SB = 32 / G;  // parts per batch; lane h + G*j holds head h of part j
+  const int my_h = lane % G, my_j = lane / G;
+  for (int h = 0; h < G; ++h) {
+    float m = -INFINITY, den = 0.f, acc[CPL];
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
+    for (int s0 = 0; s0 < total; s0 += SB) {
+      const int nb = min(SB, total - s0);
+      float ls = -INFINITY;
+      const int mine = s0 + my_j;
+      if (my_j < nb)
+        ls = __ldcg(mine < parts.n ? parts.lse(mine, my_h)
+                                   : a.part_lse + seg_at(mine - parts.n) * H + kvh * G + my_h);
+      float bm = m;
+      for (int j = 0; j < nb; ++j) bm = fmaxf(bm, __shfl_sync(0xffffffffu, ls, h + G * j));
+      const float al = m == -INFINITY ? 0.f : fast_exp2(m - bm);
+      den *= al;
+#pragma unroll
+      for (int e = 0; e < CPL; ++e) acc[e] *= al;
+      m = bm;
+      for (int j0 = 0; j0 < nb; j0 += SU) {
+        float w[SU], po[SU][CPL];
+#pragma unroll
+        for (int u = 0; u < SU; ++u) {
+          const int j = j0 + u;
+          const float l = __shfl_sync(0xffffffffu, ls, j < nb ? h + G * j : 0);
+          w[u] = j < nb && l != -INFINITY ? fast_exp2(l - m) : 0.f;
+#pragma unroll
+          for (int e = 0; e < CPL; ++e) po[u][e] = 0.f;
+          if (w[u] != 0.f) {
+            const int i = s0 + j;
+            const float* src = i < parts.n
+                                   ? parts.o(i, h, D)
+                                   : a.part_o + (seg_at(i - parts.n) * H + kvh * G + h) * D;
+            if constexpr (CPL == 4) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(src + lane * 4));
+              po[u][0] = v.x, po[u][1] = v.y, po[u][2] = v.z, po[u][3] = v.w;
+            } else {
+              const float2 v = __ldcg(reinterpret_cast<const float2*>(src + lane * 2));
+              po[u][0] = v.x, po[u][1] = v.y;
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < SU; ++u) {
+          den += w[u];
+#pragma unroll
+          for (int e = 0; e < CPL; ++e) acc[e] = fmaf(w[u], po[u][e], acc[e]);
+        }
+      }
+    }
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    uint16_t* dst =
+        static_cast<uint16_t*>(a.out) + ((int64_t)b * H + kvh * G + h) * D + lane * CPL;
+    if constexpr (CPL == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(f2_elt2<F16>(acc[0] * inv, acc[1] * inv),
+                                                  f2_elt2<F16>(acc[2] * inv, acc[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(dst) = f2_elt2<F16>(acc[0] * inv, acc[1] * inv);
+  }
+}
 
 template <int HS, bool FUSED, int D, bool F16, int FORM = kTcPlain>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -180,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* qbuf = smem + (size_t)S * TC::STAGE_BYTES;
-  using Meta = std::conditional_t<FORM == kTcMod, ModMeta, StageMeta>;
+  using Meta = std::conditional_t<FORM != kTcPlain, SpanMeta, StageMeta>;
   using Ctrl = TcCtrl<S, Meta>;
   Ctrl& ctl = *reinterpret_cast<Ctrl*>(qbuf + (size_t)TC::QS * TC::Q_BYTES);
 
@@ -196,10 +316,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int B = a.num_seqs;
   constexpr int T = TC::T;
   constexpr bool kHidden = FORM != kTcPlain;
-  // the keys of sequence b that count (every form but the modified one: all of them)
+  // kTcShared: the group arrays in shared memory while the split is found (then the stages
+  // take their place and the producer follows the groups in global memory)
+  int* g_starts = reinterpret_cast<int*>(smem);
+  int* g_prefix = g_starts;
+  bool groups_ok = false;
+  // leading keys of a group that the prefix kernel has taken
+  auto shared_of = [&](int n, int prefix) {
+    if constexpr (FORM == kTcShared) return groups_ok ? shared_len(a.sh, n, prefix) : 0;
+    else return 0;
+  };
+  auto group_low = [&](int grp) {  // from the copy in shared memory
+    return shared_of(g_starts[grp + 1] - g_starts[grp], g_prefix[grp]);
+  };
+  // the keys of sequence b that this kernel takes (the plain form: all of the context)
   auto span_of = [&](int b) {
     KeySpan<kHidden> k{load_ctx(a.context_lens, b, cap), 0, 0};
     if constexpr (FORM == kTcMod) mod_span(k, a.mod, b, k.hi - 1);
+    if constexpr (FORM == kTcShared) {
+      k.low = group_low(group_of(g_starts, a.sh.num_groups, b));
+      if (k.low >= k.hi) k.hi = k.low = 0;  // nothing behind the prefix
+    }
     return k;
   };
 
@@ -225,6 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // waits for this grid before touching its results)
   pdl_launch_dependents();
 
+  if constexpr (FORM == kTcShared) {
+    g_prefix = g_starts + a.sh.num_groups + 1;
+    groups_ok = load_groups(a.sh, B, cap, g_starts, g_prefix);
+  }
   // ---- prologue: total tiles, then the sequence that holds this CTA's first tile -----
   int64_t local = 0;
   for (int b = tid; b < B; b += kThreads) {
@@ -235,6 +376,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // FUSED: a token of an empty sequence has no position to be stored at
     if (FUSED && (raw <= 0 || raw > cap) && __ldg(a.slot_mapping + b) != -1) {
       if ((b % gridDim.x) == c && slab == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SLOT);
+    }
+    if constexpr (FORM == kTcShared) {  // a context that ends inside its group's prefix
+      if (raw > 0 && raw < group_low(group_of(g_starts, a.sh.num_groups, b)) &&
+          (b % gridDim.x) == c && slab == 0)
+        set_dev_err(a.dev_err, PA_DEV_ERR_CONTEXT);
     }
     local += span_of(b).tiles(T);
   }
@@ -337,7 +483,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   {
     const int heads_per_slab = HS * G;
     for (int b = c + warp * (int)gridDim.x; b < B; b += (kThreads / 32) * (int)gridDim.x) {
-      if (load_ctx(a.context_lens, b, cap) != 0) continue;
+      if (load_ctx(a.context_lens, b, cap) != 0) {
+        if constexpr (FORM == kTcShared) {  // all of the context is shared: only to be joined
+          if (span_of(b).hi == 0) {
+            const int grp = group_of(g_starts, a.sh.num_groups, b);
+            for (int j = 0; j < HS; ++j)
+              combine_shared<D, F16>(a, b, grp, slab * HS + j, G, 0, 0, 1, 1, 0, lane);
+          }
+        }
+        continue;
+      }
       uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
                                             ((int64_t)b * H + slab * heads_per_slab) * D);
       const int nvec = heads_per_slab * D / 8;
@@ -355,10 +510,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int64_t n_tiles = x1 - x0;
   volatile int* abort_flag = &ctl.abort;
+  int grp0 = 0;  // kTcShared: group of the CTA's first sequence
+  if constexpr (FORM == kTcShared) {
+    grp0 = group_of(g_starts, a.sh.num_groups, ctl.b0);
+    // the copies land over the group arrays once every warp has read them
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ producer
     const uint64_t policy = policy_evict_first();
+    // kTcShared: the walk through the groups, from global memory
+    int grp = grp0, grp_end = 0, grp_low = 0;
+    auto load_group = [&]() {
+      if constexpr (FORM == kTcShared) {
+        const int first = __ldg(a.sh.group_starts + grp);
+        grp_end = __ldg(a.sh.group_starts + grp + 1);
+        grp_low = shared_of(grp_end - first, __ldg(a.sh.prefix_lens + grp));
+      }
+    };
+    auto next_span = [&](int b) {  // span_of for a b that only grows
+      if constexpr (FORM == kTcShared) {
+        while (b >= grp_end && grp + 1 < a.sh.num_groups) {
+          ++grp;
+          load_group();
+        }
+        KeySpan<true> k{load_ctx(a.context_lens, b, cap), grp_low, 0};
+        if (k.low >= k.hi) k.hi = k.low = 0;
+        return k;
+      } else {
+        return span_of(b);
+      }
+    };
+    load_group();
     if (tb > 0 && lane == 0) {
       prefetch_tensor_map(&tm_k);
       prefetch_tensor_map(&tm_v);
@@ -371,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nbx = tb > 0 ? T / tb : 0;  // boxes per half
     int b = ctl.b0;
     int64_t pb = ctl.pb0;
-    KeySpan<kHidden> sp = span_of(b);
+    KeySpan<kHidden> sp = next_span(b);
     int nb = sp.tiles(T);
     int q_n = 0;  // segments whose Q has been issued
     for (int64_t it = 0; it < n_tiles; ++it) {
@@ -379,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (x >= pb + nb && b + 1 < B) {
         pb += nb;
         ++b;
-        sp = span_of(b);
+        sp = next_span(b);
         nb = sp.tiles(T);
       }
       const int s = (int)(it % S);
@@ -445,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m.keep = sp.keep;
           m.low = sp.low;
           m.pos = sp.hi - 1;
+          m.group = grp;
         }
         if (tb > 0)
           mbar_arrive_expect_tx(&ctl.full[s], (uint32_t)(nbox * 2 * TC::NH * box_bytes +
@@ -690,6 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             v = t < count && (key >= meta.low || key < meta.keep) ? v : -INFINITY;
           } else {
             v = t < count ? sc[n][e] * sl2 : -INFINITY;
+            if constexpr (FORM == kTcShared) v = meta.tok0 + t >= meta.low ? v : -INFINITY;
           }
           sc[n][e] = v;
           tmax = fmaxf(tmax, v);
@@ -791,7 +978,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // normalise and write the rows, or the partials for the combine
         const int b = meta.b;
-        if (meta.flags & kFlagWhole) {
+        bool joined = false;  // kTcShared: the prefix kernel has a part of the sequence
+        if constexpr (FORM == kTcShared) joined = meta.low > 0;
+        if ((meta.flags & kFlagWhole) && !joined) {
           if (row_ok) {
             const float inv = l_all > 0.f ? 1.f / l_all : 0.f;
             uint16_t* dst = static_cast<uint16_t*>(a.out) + ((int64_t)b * H + kvh * G + gid) * D;
@@ -825,7 +1014,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (old == nseg - 1) {
             // (4) last arrival: combine the partials of sequence b in CTA order
             __threadfence();
-            combine_partials<D, F16, kTcGMax>(a, b, kvh, G, c_lo, nseg, NT, g_eff, meta.pb, lane);
+            if constexpr (FORM == kTcShared) {
+              if (joined)
+                combine_shared<D, F16>(a, b, meta.group, kvh, G, c_lo, nseg, NT, g_eff, meta.pb,
+                                       lane);
+            }
+            if (!joined)
+              combine_partials<D, F16, kTcGMax>(a, b, kvh, G, c_lo, nseg, NT, g_eff, meta.pb, lane);
             if (lane == 0) *counter = 0;  // leave the counter zero for the next call
           }
         }

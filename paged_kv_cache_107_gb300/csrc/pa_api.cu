@@ -277,6 +277,27 @@ static int decode_check_workspace(DecodeArgs* a, const DeviceInfo& info, void* w
   return PA_OK;
 }
 
+// Points the scratch of pa_decode_shared into `ws` (may be null: only the size is wanted);
+// returns the bytes needed. Nothing in it outlives a call: the prefix kernel zeroes the
+// arrival counters.
+static size_t shared_bind_workspace(DecodeSharedArgs* a, unsigned char* ws) {
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const size_t rows = (size_t)a->num_seqs * a->num_heads;
+  const size_t more = (size_t)a->sh.prefix_grid * 256;
+  size_t at = up(decode_bind_workspace(a, ws, a->grid_ctas));
+  auto take = [&](size_t bytes) {
+    unsigned char* p = ws ? ws + at : nullptr;
+    at += up(bytes);
+    return p;
+  };
+  a->sh.first_lse = reinterpret_cast<float*>(take(rows * sizeof(float)));
+  a->sh.first_o = reinterpret_cast<float*>(take(rows * a->head_dim * sizeof(float)));
+  a->sh.more_lse = reinterpret_cast<float*>(take(more * sizeof(float)));
+  a->sh.more_o = reinterpret_cast<float*>(take(more * a->head_dim * sizeof(float)));
+  a->sh.plan = reinterpret_cast<int64_t*>(take(((size_t)a->num_seqs + 1) * sizeof(int64_t)));
+  return at;
+}
+
 // pa_decode and pa_decode_step; `step` is null for the plain call.
 static int decode_entry(void* out, const void* q, const void* k_cache, const void* v_cache,
                         const int32_t* block_tables, int max_blocks_per_seq,
@@ -441,6 +462,50 @@ int pa_prefill_mod(void* out, const void* q, const void* k_cache, const void* v_
                            causal, scale, dev_err, &a, &info, &nothing);
   if (rc != PA_OK || nothing) return rc;
   return pa::launch_prefill_mod(a, info, static_cast<cudaStream_t>(stream));
+}
+
+size_t pa_decode_shared_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                       int head_dim) {
+  if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || !pa::head_dim_supported(head_dim))
+    return 0;
+  pa::DeviceInfo info;
+  if (!pa::current_device_info(&info)) return 0;
+  pa::DecodeSharedArgs a{};
+  a.num_seqs = num_seqs > 0 ? num_seqs : 1;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.grid_ctas = a.sh.prefix_grid = info.num_sms;
+  return pa::shared_bind_workspace(&a, nullptr);
+}
+
+int pa_decode_shared(void* out, const void* q, const void* k_cache, const void* v_cache,
+                     const int32_t* block_tables, int max_blocks_per_seq,
+                     const int32_t* context_lens, const int32_t* group_starts,
+                     const int32_t* prefix_lens, int num_seqs, int num_groups, int num_heads,
+                     int num_kv_heads, int head_dim, int dtype, int block_size,
+                     int64_t num_blocks, float scale, void* workspace, size_t workspace_bytes,
+                     int* dev_err, void* stream) {
+  pa::DecodeSharedArgs a;
+  pa::DeviceInfo info;
+  bool nothing = false;
+  if (num_seqs > 0 && (num_groups < 1 || num_groups > num_seqs)) return PA_ERR_SHAPE;
+  if (num_seqs > pa::kMaxSharedSeqs) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > 0 && (!group_starts || !prefix_lens)) return PA_ERR_NULL;
+  const int rc = pa::decode_prepare(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                                    context_lens, num_seqs, num_heads, num_kv_heads, head_dim,
+                                    dtype, block_size, num_blocks, scale, 0, dev_err, nullptr,
+                                    &a, &info, &nothing);
+  if (rc != PA_OK || nothing) return rc;
+  a.sh.group_starts = group_starts;
+  a.sh.prefix_lens = prefix_lens;
+  a.sh.num_groups = num_groups;
+  a.sh.boxes = pa::prefix_box_rows(block_size) > 0;
+  a.sh.prefix_grid = info.num_sms;
+  const size_t need = pa::shared_bind_workspace(&a, static_cast<unsigned char*>(workspace));
+  if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return PA_ERR_ALIGN;
+  return pa::launch_decode_shared(a, info, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -97,6 +97,30 @@ struct DecodeModArgs : DecodeArgs {
   ScoreModArgs mod;
 };
 
+// pa_decode_shared: the groups and the prefix kernel's results.
+struct SharedArgs {
+  const int32_t* group_starts;  // [num_groups + 1]
+  const int32_t* prefix_lens;   // [num_groups]
+  int num_groups;
+  int boxes;          // 1: the block size allows the prefix kernel's TMA boxes
+  int prefix_grid;    // CTAs of the prefix kernel
+  // The partial results of a unit (normalised rows and base-2 log-sum-exps): the part that
+  // holds its first step by sequence, a part that another CTA carries on by that CTA (a CTA
+  // carries on one unit at most, its first).
+  float* first_o;     // [num_seqs * num_heads * head_dim]
+  float* first_lse;   // [num_seqs * num_heads]
+  float* more_o;      // [prefix_grid * 256 * head_dim]
+  float* more_lse;    // [prefix_grid * 256]
+  int64_t* plan;      // [0] steps, [1 + g] first step of group g
+};
+
+// The kernels keep the group arrays in shared memory while they plan: at most this many.
+constexpr int kMaxSharedSeqs = 8192;
+
+struct DecodeSharedArgs : DecodeArgs {
+  SharedArgs sh;
+};
+
 // The new tokens of pa_decode_step (null for pa_decode and pa_decode_noalloc).
 struct DecodeStepInput {
   const void* k_new;
@@ -132,6 +156,12 @@ int decode_max_ctas(const DeviceInfo& info);
 void decode_workspace_layout(int num_seqs, int num_heads, int num_kv_heads, int max_ctas,
                              size_t* off_counters, size_t* off_lse, size_t* off_o,
                              size_t* total);
+// Tokens per TMA box of the prefix kernel: the largest power of two that divides the block
+// size, at most a tile; 0 below the 8 rows of a swizzle atom.
+inline int prefix_box_rows(int block_size) {
+  const int tb = block_size & -block_size;
+  return tb > 128 ? 128 : (tb < 8 ? 0 : tb);
+}
 // Head slab (KV heads handled by one CTA) for a given num_kv_heads: 8, 4, 2 or 1.
 int decode_head_slab(int num_kv_heads);
 bool decode_supported(int num_heads, int num_kv_heads);
@@ -146,6 +176,13 @@ int launch_decode_step_tc(const DecodeArgs& a, const DeviceInfo& info, cudaStrea
 // Modified scores: the tensor-core kernel, every shape.
 int launch_decode_mod(const DecodeModArgs& a, const DeviceInfo& info, cudaStream_t stream);
 int launch_decode_mod_d64(const DecodeModArgs& a, const DeviceInfo& info, cudaStream_t stream);
+// pa_decode_shared: the prefix kernel (prefix_kernel.cuh), then the tensor-core kernel on
+// the rest of every sequence, which joins both.
+int launch_decode_shared(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream);
+int launch_decode_shared_rest_d64(const DecodeSharedArgs& a, const DeviceInfo& info,
+                                  cudaStream_t stream);
+int launch_prefix_d64(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream);
+int launch_prefix_d128(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream);
 // Shapes that take the tensor-core path: every group of 3..8 query heads per KV head, and
 // groups of 1 or 2 unless the head dimension is 128 and one slab holds all KV heads
 // (num_kv_heads 1, 2, 4 or 8), the case where a CUDA-core tile is one contiguous run of

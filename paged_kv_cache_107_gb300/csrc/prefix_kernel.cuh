@@ -1,0 +1,707 @@
+// prefix_kernel.cuh — the shared part of pa_decode_shared on the tcgen05 tensor cores.
+//
+// What it computes: for every group g of sequences that hold the same first L keys, every
+// query head h and sequence b of the group, the normalised row
+//   o = sum_{t < L} 2^(x_t - lse) v_t,  lse = log2 sum_{t < L} 2^(x_t),  x_t = log2(e) scale q.k_t,
+// of each of the key ranges that the work is cut into; the decode of the rest (decode_tc.cuh)
+// joins them with the sequence's own keys by their log-sum-exps.
+//
+// Why it pays: a decode reads the shared keys once for each sequence. Here the rows of a
+// group (n sequences x the G query heads of a KV head) are a dense matrix, so each shared
+// key and value is read once for 128 or 256 of them: below about 256 rows the bytes of the
+// prefix bound it, above the products do.
+//
+// Structure (that of prefill_kernel.cuh, whose constants and helpers it uses): one persistent
+// CTA per SM, a TMA warp, a warp that issues tcgen05.mma, a Q warp and two softmax
+// warpgroups, one for each of two slots of accumulators in tensor memory.
+//  * Work: the steps of all units (GroupWork) form one stream, cut into equal shares
+//    (stream-K): a long prefix is spread over every SM whatever the number of groups. A CTA's
+//    share is a list of segments, each a range of steps of one unit.
+//  * A unit with two row tiles takes each key tile for both slots (one load, two products). A
+//    unit with one row tile would leave the second slot idle and its own chain of product,
+//    softmax, product exposed; it gives the slots alternate key tiles instead, and the two
+//    softmax states are joined when the segment ends, through tensor memory, each warpgroup
+//    writing half of the dims.
+//  * The softmax sums, the running maxima and O stay in fp32; P is rounded to the element type
+//    for the second product, as in the prefill.
+#pragma once
+
+#include "dependent_launch.cuh"
+#include "prefill_kernel.cuh"
+#include "shared_groups.cuh"
+
+namespace pa {
+namespace {
+
+template <int D>
+struct PrefixCfg {
+  // ring depths: 160 KB of K and V tiles at both head dims
+  static constexpr int KS = D == 64 ? 4 : 2;
+  static constexpr int VS = D == 64 ? 6 : 3;
+  static constexpr int kTile = (D / 64) * kHalf;
+};
+
+template <int D>
+struct PrefixCtl {
+  using C = PrefixCfg<D>;
+  uint64_t q_full[2], q_empty[2];  // [row tile]
+  uint64_t k_full[C::KS], k_empty[C::KS];
+  uint64_t v_full[C::VS], v_empty[C::VS];
+  uint64_t s_full[2], p_full[2], o_done[2];  // [slot]
+  uint32_t tmem_base;
+  int abort;
+  int64_t nx;      // steps of the stream
+  int64_t x0, x1;  // this CTA's
+  int64_t gx;      // first step of the group that holds x0
+  int g;           // that group
+  int64_t red[kThreads / 32];
+  float2 join[kRows];  // [row] slot 1's softmax maximum and sum, then the factors of both O
+};
+
+template <int D>
+struct PrefixTiles {
+  using C = PrefixCfg<D>;
+  unsigned char q[2][C::kTile];
+  unsigned char k[C::KS][C::kTile];
+  unsigned char v[C::VS][C::kTile];
+};
+
+constexpr int kPrefixCtlBytes = 1408;
+
+template <int D>
+constexpr size_t prefix_smem_bytes() {
+  return 1023 + kPrefixCtlBytes + sizeof(PrefixTiles<D>);
+}
+
+// A range of steps of one unit.
+struct PrefixSeg {
+  int first, n;  // the group's sequences
+  int len;       // shared keys
+  int nt;        // key tiles
+  int pair, j;   // row tiles 2*pair (and 2*pair + 1 when two), KV head
+  int s0, s1;    // steps
+  bool two;      // both slots take the same key tile
+  // key tiles of slot g: tile(g, it) for it < count(g)
+  __device__ __forceinline__ int steps() const { return s1 - s0; }
+  __device__ __forceinline__ int tile(int g, int it) const {
+    return two ? s0 + it : 2 * (s0 + it) + g;
+  }
+  __device__ __forceinline__ int count(int g) const {
+    return two || g == 0 ? s1 - s0 : min(s1, nt >> 1) - s0;
+  }
+  __device__ __forceinline__ int tiles() const {  // K (or V) tiles loaded
+    return two ? s1 - s0 : count(0) + max(0, count(1));
+  }
+};
+
+// Hands out a CTA's segments in order; each role of the CTA walks its own copy.
+struct PrefixWalk {
+  int64_t x, x1;  // next step, end of the share
+  int64_t gx;     // first step of group g
+  int g;
+  int first, n, prefix;
+
+  __device__ __forceinline__ void load_group(const SharedArgs& sh) {
+    first = __ldg(sh.group_starts + g);
+    n = __ldg(sh.group_starts + g + 1) - first;
+    prefix = __ldg(sh.prefix_lens + g);
+  }
+  __device__ __forceinline__ bool next(PrefixSeg& s, const SharedArgs& sh, int Hk, int P) {
+    if (x >= x1) return false;
+    GroupWork w(sh, n, prefix, P);
+    while (x - gx >= w.steps(Hk) && g + 1 < sh.num_groups) {
+      gx += w.steps(Hk);
+      ++g;
+      load_group(sh);
+      w = GroupWork(sh, n, prefix, P);
+    }
+    const uint32_t rel = (uint32_t)(x - gx);
+    const uint32_t per_pair = (uint32_t)Hk * (uint32_t)w.nt;
+    const uint32_t pair = min(rel / per_pair, (uint32_t)w.full);
+    const uint32_t in_pair = rel - pair * per_pair;
+    const uint32_t us = (uint32_t)w.unit_steps((int)pair);
+    s.first = first;
+    s.n = n;
+    s.len = prefix;
+    s.nt = w.nt;
+    s.pair = (int)pair;
+    s.two = (int)pair < w.full;
+    s.j = (int)(in_pair / us);
+    s.s0 = (int)(in_pair % us);
+    s.s1 = (int)min((int64_t)us, (int64_t)s.s0 + (x1 - x));
+    x += s.s1 - s.s0;
+    return true;
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void note_timeout(PrefixCtl<D>& c, int* dev_err) {
+  c.abort = 1;
+  set_dev_err(dev_err, PA_DEV_ERR_TIMEOUT);
+}
+
+// named barriers of the 256 softmax threads
+template <int ID>
+__device__ __forceinline__ void bar_sync256() {
+  asm volatile("bar.sync %0, 256;" ::"n"(ID) : "memory");
+}
+template <int ID>
+__device__ __forceinline__ void bar_arrive256() {
+  asm volatile("bar.arrive %0, 256;" ::"n"(ID) : "memory");
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ CUtensorMap tm_q, const DecodeSharedArgs a,
+                         const int box_rows) {
+  using C = PrefixCfg<D>;
+  using Ctl = PrefixCtl<D>;
+  static_assert(sizeof(Ctl) <= kPrefixCtlBytes, "control block");
+  constexpr int NH = D / 64;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  Ctl& ctl = *reinterpret_cast<Ctl*>(smem_raw);
+  PrefixTiles<D>& sm = *reinterpret_cast<PrefixTiles<D>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + kPrefixCtlBytes + 1023) & ~uintptr_t(1023));
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const int H = a.num_heads, Hk = a.num_kv_heads, G = H / Hk, B = a.num_seqs;
+  const int P = kRows / G;  // sequences per row tile (rows P*G..127 are padding)
+  const int cap = a.max_blocks * a.block_size;
+  const SharedArgs& sh = a.sh;
+
+  if (tid == 0) {
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&ctl.q_full[g], 1);
+      mbar_init(&ctl.q_empty[g], 1);
+      mbar_init(&ctl.s_full[g], 1);
+      mbar_init(&ctl.p_full[g], kRows);
+      mbar_init(&ctl.o_done[g], 1);
+    }
+    for (int s = 0; s < C::KS; ++s) {
+      mbar_init(&ctl.k_full[s], 1);
+      mbar_init(&ctl.k_empty[s], 1);
+    }
+    for (int s = 0; s < C::VS; ++s) {
+      mbar_init(&ctl.v_full[s], 1);
+      mbar_init(&ctl.v_empty[s], 1);
+    }
+    ctl.abort = 0;
+    ctl.g = 0;
+    ctl.gx = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    umma::tmem_alloc(&ctl.tmem_base, kTmemCols);
+    umma::tmem_relinquish();
+  }
+  // the decode of the rest may be scheduled as this grid's CTAs leave
+  pdl_launch_dependents();
+
+  // ---- the stream of steps and this CTA's share (scratch: the K and V rings) ----------
+  {
+    int* starts = reinterpret_cast<int*>(&sm.k[0][0]);
+    int* prefix = starts + sh.num_groups + 1;
+    const bool ok = load_groups(sh, B, cap, starts, prefix);
+    if (!ok && blockIdx.x == 0 && tid == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SEQLENS);
+    const int groups = ok ? sh.num_groups : 0;
+    int64_t nx = 0;
+    for (int g = tid; g < groups; g += kThreads)
+      nx += GroupWork(sh, starts[g + 1] - starts[g], prefix[g], P).steps(Hk);
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) nx += __shfl_xor_sync(0xffffffffu, nx, m);
+    if (lane == 0) ctl.red[warp] = nx;
+    __syncthreads();
+    if (tid == 0) {
+      int64_t t = 0;
+      for (int w = 0; w < kThreads / 32; ++w) t += ctl.red[w];
+      const int ge = prefix_ctas(t, (int)gridDim.x);
+      ctl.nx = t;
+      ctl.x0 = (int)blockIdx.x < ge ? prefix_begin(blockIdx.x, t, ge) : 0;
+      ctl.x1 = (int)blockIdx.x < ge ? prefix_begin(blockIdx.x + 1, t, ge) : 0;
+    }
+    // every grid before this one is complete from here on: the workspace may be written
+    pdl_wait();
+    // first step of every group: this CTA's start, and (CTA 0) the plan for the decode
+    int64_t running = 0;
+    for (int base = 0; base < groups; base += kThreads) {
+      const int g = base + tid;
+      const int64_t n =
+          g < groups ? GroupWork(sh, starts[g + 1] - starts[g], prefix[g], P).steps(Hk) : 0;
+      int64_t incl = n;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, m);
+        if (lane >= m) incl += y;
+      }
+      __syncthreads();
+      if (lane == 31) ctl.red[warp] = incl;
+      __syncthreads();
+      int64_t before = running;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += ctl.red[w];
+        running += ctl.red[w];
+      }
+      const int64_t p = before + incl - n;
+      if (g < groups) {
+        if (blockIdx.x == 0) sh.plan[1 + g] = p;
+        if (p <= ctl.x0 && ctl.x0 < p + n) {
+          ctl.g = g;
+          ctl.gx = p;
+        }
+      }
+    }
+    if (blockIdx.x == 0 && tid == 0) sh.plan[0] = ctl.nx;
+    // the decode's arrival counters start at zero
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < (int64_t)B * Hk;
+         i += (int64_t)gridDim.x * kThreads)
+      a.counters[i] = 0;
+  }
+  // the scratch was written through the generic proxy; TMA (the async proxy) writes there next
+  fence_proxy_async_smem();
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  const uint32_t tmem = ctl.tmem_base;
+  volatile int* abort_flag = &ctl.abort;
+  PrefixWalk walk{ctl.x0, ctl.x1, ctl.gx, ctl.g, 0, 0, 0};
+  if (walk.x < walk.x1) walk.load_group(sh);
+  PrefixSeg seg;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+    if (warp == kTmaWarp) {
+      // ---------------------------------------------------------------- TMA producer
+      // Lane b owns box b of a tile (box_rows keys of one block); a step's block ids are read
+      // one step before its K loads.
+      if (lane == 0) {
+        umma::prefetch_tmap(&tm_k);
+        umma::prefetch_tmap(&tm_v);
+      }
+      const int bs = a.block_size;
+      const int boxes = kKeys / box_rows;
+      int kl = 0, vl = 0;
+      // this lane's block id of a key tile: -1 past the prefix, -2 out of the pool
+      auto read_id = [&](const PrefixSeg& s, int tile) {
+        const int key0 = tile * kKeys + lane * box_rows;
+        if (lane >= boxes || key0 >= s.len) return -1;
+        const int id = __ldg(a.block_tables + (int64_t)s.first * a.max_blocks + key0 / bs);
+        return id >= 0 && (int64_t)id < a.num_blocks ? id : -2;
+      };
+      auto load = [&](bool is_v, int j, int tile, int id) {
+        const int stages = is_v ? C::VS : C::KS;
+        const int cnt = is_v ? vl++ : kl++;
+        const int st = cnt % stages;
+        uint64_t* empty = is_v ? &ctl.v_empty[st] : &ctl.k_empty[st];
+        uint64_t* full = is_v ? &ctl.v_full[st] : &ctl.k_full[st];
+        if (lane == 0 && cnt >= stages &&
+            !mbar_wait(empty, (uint32_t)(((cnt / stages) - 1) & 1), abort_flag))
+          note_timeout(ctl, a.dev_err);
+        if (!is_v && __any_sync(0xffffffffu, id == -2) && lane == 0)
+          set_dev_err(a.dev_err, PA_DEV_ERR_BLOCK_ID);
+        const uint32_t valid = __ballot_sync(0xffffffffu, id >= 0);
+        if (lane == 0)
+          mbar_arrive_expect_tx(full, (uint32_t)__popc(valid) * NH * box_rows * 128u);
+        __syncwarp();
+        if (id >= 0) {
+          const int row0 = (tile * kKeys + lane * box_rows) % bs;
+          unsigned char* dst = (is_v ? sm.v[st] : sm.k[st]) + lane * box_rows * 128;
+          const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+          for (int h2 = 0; h2 < NH; ++h2)
+            umma::tma_load_4d(dst + h2 * kHalf, map, h2 * 64, row0, j, id, full);
+        }
+        __syncwarp();
+      };
+      bool more = walk.next(seg, sh, Hk, P);
+      int id[2] = {-1, -1};
+      if (more) {
+        id[0] = read_id(seg, seg.tile(0, 0));
+        if (!seg.two && seg.count(1) > 0) id[1] = read_id(seg, seg.tile(1, 0));
+      }
+      while (more) {
+        PrefixSeg nseg;
+        const bool nmore = walk.next(nseg, sh, Hk, P);
+        const int n = seg.steps();
+        int nid[2] = {-1, -1};
+        auto read_step = [&](const PrefixSeg& s, int it) {
+          nid[0] = read_id(s, s.tile(0, it));
+          nid[1] = !s.two && it < s.count(1) ? read_id(s, s.tile(1, it)) : -1;
+        };
+        auto load_step = [&](bool is_v, int it, const int* ids) {
+          load(is_v, seg.j, seg.tile(0, it), ids[0]);
+          if (!seg.two && it < seg.count(1)) load(is_v, seg.j, seg.tile(1, it), ids[1]);
+        };
+        load_step(false, 0, id);
+        for (int it = 0; it < n; ++it) {
+          // K runs one step ahead of V: S(it+1) is issued right after PV(it)
+          if (it + 1 < n) read_step(seg, it + 1);
+          else if (nmore) read_step(nseg, 0);
+          load_step(true, it, id);
+          if (it + 1 < n) load_step(false, it + 1, nid);
+          id[0] = nid[0];
+          id[1] = nid[1];
+        }
+        more = nmore;
+        seg = nseg;
+      }
+      if (lane == 0) {  // the last copies land before the CTA may exit
+        for (int c = kl > C::KS ? kl - C::KS : 0; c < kl; ++c)
+          mbar_wait_copies(&ctl.k_full[c % C::KS], (uint32_t)((c / C::KS) & 1));
+        for (int c = vl > C::VS ? vl - C::VS : 0; c < vl; ++c)
+          mbar_wait_copies(&ctl.v_full[c % C::VS], (uint32_t)((c / C::VS) & 1));
+      }
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------------- MMA issuer
+      constexpr uint32_t idesc_s = umma::idesc_f32acc(kRows, kKeys, false, F16);
+      constexpr uint32_t idesc_o = umma::idesc_f32acc(kRows, D, true, F16);
+      int kc = 0, vc = 0;     // K and V tiles consumed
+      int qc[2] = {0, 0};     // Q tiles consumed
+      int pc[2] = {0, 0};     // P tiles consumed
+      auto wait = [&](uint64_t* bar, int phase) {
+        if (!mbar_wait(bar, (uint32_t)(phase & 1), abort_flag)) note_timeout(ctl, a.dev_err);
+        umma::fence_after_sync();
+      };
+      auto commit1 = [&](uint64_t* bar) {
+        if (elect_one()) umma::commit(bar);
+        __syncwarp();
+      };
+      auto wait_k = [&]() { wait(&ctl.k_full[kc % C::KS], kc / C::KS); };
+      auto wait_v = [&]() { wait(&ctl.v_full[vc % C::VS], vc / C::VS); };
+      auto free_k = [&]() { commit1(&ctl.k_empty[kc++ % C::KS]); };
+      auto free_v = [&]() { commit1(&ctl.v_empty[vc++ % C::VS]); };
+      auto issue_s = [&](int g, int qt) {  // S_g = Q_qt K^T
+        const uint64_t qd = umma::smem_desc(smem_u32(sm.q[qt]), 16, 1024);
+        const uint64_t kd = umma::smem_desc(smem_u32(sm.k[kc % C::KS]), 16, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off16 = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+            umma::mma_bf16(tmem + col_s(g), qd + off16, kd + off16, idesc_s, kk > 0);
+          }
+          umma::commit(&ctl.s_full[g]);
+        }
+        __syncwarp();
+      };
+      auto issue_pv = [&](int g, bool first) {  // O_g (+)= P_g V
+        const uint64_t vd = umma::smem_desc(smem_u32(sm.v[vc % C::VS]), kHalf, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            umma::mma_bf16_ts(tmem + col_o(g), tmem + col_s(g) + kk * 8,
+                              vd + ((kk * 16 * 128) >> 4), idesc_o, !first || (kk > 0));
+        }
+        __syncwarp();
+      };
+      // the S products of step `it` (both slots), then its K tiles are free
+      auto first_s = [&](const PrefixSeg& s) {
+        wait(&ctl.q_full[0], qc[0]++);
+        if (s.two) wait(&ctl.q_full[1], qc[1]++);
+        wait_k();
+        issue_s(0, 0);
+        if (s.two) {
+          issue_s(1, 1);
+          free_k();
+        } else {
+          free_k();
+          if (s.count(1) > 0) {
+            wait_k();
+            issue_s(1, 0);
+            free_k();
+          }
+        }
+        if (s.steps() == 1) {
+          commit1(&ctl.q_empty[0]);
+          if (s.two) commit1(&ctl.q_empty[1]);
+        }
+      };
+      bool more = walk.next(seg, sh, Hk, P);
+      if (more) first_s(seg);
+      while (more) {
+        const int n = seg.steps();
+        for (int it = 0; it < n; ++it) {
+          if (seg.two) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              wait(&ctl.p_full[g], pc[g]++);
+              if (g == 0) wait_v();
+              issue_pv(g, it == 0);
+              if (it == n - 1) commit1(&ctl.o_done[g]);
+              if (it + 1 < n) {
+                if (g == 0) wait_k();
+                issue_s(g, g);
+              }
+            }
+            free_v();
+            if (it + 1 < n) free_k();
+          } else {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              if (it >= seg.count(g)) continue;
+              wait(&ctl.p_full[g], pc[g]++);
+              wait_v();
+              issue_pv(g, it == 0);
+              free_v();
+              if (it == seg.count(g) - 1) commit1(&ctl.o_done[g]);
+              if (it + 1 < seg.count(g)) {
+                wait_k();
+                issue_s(g, 0);
+                free_k();
+              }
+            }
+          }
+          if (it + 2 == n) {  // the segment's last S products are issued
+            commit1(&ctl.q_empty[0]);
+            if (seg.two) commit1(&ctl.q_empty[1]);
+          }
+        }
+        more = walk.next(seg, sh, Hk, P);
+        if (more) first_s(seg);
+      }
+    } else if (warp == kQWarp) {
+      // ---------------------------------------------------------------- Q loader
+      // P sequences x G heads of a row tile, one box per 64 dims; rows of the next group or
+      // past the batch (zeros) land too and are never stored.
+      if (lane == 0) {
+        umma::prefetch_tmap(&tm_q);
+        int qn[2] = {0, 0};
+        while (walk.next(seg, sh, Hk, P)) {
+          for (int qt = 0; qt < (seg.two ? 2 : 1); ++qt) {
+            if (qn[qt] > 0 &&
+                !mbar_wait(&ctl.q_empty[qt], (uint32_t)((qn[qt] - 1) & 1), abort_flag))
+              note_timeout(ctl, a.dev_err);
+            ++qn[qt];
+            mbar_arrive_expect_tx(&ctl.q_full[qt], (uint32_t)(P * G * D * 2));
+#pragma unroll
+            for (int h2 = 0; h2 < NH; ++h2)
+              umma::tma_load_3d(sm.q[qt] + h2 * kHalf, &tm_q, h2 * 64, seg.j * G,
+                                seg.first + (2 * seg.pair + qt) * P, &ctl.q_full[qt]);
+          }
+        }
+        for (int qt = 0; qt < 2; ++qt)
+          if (qn[qt] > 0) mbar_wait_copies(&ctl.q_full[qt], (uint32_t)((qn[qt] - 1) & 1));
+      }
+    }
+    __syncwarp();
+    umma::fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+      umma::fence_after_sync();
+      umma::tmem_dealloc(tmem, kTmemCols);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ------------------------------------------------------------------ softmax warpgroups
+    const int g = warp >> 2;  // slot
+    const int r = tid & 127;  // row == TMEM lane
+    const int pos = r / G, hh = r % G;
+    const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    int sc = 0;             // S tiles of this slot consumed
+    int oc[2] = {0, 0};     // o_done phases consumed, per slot
+    int vbase = 0;          // V tiles of the earlier segments
+
+    while (walk.next(seg, sh, Hk, P)) {
+      const int cnt = seg.count(g);
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int it = 0; it < cnt; ++it) {
+        if (!mbar_wait(&ctl.s_full[g], (uint32_t)(sc & 1), abort_flag)) note_timeout(ctl, a.dev_err);
+        ++sc;
+        umma::fence_after_sync();
+        float sv[kKeys];
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) umma::tmem_ld32(lane_addr + col_s(g) + 32 * c4, sv + 32 * c4);
+        umma::tmem_ld_wait();
+
+        const int left = seg.len - seg.tile(g, it) * kKeys;  // keys of the tile that count
+        if (left < kKeys) {
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c)
+            if (c >= left) sv[c] = -INFINITY;
+        }
+        float mx[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) mx[c] = sv[c];
+#pragma unroll
+        for (int c = 8; c < kKeys; ++c) mx[c & 7] = fmaxf(mx[c & 7], sv[c]);
+        const float mt = a.scale_log2 * fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                              fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        // the running maximum only moves when it grows by more than 2^8 (then O is rescaled)
+        float alpha = 1.f;
+        bool rescale = false;
+        if (it == 0) {
+          m_run = mt;
+        } else if (mt > m_run + kRescaleThreshold) {
+          alpha = fast_exp2(m_run - mt);
+          m_run = mt;
+          rescale = true;
+        }
+        const float m_safe = m_run == -INFINITY ? 0.f : m_run;
+        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+        const float2 nm2 = make_float2(-m_safe, -m_safe);
+        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                         make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < kKeys / 2; ++c) {
+          const float2 x = umma::ffma2(make_float2(sv[2 * c], sv[2 * c + 1]), sc2, nm2);
+          const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          acc[c & 3] = umma::fadd2(acc[c & 3], p);
+          sv[c] = __uint_as_float(pack_elt2<F16>(p.x, p.y));
+        }
+        const float2 tt = umma::fadd2(umma::fadd2(acc[0], acc[1]), umma::fadd2(acc[2], acc[3]));
+        l_run = l_run * alpha + (tt.x + tt.y);
+        umma::tmem_st32(lane_addr + col_s(g), sv);
+        umma::tmem_st32(lane_addr + col_s(g) + 32, sv + 32);
+        if (__any_sync(0xffffffffu, rescale)) {  // S_g(it) completed after PV_g(it-1)
+          float ob[32];
+#pragma unroll
+          for (int c4 = 0; c4 < D / 32; ++c4) {
+            umma::tmem_ld32(lane_addr + col_o(g) + 32 * c4, ob);
+            umma::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ob[e] *= alpha;
+            umma::tmem_st32(lane_addr + col_o(g) + 32 * c4, ob);
+          }
+        }
+        if (left < kKeys) {  // rows of V past the prefix must not meet a zero probability
+          const int vi = vbase + (seg.two ? it : 2 * it + g);
+          const int st = vi % C::VS;
+          if (!mbar_wait(&ctl.v_full[st], (uint32_t)((vi / C::VS) & 1), abort_flag))
+            note_timeout(ctl, a.dev_err);
+          if (r >= left) {
+#pragma unroll
+            for (int ch = 0; ch < D / 8; ++ch)
+              *reinterpret_cast<uint4*>(sm.v[st] + (ch >> 3) * kHalf + r * 128 + (ch & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        umma::tmem_st_wait();
+        umma::fence_before_sync();
+        mbar_arrive(&ctl.p_full[g]);
+      }
+      vbase += seg.tiles();
+
+      // ---- the segment's rows: O / l and the log-sum-exp ------------------------------
+      const int tile = seg.two ? 2 * seg.pair + g : 2 * seg.pair;
+      const int b = seg.first + tile * P + pos;
+      const bool row_ok = pos < P && b < seg.first + seg.n;
+      const int hq = seg.j * G + hh;
+      float* dst;
+      float* dst_lse;
+      if (seg.s0 == 0) {
+        dst = sh.first_o + ((int64_t)b * H + hq) * D;
+        dst_lse = sh.first_lse + (int64_t)b * H + hq;
+      } else {
+        const int64_t at = (int64_t)blockIdx.x * 256 + (seg.two ? g * kRows : 0) + r;
+        dst = sh.more_o + at * D;
+        dst_lse = sh.more_lse + at;
+      }
+      auto wait_o = [&](int s) {
+        if (!mbar_wait(&ctl.o_done[s], (uint32_t)(oc[s] & 1), abort_flag)) note_timeout(ctl, a.dev_err);
+        ++oc[s];
+      };
+      if (seg.two) {
+        wait_o(g);
+        umma::fence_after_sync();
+        const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+        if (row_ok) *dst_lse = l_run > 0.f ? m_run + fast_log2(l_run) : -INFINITY;
+#pragma unroll
+        for (int c4 = 0; c4 < D / 32; ++c4) {
+          float ob[32];
+          umma::tmem_ld32(lane_addr + col_o(g) + 32 * c4, ob);
+          umma::tmem_ld_wait();
+          if (row_ok) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(dst + 32 * c4 + e) =
+                  make_float4(ob[e] * inv, ob[e + 1] * inv, ob[e + 2] * inv, ob[e + 3] * inv);
+          }
+        }
+        wait_o(1 - g);  // its phase ends about now; a later join waits for the one after
+      } else {
+        // join the slots: warpgroup 1 hands over its maximum and sum, warpgroup 0 returns the
+        // factors of both accumulators, and each takes half of the dims of both
+        const bool has_b = seg.count(1) > 0;
+        float fa, fb;
+        if (g == 1) {
+          ctl.join[r] = make_float2(m_run, l_run);
+          bar_arrive256<1>();
+          bar_sync256<2>();
+          fa = ctl.join[r].x;
+          fb = ctl.join[r].y;
+        } else {
+          bar_sync256<1>();
+          const float2 ml = ctl.join[r];  // (-inf, 0) without a tile
+          const float m = fmaxf(m_run, ml.x);
+          fa = m == -INFINITY ? 0.f : fast_exp2(m_run - m);
+          fb = m == -INFINITY ? 0.f : fast_exp2(ml.x - m);
+          const float l = l_run * fa + ml.y * fb;
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          if (row_ok) *dst_lse = l > 0.f ? m + fast_log2(l) : -INFINITY;
+          fa *= inv;
+          fb *= inv;
+          ctl.join[r] = make_float2(fa, fb);
+          bar_arrive256<2>();
+        }
+        wait_o(0);
+        if (has_b) wait_o(1);
+        umma::fence_after_sync();
+#pragma unroll
+        for (int c4 = 0; c4 < D / 64; ++c4) {
+          const int col = g * (D / 2) + 32 * c4;
+          float oa[32], ob[32];
+          umma::tmem_ld32(lane_addr + col_o(0) + col, oa);
+          if (has_b) umma::tmem_ld32(lane_addr + col_o(1) + col, ob);
+          umma::tmem_ld_wait();
+          if (row_ok) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) oa[e] = oa[e] * fa + (has_b ? ob[e] * fb : 0.f);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(dst + col + e) =
+                  make_float4(oa[e], oa[e + 1], oa[e + 2], oa[e + 3]);
+          }
+        }
+        // neither slot's O (nor join) is written again before both warpgroups have read them
+        umma::fence_before_sync();
+        bar_sync256<3>();
+      }
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+  }
+}
+
+template <int D, bool F16>
+int launch_prefix_t(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream) {
+  constexpr size_t smem = prefix_smem_bytes<D>();
+  static_assert(smem <= 232448, "shared memory budget (opt-in maximum)");
+  static std::atomic<bool> attr_done[64];  // zero-initialised: false
+  if (info.device < 0 || info.device >= 64) return PA_ERR_CUDA;
+  if ((size_t)info.max_smem_optin < smem) return PA_ERR_UNSUPPORTED;
+  if (!attr_done[info.device].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(shared_prefix_kernel<D, F16>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return PA_ERR_CUDA;
+    attr_done[info.device].store(true, std::memory_order_release);
+  }
+  const int G = a.num_heads / a.num_kv_heads;
+  const int box = prefix_box_rows(a.block_size);
+  CUtensorMap mk, mv, mq;
+  if (!make_slab_map(&mk, a.k_cache, a.num_kv_heads, D, F16, a.block_size, a.num_blocks,
+                     box ? box : 1, 1) ||
+      !make_slab_map(&mv, a.v_cache, a.num_kv_heads, D, F16, a.block_size, a.num_blocks,
+                     box ? box : 1, 1) ||
+      !make_rows_map(&mq, a.q, a.num_seqs, a.num_heads, D, F16, G, kRows / G))
+    return PA_ERR_CUDA;
+  if (launch_dependent(shared_prefix_kernel<D, F16>, dim3((unsigned)a.sh.prefix_grid),
+                       dim3(kThreads), smem, stream, mk, mv, mq, a, box ? box : kKeys) !=
+      cudaSuccess)
+    return PA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace pa
