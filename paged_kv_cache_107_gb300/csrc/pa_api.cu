@@ -55,6 +55,14 @@ static int resolve_mod(const pa_score_mod* mod, float scale, int head_dim, Score
   m->cap2 = mod->softcap * kLog2e;
   m->cap_in = mod->softcap > 0.f ? natural_scale(scale, head_dim) / mod->softcap : 0.f;
   if (isinf(m->cap2) || isinf(m->cap_in)) return PA_ERR_SHAPE;
+  const double z = (double)m->cap_in * m->cap_in;
+  double f = (double)m->cap2 * m->cap_in;
+  for (int i = 0; i < 6; ++i, f *= z) {
+    m->poly[i][0] = m->poly[i][1] = (float)(f * kTanhPoly[i]);
+    if (i < 4) m->poly3[i][0] = m->poly3[i][1] = (float)(f * kTanhPoly3[i]);
+  }
+  m->z_lim = z > 0 ? (float)(1.0 / z) : 0.f;
+  m->z_lim3 = z > 0 ? (float)(0.36 / z) : 0.f;
   m->slopes = mod->slopes;
   m->window = mod->window;
   m->sink = mod->sink;

@@ -83,8 +83,22 @@ struct DecodeArgs {
 //   x = q.k * scale_log2 - slope_h * log2(e) * |p - t|            (cap2 = 0)
 // and is visible when (t <= p or the call is not causal or t < prefix) and (window = 0 or
 // t > p - window or t < max(sink, prefix)).
+// tanh(u) = u P(u^2) for |u| < 1: P of degree 5 fitted on Chebyshev nodes of [0, 1],
+// reweighted toward the largest relative error: 6e-7 relative.
+constexpr float kTanhPoly[6] = {0.9999994039535522f,   -0.3332904279232025f,
+                                0.13281433284282684f,  -0.051605675369501114f,
+                                0.016743116080760956f, -0.0030670606065541506f};
+// The same of degree 3 for |u| < 0.6: 2.2e-6 relative.
+constexpr float kTanhPoly3[4] = {0.9999978542327881f, -0.33314040303230286f,
+                                 0.13057856261730194f, -0.04092942550778389f};
 struct ScoreModArgs {
   float cap2;                  // softcap * log2(e); 0 = no cap
+  // kTanhPoly and kTanhPoly3 scaled by cap2 * cap_in^(2i+1), so that raw products go in and
+  // log2 units come out; each coefficient twice, for packed arithmetic
+  alignas(8) float poly[6][2];
+  alignas(8) float poly3[4][2];
+  float z_lim;                 // squares of raw products below which they hold: 1 / cap_in^2,
+  float z_lim3;                // 0.6^2 / cap_in^2
   float cap_in;                // scale / softcap
   const float* slopes;         // [num_heads]; null = no bias
   int window;                  // 0 = none
@@ -230,18 +244,10 @@ struct PrefillModArgs : PrefillArgs {
 bool prefill_supported(int num_heads, int num_kv_heads, int block_size);
 int launch_prefill(const PrefillArgs& a, const DeviceInfo& info, cudaStream_t stream);
 int launch_prefill_mod(const PrefillModArgs& a, const DeviceInfo& info, cudaStream_t stream);
-int launch_prefill_mod_d64_bf16(const PrefillModArgs& a, const DeviceInfo& info,
-                                cudaStream_t stream, const CUtensorMap& mk,
-                                const CUtensorMap& mv);
-int launch_prefill_mod_d64_f16(const PrefillModArgs& a, const DeviceInfo& info,
-                               cudaStream_t stream, const CUtensorMap& mk,
-                               const CUtensorMap& mv);
-int launch_prefill_mod_d128_bf16(const PrefillModArgs& a, const DeviceInfo& info,
-                                 cudaStream_t stream, const CUtensorMap& mk,
-                                 const CUtensorMap& mv);
-int launch_prefill_mod_d128_f16(const PrefillModArgs& a, const DeviceInfo& info,
-                                cudaStream_t stream, const CUtensorMap& mk,
-                                const CUtensorMap& mv);
+// One translation unit for each head_dim, element type and form (prefill_kernel.cuh).
+template <int D, bool F16, int FORM>
+int launch_prefill_form(const PrefillModArgs& a, const DeviceInfo& info, cudaStream_t stream,
+                        const CUtensorMap& mk, const CUtensorMap& mv);
 // The prefill instantiations other than head_dim 128 with bf16, one translation unit each.
 int launch_prefill_d64_bf16(const PrefillArgs& a, const DeviceInfo& info, cudaStream_t stream,
                             const CUtensorMap& mk, const CUtensorMap& mv);

@@ -62,11 +62,21 @@ int launch_prefill_mod(const PrefillModArgs& a, const DeviceInfo& info, cudaStre
   CUtensorMap mk, mv;
   const int rc = cache_maps(a, &mk, &mv);
   if (rc != PA_OK) return rc;
-  if (a.head_dim == 128) return a.f16 ? launch_prefill_mod_d128_f16(a, info, stream, mk, mv)
-                                      : launch_prefill_mod_d128_bf16(a, info, stream, mk, mv);
-  if (a.head_dim == 64) return a.f16 ? launch_prefill_mod_d64_f16(a, info, stream, mk, mv)
-                                     : launch_prefill_mod_d64_bf16(a, info, stream, mk, mv);
-  return PA_ERR_UNSUPPORTED;
+  const int form = a.mod.slopes ? kFormBias : a.mod.cap2 > 0.f ? kFormCap : kFormSpan;
+  switch ((a.head_dim == 64 ? 6 : 0) + (a.f16 ? 3 : 0) + form - kFormSpan) {
+    case 0: return launch_prefill_form<128, false, kFormSpan>(a, info, stream, mk, mv);
+    case 1: return launch_prefill_form<128, false, kFormCap>(a, info, stream, mk, mv);
+    case 2: return launch_prefill_form<128, false, kFormBias>(a, info, stream, mk, mv);
+    case 3: return launch_prefill_form<128, true, kFormSpan>(a, info, stream, mk, mv);
+    case 4: return launch_prefill_form<128, true, kFormCap>(a, info, stream, mk, mv);
+    case 5: return launch_prefill_form<128, true, kFormBias>(a, info, stream, mk, mv);
+    case 6: return launch_prefill_form<64, false, kFormSpan>(a, info, stream, mk, mv);
+    case 7: return launch_prefill_form<64, false, kFormCap>(a, info, stream, mk, mv);
+    case 8: return launch_prefill_form<64, false, kFormBias>(a, info, stream, mk, mv);
+    case 9: return launch_prefill_form<64, true, kFormSpan>(a, info, stream, mk, mv);
+    case 10: return launch_prefill_form<64, true, kFormCap>(a, info, stream, mk, mv);
+    default: return launch_prefill_form<64, true, kFormBias>(a, info, stream, mk, mv);
+  }
 }
 
 }  // namespace pa

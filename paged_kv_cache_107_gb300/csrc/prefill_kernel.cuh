@@ -75,6 +75,17 @@
 namespace pa {
 namespace {
 
+// cap2 tanh(cap_in v) / v given z = v^2, by the polynomial of degree 5 (z < z_lim) or 3
+// (z < z_lim3).
+template <int DEG>
+__device__ __forceinline__ float2 cap_poly2(float2 z, const ScoreModArgs& m) {
+  const float2* c = reinterpret_cast<const float2*>(DEG == 5 ? m.poly : m.poly3);
+  float2 p = umma::ffma2(c[DEG], z, c[DEG - 1]);
+#pragma unroll
+  for (int i = DEG - 2; i >= 0; --i) p = umma::ffma2(p, z, c[i]);
+  return p;
+}
+
 constexpr int kRows = 128;                 // query rows per tile (TMEM lanes)
 constexpr int kKeys = 128;                 // keys per K/V tile
 constexpr int kKStages = 2, kVStages = 3;  // ring depths
@@ -115,15 +126,19 @@ struct UnitRec {
   int nt;      // key tiles of tile A (bits 0..15) and of tile B (bits 16..31; may be 0)
 };
 
-// With modified scores (MOD) a record also holds the unit's hidden range: the keys from keep
+// The kernel's forms: plain, and those of pa_prefill_mod, which all take its masks: scores as
+// they are, under a cap, or with a bias by distance (under a cap or not).
+enum PrefillForm { kFormPlain = 0, kFormSpan = 1, kFormCap = 2, kFormBias = 3 };
+
+// With modified scores a record also holds the unit's hidden range: the keys from keep
 // up to low are seen by none of its queries; keys below prefix are seen by all of them.
 struct UnitRecMod : UnitRec {
   int prefix, keep, low;
 };
-template <bool MOD>
-using RecT = std::conditional_t<MOD, UnitRecMod, UnitRec>;
-template <bool MOD>
-using ArgsT = std::conditional_t<MOD, PrefillModArgs, PrefillArgs>;
+template <int FORM>
+using RecT = std::conditional_t<FORM != kFormPlain, UnitRecMod, UnitRec>;
+template <int FORM>
+using ArgsT = std::conditional_t<FORM != kFormPlain, PrefillModArgs, PrefillArgs>;
 
 // Barriers and schedule state; first in shared memory, then the unit records, then the
 // tiles from the next 1024-byte boundary (128-byte swizzle atoms are 1024 bytes).
@@ -155,9 +170,9 @@ struct PrefillTiles {
 
 constexpr int kCtlBytes = 256;
 constexpr int kRecBytes = 1792;  // fills the opt-in limit at head_dim 128 with the slack below
-// (56 records)
-template <bool MOD>
-constexpr int kMaxUnitRecs = kRecBytes / (int)sizeof(RecT<MOD>);
+// (56 records; 40 with modified scores)
+template <int FORM>
+constexpr int kMaxUnitRecs = kRecBytes / (int)sizeof(RecT<FORM>);
 static_assert(sizeof(PrefillCtl) <= kCtlBytes, "control block");
 
 template <int D>
@@ -220,15 +235,15 @@ __device__ __forceinline__ bool seq_ok(int n, int kv_len, int cap, int max_q) {
 
 // The keys that the queries of tile g of a unit see: up to hi for the last of them, from low
 // on for the first of the unit's queries (every tile of a unit walks the same key tiles).
-template <int P, bool MOD>
-__device__ __forceinline__ KeySpan<MOD> tile_span(const ArgsT<MOD>& a, int s, int n, int kv_len,
+template <int P, int FORM>
+__device__ __forceinline__ KeySpan<FORM != kFormPlain> tile_span(const ArgsT<FORM>& a, int s, int n, int kv_len,
                                                   int i0, int g) {
   const int c_len = kv_len - n;
   const int rows = min(P, n - (i0 + g * P));
-  KeySpan<MOD> k{0, 0, 0};
+  KeySpan<FORM != kFormPlain> k{0, 0, 0};
   if (rows <= 0) return k;
   k.hi = a.causal ? c_len + i0 + g * P + rows : kv_len;
-  if constexpr (MOD) {
+  if constexpr (FORM != kFormPlain) {
     k.hi = max(k.hi, min(kv_len, mod_prefix(a.mod, s)));
     mod_span(k, a.mod, s, c_len + i0);
   }
@@ -239,12 +254,12 @@ __device__ __forceinline__ KeySpan<MOD> tile_span(const ArgsT<MOD>& a, int s, in
 // a key-tile step that both tiles take costs about 2.1 us on GB300, a step of one tile
 // alone about 1.8 us, and a unit's start and end about 5 us (measured per unit with clock
 // traces of this kernel on the chunked-prefill workload); in units of 0.1 us.
-template <int P, bool MOD>
-__device__ __forceinline__ uint32_t pair_cost(const ArgsT<MOD>& a, int s, int n, int kv_len,
+template <int P, int FORM>
+__device__ __forceinline__ uint32_t pair_cost(const ArgsT<FORM>& a, int s, int n, int kv_len,
                                               int i0) {
   int nt[2];
 #pragma unroll
-  for (int g = 0; g < 2; ++g) nt[g] = tile_span<P, MOD>(a, s, n, kv_len, i0, g).tiles(kKeys);
+  for (int g = 0; g < 2; ++g) nt[g] = tile_span<P, FORM>(a, s, n, kv_len, i0, g).tiles(kKeys);
   const uint32_t both = (uint32_t)min(nt[0], nt[1]);
   const uint32_t single = (uint32_t)abs(nt[0] - nt[1]);
   return 21u * both + 18u * single + 50u;
@@ -252,12 +267,12 @@ __device__ __forceinline__ uint32_t pair_cost(const ArgsT<MOD>& a, int s, int n,
 
 // Key tiles each tile of a unit multiplies (causal: up to its last position); tile B may
 // have none.
-template <int P, bool MOD>
-__device__ __forceinline__ int unit_tiles(const ArgsT<MOD>& a, int s, int n, int kv_len, int i0) {
+template <int P, int FORM>
+__device__ __forceinline__ int unit_tiles(const ArgsT<FORM>& a, int s, int n, int kv_len, int i0) {
   int packed = 0;
 #pragma unroll
   for (int g = 0; g < 2; ++g)
-    packed |= tile_span<P, MOD>(a, s, n, kv_len, i0, g).tiles(kKeys) << (16 * g);
+    packed |= tile_span<P, FORM>(a, s, n, kv_len, i0, g).tiles(kKeys) << (16 * g);
   return packed;
 }
 __device__ __forceinline__ int nt_of(int nt, int g) { return (nt >> (16 * g)) & 0xFFFF; }
@@ -265,16 +280,16 @@ __device__ __forceinline__ int nt_all(int nt) { return max(nt & 0xFFFF, nt >> 16
 
 // Completes this CTA's records (ring positions and tile counts; thread 0) and publishes the
 // count. Ends with a block-wide barrier.
-template <int P, bool MOD>
-__device__ void finish_records(PrefillCtl& ctl, RecT<MOD>* recs, int count,
-                               const ArgsT<MOD>& a) {
+template <int P, int FORM>
+__device__ void finish_records(PrefillCtl& ctl, RecT<FORM>* recs, int count,
+                               const ArgsT<FORM>& a) {
   if (threadIdx.x == 0) {
     int v = 0;
     for (int k = 0; k < count; ++k) {
-      recs[k].nt = unit_tiles<P, MOD>(a, recs[k].s, recs[k].n, recs[k].kv_len, recs[k].i0);
-      if constexpr (MOD) {
+      recs[k].nt = unit_tiles<P, FORM>(a, recs[k].s, recs[k].n, recs[k].kv_len, recs[k].i0);
+      if constexpr (FORM != kFormPlain) {
         const KeySpan<true> sp =
-            tile_span<P, MOD>(a, recs[k].s, recs[k].n, recs[k].kv_len, recs[k].i0, 0);
+            tile_span<P, FORM>(a, recs[k].s, recs[k].n, recs[k].kv_len, recs[k].i0, 0);
         recs[k].prefix = mod_prefix(a.mod, recs[k].s);
         recs[k].keep = sp.keep;
         recs[k].low = sp.low;
@@ -288,8 +303,8 @@ __device__ void finish_records(PrefillCtl& ctl, RecT<MOD>* recs, int count,
 }
 
 // One unit per CTA: (KV head, sequence, pair) from the grid, latest pairs first.
-template <int P, bool MOD>
-__device__ void single_schedule(PrefillCtl& ctl, RecT<MOD>* recs, const ArgsT<MOD>& a) {
+template <int P, int FORM>
+__device__ void single_schedule(PrefillCtl& ctl, RecT<FORM>* recs, const ArgsT<FORM>& a) {
   int count = 0;
   if (threadIdx.x == 0) {
     const int j = blockIdx.x, s = blockIdx.y;
@@ -306,16 +321,16 @@ __device__ void single_schedule(PrefillCtl& ctl, RecT<MOD>* recs, const ArgsT<MO
     ctl.n_units = count;
   }
   __syncthreads();
-  finish_records<P, MOD>(ctl, recs, ctl.n_units, a);
+  finish_records<P, FORM>(ctl, recs, ctl.n_units, a);
 }
 
 // Builds the sorted schedule (all threads of the CTA take part; ends with a block-wide
 // barrier). The scratch (cu_seqlens copies, per-sequence pair offsets, sort keys) lives in
 // the K ring, which no copy has touched yet. The launcher takes this schedule only when
 // the batch's bounds (num_seqs, max_seqlen_q, KV heads) guarantee that it fits.
-template <int P, bool MOD>
-__device__ void build_schedule(PrefillCtl& ctl, RecT<MOD>* recs, unsigned char* scratch,
-                               const ArgsT<MOD>& a, int cu_q0, int cu_k0) {
+template <int P, int FORM>
+__device__ void build_schedule(PrefillCtl& ctl, RecT<FORM>* recs, unsigned char* scratch,
+                               const ArgsT<FORM>& a, int cu_q0, int cu_k0) {
   const int tid = threadIdx.x;
   const int S = a.num_seqs, Hk = a.num_kv_heads;
   if (S > kMaxSortSeqs) {  // excluded by the launcher
@@ -375,7 +390,7 @@ __device__ void build_schedule(PrefillCtl& ctl, RecT<MOD>* recs, unsigned char* 
   const int npairs = carry;
   const int64_t nunits = (int64_t)npairs * Hk;
   const int64_t per_cta = (nunits + gridDim.x - 1) / gridDim.x + 1;
-  if (npairs > kMaxSortPairs || per_cta > kMaxUnitRecs<MOD>) {  // excluded by the launcher
+  if (npairs > kMaxSortPairs || per_cta > kMaxUnitRecs<FORM>) {  // excluded by the launcher
     if (tid == 0) {
       ctl.n_units = 0;
       if (blockIdx.x == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SEQLENS);
@@ -401,7 +416,7 @@ __device__ void build_schedule(PrefillCtl& ctl, RecT<MOD>* recs, unsigned char* 
     const int n = cuq[s + 1] - cuq[s];
     const int kv = cuk[s + 1] - cuk[s];
     const uint32_t id = ((uint32_t)s << 12) | (uint32_t)qt;
-    const uint32_t cost = pair_cost<P, MOD>(a, s, n, kv, qt * 2 * P);
+    const uint32_t cost = pair_cost<P, FORM>(a, s, n, kv, qt * 2 * P);
     keys[p] = ((unsigned long long)cost << 32) | (unsigned long long)(0xFFFFFFFFu - id);
   }
   for (int i = npairs + tid; i < n2; i += kThreads) keys[i] = 0ull;
@@ -438,7 +453,7 @@ __device__ void build_schedule(PrefillCtl& ctl, RecT<MOD>* recs, unsigned char* 
   }
   // this CTA's units: the deal indices k with serp_index(k) < nunits form a prefix
   const int c = (int)blockIdx.x, G = (int)gridDim.x;
-  for (int k = tid; k < kMaxUnitRecs<MOD>; k += kThreads) {
+  for (int k = tid; k < kMaxUnitRecs<FORM>; k += kThreads) {
     const int64_t idx = serp_index(k, c, G);
     if (idx >= nunits) continue;
     const unsigned long long key = keys[idx / Hk];
@@ -448,40 +463,278 @@ __device__ void build_schedule(PrefillCtl& ctl, RecT<MOD>* recs, unsigned char* 
                                              qt * 2 * P, (int)(idx % Hk), 0, 0};
   }
   int count = 0;
-  while (count < kMaxUnitRecs<MOD> && serp_index(count, c, G) < nunits) ++count;
+  while (count < kMaxUnitRecs<FORM> && serp_index(count, c, G) < nunits) ++count;
   __syncthreads();
-  finish_records<P, MOD>(ctl, recs, count, a);
+  finish_records<P, FORM>(ctl, recs, count, a);
 }
 
-// Raw products q.k of one row and tile to scores in log2 units (ScoreModArgs), in place; dist
-// is the row's position minus the tile's first key. Without a cap or slopes the products
-// stay as they are (the softmax scales them).
-__device__ __forceinline__ void mod_scores(float* sv, const ScoreModArgs& m, float scale_log2,
-                                           float slope2, int dist) {
-  if (m.cap2 > 0.f) {
+// The softmax of the modified forms over one unit's key tiles: thread = row and the row's 128
+// products in registers, as in the plain form. Added are:
+//  * the masks of pa_prefill_mod, on the tiles that need one;
+//  * bias: one multiply-add and one add for two keys, in place;
+//  * cap: the exponent's argument is v P(v^2) - m with a polynomial P, on packed multiply-adds
+//    that run beside the exponentials (an exact tanh takes an exp2 and a reciprocal more for
+//    each score: three times the special-function unit's time). It holds within its fit's
+//    range only, so the warp's largest v^2 is tracked and a tile that leaves the range is
+//    computed again by the next finer way: degree 3, degree 5, exact. A tile starts with the
+//    way that the last one would have needed. The finer ways, and the tiles with hidden
+//    keys, run as a loop over chunks of the row, read again from tensor memory: unrolled
+//    over the row as well they left the instruction caches (straight-line code of 46 KB
+//    ran at two thirds of the speed of 23 KB).
+template <int G, int D, bool F16, int FORM>
+__device__ __forceinline__ void mod_tiles(PrefillCtl& ctl, PrefillTiles<D>& sm,
+                                          const RecT<FORM>& u, const ArgsT<FORM>& a, int g, int r,
+                                          uint32_t lane_addr, int& sc, float& l_out) {
+  constexpr int P = kRows / G;
+  constexpr bool kSepP = D == 64;
+  constexpr bool kCap = FORM == kFormCap, kBias = FORM == kFormBias;
+  const bool causal = a.causal != 0;
+  volatile int* abort_flag = &ctl.abort;
+  const uint32_t s_addr = lane_addr + col_s(g);
+  const uint32_t p_addr = lane_addr + (kSepP ? col_p(g) : col_s(g));
+  const int my_nt = nt_of(u.nt, g), kv_len = u.kv_len, u_keep = u.keep, u_low = u.low;
+  const KeySpan<true> span{kv_len, u_low, u_keep};
+  const int kept = span.kept(kKeys), skip_keys = span.skipped(kKeys) * kKeys;
+  const int pos0 = (kv_len - u.n) + u.i0 + g * P;  // position of the tile's first row
+  const int w0 = r & ~31;                          // first row of the warp
+  const int qpos = pos0 + r / G;
+  // of the row's keys [0, lim), those below keep or from low on count; the warp's smallest
+  // lim and largest low
+  auto lim_of = [&](int p) {
+    return max(causal ? min(kv_len, p + 1) : kv_len, min(kv_len, u.prefix));
+  };
+  const int lim = lim_of(qpos), lim_min = lim_of(pos0 + w0 / G);
+  const int low = a.mod.window > 0 ? qpos - a.mod.window + 1 : 0;
+  const int low_max = a.mod.window > 0 ? pos0 + (w0 + 31) / G - a.mod.window + 1 : 0;
+  float slope2 = 0.f;
+  if constexpr (kBias) slope2 = __ldg(a.mod.slopes + u.j * G + r % G) * 1.4426950408889634f;
+  float m_run = -INFINITY, l_run = 0.f;
+  int way = 1;  // cap: 0 degree 3, 1 degree 5, 2 exact
+
+#pragma unroll 1
+  for (int it = 0; it < my_nt; ++it) {
+    const int t0 = it * kKeys + (it >= kept ? skip_keys : 0);
+    const bool past = t0 + kKeys > lim_min;
+    const bool before = t0 < low_max && t0 + kKeys > u_keep;
+    if (!mbar_wait(&ctl.s_full[g], (uint32_t)(sc & 1), abort_flag)) note_timeout(ctl, a.dev_err);
+    ++sc;
+    umma::fence_after_sync();
+    float sv[kKeys];
 #pragma unroll
-    for (int c = 0; c < kKeys; ++c) sv[c] = m.cap2 * cap_tanh(sv[c] * m.cap_in);
-  }
-  if (m.slopes) {
-    const float pre = m.cap2 > 0.f ? 1.f : scale_log2;
+    for (int c4 = 0; c4 < 4; ++c4) umma::tmem_ld32(s_addr + 32 * c4, sv + 32 * c4);
+    umma::tmem_ld_wait();
+    if constexpr (kSepP && !kCap) {  // S_g may be overwritten by the next product
+      umma::fence_before_sync();
+      mbar_arrive(&ctl.s_free[g]);
+    }
+
+    if constexpr (kBias) {
+      if (a.mod.cap2 > 0.f) {  // a cap under the bias
 #pragma unroll
-    for (int c = 0; c < kKeys; ++c)
-      sv[c] = fmaf(sv[c], pre, -slope2 * fabsf((float)(dist - c)));
+        for (int c = 0; c < kKeys; ++c) sv[c] = a.mod.cap2 * cap_tanh(sv[c] * a.mod.cap_in);
+      }
+      const float pre = a.mod.cap2 > 0.f ? 1.f : a.scale_log2;
+      const int dist = qpos - t0;             // from the tile's first key to the query
+      if (t0 + kKeys - 1 <= pos0 + w0 / G) {  // every key at the warp's queries or before
+        const float2 pre2 = make_float2(pre, pre);
+        const float2 step = make_float2(16.f * slope2, 16.f * slope2);
+        float2 bias[8];  // of keys 2i, 2i + 1; then of those 16 later
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          bias[i] = make_float2(slope2 * (float)(2 * i - dist), slope2 * (float)(2 * i + 1 - dist));
+#pragma unroll
+        for (int c = 0; c < kKeys / 2; ++c) {
+          const float2 x = umma::ffma2(make_float2(sv[2 * c], sv[2 * c + 1]), pre2, bias[c & 7]);
+          bias[c & 7] = umma::fadd2(bias[c & 7], step);
+          sv[2 * c] = x.x;
+          sv[2 * c + 1] = x.y;
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c)
+          sv[c] = fmaf(sv[c], pre, -slope2 * fabsf((float)(dist - c)));
+      }
+    }
+    if (past) {
+      const int n = lim - t0;
+#pragma unroll
+      for (int c = 0; c < kKeys; ++c)
+        if (c >= n) sv[c] = -INFINITY;
+    }
+    if (before) {
+      const int n0 = u_keep - t0, n1 = low - t0;
+#pragma unroll
+      for (int c = 0; c < kKeys; ++c)
+        if (c < n1 && c >= n0) sv[c] = -INFINITY;
+    }
+    float mx[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) mx[c] = fmaxf(sv[2 * c], sv[2 * c + 1]);
+#pragma unroll
+    for (int c = 4; c < kKeys / 2; ++c) mx[c & 3] = fmaxf(mx[c & 3], fmaxf(sv[2 * c], sv[2 * c + 1]));
+    // the scale is positive and the cap monotone: the maximum's score is the maximum
+    float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    if constexpr (kCap) mt = mt == -INFINITY ? mt : a.mod.cap2 * cap_tanh(mt * a.mod.cap_in);
+    else if constexpr (!kBias) mt *= a.scale_log2;
+    float alpha = 1.f;
+    bool rescale = false;
+    if (it == 0) {
+      m_run = mt;
+    } else if (mt > m_run + kRescaleThreshold) {
+      alpha = fast_exp2(m_run - mt);
+      m_run = mt;
+      rescale = true;
+    }
+    const float m_safe = m_run == -INFINITY ? 0.f : m_run;
+
+    // ---- p = 2^(score - m), packed as 16-bit pairs in the element type of V
+    const float2 nm2 = make_float2(-m_safe, -m_safe);
+    float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                     make_float2(0.f, 0.f)};
+    auto exp_pair = [&](float* w, int c, float2 e) {
+      const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+      acc[c & 3] = umma::fadd2(acc[c & 3], p);
+      w[c] = __uint_as_float(pack_elt2<F16>(p.x, p.y));
+    };
+    bool chunks = false;
+    if constexpr (kCap) {
+      chunks = past || before || way > 0;
+      if (!chunks) {
+        float zm[2] = {0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kKeys / 2; ++c) {
+          const float2 v = make_float2(sv[2 * c], sv[2 * c + 1]);
+          const float2 z = umma::fmul2(v, v);
+          zm[c & 1] = fmaxf(zm[c & 1], fmaxf(z.x, z.y));
+          exp_pair(sv, c, umma::ffma2(v, cap_poly2<3>(z, a.mod), nm2));
+        }
+        if (!__all_sync(0xffffffffu, fmaxf(zm[0], zm[1]) < a.mod.z_lim3)) {
+          chunks = true;
+          way = 1;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[c] = make_float2(0.f, 0.f);
+        }
+      }
+    } else {
+      const float sc1 = kBias ? 1.f : a.scale_log2;
+      const float2 sc2 = make_float2(sc1, sc1);
+#pragma unroll
+      for (int c = 0; c < kKeys / 2; ++c)
+        exp_pair(sv, c, umma::ffma2(make_float2(sv[2 * c], sv[2 * c + 1]), sc2, nm2));
+    }
+    if constexpr (kSepP) {
+      // the previous P.V of this tile has read P_g and landed in O_g
+      if (sc > 1 && !mbar_wait(&ctl.pv_done[g], (uint32_t)((sc - 2) & 1), abort_flag))
+        note_timeout(ctl, a.dev_err);
+      umma::fence_after_sync();
+    }
+    if (!chunks) {
+      umma::tmem_st32(p_addr, sv);
+      umma::tmem_st32(p_addr + 32, sv + 32);
+    }
+    if constexpr (kCap) {
+      if (chunks) {
+        float z_max = 0.f;
+        int used = way > 0 ? way : 1;
+#pragma unroll 1
+        for (int k0 = 0; k0 < kKeys; k0 += 32) {
+          // P of the chunks before lies over the first half of their columns
+          float y[32], w[16];
+          umma::tmem_ld32(s_addr + k0, y);
+          umma::tmem_ld_wait();
+          const int n = lim - t0 - k0, n0 = u_keep - t0 - k0, n1 = low - t0 - k0;
+          auto on = [&](int c) { return c < n && (c >= n1 || c < n0); };
+          const float2 acc0[4] = {acc[0], acc[1], acc[2], acc[3]};
+          if (used == 1) {
+            float zm[2] = {0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float2 v = make_float2(y[2 * c], y[2 * c + 1]);
+              const float2 z = umma::fmul2(v, v);
+              const float2 e = umma::ffma2(v, cap_poly2<5>(z, a.mod), nm2);
+              const bool a0 = on(2 * c), a1 = on(2 * c + 1);
+              zm[c & 1] = fmaxf(zm[c & 1], fmaxf(a0 ? z.x : 0.f, a1 ? z.y : 0.f));
+              exp_pair(w, c, make_float2(a0 ? e.x : -INFINITY, a1 ? e.y : -INFINITY));
+            }
+            z_max = fmaxf(z_max, fmaxf(zm[0], zm[1]));
+            if (!__all_sync(0xffffffffu, z_max < a.mod.z_lim)) {
+              used = 2;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) acc[c] = acc0[c];
+            }
+          }
+          if (used == 2) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              float e[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float v = y[2 * c + i];
+                const bool a0 = on(2 * c + i);
+                z_max = fmaxf(z_max, a0 ? v * v : 0.f);
+                e[i] = a0 ? a.mod.cap2 * cap_tanh(v * a.mod.cap_in) - m_safe : -INFINITY;
+              }
+              exp_pair(w, c, make_float2(e[0], e[1]));
+            }
+          }
+          umma::tmem_st16(p_addr + (k0 >> 1), w);
+        }
+        way = __all_sync(0xffffffffu, z_max < 0.7f * a.mod.z_lim3)  ? 0
+              : __all_sync(0xffffffffu, z_max < 0.7f * a.mod.z_lim) ? 1
+                                                                    : 2;
+      }
+    }
+    const float2 tt = umma::fadd2(umma::fadd2(acc[0], acc[1]), umma::fadd2(acc[2], acc[3]));
+    l_run = l_run * alpha + (tt.x + tt.y);
+    // O_g is stable here (as in the plain form); PV_g(it) waits for p_full
+    if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+      for (int c4 = 0; c4 < D / 64; ++c4) {
+        float ob[64];
+        umma::tmem_ld32(lane_addr + col_o(g) + 64 * c4, ob);
+        umma::tmem_ld32(lane_addr + col_o(g) + 64 * c4 + 32, ob + 32);
+        umma::tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 64; ++e) ob[e] *= alpha;
+        umma::tmem_st32(lane_addr + col_o(g) + 64 * c4, ob);
+        umma::tmem_st32(lane_addr + col_o(g) + 64 * c4 + 32, ob + 32);
+      }
+    }
+    // rows of the V tile beyond the sequence, and rows that no query of the unit sees: zero
+    // them (never multiply a stale row)
+    if (t0 + kKeys > kv_len || (t0 < u_low && t0 + kKeys > u_keep)) {
+      const int vi = u.vbase + it;
+      const int st = vi % kVStages;
+      if (!mbar_wait(&ctl.v_full[st], (uint32_t)((vi / kVStages) & 1), abort_flag))
+        note_timeout(ctl, a.dev_err);
+      if (t0 + r >= kv_len || (t0 + r < u_low && t0 + r >= u_keep)) {
+#pragma unroll
+        for (int ch = 0; ch < D / 8; ++ch)
+          *reinterpret_cast<uint4*>(sm.v[st] + (ch >> 3) * kHalf + r * 128 + (ch & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+    }
+    umma::tmem_st_wait();
+    umma::fence_before_sync();
+    if constexpr (kSepP && kCap) mbar_arrive(&ctl.s_free[g]);  // S_g may be overwritten
+    mbar_arrive(&ctl.p_full[g]);
   }
+  l_out = l_run;
 }
 
-template <int G, int D, bool F16, bool MOD = false>
+template <int G, int D, bool F16, int FORM = kFormPlain>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
-                         const __grid_constant__ CUtensorMap tm_q, const ArgsT<MOD> a) {
+                         const __grid_constant__ CUtensorMap tm_q, const ArgsT<FORM> a) {
   constexpr int P = kRows / G;  // query positions per tile
   constexpr int NH = D / 64;    // 64-dim swizzled column blocks per row
   constexpr bool kSepP = D == 64;  // P in its own tensor-memory columns (see col_p)
   using Tiles = PrefillTiles<D>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   PrefillCtl& ctl = *reinterpret_cast<PrefillCtl*>(smem_raw);
-  using Rec = RecT<MOD>;
+  using Rec = RecT<FORM>;
   Rec* recs = reinterpret_cast<Rec*>(smem_raw + kCtlBytes);
   Tiles& sm = *reinterpret_cast<Tiles*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + kCtlBytes + kRecBytes + 1023) & ~uintptr_t(1023));
@@ -528,11 +781,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     umma::tmem_relinquish();
   }
   __syncthreads();
-  if (a.persistent) build_schedule<P, MOD>(ctl, recs, &sm.k[0][0], a, cu_q0, cu_k0);
-  else single_schedule<P, MOD>(ctl, recs, a);
-  // first key of the it-th key tile of a unit (MOD: the hidden tiles are left out)
+  if (a.persistent) build_schedule<P, FORM>(ctl, recs, &sm.k[0][0], a, cu_q0, cu_k0);
+  else single_schedule<P, FORM>(ctl, recs, a);
+  // first key of the it-th key tile of a unit (modified: the hidden tiles are left out)
   auto tile_key0 = [&](const Rec& u, int it) {
-    if constexpr (MOD) return KeySpan<true>{u.kv_len, u.low, u.keep}.first_key(kKeys, it);
+    if constexpr (FORM != kFormPlain) return KeySpan<true>{u.kv_len, u.low, u.keep}.first_key(kKeys, it);
     else return it * kKeys;
   };
   // the schedule's scratch in the K ring was written through the generic proxy; TMA (the
@@ -570,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Rec& u = recs[k];
       const int key0 = tile_key0(u, it) + lane * box_rows;
       if (key0 >= u.kv_len) return -1;
-      if constexpr (MOD) {  // a box that no query of the unit sees is not read
+      if constexpr (FORM != kFormPlain) {  // a box that no query of the unit sees is not read
         if (key0 >= u.keep && key0 + box_rows <= u.low) return -1;
       }
       const int id = __ldg(a.block_tables + (int64_t)u.s * a.max_blocks + key0 / bs);
@@ -877,28 +1130,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (k < n_units) {
       const int kn = next_unit(k);
       int lim_row, kv_len, vbase, my_nt;
-      int qpos;          // absolute position of the row
-      int low_row = 0;   // MOD: of the keys [0, lim_row) those below keep or from low_row on
-      {                  // count
+      {
         const Rec& u = recs[k];
-        qpos = (u.kv_len - u.n) + u.i0 + g * P + pos;
+        const int qpos = (u.kv_len - u.n) + u.i0 + g * P + pos;  // absolute position of the row
         kv_len = u.kv_len;
         lim_row = causal ? min(kv_len, qpos + 1) : kv_len;  // keys [0, lim_row) count
         vbase = u.vbase;
         my_nt = nt_of(u.nt, g);
-        if constexpr (MOD) {
-          lim_row = max(lim_row, min(kv_len, u.prefix));
-          if (a.mod.window > 0) low_row = qpos - a.mod.window + 1;
-        }
-      }
-      float score_scale = a.scale_log2;  // of the values that the softmax below reads
-      float slope2 = 0.f;
-      if constexpr (MOD) {
-        if (a.mod.slopes)
-          slope2 = __ldg(a.mod.slopes + recs[k].j * G + hh) * 1.4426950408889634f;
-        if (a.mod.slopes || a.mod.cap2 > 0.f) score_scale = 1.f;
       }
       float m_run = -INFINITY, l_run = 0.f;
+      if constexpr (FORM != kFormPlain) {
+        mod_tiles<G, D, F16, FORM>(ctl, sm, recs[k], a, g, r, lane_addr, sc, l_run);
+      } else
       for (int it = 0; it < my_nt; ++it) {
         if (!mbar_wait(&ctl.s_full[g], (uint32_t)(sc & 1), abort_flag)) note_timeout(ctl, a.dev_err);
         ++sc;
@@ -912,22 +1155,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&ctl.s_free[g]);
         }
 
-        const int t0 = tile_key0(recs[k], it);
-        if constexpr (MOD) mod_scores(sv, a.mod, a.scale_log2, slope2, qpos - t0);
+        const int t0 = it * kKeys;
         // only tiles that reach past this row's last visible key need a mask
         if (__any_sync(0xffffffffu, t0 + kKeys > lim_row)) {
 #pragma unroll
           for (int c = 0; c < kKeys; ++c)
             if (t0 + c >= lim_row) sv[c] = -INFINITY;
-        }
-        if constexpr (MOD) {
-          // ... or that hold keys before its window
-          const int keep = recs[k].keep;
-          if (__any_sync(0xffffffffu, t0 < low_row && t0 + kKeys > keep)) {
-#pragma unroll
-            for (int c = 0; c < kKeys; ++c)
-              if (t0 + c < low_row && t0 + c >= keep) sv[c] = -INFINITY;
-          }
         }
         float mx[8];
 #pragma unroll
@@ -935,8 +1168,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 8; c < kKeys; ++c) mx[c & 7] = fmaxf(mx[c & 7], sv[c]);
         // the scale is positive, so the max of the scaled scores is the scaled max
-        const float mt = score_scale * fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                             fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        const float mt = a.scale_log2 * fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                              fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
         float m_use, alpha;
         bool rescale = false;
         if (it == 0) {
@@ -953,7 +1186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m_safe = (m_use == -INFINITY) ? 0.f : m_use;
         // p = 2^(s*scale - m): one packed fma per pair, then ex2; P packed as 16-bit pairs
         // over S, in the element type of V (the PV product takes both operands in one type)
-        const float2 sc2 = make_float2(score_scale, score_scale);
+        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
         const float2 nm2 = make_float2(-m_safe, -m_safe);
         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                          make_float2(0.f, 0.f)};
@@ -994,18 +1227,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma::tmem_st32(lane_addr + col_o(g) + 32 * c4, ob);
           }
         }
-        // rows of the last V tile beyond the sequence (MOD: and rows that no query of the unit
-        // sees): zero them (never multiply a stale row)
-        bool v_hidden = false;
-        if constexpr (MOD) v_hidden = t0 < recs[k].low && t0 + kKeys > recs[k].keep;
-        if (t0 + kKeys > kv_len || v_hidden) {
+        // rows of the last V tile beyond the sequence: zero them (never multiply a stale row)
+        if (t0 + kKeys > kv_len) {
           const int vi = vbase + it;
           const int st = vi % kVStages;
           if (!mbar_wait(&ctl.v_full[st], (uint32_t)((vi / kVStages) & 1), abort_flag))
             note_timeout(ctl, a.dev_err);
-          bool bad = t0 + r >= kv_len;
-          if constexpr (MOD) bad = bad || (t0 + r < recs[k].low && t0 + r >= recs[k].keep);
-          if (bad) {
+          const int first_bad = kv_len - t0;
+          if (r >= first_bad) {
 #pragma unroll
             for (int ch = 0; ch < D / 8; ++ch)
               *reinterpret_cast<uint4*>(sm.v[st] + (ch >> 3) * kHalf + r * 128 + (ch & 7) * 16) =
@@ -1067,8 +1296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }
 
-template <int G, int D, bool F16, bool MOD = false>
-int launch_prefill_t(const ArgsT<MOD>& a, const DeviceInfo& info, cudaStream_t stream,
+template <int G, int D, bool F16, int FORM = kFormPlain>
+int launch_prefill_t(const ArgsT<FORM>& a, const DeviceInfo& info, cudaStream_t stream,
                      const CUtensorMap& mk, const CUtensorMap& mv) {
   constexpr int P = kRows / G;
   constexpr size_t smem = prefill_smem_bytes<D>();
@@ -1077,7 +1306,7 @@ int launch_prefill_t(const ArgsT<MOD>& a, const DeviceInfo& info, cudaStream_t s
   if (info.device < 0 || info.device >= 64) return PA_ERR_CUDA;
   if ((size_t)info.max_smem_optin < smem) return PA_ERR_UNSUPPORTED;
   if (!attr_done[info.device].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(paged_prefill_kernel<G, D, F16, MOD>,
+    if (cudaFuncSetAttribute(paged_prefill_kernel<G, D, F16, FORM>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem) != cudaSuccess)
       return PA_ERR_CUDA;
@@ -1086,33 +1315,33 @@ int launch_prefill_t(const ArgsT<MOD>& a, const DeviceInfo& info, cudaStream_t s
   const int64_t qt_n = (a.max_seqlen_q + 2 * P - 1) / (2 * P);  // pairs per sequence at most
   const int64_t max_pairs = qt_n * a.num_seqs;
   const int64_t max_units = max_pairs * a.num_kv_heads;
-  ArgsT<MOD> args = a;
+  ArgsT<FORM> args = a;
   CUtensorMap mq;
   if (!make_rows_map(&mq, a.q, q_map_rows(a), a.num_heads, D, F16, G, P)) return PA_ERR_CUDA;
   // persistent (one CTA per SM, fewer when the batch has fewer units) when the in-kernel
   // sort and every CTA's records are sure to hold the batch; else one unit per CTA
   const int grid1 = (int)(max_units < info.num_sms ? max_units : info.num_sms);
   args.persistent = a.num_seqs <= kMaxSortSeqs && max_pairs <= kMaxSortPairs && grid1 > 0 &&
-                    (max_units + grid1 - 1) / grid1 + 1 <= kMaxUnitRecs<MOD>;
+                    (max_units + grid1 - 1) / grid1 + 1 <= kMaxUnitRecs<FORM>;
   if (args.persistent) {
-    paged_prefill_kernel<G, D, F16, MOD><<<grid1, kThreads, smem, stream>>>(mk, mv, mq, args);
+    paged_prefill_kernel<G, D, F16, FORM><<<grid1, kThreads, smem, stream>>>(mk, mv, mq, args);
   } else {
     if (qt_n > 65535) return PA_ERR_UNSUPPORTED;
     dim3 grid((unsigned)a.num_kv_heads, (unsigned)a.num_seqs, (unsigned)qt_n);
-    paged_prefill_kernel<G, D, F16, MOD><<<grid, kThreads, smem, stream>>>(mk, mv, mq, args);
+    paged_prefill_kernel<G, D, F16, FORM><<<grid, kThreads, smem, stream>>>(mk, mv, mq, args);
   }
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 // Every GQA group size for one (head_dim, element type, form) combination.
-template <int D, bool F16, bool MOD = false>
-int dispatch_prefill(const ArgsT<MOD>& a, const DeviceInfo& info, cudaStream_t stream,
+template <int D, bool F16, int FORM = kFormPlain>
+int dispatch_prefill(const ArgsT<FORM>& a, const DeviceInfo& info, cudaStream_t stream,
                      const CUtensorMap& mk, const CUtensorMap& mv) {
   switch (a.num_heads / a.num_kv_heads) {
-    case 1: return launch_prefill_t<1, D, F16, MOD>(a, info, stream, mk, mv);
-    case 2: return launch_prefill_t<2, D, F16, MOD>(a, info, stream, mk, mv);
-    case 4: return launch_prefill_t<4, D, F16, MOD>(a, info, stream, mk, mv);
-    case 8: return launch_prefill_t<8, D, F16, MOD>(a, info, stream, mk, mv);
+    case 1: return launch_prefill_t<1, D, F16, FORM>(a, info, stream, mk, mv);
+    case 2: return launch_prefill_t<2, D, F16, FORM>(a, info, stream, mk, mv);
+    case 4: return launch_prefill_t<4, D, F16, FORM>(a, info, stream, mk, mv);
+    case 8: return launch_prefill_t<8, D, F16, FORM>(a, info, stream, mk, mv);
     default: return PA_ERR_UNSUPPORTED;
   }
 }

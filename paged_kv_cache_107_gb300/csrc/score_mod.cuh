@@ -45,11 +45,9 @@ __device__ __forceinline__ void mod_span(KeySpan<true>& k, const ScoreModArgs& m
   k.keep = max(m.sink, mod_prefix(m, s));
 }
 
-// tanh(u) for the score cap. Below |u| = 1 an odd polynomial, tanh(u) = u P(u^2), P of degree
-// 5 fitted on Chebyshev nodes of [0, 1], reweighted toward the largest relative error: 6e-7
-// relative. From 1 on 1 - 2 / (1 + e^(2u)) with the hardware's exp2 and reciprocal: about
-// 2e-7 absolute. (The hardware's own tanh is off by 5e-4 relative, 0.02 in a score near a
-// cap of 50.) NaN stays NaN, +-inf gives +-1.
+// tanh(u) for the score cap: kTanhPoly below |u| = 1; from there on 1 - 2 / (1 + e^(2u)) with
+// the hardware's exp2 and reciprocal, about 2e-7 absolute. (The hardware's own tanh is off by
+// 5e-4 relative, 0.02 in a score near a cap of 50.) NaN stays NaN, +-inf gives +-1.
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -57,10 +55,9 @@ __device__ __forceinline__ float fast_rcp(float x) {
 }
 
 __device__ __forceinline__ float cap_tanh(float u) {
-  constexpr float c0 = 0.9999994039535522f, c1 = -0.3332904279232025f,
-                  c2 = 0.13281433284282684f, c3 = -0.051605675369501114f,
-                  c4 = 0.016743116080760956f, c5 = -0.0030670606065541506f;
   const float z = u * u;
+  constexpr float c0 = kTanhPoly[0], c1 = kTanhPoly[1], c2 = kTanhPoly[2], c3 = kTanhPoly[3],
+                  c4 = kTanhPoly[4], c5 = kTanhPoly[5];
   const float p = fmaf(fmaf(fmaf(fmaf(fmaf(c5, z, c4), z, c3), z, c2), z, c1), z, c0);
   const float far =
       fmaf(-2.f, fast_rcp(1.f + fast_exp2(u * (2.f * 1.4426950408889634f))), 1.f);
