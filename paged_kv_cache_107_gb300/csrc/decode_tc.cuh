@@ -50,9 +50,9 @@ namespace {
 constexpr int kTcGMax = 8;   // query heads per KV head on this path (rows of the 16-row tile)
 
 // What a stage's tile needs beyond StageMeta where keys may be hidden: key t of the sequence
-// is visible when t < keep or t >= low; the position of the query; the sequence's group.
+// is visible when t < keep or t >= low; the position of the query.
 struct __align__(16) SpanMeta : StageMeta {
-  int keep, low, pos, group;
+  int keep, low, pos;
 };
 
 template <int S, typename Meta = StageMeta>
@@ -159,7 +159,7 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 }
 
 // The kernel's forms: plain; with modified scores (pa_decode_mod); the part of pa_decode_shared
-// behind the shared prefix, joined with the prefix kernel's partial results.
+// behind the shared prefixes, whose partial results shared_join.cu joins with the prefixes'.
 enum TcForm { kTcPlain = 0, kTcMod = 1, kTcShared = 2 };
 template <int FORM>
 struct TcArgs {
@@ -174,119 +174,6 @@ template <>
 struct TcArgs<kTcShared> {
   using type = DecodeSharedArgs;
 };
-
-// The partial results that the prefix kernel left for (sequence b of group grp, KV head kvh).
-struct PrefixParts {
-  int n;            // parts
-  int64_t c0;       // CTA of the first
-  int row;          // row of the sequence's first head within a CTA's 256
-  const float *first_o, *first_lse, *more_o, *more_lse;  // first_*: at (b, first head of kvh)
-  // log-sum-exp and row of head h in part i
-  __device__ __forceinline__ const float* lse(int i, int h) const {
-    return i == 0 ? first_lse + h : more_lse + (c0 + i) * 256 + row + h;
-  }
-  __device__ __forceinline__ const float* o(int i, int h, int D) const {
-    return i == 0 ? first_o + (int64_t)h * D : more_o + ((c0 + i) * 256 + row + h) * D;
-  }
-};
-
-__device__ __forceinline__ PrefixParts prefix_parts(const DecodeSharedArgs& a, int b, int grp,
-                                                    int kvh, int D) {
-  const SharedArgs& sh = a.sh;
-  const int H = a.num_heads, Hk = a.num_kv_heads, G = H / Hk, P = kPrefixRows / G;
-  const int first = __ldg(sh.group_starts + grp);
-  const GroupWork w(sh, __ldg(sh.group_starts + grp + 1) - first, __ldg(sh.prefix_lens + grp), P);
-  const int tile = (b - first) / P;
-  const int64_t nx = __ldcg(sh.plan);
-  const int64_t x = __ldcg(sh.plan + 1 + grp) + w.unit_first(Hk, tile >> 1, kvh);
-  const int ctas = prefix_ctas(nx, sh.prefix_grid);
-  PrefixParts p;
-  p.c0 = prefix_cta_of(x, nx, ctas);
-  p.n = (int)(prefix_cta_of(x + w.unit_steps(tile >> 1) - 1, nx, ctas) - p.c0) + 1;
-  p.row = (tile & 1) * kPrefixRows + ((b - first) % P) * G;
-  p.first_o = sh.first_o + ((int64_t)b * H + kvh * G) * D;
-  p.first_lse = sh.first_lse + (int64_t)b * H + kvh * G;
-  p.more_o = sh.more_o;
-  p.more_lse = sh.more_lse;
-  return p;
-}
-
-// combine_partials with the prefix's parts before the nseg segments of the rest (in that
-// order; nseg may be 0). One warp.
-template <int D, bool F16>
-__device__ __forceinline__ void combine_shared(const DecodeSharedArgs& a, int b, int grp, int kvh,
-                                               int G, int64_t c_lo, int nseg, int64_t NT,
-                                               int g_eff, int64_t pb, int lane) {
-  constexpr int CPL = D / 32;  // combined dims per lane
-  constexpr int SU = 4;        // parts whose loads are in flight together
-  const int H = a.num_heads;
-  const PrefixParts parts = prefix_parts(a, b, grp, kvh, D);
-  const int total = parts.n + nseg;
-  auto seg_at = [&](int i) {  // slot of segment i of the rest
-    const int64_t c = c_lo + i;
-    return c * 2 + (tile_begin(c, NT, g_eff) < pb ? 1 : 0);
-  };
-  const int SB = 32 / G;  // parts per batch; lane h + G*j holds head h of part j
-  const int my_h = lane % G, my_j = lane / G;
-  for (int h = 0; h < G; ++h) {
-    float m = -INFINITY, den = 0.f, acc[CPL];
-#pragma unroll
-    for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
-    for (int s0 = 0; s0 < total; s0 += SB) {
-      const int nb = min(SB, total - s0);
-      float ls = -INFINITY;
-      const int mine = s0 + my_j;
-      if (my_j < nb)
-        ls = __ldcg(mine < parts.n ? parts.lse(mine, my_h)
-                                   : a.part_lse + seg_at(mine - parts.n) * H + kvh * G + my_h);
-      float bm = m;
-      for (int j = 0; j < nb; ++j) bm = fmaxf(bm, __shfl_sync(0xffffffffu, ls, h + G * j));
-      const float al = m == -INFINITY ? 0.f : fast_exp2(m - bm);
-      den *= al;
-#pragma unroll
-      for (int e = 0; e < CPL; ++e) acc[e] *= al;
-      m = bm;
-      for (int j0 = 0; j0 < nb; j0 += SU) {
-        float w[SU], po[SU][CPL];
-#pragma unroll
-        for (int u = 0; u < SU; ++u) {
-          const int j = j0 + u;
-          const float l = __shfl_sync(0xffffffffu, ls, j < nb ? h + G * j : 0);
-          w[u] = j < nb && l != -INFINITY ? fast_exp2(l - m) : 0.f;
-#pragma unroll
-          for (int e = 0; e < CPL; ++e) po[u][e] = 0.f;
-          if (w[u] != 0.f) {
-            const int i = s0 + j;
-            const float* src = i < parts.n
-                                   ? parts.o(i, h, D)
-                                   : a.part_o + (seg_at(i - parts.n) * H + kvh * G + h) * D;
-            if constexpr (CPL == 4) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(src + lane * 4));
-              po[u][0] = v.x, po[u][1] = v.y, po[u][2] = v.z, po[u][3] = v.w;
-            } else {
-              const float2 v = __ldcg(reinterpret_cast<const float2*>(src + lane * 2));
-              po[u][0] = v.x, po[u][1] = v.y;
-            }
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < SU; ++u) {
-          den += w[u];
-#pragma unroll
-          for (int e = 0; e < CPL; ++e) acc[e] = fmaf(w[u], po[u][e], acc[e]);
-        }
-      }
-    }
-    const float inv = den > 0.f ? 1.f / den : 0.f;
-    uint16_t* dst =
-        static_cast<uint16_t*>(a.out) + ((int64_t)b * H + kvh * G + h) * D + lane * CPL;
-    if constexpr (CPL == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(f2_elt2<F16>(acc[0] * inv, acc[1] * inv),
-                                                  f2_elt2<F16>(acc[2] * inv, acc[3] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(dst) = f2_elt2<F16>(acc[0] * inv, acc[1] * inv);
-  }
-}
 
 template <int HS, bool FUSED, int D, bool F16, int FORM = kTcPlain>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -484,14 +371,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int heads_per_slab = HS * G;
     for (int b = c + warp * (int)gridDim.x; b < B; b += (kThreads / 32) * (int)gridDim.x) {
       if (load_ctx(a.context_lens, b, cap) != 0) {
-        if constexpr (FORM == kTcShared) {  // all of the context is shared: only to be joined
-          if (span_of(b).hi == 0) {
-            const int grp = group_of(g_starts, a.sh.num_groups, b);
-            for (int j = 0; j < HS; ++j)
-              combine_shared<D, F16>(a, b, grp, slab * HS + j, G, 0, 0, 1, 1, 0, lane);
-          }
+        if constexpr (FORM == kTcShared) {  // all of the context is shared: no segment here
+          if (slab == 0 && lane == 0 && span_of(b).hi == 0) a.sh.rest[b] = RestSegments{0, 0};
         }
         continue;
+      }
+      if constexpr (FORM == kTcShared) {
+        if (slab == 0 && lane == 0) a.sh.rest[b] = RestSegments{0, -1};
       }
       uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
                                             ((int64_t)b * H + slab * heads_per_slab) * D);
@@ -630,7 +516,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           m.keep = sp.keep;
           m.low = sp.low;
           m.pos = sp.hi - 1;
-          m.group = grp;
         }
         if (tb > 0)
           mbar_arrive_expect_tx(&ctl.full[s], (uint32_t)(nbox * 2 * TC::NH * box_bytes +
@@ -978,7 +863,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // normalise and write the rows, or the partials for the combine
         const int b = meta.b;
-        bool joined = false;  // kTcShared: the prefix kernel has a part of the sequence
+        if constexpr (FORM == kTcShared) {
+          if (kvh == 0 && lane == 0 && meta.pb >= x0) {  // where the join finds the segments
+            const int last = (int)cta_of(meta.pb + meta.nb - 1, NT, g_eff);
+            const bool done = (meta.flags & kFlagWhole) && meta.low == 0;
+            a.sh.rest[b] = RestSegments{c, done ? -1 : last - c + 1};
+          }
+        }
+        // kTcShared: the sequence also has a prefix part, and the join is still to come
+        bool joined = false;
         if constexpr (FORM == kTcShared) joined = meta.low > 0;
         if ((meta.flags & kFlagWhole) && !joined) {
           if (row_ok) {
@@ -988,6 +881,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int n = 0; n < NO; ++n)
               *reinterpret_cast<uint32_t*>(dst + n * 8 + 2 * tig) =
                   f2_elt2<F16>(o[n][0] * inv, o[n][1] * inv);
+          }
+        } else if constexpr (FORM == kTcShared) {
+          // the segment with the sequence's first tile by sequence, a later one by CTA
+          const bool first_seg = meta.pb >= x0;
+          if (row_ok) {
+            const int hg = kvh * G + gid;
+            const float inv = l_all > 0.f ? 1.f / l_all : 0.f;
+            const int64_t row = first_seg ? (int64_t)b * H + hg : (int64_t)c * H + hg;
+            float* dst = (first_seg ? a.sh.rest_o : a.part_o) + row * D;
+#pragma unroll
+            for (int n = 0; n < NO; ++n)
+              *reinterpret_cast<float2*>(dst + n * 8 + 2 * tig) = make_float2(o[n][0] * inv, o[n][1] * inv);
+            if (tig == 0)
+              (first_seg ? a.sh.rest_lse : a.part_lse)[row] =
+                  (l_all > 0.f) ? m_run + fast_log2(l_all) : -INFINITY;
           }
         } else {
           const int slot = (x0 < meta.pb) ? 1 : 0;
@@ -1014,13 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (old == nseg - 1) {
             // (4) last arrival: combine the partials of sequence b in CTA order
             __threadfence();
-            if constexpr (FORM == kTcShared) {
-              if (joined)
-                combine_shared<D, F16>(a, b, meta.group, kvh, G, c_lo, nseg, NT, g_eff, meta.pb,
-                                       lane);
-            }
-            if (!joined)
-              combine_partials<D, F16, kTcGMax>(a, b, kvh, G, c_lo, nseg, NT, g_eff, meta.pb, lane);
+            combine_partials<D, F16, kTcGMax>(a, b, kvh, G, c_lo, nseg, NT, g_eff, meta.pb, lane);
             if (lane == 0) *counter = 0;  // leave the counter zero for the next call
           }
         }

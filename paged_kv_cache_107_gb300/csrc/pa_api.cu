@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/pa.h"
 #include "pa_launch.h"
@@ -286,23 +287,28 @@ static int decode_check_workspace(DecodeArgs* a, const DeviceInfo& info, void* w
 }
 
 // Points the scratch of pa_decode_shared into `ws` (may be null: only the size is wanted);
-// returns the bytes needed. Nothing in it outlives a call: the prefix kernel zeroes the
-// arrival counters.
+// returns the bytes needed. Nothing in it outlives a call.
 static size_t shared_bind_workspace(DecodeSharedArgs* a, unsigned char* ws) {
-  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  size_t at = 0;
+  auto take = [&](auto** p, size_t n) {
+    using T = std::remove_reference_t<decltype(**p)>;
+    *p = ws ? reinterpret_cast<T*>(ws + at) : nullptr;
+    at += (n * sizeof(T) + 255) & ~size_t(255);
+  };
   const size_t rows = (size_t)a->num_seqs * a->num_heads;
   const size_t more = (size_t)a->sh.prefix_grid * 256;
-  size_t at = up(decode_bind_workspace(a, ws, a->grid_ctas));
-  auto take = [&](size_t bytes) {
-    unsigned char* p = ws ? ws + at : nullptr;
-    at += up(bytes);
-    return p;
-  };
-  a->sh.first_lse = reinterpret_cast<float*>(take(rows * sizeof(float)));
-  a->sh.first_o = reinterpret_cast<float*>(take(rows * a->head_dim * sizeof(float)));
-  a->sh.more_lse = reinterpret_cast<float*>(take(more * sizeof(float)));
-  a->sh.more_o = reinterpret_cast<float*>(take(more * a->head_dim * sizeof(float)));
-  a->sh.plan = reinterpret_cast<int64_t*>(take(((size_t)a->num_seqs + 1) * sizeof(int64_t)));
+  const size_t cut = (size_t)a->grid_ctas * a->num_heads;
+  take(&a->sh.more_o, more * a->head_dim);
+  take(&a->sh.more_lse, more);
+  take(&a->part_o, cut * a->head_dim);
+  take(&a->part_lse, cut);
+  take(&a->sh.first_o, rows * a->head_dim);
+  take(&a->sh.first_lse, rows);
+  take(&a->sh.rest_o, rows * a->head_dim);
+  take(&a->sh.rest_lse, rows);
+  take(&a->sh.steps, 1);
+  take(&a->sh.where, (size_t)a->num_seqs);
+  take(&a->sh.rest, (size_t)a->num_seqs);
   return at;
 }
 

@@ -111,21 +111,40 @@ struct DecodeModArgs : DecodeArgs {
   ScoreModArgs mod;
 };
 
-// pa_decode_shared: the groups and the prefix kernel's results.
+// Where the join of pa_decode_shared finds a sequence's parts. Prefix parts are addressed
+// through the steps of the prefix kernel's stream (shared_groups.cuh).
+struct PrefixWhere {
+  int64_t group_x;  // first step of the sequence's group
+  int32_t first;    // first sequence of the group
+  int32_t n;        // its sequences
+  int32_t prefix;   // its prefix_lens entry (0 where nothing is shared)
+  int32_t unused;
+};
+struct RestSegments {
+  int32_t c0;  // CTA of the segment that holds the sequence's first tile
+  int32_t n;   // segments, one for each CTA from c0 on; -1: the row is written already
+};
+
+// pa_decode_shared: the groups and the partial results (normalised rows and base-2
+// log-sum-exps). Of a prefix unit or a sequence's rest, the part that holds the first step or
+// tile is stored by sequence, a part that another CTA carries on by that CTA (a CTA carries
+// on one unit and one sequence at most, its first; DecodeArgs::part_o and part_lse hold
+// those of the rests).
 struct SharedArgs {
   const int32_t* group_starts;  // [num_groups + 1]
   const int32_t* prefix_lens;   // [num_groups]
   int num_groups;
   int boxes;          // 1: the block size allows the prefix kernel's TMA boxes
   int prefix_grid;    // CTAs of the prefix kernel
-  // The partial results of a unit (normalised rows and base-2 log-sum-exps): the part that
-  // holds its first step by sequence, a part that another CTA carries on by that CTA (a CTA
-  // carries on one unit at most, its first).
-  float* first_o;     // [num_seqs * num_heads * head_dim]
+  float* first_o;     // [num_seqs * num_heads * head_dim]: prefixes
   float* first_lse;   // [num_seqs * num_heads]
   float* more_o;      // [prefix_grid * 256 * head_dim]
   float* more_lse;    // [prefix_grid * 256]
-  int64_t* plan;      // [0] steps, [1 + g] first step of group g
+  float* rest_o;      // [num_seqs * num_heads * head_dim]: rests
+  float* rest_lse;    // [num_seqs * num_heads]
+  int64_t* steps;     // [1]: steps of the prefix kernel's stream
+  PrefixWhere* where; // [num_seqs]
+  RestSegments* rest; // [num_seqs]
 };
 
 // The kernels keep the group arrays in shared memory while they plan: at most this many.
@@ -190,8 +209,9 @@ int launch_decode_step_tc(const DecodeArgs& a, const DeviceInfo& info, cudaStrea
 // Modified scores: the tensor-core kernel, every shape.
 int launch_decode_mod(const DecodeModArgs& a, const DeviceInfo& info, cudaStream_t stream);
 int launch_decode_mod_d64(const DecodeModArgs& a, const DeviceInfo& info, cudaStream_t stream);
-// pa_decode_shared: the prefix kernel (prefix_kernel.cuh), then the tensor-core kernel on
-// the rest of every sequence, which joins both.
+// pa_decode_shared: the prefix kernel (prefix_kernel.cuh), the tensor-core kernel on the rest
+// of every sequence (decode_tc.cuh), and the join of their parts.
+int launch_shared_join(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream);
 int launch_decode_shared(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream);
 int launch_decode_shared_rest_d64(const DecodeSharedArgs& a, const DeviceInfo& info,
                                   cudaStream_t stream);

@@ -4,7 +4,7 @@
 // query head h and sequence b of the group, the normalised row
 //   o = sum_{t < L} 2^(x_t - lse) v_t,  lse = log2 sum_{t < L} 2^(x_t),  x_t = log2(e) scale q.k_t,
 // of each of the key ranges that the work is cut into; the decode of the rest (decode_tc.cuh)
-// joins them with the sequence's own keys by their log-sum-exps.
+// those ranges and the sequence's own keys are joined by their log-sum-exps (shared_join.cu).
 //
 // Why it pays: a decode reads the shared keys once for each sequence. Here the rows of a
 // group (n sequences x the G query heads of a KV head) are a dense matrix, so each shared
@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every grid before this one is complete from here on: the workspace may be written
     pdl_wait();
-    // first step of every group: this CTA's start, and (CTA 0) the plan for the decode
+    // first step of every group: this CTA's start, and for the join
+    int64_t* first_x = reinterpret_cast<int64_t*>(starts + ((2 * sh.num_groups + 2) & ~1));
     int64_t running = 0;
     for (int base = 0; base < groups; base += kThreads) {
       const int g = base + tid;
@@ -247,18 +248,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int64_t p = before + incl - n;
       if (g < groups) {
-        if (blockIdx.x == 0) sh.plan[1 + g] = p;
+        first_x[g] = p;
         if (p <= ctl.x0 && ctl.x0 < p + n) {
           ctl.g = g;
           ctl.gx = p;
         }
       }
     }
-    if (blockIdx.x == 0 && tid == 0) sh.plan[0] = ctl.nx;
-    // the decode's arrival counters start at zero
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < (int64_t)B * Hk;
-         i += (int64_t)gridDim.x * kThreads)
-      a.counters[i] = 0;
+    if (blockIdx.x == 0 && tid == 0) *sh.steps = ctl.nx;
+    __syncthreads();
+    for (int b = (int)blockIdx.x + tid * (int)gridDim.x; b < B; b += (int)gridDim.x * kThreads) {
+      PrefixWhere w{0, 0, 0, 0, 0};
+      if (ok) {
+        const int g = group_of(starts, groups, b);
+        w = PrefixWhere{first_x[g], starts[g], starts[g + 1] - starts[g], prefix[g], 0};
+      }
+      sh.where[b] = w;
+    }
   }
   // the scratch was written through the generic proxy; TMA (the async proxy) writes there next
   fence_proxy_async_smem();
