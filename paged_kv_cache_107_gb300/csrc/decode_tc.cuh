@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   if constexpr (FORM == kTcShared) {
+    if (warp == kProducerWarp && tb > 0 && lane < 2) prefetch_tensor_map(lane ? &tm_v : &tm_k);
     g_prefix = g_starts + a.sh.num_groups + 1;
     groups_ok = load_groups(a.sh, B, cap, g_starts, g_prefix);
   }
@@ -364,7 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // everything above read only context_lens (an input no earlier kernel of the step
   // writes); from here on the kernel reads q, the new rows and the caches and writes out
   // and the workspace, so the grids launched before it must be complete
-  pdl_wait();
+  // (kTcShared: they were complete before the prefix kernel let this grid start; it reads
+  // nothing that the prefix kernel writes, and writes nothing that it reads)
+  if constexpr (FORM != kTcShared) pdl_wait();
 
   // zero rows of empty (or invalid) sequences assigned to this CTA: one warp per row
   {
@@ -388,9 +391,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // no tiles (all barriers idle; nothing in flight); a start that cannot be located means
   // context_lens changed under the kernel: flag it and do nothing
-  if (x0 >= x1) return;
+  if (x0 >= x1) {
+    if constexpr (FORM == kTcShared) pdl_wait();
+    return;
+  }
   if (!ctl.found) {
     if (tid == 0) set_dev_err(a.dev_err, PA_DEV_ERR_CONTEXT);
+    if constexpr (FORM == kTcShared) pdl_wait();
     return;
   }
 
@@ -604,6 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int n = q_n > TC::QS ? q_n - TC::QS : 0; n < q_n; ++n)
       mbar_wait_copies(&ctl.q_full[n % TC::QS], (uint32_t)((n / TC::QS) & 1));
+    // the join waits for this grid and so, through it, for the prefix kernel's parts
+    if constexpr (FORM == kTcShared) pdl_wait();
     return;
   }
 

@@ -306,8 +306,7 @@ static size_t shared_bind_workspace(DecodeSharedArgs* a, unsigned char* ws) {
   take(&a->sh.first_lse, rows);
   take(&a->sh.rest_o, rows * a->head_dim);
   take(&a->sh.rest_lse, rows);
-  take(&a->sh.steps, 1);
-  take(&a->sh.where, (size_t)a->num_seqs);
+  take(&a->sh.prefix, (size_t)a->num_seqs * a->num_kv_heads);
   take(&a->sh.rest, (size_t)a->num_seqs);
   return at;
 }

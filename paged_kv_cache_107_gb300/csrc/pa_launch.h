@@ -111,13 +111,11 @@ struct DecodeModArgs : DecodeArgs {
   ScoreModArgs mod;
 };
 
-// Where the join of pa_decode_shared finds a sequence's parts. Prefix parts are addressed
-// through the steps of the prefix kernel's stream (shared_groups.cuh).
-struct PrefixWhere {
-  int64_t group_x;  // first step of the sequence's group
-  int32_t first;    // first sequence of the group
-  int32_t n;        // its sequences
-  int32_t prefix;   // its prefix_lens entry (0 where nothing is shared)
+// Where the join of pa_decode_shared finds the parts of a sequence's rows.
+struct PrefixParts {  // of one KV head
+  int32_t c0;   // CTA of the part that holds the unit's first step
+  int32_t n;    // parts, one for each CTA from c0 on; 0 where nothing is shared
+  int32_t row;  // row of the sequence's first head among a CTA's 256
   int32_t unused;
 };
 struct RestSegments {
@@ -142,9 +140,8 @@ struct SharedArgs {
   float* more_lse;    // [prefix_grid * 256]
   float* rest_o;      // [num_seqs * num_heads * head_dim]: rests
   float* rest_lse;    // [num_seqs * num_heads]
-  int64_t* steps;     // [1]: steps of the prefix kernel's stream
-  PrefixWhere* where; // [num_seqs]
-  RestSegments* rest; // [num_seqs]
+  PrefixParts* prefix;  // [num_seqs * num_kv_heads]
+  RestSegments* rest;   // [num_seqs]
 };
 
 // The kernels keep the group arrays in shared memory while they plan: at most this many.

@@ -140,6 +140,16 @@ __device__ __forceinline__ void note_timeout(PrefixCtl<D>& c, int* dev_err) {
   set_dev_err(dev_err, PA_DEV_ERR_TIMEOUT);
 }
 
+// 32 consecutive floats, one full 32-byte sector per store (p 32-byte aligned).
+__device__ __forceinline__ void store32(float* p, const float* v) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 8)
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p + e), "f"(v[e]),
+                 "f"(v[e + 1]), "f"(v[e + 2]), "f"(v[e + 3]), "f"(v[e + 4]), "f"(v[e + 5]),
+                 "f"(v[e + 6]), "f"(v[e + 7])
+                 : "memory");
+}
+
 // named barriers of the 256 softmax threads
 template <int ID>
 __device__ __forceinline__ void bar_sync256() {
@@ -194,13 +204,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl.gx = 0;
     fence_mbar_init();
   }
+  if (warp == kTmaWarp && lane < 3)
+    umma::prefetch_tmap(lane == 0 ? &tm_k : lane == 1 ? &tm_v : &tm_q);
   if (warp == kMmaWarp) {
     umma::tmem_alloc(&ctl.tmem_base, kTmemCols);
     umma::tmem_relinquish();
   }
-  // the decode of the rest may be scheduled as this grid's CTAs leave
-  pdl_launch_dependents();
-
   // ---- the stream of steps and this CTA's share (scratch: the K and V rings) ----------
   {
     int* starts = reinterpret_cast<int*>(&sm.k[0][0]);
@@ -223,8 +232,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ctl.x0 = (int)blockIdx.x < ge ? prefix_begin(blockIdx.x, t, ge) : 0;
       ctl.x1 = (int)blockIdx.x < ge ? prefix_begin(blockIdx.x + 1, t, ge) : 0;
     }
-    // every grid before this one is complete from here on: the workspace may be written
+    // every grid before this one is complete from here on: the workspace may be written. Only
+    // then may the decode of the rest start (as this grid's CTAs leave): it reads what those
+    // grids wrote without waiting for this one.
     pdl_wait();
+    pdl_launch_dependents();
     // first step of every group: this CTA's start, and for the join
     int64_t* first_x = reinterpret_cast<int64_t*>(starts + ((2 * sh.num_groups + 2) & ~1));
     int64_t running = 0;
@@ -255,15 +267,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (blockIdx.x == 0 && tid == 0) *sh.steps = ctl.nx;
     __syncthreads();
-    for (int b = (int)blockIdx.x + tid * (int)gridDim.x; b < B; b += (int)gridDim.x * kThreads) {
-      PrefixWhere w{0, 0, 0, 0, 0};
+    // where the join finds every sequence's parts
+    const int ctas = prefix_ctas(ctl.nx, (int)gridDim.x);
+    for (int i = (int)blockIdx.x + tid * (int)gridDim.x; i < B * Hk; i += (int)gridDim.x * kThreads) {
+      PrefixParts w{0, 0, 0, 0};
       if (ok) {
-        const int g = group_of(starts, groups, b);
-        w = PrefixWhere{first_x[g], starts[g], starts[g + 1] - starts[g], prefix[g], 0};
+        const int b = i / Hk, j = i % Hk, g = group_of(starts, groups, b);
+        const GroupWork work(sh, starts[g + 1] - starts[g], prefix[g], P);
+        if (work.nt > 0) {
+          const int at = b - starts[g], tile = at / P, pair = tile >> 1;
+          const int64_t x = first_x[g] + work.unit_first(Hk, pair, j);
+          w.c0 = (int)prefix_cta_of(x, ctl.nx, ctas);
+          w.n = (int)prefix_cta_of(x + work.unit_steps(pair) - 1, ctl.nx, ctas) - w.c0 + 1;
+          w.row = (pair < work.full ? (tile & 1) * kRows : 0) + at % P * G;
+        }
       }
-      sh.where[b] = w;
+      sh.prefix[i] = w;
     }
   }
   // the scratch was written through the generic proxy; TMA (the async proxy) writes there next
@@ -283,10 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- TMA producer
       // Lane b owns box b of a tile (box_rows keys of one block); a step's block ids are read
       // one step before its K loads.
-      if (lane == 0) {
-        umma::prefetch_tmap(&tm_k);
-        umma::prefetch_tmap(&tm_v);
-      }
       const int bs = a.block_size;
       const int boxes = kKeys / box_rows;
       int kl = 0, vl = 0;
@@ -471,7 +487,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // P sequences x G heads of a row tile, one box per 64 dims; rows of the next group or
       // past the batch (zeros) land too and are never stored.
       if (lane == 0) {
-        umma::prefetch_tmap(&tm_q);
         int qn[2] = {0, 0};
         while (walk.next(seg, sh, Hk, P)) {
           for (int qt = 0; qt < (seg.two ? 2 : 1); ++qt) {
@@ -618,12 +633,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float ob[32];
           umma::tmem_ld32(lane_addr + col_o(g) + 32 * c4, ob);
           umma::tmem_ld_wait();
-          if (row_ok) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(dst + 32 * c4 + e) =
-                  make_float4(ob[e] * inv, ob[e + 1] * inv, ob[e + 2] * inv, ob[e + 3] * inv);
-          }
+          for (int e = 0; e < 32; ++e) ob[e] *= inv;
+          if (row_ok) store32(dst + 32 * c4, ob);
         }
         wait_o(1 - g);  // its phase ends about now; a later join waits for the one after
       } else {
@@ -661,14 +673,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma::tmem_ld32(lane_addr + col_o(0) + col, oa);
           if (has_b) umma::tmem_ld32(lane_addr + col_o(1) + col, ob);
           umma::tmem_ld_wait();
-          if (row_ok) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) oa[e] = oa[e] * fa + (has_b ? ob[e] * fb : 0.f);
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(dst + col + e) =
-                  make_float4(oa[e], oa[e + 1], oa[e + 2], oa[e + 3]);
-          }
+          for (int e = 0; e < 32; ++e) oa[e] = oa[e] * fa + (has_b ? ob[e] * fb : 0.f);
+          if (row_ok) store32(dst + col, oa);
         }
         // neither slot's O (nor join) is written again before both warpgroups have read them
         umma::fence_before_sync();
