@@ -159,7 +159,8 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 }
 
 // The kernel's forms: plain; with modified scores (pa_decode_mod); the part of pa_decode_shared
-// behind the shared prefixes, whose partial results shared_join.cu joins with the prefixes'.
+// behind the shared prefixes (launched by shared_decode.cuh), whose partial results
+// shared_join.cu joins with the prefixes'.
 enum TcForm { kTcPlain = 0, kTcMod = 1, kTcShared = 2 };
 template <int FORM>
 struct TcArgs {
@@ -175,15 +176,16 @@ struct TcArgs<kTcShared> {
   using type = DecodeSharedArgs;
 };
 
-template <int HS, bool FUSED, int D, bool F16, int FORM = kTcPlain>
-__global__ void __launch_bounds__(kThreads, 1)
-    paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
-                           const __grid_constant__ CUtensorMap tm_v,
-                           const typename TcArgs<FORM>::type a, const int tb) {
+// The CTA of rank c among nctas of a KV head slab (kTcShared: of the launch's plan).
+template <int HS, bool FUSED, int D, bool F16, int FORM>
+__device__ __forceinline__ void decode_tc_body(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                               const typename TcArgs<FORM>::type& a, const int tb,
+                                               unsigned char* smem_raw, const int c,
+                                               const int slab, const int nctas,
+                                               const SharedPlan* plan) {
   static_assert(!FUSED || FORM == kTcPlain, "the fused store has no modified form");
   using TC = TcCfg<HS, D>;
   constexpr int S = TC::STAGES;
-  extern __shared__ __align__(128) unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* qbuf = smem + (size_t)S * TC::STAGE_BYTES;
@@ -194,8 +196,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const int c = blockIdx.x;
-  const int slab = blockIdx.y;
   const int H = a.num_heads;
   const int Hk = a.num_kv_heads;
   const int G = H / Hk;  // 1..8
@@ -203,25 +203,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int B = a.num_seqs;
   constexpr int T = TC::T;
   constexpr bool kHidden = FORM != kTcPlain;
-  // kTcShared: the group arrays in shared memory while the split is found (then the stages
-  // take their place and the producer follows the groups in global memory)
-  int* g_starts = reinterpret_cast<int*>(smem);
-  int* g_prefix = g_starts;
-  bool groups_ok = false;
-  // leading keys of a group that the prefix kernel has taken
+  // kTcShared: the plan's group arrays stay in shared memory until the first copies land; from
+  // then on the producer follows the groups in global memory
+  // leading keys of a group that its prefix part takes
   auto shared_of = [&](int n, int prefix) {
-    if constexpr (FORM == kTcShared) return groups_ok ? shared_len(a.sh, n, prefix) : 0;
+    if constexpr (FORM == kTcShared) return plan->ok ? shared_len(a.sh, n, prefix) : 0;
     else return 0;
-  };
-  auto group_low = [&](int grp) {  // from the copy in shared memory
-    return shared_of(g_starts[grp + 1] - g_starts[grp], g_prefix[grp]);
   };
   // the keys of sequence b that this kernel takes (the plain form: all of the context)
   auto span_of = [&](int b) {
     KeySpan<kHidden> k{load_ctx(a.context_lens, b, cap), 0, 0};
     if constexpr (FORM == kTcMod) mod_span(k, a.mod, b, k.hi - 1);
     if constexpr (FORM == kTcShared) {
-      k.low = group_low(group_of(g_starts, a.sh.num_groups, b));
+      const int g = group_of(plan->starts, a.sh.num_groups, b);
+      k.low = shared_of(plan->starts[g + 1] - plan->starts[g], plan->prefix[g]);
       if (k.low >= k.hi) k.hi = k.low = 0;  // nothing behind the prefix
     }
     return k;
@@ -249,26 +244,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   // waits for this grid before touching its results)
   pdl_launch_dependents();
 
-  if constexpr (FORM == kTcShared) {
-    if (warp == kProducerWarp && tb > 0 && lane < 2) prefetch_tensor_map(lane ? &tm_v : &tm_k);
-    g_prefix = g_starts + a.sh.num_groups + 1;
-    groups_ok = load_groups(a.sh, B, cap, g_starts, g_prefix);
-  }
   // ---- prologue: total tiles, then the sequence that holds this CTA's first tile -----
+  if constexpr (FORM == kTcShared) {
+    if (tid == 0) {
+      ctl.nt = plan->nt;
+      ctl.g_eff = nctas;
+      ctl.x0 = plan->nt > 0 ? tile_begin(c, plan->nt, nctas) : 0;
+      ctl.x1 = plan->nt > 0 ? tile_begin(c + 1, plan->nt, nctas) : 0;
+    }
+  } else {
   int64_t local = 0;
   for (int b = tid; b < B; b += kThreads) {
     const int raw = __ldg(a.context_lens + b);
     if (raw < 0 || raw > cap) {
-      if ((b % gridDim.x) == c && slab == 0) set_dev_err(a.dev_err, PA_DEV_ERR_CONTEXT);
+      if ((b % nctas) == c && slab == 0) set_dev_err(a.dev_err, PA_DEV_ERR_CONTEXT);
     }
     // FUSED: a token of an empty sequence has no position to be stored at
     if (FUSED && (raw <= 0 || raw > cap) && __ldg(a.slot_mapping + b) != -1) {
-      if ((b % gridDim.x) == c && slab == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SLOT);
-    }
-    if constexpr (FORM == kTcShared) {  // a context that ends inside its group's prefix
-      if (raw > 0 && raw < group_low(group_of(g_starts, a.sh.num_groups, b)) &&
-          (b % gridDim.x) == c && slab == 0)
-        set_dev_err(a.dev_err, PA_DEV_ERR_CONTEXT);
+      if ((b % nctas) == c && slab == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SLOT);
     }
     local += span_of(b).tiles(T);
   }
@@ -284,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // each at least min_tiles
     const int64_t mt = a.min_tiles > 1 ? a.min_tiles : 1;
     const int64_t want = (nt + mt - 1) / mt;
-    const int g_eff = (int)(want < (int64_t)gridDim.x ? want : (int64_t)gridDim.x);
+    const int g_eff = (int)(want < (int64_t)nctas ? want : (int64_t)nctas);
     ctl.g_eff = g_eff;
     if (c < g_eff) {
       ctl.x0 = tile_begin(c, nt, g_eff);
@@ -292,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       ctl.x0 = ctl.x1 = 0;
     }
+  }
   }
   __syncthreads();
   const int64_t NT = ctl.nt;
@@ -365,14 +359,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // everything above read only context_lens (an input no earlier kernel of the step
   // writes); from here on the kernel reads q, the new rows and the caches and writes out
   // and the workspace, so the grids launched before it must be complete
-  // (kTcShared: they were complete before the prefix kernel let this grid start; it reads
-  // nothing that the prefix kernel writes, and writes nothing that it reads)
-  if constexpr (FORM != kTcShared) pdl_wait();
+  pdl_wait();
 
+  if constexpr (FORM == kTcShared)
+    write_prefix_parts(a, *plan, plan->prefix_ctas + plan->rest_ctas * (Hk / HS), kThreads);
   // zero rows of empty (or invalid) sequences assigned to this CTA: one warp per row
   {
     const int heads_per_slab = HS * G;
-    for (int b = c + warp * (int)gridDim.x; b < B; b += (kThreads / 32) * (int)gridDim.x) {
+    for (int b = c + warp * nctas; b < B; b += (kThreads / 32) * nctas) {
       if (load_ctx(a.context_lens, b, cap) != 0) {
         if constexpr (FORM == kTcShared) {  // all of the context is shared: no segment here
           if (slab == 0 && lane == 0 && span_of(b).hi == 0) a.sh.rest[b] = RestSegments{0, 0};
@@ -391,13 +385,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // no tiles (all barriers idle; nothing in flight); a start that cannot be located means
   // context_lens changed under the kernel: flag it and do nothing
-  if (x0 >= x1) {
-    if constexpr (FORM == kTcShared) pdl_wait();
-    return;
-  }
+  if (x0 >= x1) return;
   if (!ctl.found) {
     if (tid == 0) set_dev_err(a.dev_err, PA_DEV_ERR_CONTEXT);
-    if constexpr (FORM == kTcShared) pdl_wait();
     return;
   }
 
@@ -405,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &ctl.abort;
   int grp0 = 0;  // kTcShared: group of the CTA's first sequence
   if constexpr (FORM == kTcShared) {
-    grp0 = group_of(g_starts, a.sh.num_groups, ctl.b0);
+    grp0 = group_of(plan->starts, a.sh.num_groups, ctl.b0);
     // the copies land over the group arrays once every warp has read them
     fence_proxy_async_smem();
     __syncthreads();
@@ -611,8 +601,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int n = q_n > TC::QS ? q_n - TC::QS : 0; n < q_n; ++n)
       mbar_wait_copies(&ctl.q_full[n % TC::QS], (uint32_t)((n / TC::QS) & 1));
-    // the join waits for this grid and so, through it, for the prefix kernel's parts
-    if constexpr (FORM == kTcShared) pdl_wait();
     return;
   }
 
@@ -947,6 +935,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int HS, bool FUSED, int D, bool F16, int FORM = kTcPlain>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
+                           const __grid_constant__ CUtensorMap tm_v,
+                           const typename TcArgs<FORM>::type a, const int tb) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  decode_tc_body<HS, FUSED, D, F16, FORM>(tm_k, tm_v, a, tb, smem_raw, (int)blockIdx.x,
+                                          (int)blockIdx.y, (int)gridDim.x, nullptr);
+}
+
+// Tokens per TMA box: the largest power of two dividing block_size, at most a stage's tokens;
+// 0 below 8, where the stage is filled by 16-byte cp.async copies instead.
+inline int tc_box_tokens(int block_size, int stage_tokens) {
+  int tb = block_size & -block_size;
+  if (tb > stage_tokens) tb = stage_tokens;
+  return tb < 8 ? 0 : tb;
+}
+
+template <int HS, bool FUSED, int D, bool F16, int FORM = kTcPlain>
 int launch_decode_tc_t(const typename TcArgs<FORM>::type& a, const DeviceInfo& info,
                        cudaStream_t stream) {
   using TC = TcCfg<HS, D>;
@@ -959,11 +965,7 @@ int launch_decode_tc_t(const typename TcArgs<FORM>::type& a, const DeviceInfo& i
       return PA_ERR_CUDA;
     attr_done[dev].store(true, std::memory_order_release);
   }
-  // tokens per TMA box: the largest power of two dividing block_size, at most a stage's
-  // tokens; below 8 the stage is filled by 16-byte cp.async copies instead
-  int tb = a.block_size & -a.block_size;
-  if (tb > TC::T) tb = TC::T;
-  if (tb < 8) tb = 0;
+  const int tb = tc_box_tokens(a.block_size, TC::T);
   CUtensorMap mk, mv;
   memset(&mk, 0, sizeof(mk));
   memset(&mv, 0, sizeof(mv));

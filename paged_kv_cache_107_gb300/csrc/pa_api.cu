@@ -296,7 +296,7 @@ static size_t shared_bind_workspace(DecodeSharedArgs* a, unsigned char* ws) {
     at += (n * sizeof(T) + 255) & ~size_t(255);
   };
   const size_t rows = (size_t)a->num_seqs * a->num_heads;
-  const size_t more = (size_t)a->sh.prefix_grid * 256;
+  const size_t more = (size_t)a->grid_ctas * 256;
   const size_t cut = (size_t)a->grid_ctas * a->num_heads;
   take(&a->sh.more_o, more * a->head_dim);
   take(&a->sh.more_lse, more);
@@ -488,7 +488,7 @@ size_t pa_decode_shared_workspace_size(int num_seqs, int num_heads, int num_kv_h
   a.num_heads = num_heads;
   a.num_kv_heads = num_kv_heads;
   a.head_dim = head_dim;
-  a.grid_ctas = a.sh.prefix_grid = info.num_sms;
+  a.grid_ctas = pa::shared_ctas(info, num_kv_heads / pa::decode_head_slab(num_kv_heads));
   return pa::shared_bind_workspace(&a, nullptr);
 }
 
@@ -514,7 +514,7 @@ int pa_decode_shared(void* out, const void* q, const void* k_cache, const void* 
   a.sh.prefix_lens = prefix_lens;
   a.sh.num_groups = num_groups;
   a.sh.boxes = pa::prefix_box_rows(block_size) > 0;
-  a.sh.prefix_grid = info.num_sms;
+  a.grid_ctas = pa::shared_ctas(info, num_kv_heads / pa::decode_head_slab(num_kv_heads));
   const size_t need = pa::shared_bind_workspace(&a, static_cast<unsigned char*>(workspace));
   if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return PA_ERR_ALIGN;

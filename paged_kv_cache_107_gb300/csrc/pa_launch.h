@@ -123,6 +123,12 @@ struct RestSegments {
   int32_t n;   // segments, one for each CTA from c0 on; -1: the row is written already
 };
 
+// CTAs of pa_decode_shared: one per SM, and room for one of the prefixes beside every KV head
+// slab's.
+inline int shared_ctas(const DeviceInfo& info, int slabs) {
+  return info.num_sms > slabs + 1 ? info.num_sms : slabs + 1;
+}
+
 // pa_decode_shared: the groups and the partial results (normalised rows and base-2
 // log-sum-exps). Of a prefix unit or a sequence's rest, the part that holds the first step or
 // tile is stored by sequence, a part that another CTA carries on by that CTA (a CTA carries
@@ -132,12 +138,11 @@ struct SharedArgs {
   const int32_t* group_starts;  // [num_groups + 1]
   const int32_t* prefix_lens;   // [num_groups]
   int num_groups;
-  int boxes;          // 1: the block size allows the prefix kernel's TMA boxes
-  int prefix_grid;    // CTAs of the prefix kernel
+  int boxes;          // 1: the block size allows the prefix part's TMA boxes
   float* first_o;     // [num_seqs * num_heads * head_dim]: prefixes
   float* first_lse;   // [num_seqs * num_heads]
-  float* more_o;      // [prefix_grid * 256 * head_dim]
-  float* more_lse;    // [prefix_grid * 256]
+  float* more_o;      // [grid_ctas * 256 * head_dim]
+  float* more_lse;    // [grid_ctas * 256]
   float* rest_o;      // [num_seqs * num_heads * head_dim]: rests
   float* rest_lse;    // [num_seqs * num_heads]
   PrefixParts* prefix;  // [num_seqs * num_kv_heads]
@@ -186,7 +191,7 @@ int decode_max_ctas(const DeviceInfo& info);
 void decode_workspace_layout(int num_seqs, int num_heads, int num_kv_heads, int max_ctas,
                              size_t* off_counters, size_t* off_lse, size_t* off_o,
                              size_t* total);
-// Tokens per TMA box of the prefix kernel: the largest power of two that divides the block
+// Tokens per TMA box of the prefix part: the largest power of two that divides the block
 // size, at most a tile; 0 below the 8 rows of a swizzle atom.
 inline int prefix_box_rows(int block_size) {
   const int tb = block_size & -block_size;
@@ -206,14 +211,13 @@ int launch_decode_step_tc(const DecodeArgs& a, const DeviceInfo& info, cudaStrea
 // Modified scores: the tensor-core kernel, every shape.
 int launch_decode_mod(const DecodeModArgs& a, const DeviceInfo& info, cudaStream_t stream);
 int launch_decode_mod_d64(const DecodeModArgs& a, const DeviceInfo& info, cudaStream_t stream);
-// pa_decode_shared: the prefix kernel (prefix_kernel.cuh), the tensor-core kernel on the rest
-// of every sequence (decode_tc.cuh), and the join of their parts.
-int launch_shared_join(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream);
+// pa_decode_shared: one launch over the keys (shared_decode.cuh), one translation unit for each
+// head_dim and element type, then the join of the parts (shared_join.cu).
 int launch_decode_shared(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream);
-int launch_decode_shared_rest_d64(const DecodeSharedArgs& a, const DeviceInfo& info,
-                                  cudaStream_t stream);
-int launch_prefix_d64(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream);
-int launch_prefix_d128(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream);
+int launch_shared_d64_bf16(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream);
+int launch_shared_d64_f16(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream);
+int launch_shared_d128_bf16(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream);
+int launch_shared_d128_f16(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream);
 // Shapes that take the tensor-core path: every group of 3..8 query heads per KV head, and
 // groups of 1 or 2 unless the head dimension is 128 and one slab holds all KV heads
 // (num_kv_heads 1, 2, 4 or 8), the case where a CUDA-core tile is one contiguous run of

@@ -90,13 +90,13 @@ constexpr int kRows = 128;                 // query rows per tile (TMEM lanes)
 constexpr int kKeys = 128;                 // keys per K/V tile
 constexpr int kKStages = 2, kVStages = 3;  // ring depths
 constexpr int kHalf = 128 * 128;           // 128 rows x 64 dims: one swizzled column block
-constexpr int kThreads = 384;  // warps 0-3 tile A, 4-7 tile B, 8 K/V TMA, 9 MMA, 10 Q, 11 idle
+constexpr int kPrefillThreads = 384;  // warps 0-3 tile A, 4-7 tile B, 8 K/V TMA, 9 MMA, 10 Q, 11 idle
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kQWarp = 10;
 // Registers per thread after the set-up: the softmax warpgroups hold a 128-key score row
 // each; the third warpgroup (producers, MMA issuer, an idle warp) needs few. The sums per
 // SM sub-partition (one warp of each warpgroup) and per CTA match the launch's 168 x 384.
 constexpr int kSoftmaxRegs = 200, kControlRegs = 104;
-static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs <= 168 * kThreads, "register split");
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs <= 168 * kPrefillThreads, "register split");
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O only when the max grows 256x
 // The in-kernel sort is used when the batch has at most kMaxSortSeqs sequences and
@@ -157,7 +157,7 @@ struct PrefillCtl {
   uint32_t tmem_base;
   int abort;
   int n_units;                 // unit records of this CTA
-  int warp_sums[kThreads / 32];
+  int warp_sums[kPrefillThreads / 32];
 };
 
 template <int D>
@@ -352,15 +352,15 @@ __device__ void build_schedule(PrefillCtl& ctl, RecT<FORM>* recs, unsigned char*
     cuq[tid] = cu_q0;
     cuk[tid] = cu_k0;
   }
-  for (int i = tid + kThreads; i <= S; i += kThreads) {
+  for (int i = tid + kPrefillThreads; i <= S; i += kPrefillThreads) {
     cuq[i] = __ldg(a.cu_seqlens_q + i);
     cuk[i] = __ldg(a.cu_seqlens_k + i);
   }
   __syncthreads();
-  // pairs per sequence and their exclusive prefix, one chunk of kThreads sequences a pass
+  // pairs per sequence and their exclusive prefix, one chunk of kPrefillThreads sequences a pass
   int carry = 0;
   const int lane = tid & 31, w = tid >> 5;
-  for (int base = 0; base < S; base += kThreads) {
+  for (int base = 0; base < S; base += kPrefillThreads) {
     const int s = base + tid;
     int cnt = 0;
     if (s < S) {
@@ -379,7 +379,7 @@ __device__ void build_schedule(PrefillCtl& ctl, RecT<FORM>* recs, unsigned char*
     if (lane == 31) ctl.warp_sums[w] = incl;
     __syncthreads();
     int before = 0, chunk = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
+    for (int i = 0; i < kPrefillThreads / 32; ++i) {
       if (i < w) before += ctl.warp_sums[i];
       chunk += ctl.warp_sums[i];
     }
@@ -404,7 +404,7 @@ __device__ void build_schedule(PrefillCtl& ctl, RecT<FORM>* recs, unsigned char*
   __syncthreads();
   // key: cost (key tiles) in the high word, then ~(s, pair) so that equal costs keep the
   // sequence order; padding keys are 0 and sort last
-  for (int p = tid; p < npairs; p += kThreads) {
+  for (int p = tid; p < npairs; p += kPrefillThreads) {
     // the sequence of pair p: the last s with poff[s] <= p (poff is non-decreasing)
     int lo = 0, hi = S - 1;
     while (lo < hi) {
@@ -419,13 +419,13 @@ __device__ void build_schedule(PrefillCtl& ctl, RecT<FORM>* recs, unsigned char*
     const uint32_t cost = pair_cost<P, FORM>(a, s, n, kv, qt * 2 * P);
     keys[p] = ((unsigned long long)cost << 32) | (unsigned long long)(0xFFFFFFFFu - id);
   }
-  for (int i = npairs + tid; i < n2; i += kThreads) keys[i] = 0ull;
+  for (int i = npairs + tid; i < n2; i += kPrefillThreads) keys[i] = 0ull;
   __syncthreads();
   if (npairs <= kRankSortMax) {
     // small batches: each key's place is the number of larger keys (keys are distinct),
     // a few hundred shared-memory reads per thread instead of the network's barriers
     unsigned long long* sorted = keys + n2;
-    for (int p = tid; p < npairs; p += kThreads) {
+    for (int p = tid; p < npairs; p += kPrefillThreads) {
       const unsigned long long x = keys[p];
       int rank = 0;
       for (int q = 0; q < npairs; ++q) rank += keys[q] > x;
@@ -437,7 +437,7 @@ __device__ void build_schedule(PrefillCtl& ctl, RecT<FORM>* recs, unsigned char*
     // bitonic sort, descending
     for (int kk = 2; kk <= n2; kk <<= 1) {
       for (int jj = kk >> 1; jj > 0; jj >>= 1) {
-        for (int i = tid; i < n2; i += kThreads) {
+        for (int i = tid; i < n2; i += kPrefillThreads) {
           const int ixj = i ^ jj;
           if (ixj > i) {
             const unsigned long long x = keys[i], y = keys[ixj];
@@ -453,7 +453,7 @@ __device__ void build_schedule(PrefillCtl& ctl, RecT<FORM>* recs, unsigned char*
   }
   // this CTA's units: the deal indices k with serp_index(k) < nunits form a prefix
   const int c = (int)blockIdx.x, G = (int)gridDim.x;
-  for (int k = tid; k < kMaxUnitRecs<FORM>; k += kThreads) {
+  for (int k = tid; k < kMaxUnitRecs<FORM>; k += kPrefillThreads) {
     const int64_t idx = serp_index(k, c, G);
     if (idx >= nunits) continue;
     const unsigned long long key = keys[idx / Hk];
@@ -724,7 +724,7 @@ __device__ __forceinline__ void mod_tiles(PrefillCtl& ctl, PrefillTiles<D>& sm,
 }
 
 template <int G, int D, bool F16, int FORM = kFormPlain>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kPrefillThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ CUtensorMap tm_q, const ArgsT<FORM> a) {
@@ -732,12 +732,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int NH = D / 64;    // 64-dim swizzled column blocks per row
   constexpr bool kSepP = D == 64;  // P in its own tensor-memory columns (see col_p)
   using Tiles = PrefillTiles<D>;
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  PrefillCtl& ctl = *reinterpret_cast<PrefillCtl*>(smem_raw);
+  extern __shared__ __align__(1024) unsigned char prefill_smem[];
+  PrefillCtl& ctl = *reinterpret_cast<PrefillCtl*>(prefill_smem);
   using Rec = RecT<FORM>;
-  Rec* recs = reinterpret_cast<Rec*>(smem_raw + kCtlBytes);
+  Rec* recs = reinterpret_cast<Rec*>(prefill_smem + kCtlBytes);
   Tiles& sm = *reinterpret_cast<Tiles*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + kCtlBytes + kRecBytes + 1023) & ~uintptr_t(1023));
+      (reinterpret_cast<uintptr_t>(prefill_smem) + kCtlBytes + kRecBytes + 1023) & ~uintptr_t(1023));
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int H = a.num_heads;
   const bool causal = a.causal != 0;
   // the schedule's first inputs, requested before the set-up below so that their latency
-  // overlaps it (entries past kThreads are loaded by the schedule itself)
+  // overlaps it (entries past kPrefillThreads are loaded by the schedule itself)
   int cu_q0 = 0, cu_k0 = 0;
   if (a.persistent && tid <= a.num_seqs && a.num_seqs <= kMaxSortSeqs) {
     cu_q0 = __ldg(a.cu_seqlens_q + tid);
@@ -1324,11 +1324,11 @@ int launch_prefill_t(const ArgsT<FORM>& a, const DeviceInfo& info, cudaStream_t 
   args.persistent = a.num_seqs <= kMaxSortSeqs && max_pairs <= kMaxSortPairs && grid1 > 0 &&
                     (max_units + grid1 - 1) / grid1 + 1 <= kMaxUnitRecs<FORM>;
   if (args.persistent) {
-    paged_prefill_kernel<G, D, F16, FORM><<<grid1, kThreads, smem, stream>>>(mk, mv, mq, args);
+    paged_prefill_kernel<G, D, F16, FORM><<<grid1, kPrefillThreads, smem, stream>>>(mk, mv, mq, args);
   } else {
     if (qt_n > 65535) return PA_ERR_UNSUPPORTED;
     dim3 grid((unsigned)a.num_kv_heads, (unsigned)a.num_seqs, (unsigned)qt_n);
-    paged_prefill_kernel<G, D, F16, FORM><<<grid, kThreads, smem, stream>>>(mk, mv, mq, args);
+    paged_prefill_kernel<G, D, F16, FORM><<<grid, kPrefillThreads, smem, stream>>>(mk, mv, mq, args);
   }
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

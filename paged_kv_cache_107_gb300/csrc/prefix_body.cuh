@@ -1,4 +1,5 @@
-// prefix_kernel.cuh — the shared part of pa_decode_shared on the tcgen05 tensor cores.
+// prefix_body.cuh — the shared part of pa_decode_shared on the tcgen05 tensor cores (the body of
+// the CTAs that take it; shared_decode.cuh launches them beside those of the rests).
 //
 // What it computes: for every group g of sequences that hold the same first L keys, every
 // query head h and sequence b of the group, the normalised row
@@ -11,12 +12,11 @@
 // key and value is read once for 128 or 256 of them: below about 256 rows the bytes of the
 // prefix bound it, above the products do.
 //
-// Structure (that of prefill_kernel.cuh, whose constants and helpers it uses): one persistent
-// CTA per SM, a TMA warp, a warp that issues tcgen05.mma, a Q warp and two softmax
+// Structure (that of prefill_kernel.cuh, whose constants and helpers it uses): a TMA warp, a warp that issues tcgen05.mma, a Q warp and two softmax
 // warpgroups, one for each of two slots of accumulators in tensor memory.
 //  * Work: the steps of all units (GroupWork) form one stream, cut into equal shares
-//    (stream-K): a long prefix is spread over every SM whatever the number of groups. A CTA's
-//    share is a list of segments, each a range of steps of one unit.
+//    (stream-K): a long prefix is spread over all of these CTAs whatever the number of groups. A
+//    CTA's share is a list of segments, each a range of steps of one unit.
 //  * A unit with two row tiles takes each key tile for both slots (one load, two products). A
 //    unit with one row tile would leave the second slot idle and its own chain of product,
 //    softmax, product exposed; it gives the slots alternate key tiles instead, and the two
@@ -26,7 +26,6 @@
 //    for the second product, as in the prefill.
 #pragma once
 
-#include "dependent_launch.cuh"
 #include "prefill_kernel.cuh"
 #include "shared_groups.cuh"
 
@@ -50,11 +49,6 @@ struct PrefixCtl {
   uint64_t s_full[2], p_full[2], o_done[2];  // [slot]
   uint32_t tmem_base;
   int abort;
-  int64_t nx;      // steps of the stream
-  int64_t x0, x1;  // this CTA's
-  int64_t gx;      // first step of the group that holds x0
-  int g;           // that group
-  int64_t red[kThreads / 32];
   float2 join[kRows];  // [row] slot 1's softmax maximum and sum, then the factors of both O
 };
 
@@ -161,16 +155,14 @@ __device__ __forceinline__ void bar_arrive256() {
 }
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads, 1)
-    shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_k,
-                         const __grid_constant__ CUtensorMap tm_v,
-                         const __grid_constant__ CUtensorMap tm_q, const DecodeSharedArgs a,
-                         const int box_rows) {
+__device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                            const CUtensorMap& tm_q, const DecodeSharedArgs& a,
+                                            const int box_rows, unsigned char* smem_raw,
+                                            const SharedPlan& plan, int active_ctas) {
   using C = PrefixCfg<D>;
   using Ctl = PrefixCtl<D>;
   static_assert(sizeof(Ctl) <= kPrefixCtlBytes, "control block");
   constexpr int NH = D / 64;
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem_raw);
   PrefixTiles<D>& sm = *reinterpret_cast<PrefixTiles<D>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + kPrefixCtlBytes + 1023) & ~uintptr_t(1023));
@@ -178,9 +170,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const int H = a.num_heads, Hk = a.num_kv_heads, G = H / Hk, B = a.num_seqs;
+  const int H = a.num_heads, Hk = a.num_kv_heads, G = H / Hk;
   const int P = kRows / G;  // sequences per row tile (rows P*G..127 are padding)
-  const int cap = a.max_blocks * a.block_size;
   const SharedArgs& sh = a.sh;
 
   if (tid == 0) {
@@ -200,101 +191,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.v_empty[s], 1);
     }
     ctl.abort = 0;
-    ctl.g = 0;
-    ctl.gx = 0;
     fence_mbar_init();
   }
-  if (warp == kTmaWarp && lane < 3)
-    umma::prefetch_tmap(lane == 0 ? &tm_k : lane == 1 ? &tm_v : &tm_q);
   if (warp == kMmaWarp) {
     umma::tmem_alloc(&ctl.tmem_base, kTmemCols);
     umma::tmem_relinquish();
   }
-  // ---- the stream of steps and this CTA's share (scratch: the K and V rings) ----------
+  // this CTA's share of the steps, and the group of the first: the last one that starts at it
+  // or before
+  PrefixWalk walk{prefix_begin(blockIdx.x, plan.nx, plan.prefix_ctas),
+                  prefix_begin(blockIdx.x + 1, plan.nx, plan.prefix_ctas), 0, 0, 0, 0, 0};
   {
-    int* starts = reinterpret_cast<int*>(&sm.k[0][0]);
-    int* prefix = starts + sh.num_groups + 1;
-    const bool ok = load_groups(sh, B, cap, starts, prefix);
-    if (!ok && blockIdx.x == 0 && tid == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SEQLENS);
-    const int groups = ok ? sh.num_groups : 0;
-    int64_t nx = 0;
-    for (int g = tid; g < groups; g += kThreads)
-      nx += GroupWork(sh, starts[g + 1] - starts[g], prefix[g], P).steps(Hk);
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) nx += __shfl_xor_sync(0xffffffffu, nx, m);
-    if (lane == 0) ctl.red[warp] = nx;
-    __syncthreads();
-    if (tid == 0) {
-      int64_t t = 0;
-      for (int w = 0; w < kThreads / 32; ++w) t += ctl.red[w];
-      const int ge = prefix_ctas(t, (int)gridDim.x);
-      ctl.nx = t;
-      ctl.x0 = (int)blockIdx.x < ge ? prefix_begin(blockIdx.x, t, ge) : 0;
-      ctl.x1 = (int)blockIdx.x < ge ? prefix_begin(blockIdx.x + 1, t, ge) : 0;
+    int lo = 0, hi = sh.num_groups - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (plan.first_x[mid] <= walk.x) lo = mid;
+      else hi = mid - 1;
     }
-    // every grid before this one is complete from here on: the workspace may be written. Only
-    // then may the decode of the rest start (as this grid's CTAs leave): it reads what those
-    // grids wrote without waiting for this one.
-    pdl_wait();
-    pdl_launch_dependents();
-    // first step of every group: this CTA's start, and for the join
-    int64_t* first_x = reinterpret_cast<int64_t*>(starts + ((2 * sh.num_groups + 2) & ~1));
-    int64_t running = 0;
-    for (int base = 0; base < groups; base += kThreads) {
-      const int g = base + tid;
-      const int64_t n =
-          g < groups ? GroupWork(sh, starts[g + 1] - starts[g], prefix[g], P).steps(Hk) : 0;
-      int64_t incl = n;
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, m);
-        if (lane >= m) incl += y;
-      }
-      __syncthreads();
-      if (lane == 31) ctl.red[warp] = incl;
-      __syncthreads();
-      int64_t before = running;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += ctl.red[w];
-        running += ctl.red[w];
-      }
-      const int64_t p = before + incl - n;
-      if (g < groups) {
-        first_x[g] = p;
-        if (p <= ctl.x0 && ctl.x0 < p + n) {
-          ctl.g = g;
-          ctl.gx = p;
-        }
-      }
-    }
-    __syncthreads();
-    // where the join finds every sequence's parts
-    const int ctas = prefix_ctas(ctl.nx, (int)gridDim.x);
-    for (int i = (int)blockIdx.x + tid * (int)gridDim.x; i < B * Hk; i += (int)gridDim.x * kThreads) {
-      PrefixParts w{0, 0, 0, 0};
-      if (ok) {
-        const int b = i / Hk, j = i % Hk, g = group_of(starts, groups, b);
-        const GroupWork work(sh, starts[g + 1] - starts[g], prefix[g], P);
-        if (work.nt > 0) {
-          const int at = b - starts[g], tile = at / P, pair = tile >> 1;
-          const int64_t x = first_x[g] + work.unit_first(Hk, pair, j);
-          w.c0 = (int)prefix_cta_of(x, ctl.nx, ctas);
-          w.n = (int)prefix_cta_of(x + work.unit_steps(pair) - 1, ctl.nx, ctas) - w.c0 + 1;
-          w.row = (pair < work.full ? (tile & 1) * kRows : 0) + at % P * G;
-        }
-      }
-      sh.prefix[i] = w;
-    }
+    walk.g = lo;
+    walk.gx = plan.first_x[lo];
+    walk.first = plan.starts[lo];
+    walk.n = plan.starts[lo + 1] - walk.first;
+    walk.prefix = plan.prefix[lo];
   }
-  // the scratch was written through the generic proxy; TMA (the async proxy) writes there next
+  // every grid before this one is complete from here on: q and the caches may be read and the
+  // workspace written
+  pdl_wait();
+  write_prefix_parts(a, plan, active_ctas, kPrefillThreads);
+  // the plan's arrays lie where copies land next, written through the generic proxy
   fence_proxy_async_smem();
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
   volatile int* abort_flag = &ctl.abort;
-  PrefixWalk walk{ctl.x0, ctl.x1, ctl.gx, ctl.g, 0, 0, 0};
-  if (walk.x < walk.x1) walk.load_group(sh);
   PrefixSeg seg;
 
   if (warp >= 8) {
@@ -685,35 +615,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     umma::fence_before_sync();
     __syncthreads();
   }
-}
-
-template <int D, bool F16>
-int launch_prefix_t(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream) {
-  constexpr size_t smem = prefix_smem_bytes<D>();
-  static_assert(smem <= 232448, "shared memory budget (opt-in maximum)");
-  static std::atomic<bool> attr_done[64];  // zero-initialised: false
-  if (info.device < 0 || info.device >= 64) return PA_ERR_CUDA;
-  if ((size_t)info.max_smem_optin < smem) return PA_ERR_UNSUPPORTED;
-  if (!attr_done[info.device].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(shared_prefix_kernel<D, F16>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-      return PA_ERR_CUDA;
-    attr_done[info.device].store(true, std::memory_order_release);
-  }
-  const int G = a.num_heads / a.num_kv_heads;
-  const int box = prefix_box_rows(a.block_size);
-  CUtensorMap mk, mv, mq;
-  if (!make_slab_map(&mk, a.k_cache, a.num_kv_heads, D, F16, a.block_size, a.num_blocks,
-                     box ? box : 1, 1) ||
-      !make_slab_map(&mv, a.v_cache, a.num_kv_heads, D, F16, a.block_size, a.num_blocks,
-                     box ? box : 1, 1) ||
-      !make_rows_map(&mq, a.q, a.num_seqs, a.num_heads, D, F16, G, kRows / G))
-    return PA_ERR_CUDA;
-  if (launch_dependent(shared_prefix_kernel<D, F16>, dim3((unsigned)a.sh.prefix_grid),
-                       dim3(kThreads), smem, stream, mk, mv, mq, a, box ? box : kKeys) !=
-      cudaSuccess)
-    return PA_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace

@@ -1,7 +1,6 @@
 // shared_groups.cuh — the groups of pa_decode_shared on the device: which leading keys a
-// group computes once, how the prefix kernel cuts that work into steps, and where its
-// partial results lie. Shared by the prefix kernel (prefix_kernel.cuh) and the decode of the
-// rest (decode_tc.cuh), which both derive everything from the same two input arrays.
+// group computes once, how that work is cut into steps, which CTAs of the one launch take it
+// (prefix_body.cuh) and which the rest of the sequences (decode_tc.cuh).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -12,7 +11,7 @@
 
 namespace pa {
 
-constexpr int kPrefixRows = 128;  // query rows per tile of the prefix kernel
+constexpr int kPrefixRows = 128;  // query rows per tile of the prefix part
 constexpr int kPrefixKeys = 128;  // keys per tile
 
 // Leading positions that a group of n sequences computes once: the prefix, where there is
@@ -82,18 +81,71 @@ struct GroupWork {
   }
 };
 
-// CTAs that take steps of a stream of nx: at least kPrefixMinSteps each.
-constexpr int kPrefixMinSteps = 2;
-__device__ __forceinline__ int prefix_ctas(int64_t nx, int grid) {
-  const int64_t want = (nx + kPrefixMinSteps - 1) / kPrefixMinSteps;
-  return (int)(want < (int64_t)grid ? want : (int64_t)grid);
-}
 // CTA c of g takes steps [c*nx/g, (c+1)*nx/g).
 __device__ __forceinline__ int64_t prefix_begin(int64_t c, int64_t nx, int g) {
   return (c * nx) / g;
 }
 __device__ __forceinline__ int64_t prefix_cta_of(int64_t x, int64_t nx, int g) {
   return ((x + 1) * g - 1) / nx;
+}
+
+// The split of a launch, worked out by every CTA from the input arrays alone.
+struct SharedPlan {
+  bool ok;           // the arrays describe groups of the batch
+  int64_t nx, nt;    // steps of the prefixes; key tiles of the rests
+  int prefix_ctas;   // CTAs 0 .. prefix_ctas - 1 take the steps,
+  int rest_ctas;     // the next rest_ctas of each KV head slab the tiles
+  // in shared memory until the CTA's first copies
+  const int *starts, *prefix;
+  const int64_t* first_x;  // first step of each group
+};
+
+// Time of a step and of a 64 KB tile on one SM, in units of 0.1 us: a step of two row tiles is
+// bound by its products and softmax; a step of one row tile and a tile of a rest by what
+// one SM takes from memory (57 to 61 GB/s, measured with 8 to 114 CTAs). Side by side on the
+// SMs instead of one after the other, the two parts share one start-up, and the steps'
+// products run while the rests wait for memory: 50.7 -> TIME_PROMPT us for 64 sequences behind
+// 8,192 keys, 117.5 -> TIME_DOC us for 128 behind 32,768.
+constexpr int kStepCost = 21, kTileCost = 11;
+constexpr int kPrefixMinSteps = 2;
+
+__device__ __forceinline__ void split_shared(SharedPlan& p, int ctas, int slabs, int min_tiles) {
+  const int64_t want1 = (p.nx + kPrefixMinSteps - 1) / kPrefixMinSteps;
+  const int64_t want2 = max((int64_t)1, (p.nt + min_tiles - 1) / min_tiles);
+  const float c1 = (float)p.nx * kStepCost, c2 = (float)(p.nt * slabs) * kTileCost;
+  int64_t g1 = 0;
+  if (p.nx > 0) {
+    g1 = (int64_t)((float)ctas * (c1 / (c1 + c2)) + 0.5f);
+    g1 = max((int64_t)1, min(min(g1, want1), (int64_t)(ctas - slabs)));
+  }
+  const int64_t g2 = max((int64_t)1, min(want2, (ctas - g1) / slabs));
+  if (p.nx > 0) g1 = min(want1, ctas - g2 * slabs);  // what the rests leave
+  p.prefix_ctas = (int)g1;
+  p.rest_ctas = (int)g2;
+}
+
+// Where the join finds every sequence's prefix parts; entries dealt to the launch's CTAs.
+__device__ __forceinline__ void write_prefix_parts(const DecodeSharedArgs& a,
+                                                   const SharedPlan& plan, int active_ctas,
+                                                   int threads) {
+  const int H = a.num_heads, Hk = a.num_kv_heads, G = H / Hk, P = kPrefixRows / G;
+  for (int i = (int)(blockIdx.x + threadIdx.x * active_ctas); i < a.num_seqs * Hk;
+       i += active_ctas * threads) {
+    PrefixParts w{0, 0, 0, 0};
+    if (plan.ok && plan.nx > 0) {
+      const int b = i / Hk, j = i % Hk, g = group_of(plan.starts, a.sh.num_groups, b);
+      const GroupWork work(a.sh, plan.starts[g + 1] - plan.starts[g], plan.prefix[g], P);
+      if (work.nt > 0) {
+        const int at = b - plan.starts[g], tile = at / P, pair = tile >> 1;
+        const int64_t x = plan.first_x[g] + work.unit_first(Hk, pair, j);
+        w.c0 = (int)prefix_cta_of(x, plan.nx, plan.prefix_ctas);
+        w.n = (int)prefix_cta_of(x + work.unit_steps(pair) - 1, plan.nx, plan.prefix_ctas) -
+              w.c0 + 1;
+        w.row = (pair < work.full ? (tile & 1) * kPrefixRows : 0) + at % P * G;
+      }
+    }
+    a.sh.prefix[i] = w;
+  }
 }
 
 }  // namespace pa

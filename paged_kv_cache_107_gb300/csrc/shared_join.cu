@@ -130,7 +130,13 @@ int launch_join_t(const DecodeSharedArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-int launch_shared_join(const DecodeSharedArgs& a, const DeviceInfo&, cudaStream_t stream) {
+int launch_decode_shared(const DecodeSharedArgs& a, const DeviceInfo& info, cudaStream_t stream) {
+  if (a.head_dim != 64 && a.head_dim != 128) return PA_ERR_UNSUPPORTED;
+  const int rc = a.head_dim == 64 ? (a.f16 ? launch_shared_d64_f16(a, info, stream)
+                                           : launch_shared_d64_bf16(a, info, stream))
+                                  : (a.f16 ? launch_shared_d128_f16(a, info, stream)
+                                           : launch_shared_d128_bf16(a, info, stream));
+  if (rc != PA_OK) return rc;
   if (a.head_dim == 64) return a.f16 ? launch_join_t<64, true>(a, stream)
                                      : launch_join_t<64, false>(a, stream);
   return a.f16 ? launch_join_t<128, true>(a, stream) : launch_join_t<128, false>(a, stream);
