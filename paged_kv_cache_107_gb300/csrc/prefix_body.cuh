@@ -12,7 +12,7 @@
 // key and value is read once for 128 or 256 of them: below about 256 rows the bytes of the
 // prefix bound it, above the products do.
 //
-// Structure (that of prefill_kernel.cuh, whose constants and helpers it uses): a TMA warp, a warp that issues tcgen05.mma, a Q warp and two softmax
+// Structure (that of prefill_kernel.cuh, whose constants and helpers it uses): TMA warps for K, V and Q, a warp that issues tcgen05.mma and two softmax
 // warpgroups, one for each of two slots of accumulators in tensor memory.
 //  * Work: the steps of all units (GroupWork) form one stream, cut into equal shares
 //    (stream-K): a long prefix is spread over all of these CTAs whatever the number of groups. A
@@ -40,41 +40,14 @@ struct PrefixCfg {
   static constexpr int kTile = (D / 64) * kHalf;
 };
 
-template <int D>
-struct PrefixCtl {
-  using C = PrefixCfg<D>;
-  uint64_t q_full[2], q_empty[2];  // [row tile]
-  uint64_t k_full[C::KS], k_empty[C::KS];
-  uint64_t v_full[C::VS], v_empty[C::VS];
-  uint64_t s_full[2], p_full[2], o_done[2];  // [slot]
-  uint32_t tmem_base;
-  int abort;
-  float2 join[kRows];  // [row] slot 1's softmax maximum and sum, then the factors of both O
-};
-
-template <int D>
-struct PrefixTiles {
-  using C = PrefixCfg<D>;
-  unsigned char q[2][C::kTile];
-  unsigned char k[C::KS][C::kTile];
-  unsigned char v[C::VS][C::kTile];
-};
-
-constexpr int kPrefixCtlBytes = 1408;
-
-template <int D>
-constexpr size_t prefix_smem_bytes() {
-  return 1023 + kPrefixCtlBytes + sizeof(PrefixTiles<D>);
-}
-
-// A range of steps of one unit.
+// A range of steps of one unit (n = 0: the end of the share).
 struct PrefixSeg {
   int first, n;  // the group's sequences
   int len;       // shared keys
   int nt;        // key tiles
   int pair, j;   // row tiles 2*pair (and 2*pair + 1 when two), KV head
   int s0, s1;    // steps
-  bool two;      // both slots take the same key tile
+  int two;       // both slots take the same key tile
   // key tiles of slot g: tile(g, it) for it < count(g)
   __device__ __forceinline__ int steps() const { return s1 - s0; }
   __device__ __forceinline__ int tile(int g, int it) const {
@@ -88,7 +61,42 @@ struct PrefixSeg {
   }
 };
 
-// Hands out a CTA's segments in order; each role of the CTA walks its own copy.
+// Segments on their way from the warp that works them out to the other roles.
+constexpr int kSegSlots = 4;
+constexpr int kSegReaders = 3 + 8;  // warps: V, MMA, Q, the softmax's
+constexpr int kVWarp = 11;          // beside kTmaWarp (here K's), kMmaWarp and kQWarp
+
+template <int D>
+struct PrefixCtl {
+  using C = PrefixCfg<D>;
+  uint64_t q_full[2], q_empty[2];  // [row tile]
+  uint64_t k_full[C::KS], k_empty[C::KS];
+  uint64_t v_full[C::VS], v_empty[C::VS];
+  uint64_t s_full[2], p_full[2], o_done[2];  // [slot]
+  uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
+  uint64_t join_there, join_back, join_read;
+  uint32_t tmem_base;
+  int abort;
+  PrefixSeg segs[kSegSlots];
+  float2 join[kRows];  // [row] slot 1's softmax maximum and sum, then the factors of both O
+};
+
+template <int D>
+struct PrefixTiles {
+  using C = PrefixCfg<D>;
+  unsigned char q[2][C::kTile];
+  unsigned char k[C::KS][C::kTile];
+  unsigned char v[C::VS][C::kTile];
+};
+
+constexpr int kPrefixCtlBytes = 1616;
+
+template <int D>
+constexpr size_t prefix_smem_bytes() {
+  return 1023 + kPrefixCtlBytes + sizeof(PrefixTiles<D>);
+}
+
+// Hands out a CTA's segments in order.
 struct PrefixWalk {
   int64_t x, x1;  // next step, end of the share
   int64_t gx;     // first step of group g
@@ -101,30 +109,35 @@ struct PrefixWalk {
     prefix = __ldg(sh.prefix_lens + g);
   }
   __device__ __forceinline__ bool next(PrefixSeg& s, const SharedArgs& sh, int Hk, int P) {
-    if (x >= x1) return false;
-    GroupWork w(sh, n, prefix, P);
-    while (x - gx >= w.steps(Hk) && g + 1 < sh.num_groups) {
-      gx += w.steps(Hk);
-      ++g;
-      load_group(sh);
-      w = GroupWork(sh, n, prefix, P);
+    while (x < x1) {
+      GroupWork w(sh, n, prefix, P);
+      while (x - gx >= w.steps(Hk) && g + 1 < sh.num_groups) {
+        gx += w.steps(Hk);
+        ++g;
+        load_group(sh);
+        w = GroupWork(sh, n, prefix, P);
+      }
+      const uint32_t rel = (uint32_t)(x - gx);
+      const uint32_t per_pair = (uint32_t)Hk * (uint32_t)(kUnitSteps + w.nt);
+      const uint32_t pair = min(rel / per_pair, (uint32_t)w.full);
+      const uint32_t in_pair = rel - pair * per_pair;
+      const uint32_t us = (uint32_t)w.unit_steps((int)pair);
+      const int v0 = (int)(in_pair % us);
+      const int v1 = (int)min((int64_t)us, (int64_t)v0 + (x1 - x));
+      x += v1 - v0;
+      if (v1 <= kUnitSteps) continue;  // nothing but the start's share
+      s.first = first;
+      s.n = n;
+      s.len = prefix;
+      s.nt = w.nt;
+      s.pair = (int)pair;
+      s.two = (int)pair < w.full;
+      s.j = (int)(in_pair / us);
+      s.s0 = max(0, v0 - kUnitSteps);
+      s.s1 = v1 - kUnitSteps;
+      return true;
     }
-    const uint32_t rel = (uint32_t)(x - gx);
-    const uint32_t per_pair = (uint32_t)Hk * (uint32_t)w.nt;
-    const uint32_t pair = min(rel / per_pair, (uint32_t)w.full);
-    const uint32_t in_pair = rel - pair * per_pair;
-    const uint32_t us = (uint32_t)w.unit_steps((int)pair);
-    s.first = first;
-    s.n = n;
-    s.len = prefix;
-    s.nt = w.nt;
-    s.pair = (int)pair;
-    s.two = (int)pair < w.full;
-    s.j = (int)(in_pair / us);
-    s.s0 = (int)(in_pair % us);
-    s.s1 = (int)min((int64_t)us, (int64_t)s.s0 + (x1 - x));
-    x += s.s1 - s.s0;
-    return true;
+    return false;
   }
 };
 
@@ -142,16 +155,6 @@ __device__ __forceinline__ void store32(float* p, const float* v) {
                  "f"(v[e + 1]), "f"(v[e + 2]), "f"(v[e + 3]), "f"(v[e + 4]), "f"(v[e + 5]),
                  "f"(v[e + 6]), "f"(v[e + 7])
                  : "memory");
-}
-
-// named barriers of the 256 softmax threads
-template <int ID>
-__device__ __forceinline__ void bar_sync256() {
-  asm volatile("bar.sync %0, 256;" ::"n"(ID) : "memory");
-}
-template <int ID>
-__device__ __forceinline__ void bar_arrive256() {
-  asm volatile("bar.arrive %0, 256;" ::"n"(ID) : "memory");
 }
 
 template <int D, bool F16>
@@ -190,6 +193,14 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
       mbar_init(&ctl.v_full[s], 1);
       mbar_init(&ctl.v_empty[s], 1);
     }
+    for (int i = 0; i < kSegSlots; ++i) {
+      mbar_init(&ctl.seg_full[i], 1);
+      mbar_init(&ctl.seg_empty[i], kSegReaders);
+      ctl.segs[i].n = 0;
+    }
+    mbar_init(&ctl.join_there, kRows);
+    mbar_init(&ctl.join_back, kRows);
+    mbar_init(&ctl.join_read, 2 * kRows);
     ctl.abort = 0;
     fence_mbar_init();
   }
@@ -226,84 +237,116 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
   const uint32_t tmem = ctl.tmem_base;
   volatile int* abort_flag = &ctl.abort;
   PrefixSeg seg;
+  int seg_n = 0;  // segments read
+  // The next segment into s (a whole warp calls it); false at the end. After a wait that ran
+  // out a role may read an old segment again, never one that was not written.
+  auto next_seg = [&](PrefixSeg& s) {
+    const int slot = seg_n % kSegSlots;
+    if (!mbar_wait(&ctl.seg_full[slot], (uint32_t)((seg_n / kSegSlots) & 1), abort_flag))
+      note_timeout(ctl, a.dev_err);
+    ++seg_n;
+    s = ctl.segs[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl.seg_empty[slot]);
+    return s.n != 0;
+  };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
-    if (warp == kTmaWarp) {
-      // ---------------------------------------------------------------- TMA producer
-      // Lane b owns box b of a tile (box_rows keys of one block); a step's block ids are read
-      // one step before its K loads.
+    if (warp == kTmaWarp || warp == kVWarp) {
+      // ---------------------------------------------------------------- TMA producers
+      // One warp for K, one for V: at small block sizes a tile takes many boxes, and the warp
+      // that issues them is what a step waits for (16 steps of a lone row tile at block size
+      // 16, head_dim 64: 44 us with one warp for both). Lane b owns box b of a tile (box_rows
+      // keys of one block). The K warp also works out the segments and hands them on.
+      const bool is_v = warp == kVWarp;
       const int bs = a.block_size;
       const int boxes = kKeys / box_rows;
-      int kl = 0, vl = 0;
+      const int stages = is_v ? C::VS : C::KS;
+      uint64_t* const empty = is_v ? ctl.v_empty : ctl.k_empty;
+      uint64_t* const full = is_v ? ctl.v_full : ctl.k_full;
+      unsigned char* const ring = is_v ? sm.v[0] : sm.k[0];
+      const CUtensorMap* const map = is_v ? &tm_v : &tm_k;
+      int cnt = 0;  // tiles loaded
+      int pub = 0;  // segments handed on
+      auto my_next_seg = [&](PrefixSeg& t) {
+        if (is_v) return next_seg(t);
+        const bool more = walk.next(t, sh, Hk, P);
+        if (!more) t.n = 0;
+        if (lane == 0) {
+          const int slot = pub % kSegSlots;
+          if (pub >= kSegSlots && !mbar_wait(&ctl.seg_empty[slot],
+                                             (uint32_t)(((pub / kSegSlots) - 1) & 1), abort_flag))
+            note_timeout(ctl, a.dev_err);
+          ctl.segs[slot] = t;
+          mbar_arrive(&ctl.seg_full[slot]);
+        }
+        ++pub;
+        __syncwarp();
+        return more;
+      };
       // this lane's block id of a key tile: -1 past the prefix, -2 out of the pool
-      auto read_id = [&](const PrefixSeg& s, int tile) {
+      auto read_id = [&](const PrefixSeg& t, int tile) {
         const int key0 = tile * kKeys + lane * box_rows;
-        if (lane >= boxes || key0 >= s.len) return -1;
-        const int id = __ldg(a.block_tables + (int64_t)s.first * a.max_blocks + key0 / bs);
+        if (lane >= boxes || key0 >= t.len) return -1;
+        const int id = __ldg(a.block_tables + (int64_t)t.first * a.max_blocks + key0 / bs);
         return id >= 0 && (int64_t)id < a.num_blocks ? id : -2;
       };
-      auto load = [&](bool is_v, int j, int tile, int id) {
-        const int stages = is_v ? C::VS : C::KS;
-        const int cnt = is_v ? vl++ : kl++;
+      auto load = [&](int j, int tile, int id) {
         const int st = cnt % stages;
-        uint64_t* empty = is_v ? &ctl.v_empty[st] : &ctl.k_empty[st];
-        uint64_t* full = is_v ? &ctl.v_full[st] : &ctl.k_full[st];
         if (lane == 0 && cnt >= stages &&
-            !mbar_wait(empty, (uint32_t)(((cnt / stages) - 1) & 1), abort_flag))
+            !mbar_wait(&empty[st], (uint32_t)(((cnt / stages) - 1) & 1), abort_flag))
           note_timeout(ctl, a.dev_err);
+        ++cnt;
         if (!is_v && __any_sync(0xffffffffu, id == -2) && lane == 0)
           set_dev_err(a.dev_err, PA_DEV_ERR_BLOCK_ID);
         const uint32_t valid = __ballot_sync(0xffffffffu, id >= 0);
         if (lane == 0)
-          mbar_arrive_expect_tx(full, (uint32_t)__popc(valid) * NH * box_rows * 128u);
+          mbar_arrive_expect_tx(&full[st], (uint32_t)__popc(valid) * NH * box_rows * 128u);
         __syncwarp();
         if (id >= 0) {
           const int row0 = (tile * kKeys + lane * box_rows) % bs;
-          unsigned char* dst = (is_v ? sm.v[st] : sm.k[st]) + lane * box_rows * 128;
-          const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+          unsigned char* dst = ring + st * C::kTile + lane * box_rows * 128;
+#pragma unroll
           for (int h2 = 0; h2 < NH; ++h2)
-            umma::tma_load_4d(dst + h2 * kHalf, map, h2 * 64, row0, j, id, full);
+            umma::tma_load_4d(dst + h2 * kHalf, map, h2 * 64, row0, j, id, &full[st]);
         }
         __syncwarp();
       };
-      bool more = walk.next(seg, sh, Hk, P);
-      int id[2] = {-1, -1};
-      if (more) {
-        id[0] = read_id(seg, seg.tile(0, 0));
-        if (!seg.two && seg.count(1) > 0) id[1] = read_id(seg, seg.tile(1, 0));
-      }
-      while (more) {
-        PrefixSeg nseg;
-        const bool nmore = walk.next(nseg, sh, Hk, P);
-        const int n = seg.steps();
-        int nid[2] = {-1, -1};
-        auto read_step = [&](const PrefixSeg& s, int it) {
-          nid[0] = read_id(s, s.tile(0, it));
-          nid[1] = !s.two && it < s.count(1) ? read_id(s, s.tile(1, it)) : -1;
-        };
-        auto load_step = [&](bool is_v, int it, const int* ids) {
-          load(is_v, seg.j, seg.tile(0, it), ids[0]);
-          if (!seg.two && it < seg.count(1)) load(is_v, seg.j, seg.tile(1, it), ids[1]);
-        };
-        load_step(false, 0, id);
-        for (int it = 0; it < n; ++it) {
-          // K runs one step ahead of V: S(it+1) is issued right after PV(it)
-          if (it + 1 < n) read_step(seg, it + 1);
-          else if (nmore) read_step(nseg, 0);
-          load_step(true, it, id);
-          if (it + 1 < n) load_step(false, it + 1, nid);
-          id[0] = nid[0];
-          id[1] = nid[1];
+      // a step of the stream: the key tiles of both slots (two: one for both) and this lane's
+      // block ids of them, read one step before the loads
+      struct Step {
+        int n, j;
+        int tile[2], id[2];
+      };
+      bool more = my_next_seg(seg);
+      int it = 0;
+      auto next_step = [&]() {
+        Step t{0, 0, {0, 0}, {-1, -1}};
+        if (!more) return t;
+        t.n = !seg.two && it < seg.count(1) ? 2 : 1;
+        t.j = seg.j;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          t.tile[g] = seg.tile(g, it);
+          if (g < t.n) t.id[g] = read_id(seg, t.tile[g]);
         }
-        more = nmore;
-        seg = nseg;
+        if (++it == seg.steps()) {
+          more = my_next_seg(seg);
+          it = 0;
+        }
+        return t;
+      };
+      Step cur = next_step();
+      while (cur.n) {
+        const Step after = next_step();
+        load(cur.j, cur.tile[0], cur.id[0]);
+        if (cur.n == 2) load(cur.j, cur.tile[1], cur.id[1]);
+        cur = after;
       }
       if (lane == 0) {  // the last copies land before the CTA may exit
-        for (int c = kl > C::KS ? kl - C::KS : 0; c < kl; ++c)
-          mbar_wait_copies(&ctl.k_full[c % C::KS], (uint32_t)((c / C::KS) & 1));
-        for (int c = vl > C::VS ? vl - C::VS : 0; c < vl; ++c)
-          mbar_wait_copies(&ctl.v_full[c % C::VS], (uint32_t)((c / C::VS) & 1));
+        for (int c = cnt > stages ? cnt - stages : 0; c < cnt; ++c)
+          mbar_wait_copies(&full[c % stages], (uint32_t)((c / stages) & 1));
       }
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- MMA issuer
@@ -369,7 +412,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
           if (s.two) commit1(&ctl.q_empty[1]);
         }
       };
-      bool more = walk.next(seg, sh, Hk, P);
+      bool more = next_seg(seg);
       if (more) first_s(seg);
       while (more) {
         const int n = seg.steps();
@@ -409,28 +452,30 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
             if (seg.two) commit1(&ctl.q_empty[1]);
           }
         }
-        more = walk.next(seg, sh, Hk, P);
+        more = next_seg(seg);
         if (more) first_s(seg);
       }
     } else if (warp == kQWarp) {
       // ---------------------------------------------------------------- Q loader
       // P sequences x G heads of a row tile, one box per 64 dims; rows of the next group or
       // past the batch (zeros) land too and are never stored.
-      if (lane == 0) {
-        int qn[2] = {0, 0};
-        while (walk.next(seg, sh, Hk, P)) {
-          for (int qt = 0; qt < (seg.two ? 2 : 1); ++qt) {
+      int qn[2] = {0, 0};
+      while (next_seg(seg)) {
+        for (int qt = 0; qt < (seg.two ? 2 : 1); ++qt) {
+          if (lane == 0) {
             if (qn[qt] > 0 &&
                 !mbar_wait(&ctl.q_empty[qt], (uint32_t)((qn[qt] - 1) & 1), abort_flag))
               note_timeout(ctl, a.dev_err);
-            ++qn[qt];
             mbar_arrive_expect_tx(&ctl.q_full[qt], (uint32_t)(P * G * D * 2));
 #pragma unroll
             for (int h2 = 0; h2 < NH; ++h2)
               umma::tma_load_3d(sm.q[qt] + h2 * kHalf, &tm_q, h2 * 64, seg.j * G,
                                 seg.first + (2 * seg.pair + qt) * P, &ctl.q_full[qt]);
           }
+          ++qn[qt];
         }
+      }
+      if (lane == 0) {
         for (int qt = 0; qt < 2; ++qt)
           if (qn[qt] > 0) mbar_wait_copies(&ctl.q_full[qt], (uint32_t)((qn[qt] - 1) & 1));
       }
@@ -453,7 +498,8 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
     int oc[2] = {0, 0};     // o_done phases consumed, per slot
     int vbase = 0;          // V tiles of the earlier segments
 
-    while (walk.next(seg, sh, Hk, P)) {
+    int jc = 0;  // segments whose slots were joined
+    while (next_seg(seg)) {
       const int cnt = seg.count(g);
       float m_run = -INFINITY, l_run = 0.f;
       for (int it = 0; it < cnt; ++it) {
@@ -575,12 +621,14 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
         float fa, fb;
         if (g == 1) {
           ctl.join[r] = make_float2(m_run, l_run);
-          bar_arrive256<1>();
-          bar_sync256<2>();
+          mbar_arrive(&ctl.join_there);
+          if (!mbar_wait(&ctl.join_back, (uint32_t)(jc & 1), abort_flag))
+            note_timeout(ctl, a.dev_err);
           fa = ctl.join[r].x;
           fb = ctl.join[r].y;
         } else {
-          bar_sync256<1>();
+          if (!mbar_wait(&ctl.join_there, (uint32_t)(jc & 1), abort_flag))
+            note_timeout(ctl, a.dev_err);
           const float2 ml = ctl.join[r];  // (-inf, 0) without a tile
           const float m = fmaxf(m_run, ml.x);
           fa = m == -INFINITY ? 0.f : fast_exp2(m_run - m);
@@ -591,7 +639,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
           fa *= inv;
           fb *= inv;
           ctl.join[r] = make_float2(fa, fb);
-          bar_arrive256<2>();
+          mbar_arrive(&ctl.join_back);
         }
         wait_o(0);
         if (has_b) wait_o(1);
@@ -609,7 +657,11 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
         }
         // neither slot's O (nor join) is written again before both warpgroups have read them
         umma::fence_before_sync();
-        bar_sync256<3>();
+        mbar_arrive(&ctl.join_read);
+        if (!mbar_wait(&ctl.join_read, (uint32_t)(jc & 1), abort_flag))
+          note_timeout(ctl, a.dev_err);
+        umma::fence_after_sync();
+        ++jc;
       }
     }
     umma::fence_before_sync();

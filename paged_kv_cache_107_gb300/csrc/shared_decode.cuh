@@ -80,7 +80,7 @@ __device__ __forceinline__ SharedPlan make_plan(const DecodeSharedArgs& a, unsig
   p.nt = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) p.nt += red_t[w];
-  split_shared(p, (int)gridDim.x, Hk / HS, a.min_tiles);
+  split_shared(p, (int)gridDim.x, Hk / HS, a.min_tiles, B);
   __syncthreads();
   return p;
 }

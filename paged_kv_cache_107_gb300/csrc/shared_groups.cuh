@@ -56,11 +56,14 @@ __device__ __forceinline__ int group_of(const int* starts, int num_groups, int b
 // The prefix work of one group. Its query rows (sequences x the G heads of a KV head) fill
 // tiles of P sequences; a unit is one KV head with two tiles that take every key tile
 // together (a step: one key tile for both), or the last tile alone, which takes two key
-// tiles at a time (a step: two key tiles, one in each slot of the kernel).
+// tiles at a time (a step: two key tiles, one in each slot). A unit's start and end (its Q,
+// the first products, the rows written out) cost about as much as kUnitSteps steps, which
+// are counted before its own so that equal shares of the stream take equal times.
+constexpr int kUnitSteps = 3;
 struct GroupWork {
-  int nt;     // key tiles
-  int full;   // units per KV head with two row tiles
-  int single; // 1: one more with a single row tile
+  int nt;      // key tiles
+  int full;    // units per KV head with two row tiles
+  int single;  // 1: one more with a single row tile
 
   __device__ __forceinline__ GroupWork(const SharedArgs& sh, int n, int prefix, int P) {
     const int len = shared_len(sh, n, prefix);
@@ -69,15 +72,16 @@ struct GroupWork {
     full = len > 0 ? tiles >> 1 : 0;
     single = len > 0 ? tiles & 1 : 0;
   }
-  __device__ __forceinline__ int unit_steps(int pair) const {
-    return pair < full ? nt : (nt + 1) >> 1;
+  __device__ __forceinline__ int unit_steps(int pair) const {  // kUnitSteps included
+    return kUnitSteps + (pair < full ? nt : (nt + 1) >> 1);
   }
   __device__ __forceinline__ int64_t steps(int Hk) const {
-    return (int64_t)Hk * ((int64_t)full * nt + (single ? (nt + 1) >> 1 : 0));
+    return (int64_t)Hk * ((int64_t)full * (kUnitSteps + nt) +
+                          (single ? kUnitSteps + ((nt + 1) >> 1) : 0));
   }
   // first step of unit (pair, KV head j), counted from the group's first
   __device__ __forceinline__ int64_t unit_first(int Hk, int pair, int j) const {
-    return (int64_t)Hk * pair * nt + (int64_t)j * unit_steps(pair);
+    return (int64_t)Hk * pair * (kUnitSteps + nt) + (int64_t)j * unit_steps(pair);
   }
 };
 
@@ -100,23 +104,32 @@ struct SharedPlan {
   const int64_t* first_x;  // first step of each group
 };
 
-// Time of a step and of a 64 KB tile on one SM, in units of 0.1 us: a step of two row tiles is
-// bound by its products and softmax; a step of one row tile and a tile of a rest by what
-// one SM takes from memory (57 to 61 GB/s, measured with 8 to 114 CTAs). Side by side on the
-// SMs instead of one after the other, the two parts share one start-up, and the steps'
-// products run while the rests wait for memory: 50.7 -> TIME_PROMPT us for 64 sequences behind
-// 8,192 keys, 117.5 -> TIME_DOC us for 128 behind 32,768.
-constexpr int kStepCost = 21, kTileCost = 11;
-constexpr int kPrefixMinSteps = 2;
+// Times on one SM in units of 0.1 us, from timelines of both parts: a step, bound by its
+// products and softmax or by what one SM takes from memory (57 to 61 GB/s, measured with 8
+// to 114 CTAs); a 64 KB tile of a rest; a rest's start and end. Side by side on the SMs instead
+// of one after the other, the two parts share one start-up, and the steps' products run
+// while the rests wait for memory: 50.7 -> TIME_PROMPT us for 64 sequences behind 8,192 keys,
+// 117.5 -> TIME_DOC us for 128 behind 32,768.
+constexpr int kStepCost = 18, kTileCost = 11, kRestCost = 20;
+// A prefix CTA's start and end beyond a rest CTA's.
+constexpr int kPrefixCtaCost = 33;
+constexpr int kPrefixMinSteps = kUnitSteps + 2;
 
-__device__ __forceinline__ void split_shared(SharedPlan& p, int ctas, int slabs, int min_tiles) {
+__device__ __forceinline__ void split_shared(SharedPlan& p, int ctas, int slabs, int min_tiles,
+                                             int seqs) {
   const int64_t want1 = (p.nx + kPrefixMinSteps - 1) / kPrefixMinSteps;
   const int64_t want2 = max((int64_t)1, (p.nt + min_tiles - 1) / min_tiles);
-  const float c1 = (float)p.nx * kStepCost, c2 = (float)(p.nt * slabs) * kTileCost;
   int64_t g1 = 0;
   if (p.nx > 0) {
-    g1 = (int64_t)((float)ctas * (c1 / (c1 + c2)) + 0.5f);
-    g1 = max((int64_t)1, min(min(g1, want1), (int64_t)(ctas - slabs)));
+    // c1 / g1 + kPrefixCtaCost = c2 / (ctas - g1), in two rounds
+    const float c1 = (float)p.nx * kStepCost;
+    const float c2 = (float)(p.nt * kTileCost + (int64_t)seqs * kRestCost) * (float)slabs;
+    float g = (float)ctas * (c1 / (c1 + c2));
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i)
+      g = c1 / fmaxf((c1 + c2 + kPrefixCtaCost * g) / (float)ctas - kPrefixCtaCost,
+                     c1 / (float)ctas);
+    g1 = max((int64_t)1, min(min((int64_t)(g + 0.5f), want1), (int64_t)(ctas - slabs)));
   }
   const int64_t g2 = max((int64_t)1, min(want2, (ctas - g1) / slabs));
   if (p.nx > 0) g1 = min(want1, ctas - g2 * slabs);  // what the rests leave
@@ -138,7 +151,7 @@ __device__ __forceinline__ void write_prefix_parts(const DecodeSharedArgs& a,
       if (work.nt > 0) {
         const int at = b - plan.starts[g], tile = at / P, pair = tile >> 1;
         const int64_t x = plan.first_x[g] + work.unit_first(Hk, pair, j);
-        w.c0 = (int)prefix_cta_of(x, plan.nx, plan.prefix_ctas);
+        w.c0 = (int)prefix_cta_of(x + kUnitSteps, plan.nx, plan.prefix_ctas);
         w.n = (int)prefix_cta_of(x + work.unit_steps(pair) - 1, plan.nx, plan.prefix_ctas) -
               w.c0 + 1;
         w.row = (pair < work.full ? (tile & 1) * kPrefixRows : 0) + at % P * G;
