@@ -533,20 +533,24 @@ class ScoreMod:
     prefix_lens: Optional[torch.Tensor] = None
 
     def _check(self, num_heads: int, num_seqs: int) -> _PaScoreMod:
-        for name, t, dt, n in (("slopes", self.slopes, torch.float32, num_heads),
-                               ("prefix_lens", self.prefix_lens, torch.int32, num_seqs)):
-            if t is None:
-                continue
-            _need(t, name, dt, 1)
-            if t.shape[0] != n or not t.is_contiguous():
-                raise PagedAttentionError(f"{name} must be contiguous with {n} entries")
+        slopes, prefix = self.slopes, self.prefix_lens
+        if slopes is not None:
+            self._array("slopes", slopes, torch.float32, num_heads)
+        if prefix is not None:
+            self._array("prefix_lens", prefix, torch.int32, num_seqs)
         if not (self.softcap >= 0.0 and math.isfinite(self.softcap)):
             raise PagedAttentionError(f"softcap must be finite and >= 0, got {self.softcap}")
         if not (0 <= self.window < 1 << 31 and 0 <= self.sink < 1 << 31):
             raise PagedAttentionError("window and sink must be >= 0 (32-bit)")
         return _PaScoreMod(self.softcap, self.window, self.sink,
-                           None if self.slopes is None else self.slopes.data_ptr(),
-                           None if self.prefix_lens is None else self.prefix_lens.data_ptr())
+                           None if slopes is None else slopes.data_ptr(),
+                           None if prefix is None else prefix.data_ptr())
+
+    @staticmethod
+    def _array(name, t, dtype, n):
+        _need(t, name, dtype, 1)
+        if t.shape[0] != n or not t.is_contiguous():
+            raise PagedAttentionError(f"{name} must be contiguous with {n} entries")
 
 
 _stream_ws = {}
@@ -569,14 +573,51 @@ def _stream_workspace(key: tuple, make, fits, device, stream):
     return ws
 
 
+_VP, _I32, _I64, _F32, _SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
+                              ctypes.c_size_t)
+_fns = {}
+
+
 def _typed(name: str, argtypes, restype=ctypes.c_int):
     """The library's function `name` with its argument types set."""
-    fn = getattr(load_library(), name)
-    if not getattr(fn, "_pa_typed", False):
+    fn = _fns.get(name)
+    if fn is None:
+        fn = getattr(load_library(), name)
         fn.argtypes = argtypes
         fn.restype = restype
-        fn._pa_typed = True
+        _fns[name] = fn
     return fn
+
+
+def _ready(specs, others, stream) -> None:
+    """The tensors of a call, (name, tensor, dtype, dims) each: CUDA, of that type and shape
+    rank, contiguous, and with `others` on the current device (_one_device). One quick pass
+    for the usual case; the first fault found raises its own message."""
+    dev = specs[0][1].device
+    if dev.type == "cuda" and dev.index == torch.cuda.current_device():
+        for _, t, dtype, ndim in specs:
+            if (t.dtype is not dtype or t.dim() != ndim or t.device != dev
+                    or not t.is_contiguous()):
+                break
+        else:
+            if all(t is None or t.device == dev for t in others) and (
+                    stream is None or stream.device == dev):
+                return
+    for name, t, dtype, ndim in specs:
+        _need(t, name, dtype, ndim)
+        if not t.is_contiguous():
+            raise PagedAttentionError(f"{name} must be contiguous")
+    _one_device(*(t for _, t, _, _ in specs), *others, stream=stream)
+
+
+def _raw_stream(stream, device) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _scale(scale) -> float:
+    return 0.0 if scale is None else float(scale)
 
 
 def pa_decode_mod(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
@@ -585,17 +626,14 @@ def pa_decode_mod(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
                   grid_ctas: int = 0, workspace: Optional[DecodeWorkspace] = None,
                   dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pa_decode under the rules of `mod`: the same tensors and the same workspace."""
-    vp, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
-                             ctypes.c_size_t)
-    _need16(q, "q", 3)
-    for name, t, dt, nd in (("out", out, q.dtype, 3), ("q", q, q.dtype, 3),
-                            ("k_cache", k_cache, q.dtype, 4),
-                            ("v_cache", v_cache, q.dtype, 4),
-                            ("block_tables", block_tables, torch.int32, 2),
-                            ("context_lens", context_lens, torch.int32, 1)):
-        _need(t, name, dt, nd)
-        if not t.is_contiguous():
-            raise PagedAttentionError(f"{name} must be contiguous")
+    dt = q.dtype
+    if dt not in _ATTN_TYPES:
+        _need16(q, "q", 3)
+    _ready((("q", q, dt, 3), ("out", out, dt, 3), ("k_cache", k_cache, dt, 4),
+            ("v_cache", v_cache, dt, 4), ("block_tables", block_tables, torch.int32, 2),
+            ("context_lens", context_lens, torch.int32, 1)),
+           (mod.slopes, mod.prefix_lens, None if workspace is None else workspace.buffer,
+            dev_err), stream)
     B, H, D = q.shape
     nb, bs, hk, d2 = k_cache.shape
     if out.shape != q.shape or d2 != D or v_cache.shape != k_cache.shape:
@@ -603,20 +641,20 @@ def pa_decode_mod(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
     if block_tables.shape[0] != B or context_lens.shape[0] != B:
         raise PagedAttentionError("block_tables / context_lens batch mismatch")
     rules = mod._check(H, B)
-    _one_device(out, q, k_cache, v_cache, block_tables, context_lens, mod.slopes,
-                mod.prefix_lens, None if workspace is None else workspace.buffer, dev_err,
-                stream=stream)
     if workspace is None:
         workspace = _stream_workspace(("decode", H, hk, D),
                                       lambda: DecodeWorkspace(max(B, 1), H, hk, D, q.device),
                                       lambda w: w.fits(B, H, hk, D), q.device, stream)
-    fn = _typed("pa_decode_mod", [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i64,
-                                  f32, vp, i32, vp, sz, vp, vp])
-    rc = fn(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-            block_tables.shape[1], _ptr(context_lens), B, H, hk, D, PA_DTYPE[q.dtype], bs, nb,
-            float(scale) if scale is not None else 0.0, ctypes.byref(rules), int(grid_ctas),
-            _ptr(workspace.buffer), workspace.nbytes, _ptr(dev_err), _stream(stream))
-    _check(rc, "pa_decode_mod")
+    fn = _fns.get("pa_decode_mod") or _typed(
+        "pa_decode_mod", [_VP, _VP, _VP, _VP, _VP, _I32, _VP, _I32, _I32, _I32, _I32, _I32, _I32,
+                          _I64, _F32, _VP, _I32, _VP, _SZ, _VP, _VP])
+    rc = fn(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, H, hk, D,
+            PA_DTYPE[dt], bs, nb, _scale(scale), ctypes.byref(rules), grid_ctas,
+            workspace.buffer.data_ptr(), workspace.nbytes,
+            None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, q.device))
+    if rc:
+        _check(rc, "pa_decode_mod")
     return out
 
 
@@ -627,18 +665,15 @@ def pa_prefill_mod(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
                    scale: Optional[float] = None, dev_err: Optional[torch.Tensor] = None,
                    stream=None) -> torch.Tensor:
     """pa_prefill_varlen under the rules of `mod`: the same tensors."""
-    vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
-    _need16(q, "q", 3)
-    for name, t, dt, nd in (("out", out, q.dtype, 3), ("q", q, q.dtype, 3),
-                            ("k_cache", k_cache, q.dtype, 4),
-                            ("v_cache", v_cache, q.dtype, 4),
-                            ("block_tables", block_tables, torch.int32, 2),
-                            ("cu_seqlens_q", cu_seqlens_q, torch.int32, 1),
-                            ("cu_seqlens_k", cu_seqlens_k, torch.int32, 1)):
-        _need(t, name, dt, nd)
-        if not t.is_contiguous():
-            raise PagedAttentionError(f"{name} must be contiguous")
-    T, H, D = q.shape
+    dt = q.dtype
+    if dt not in _ATTN_TYPES:
+        _need16(q, "q", 3)
+    _ready((("q", q, dt, 3), ("out", out, dt, 3), ("k_cache", k_cache, dt, 4),
+            ("v_cache", v_cache, dt, 4), ("block_tables", block_tables, torch.int32, 2),
+            ("cu_seqlens_q", cu_seqlens_q, torch.int32, 1),
+            ("cu_seqlens_k", cu_seqlens_k, torch.int32, 1)),
+           (mod.slopes, mod.prefix_lens, dev_err), stream)
+    _, H, D = q.shape
     nb, bs, hk, d2 = k_cache.shape
     S = cu_seqlens_q.shape[0] - 1
     if out.shape != q.shape or d2 != D or v_cache.shape != k_cache.shape:
@@ -646,24 +681,23 @@ def pa_prefill_mod(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
     if cu_seqlens_k.shape[0] != S + 1 or block_tables.shape[0] != S:
         raise PagedAttentionError("cu_seqlens / block_tables batch mismatch")
     rules = mod._check(H, S)
-    _one_device(out, q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, mod.slopes,
-                mod.prefix_lens, dev_err, stream=stream)
-    fn = _typed("pa_prefill_mod", [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
-                                   i32, i32, i64, i32, f32, vp, vp, vp])
-    rc = fn(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-            block_tables.shape[1], _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), S, int(max_seqlen_q),
-            int(max_seqlen_k), H, hk, D, PA_DTYPE[q.dtype], bs, nb, 1 if causal else 0,
-            float(scale) if scale is not None else 0.0, ctypes.byref(rules), _ptr(dev_err),
-            _stream(stream))
-    _check(rc, "pa_prefill_mod")
+    fn = _fns.get("pa_prefill_mod") or _typed(
+        "pa_prefill_mod", [_VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _I32, _I32, _I32, _I32, _I32,
+                           _I32, _I32, _I32, _I64, _I32, _F32, _VP, _VP, _VP])
+    rc = fn(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_tables.data_ptr(), block_tables.shape[1], cu_seqlens_q.data_ptr(),
+            cu_seqlens_k.data_ptr(), S, max_seqlen_q, max_seqlen_k, H, hk, D, PA_DTYPE[dt], bs, nb,
+            1 if causal else 0, _scale(scale), ctypes.byref(rules),
+            None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, q.device))
+    if rc:
+        _check(rc, "pa_prefill_mod")
     return out
 
 
 # ---------------------------------------------------------------- shared prefixes
 def pa_decode_shared_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int,
                                     head_dim: int = 128) -> int:
-    i32 = ctypes.c_int
-    fn = _typed("pa_decode_shared_workspace_size", [i32, i32, i32, i32], ctypes.c_size_t)
+    fn = _typed("pa_decode_shared_workspace_size", [_I32, _I32, _I32, _I32], _SZ)
     return int(fn(num_seqs, num_heads, num_kv_heads, head_dim))
 
 
@@ -693,19 +727,15 @@ def pa_decode_shared(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
     """pa_decode for a batch in groups: sequences group_starts[g]..group_starts[g+1]-1 (int32
     [groups + 1]) hold the same first prefix_lens[g] positions (int32 [groups]), which are read
     once for the group."""
-    vp, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
-                             ctypes.c_size_t)
-    _need16(q, "q", 3)
-    for name, t, dt, nd in (("out", out, q.dtype, 3), ("q", q, q.dtype, 3),
-                            ("k_cache", k_cache, q.dtype, 4),
-                            ("v_cache", v_cache, q.dtype, 4),
-                            ("block_tables", block_tables, torch.int32, 2),
-                            ("context_lens", context_lens, torch.int32, 1),
-                            ("group_starts", group_starts, torch.int32, 1),
-                            ("prefix_lens", prefix_lens, torch.int32, 1)):
-        _need(t, name, dt, nd)
-        if not t.is_contiguous():
-            raise PagedAttentionError(f"{name} must be contiguous")
+    dt = q.dtype
+    if dt not in _ATTN_TYPES:
+        _need16(q, "q", 3)
+    _ready((("q", q, dt, 3), ("out", out, dt, 3), ("k_cache", k_cache, dt, 4),
+            ("v_cache", v_cache, dt, 4), ("block_tables", block_tables, torch.int32, 2),
+            ("context_lens", context_lens, torch.int32, 1),
+            ("group_starts", group_starts, torch.int32, 1),
+            ("prefix_lens", prefix_lens, torch.int32, 1)),
+           (None if workspace is None else workspace.buffer, dev_err), stream)
     B, H, D = q.shape
     nb, bs, hk, d2 = k_cache.shape
     groups = prefix_lens.shape[0]
@@ -715,18 +745,18 @@ def pa_decode_shared(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
         raise PagedAttentionError("block_tables / context_lens batch mismatch")
     if group_starts.shape[0] != groups + 1:
         raise PagedAttentionError("group_starts must have one entry more than prefix_lens")
-    _one_device(out, q, k_cache, v_cache, block_tables, context_lens, group_starts, prefix_lens,
-                None if workspace is None else workspace.buffer, dev_err, stream=stream)
     if workspace is None:
         workspace = _stream_workspace(
             ("shared", H, hk, D), lambda: SharedDecodeWorkspace(max(B, 1), H, hk, D, q.device),
             lambda w: w.fits(B, H, hk, D), q.device, stream)
-    fn = _typed("pa_decode_shared", [vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32,
-                                     i32, i32, i64, f32, vp, sz, vp, vp])
-    rc = fn(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-            block_tables.shape[1], _ptr(context_lens), _ptr(group_starts), _ptr(prefix_lens), B,
-            groups, H, hk, D, PA_DTYPE[q.dtype], bs, nb,
-            float(scale) if scale is not None else 0.0, _ptr(workspace.buffer), workspace.nbytes,
-            _ptr(dev_err), _stream(stream))
-    _check(rc, "pa_decode_shared")
+    fn = _fns.get("pa_decode_shared") or _typed(
+        "pa_decode_shared", [_VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _I32, _I32, _I32, _I32,
+                             _I32, _I32, _I32, _I64, _F32, _VP, _SZ, _VP, _VP])
+    rc = fn(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+            group_starts.data_ptr(), prefix_lens.data_ptr(), B, groups, H, hk, D, PA_DTYPE[dt],
+            bs, nb, _scale(scale), workspace.buffer.data_ptr(), workspace.nbytes,
+            None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, q.device))
+    if rc:
+        _check(rc, "pa_decode_shared")
     return out
