@@ -533,6 +533,7 @@ class ScoreMod:
     prefix_lens: Optional[torch.Tensor] = None
 
     def _check(self, num_heads: int, num_seqs: int) -> _PaScoreMod:
+        """The C struct of the rules, after their checks."""
         slopes, prefix = self.slopes, self.prefix_lens
         if slopes is not None:
             self._array("slopes", slopes, torch.float32, num_heads)
@@ -626,6 +627,8 @@ def pa_decode_mod(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
                   grid_ctas: int = 0, workspace: Optional[DecodeWorkspace] = None,
                   dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pa_decode under the rules of `mod`: the same tensors and the same workspace."""
+    if not isinstance(mod, ScoreMod):
+        raise PagedAttentionError("mod must be a ScoreMod")
     dt = q.dtype
     if dt not in _ATTN_TYPES:
         _need16(q, "q", 3)
@@ -650,7 +653,7 @@ def pa_decode_mod(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
                           _I64, _F32, _VP, _I32, _VP, _SZ, _VP, _VP])
     rc = fn(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, H, hk, D,
-            PA_DTYPE[dt], bs, nb, _scale(scale), ctypes.byref(rules), grid_ctas,
+            PA_DTYPE[dt], bs, nb, _scale(scale), ctypes.byref(rules), int(grid_ctas),
             workspace.buffer.data_ptr(), workspace.nbytes,
             None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, q.device))
     if rc:
@@ -665,6 +668,8 @@ def pa_prefill_mod(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
                    scale: Optional[float] = None, dev_err: Optional[torch.Tensor] = None,
                    stream=None) -> torch.Tensor:
     """pa_prefill_varlen under the rules of `mod`: the same tensors."""
+    if not isinstance(mod, ScoreMod):
+        raise PagedAttentionError("mod must be a ScoreMod")
     dt = q.dtype
     if dt not in _ATTN_TYPES:
         _need16(q, "q", 3)
@@ -686,8 +691,8 @@ def pa_prefill_mod(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
                            _I32, _I32, _I32, _I64, _I32, _F32, _VP, _VP, _VP])
     rc = fn(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_tables.data_ptr(), block_tables.shape[1], cu_seqlens_q.data_ptr(),
-            cu_seqlens_k.data_ptr(), S, max_seqlen_q, max_seqlen_k, H, hk, D, PA_DTYPE[dt], bs, nb,
-            1 if causal else 0, _scale(scale), ctypes.byref(rules),
+            cu_seqlens_k.data_ptr(), S, int(max_seqlen_q), int(max_seqlen_k), H, hk, D,
+            PA_DTYPE[dt], bs, nb, 1 if causal else 0, _scale(scale), ctypes.byref(rules),
             None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, q.device))
     if rc:
         _check(rc, "pa_prefill_mod")
