@@ -411,9 +411,10 @@ int pa_prefill_varlen(void* out, const void* q, const void* k_cache, const void*
  * sight of every later query. (A mask by documents needs no rule here: each document of a
  * packed batch is a sequence of its own.)
  *
- *   softcap         >= 0 and finite; 0 = no cap.
+ *   softcap         >= 0 and finite; 0 = no cap. softcap * log2(e) must be finite too, and
+ *                   scale / softcap a normal fp32 number.
  *   window, sink    >= 0; window 0 = no window (sink then changes nothing).
- *   slopes          device, fp32 [num_heads], or NULL.
+ *   slopes          device, fp32 [num_heads], finite, of either sign; or NULL.
  *   prefix_lens     device, int32 [num_seqs], or NULL (all 0); negative values count as 0,
  *                   values beyond the sequence as its length.
  *
@@ -484,10 +485,11 @@ int pa_prefill_mod(void* out, const void* q, const void* k_cache, const void* v_
  * set PA_DEV_ERR_SEQLENS; the sequences are then decoded as by pa_decode.
  * Block sizes that no power of two from 8 up divides are accepted, without sharing.
  *
- * Two launches: the shared parts on the tcgen05 tensor cores, then the rest of every sequence
- * and the combine. Both are programmatic dependents: the rule of pa_decode on context_lens
- * and block_tables holds for group_starts and prefix_lens too. Graph-capturable: the arrays
- * may change between replays. The result does not depend on the order in which CTAs finish.
+ * Two launches: one reads the keys, the shared parts on the tcgen05 tensor cores of some SMs
+ * and the rest of every sequence on the others; the second joins the parts of every row. Both
+ * are programmatic dependents: the rule of pa_decode on context_lens and block_tables holds
+ * for group_starts and prefix_lens too. Graph-capturable: the arrays may change between
+ * replays. The result does not depend on the order in which CTAs finish.
  */
 size_t pa_decode_shared_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
                                        int head_dim);

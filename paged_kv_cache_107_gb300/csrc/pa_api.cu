@@ -1,6 +1,7 @@
 // pa_api.cu — the exported C ABI (include/pa.h): argument validation, then launch.
 // Nothing here allocates device memory or synchronises the host.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -55,7 +56,9 @@ static int resolve_mod(const pa_score_mod* mod, float scale, int head_dim, Score
   if (head_dim <= 0) return PA_ERR_UNSUPPORTED;
   m->cap2 = mod->softcap * kLog2e;
   m->cap_in = mod->softcap > 0.f ? natural_scale(scale, head_dim) / mod->softcap : 0.f;
-  if (isinf(m->cap2) || isinf(m->cap_in)) return PA_ERR_SHAPE;
+  // (below FLT_MIN the quotient loses bits, to the last one)
+  if (isinf(m->cap2) || isinf(m->cap_in) || (m->cap2 > 0.f && m->cap_in < FLT_MIN))
+    return PA_ERR_SHAPE;
   const double z = (double)m->cap_in * m->cap_in;
   double f = (double)m->cap2 * m->cap_in;
   for (int i = 0; i < 6; ++i, f *= z) {
@@ -64,6 +67,13 @@ static int resolve_mod(const pa_score_mod* mod, float scale, int head_dim, Score
   }
   m->z_lim = z > 0 ? (float)(1.0 / z) : 0.f;
   m->z_lim3 = z > 0 ? (float)(0.36 / z) : 0.f;
+  // A cap so small that a coefficient leaves fp32 (inf * 0 for a zero product): no product but
+  // zero is in the polynomials' range, and every tile takes the exact way.
+  if (isinf(m->poly[5][0])) {
+    for (int i = 0; i < 6; ++i) m->poly[i][0] = m->poly[i][1] = 0.f;
+    for (int i = 0; i < 4; ++i) m->poly3[i][0] = m->poly3[i][1] = 0.f;
+    m->z_lim = m->z_lim3 = 0.f;
+  }
   m->slopes = mod->slopes;
   m->window = mod->window;
   m->sink = mod->sink;

@@ -41,6 +41,7 @@ def test_c_refusals(lib, call):
     # factors that leave fp32: scale / softcap, softcap * log2(e)
     assert call(lib, rules(softcap=1e-30), scale=1e30) == 2
     assert call(lib, rules(softcap=3e38)) == 2
+    assert call(lib, rules(softcap=1e30), scale=1e-9) == 2
     assert call(lib, rules(window=-1)) == 2
     assert call(lib, rules(sink=-1)) == 2
     assert call(lib, rules(), H=12) == 2
@@ -77,3 +78,13 @@ def test_binding_refuses_host_tensors():
 def test_binding_refuses_rules(kw):
     with pytest.raises(pk.PagedAttentionError):
         pk.ScoreMod(**kw)._check(16, 2)
+
+
+@pytest.mark.parametrize("mod", [None, dict(softcap=1.0), 30.0])
+def test_binding_wants_a_score_mod(mod):
+    cu = torch.zeros(2, dtype=torch.int32)
+    o, q, kc, vc, bt, ctx = tensors()
+    with pytest.raises(pk.PagedAttentionError, match="ScoreMod"):
+        pk.pa_decode_mod(o, q, kc, vc, bt, ctx, mod)
+    with pytest.raises(pk.PagedAttentionError, match="ScoreMod"):
+        pk.pa_prefill_mod(o, q, kc, vc, bt[:1], cu, cu, 1, 1, mod)
