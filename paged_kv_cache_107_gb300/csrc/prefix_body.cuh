@@ -2,21 +2,23 @@
 // the CTAs that take it; shared_decode.cuh launches them beside those of the rests).
 //
 // What it computes: for every group g of sequences that hold the same first L keys, every
-// query head h and sequence b of the group, the normalised row
-//   o = sum_{t < L} 2^(x_t - lse) v_t,  lse = log2 sum_{t < L} 2^(x_t),  x_t = log2(e) scale q.k_t,
-// of each of the key ranges that the work is cut into; the decode of the rest (decode_tc.cuh)
-// those ranges and the sequence's own keys are joined by their log-sum-exps (shared_join.cu).
+// query head h and sequence b of the group, over each of the key ranges S that the work is cut
+// into, the normalised row and its log-sum-exp
+//   o = sum_{t in S} 2^(x_t - lse) v_t,  lse = log2 sum_{t in S} 2^(x_t),  x_t = log2(e) scale q.k_t.
+// shared_join.cu joins them with those of the sequence's own keys (decode_tc.cuh).
 //
 // Why it pays: a decode reads the shared keys once for each sequence. Here the rows of a
 // group (n sequences x the G query heads of a KV head) are a dense matrix, so each shared
 // key and value is read once for 128 or 256 of them: below about 256 rows the bytes of the
 // prefix bound it, above the products do.
 //
-// Structure (that of prefill_kernel.cuh, whose constants and helpers it uses): TMA warps for K, V and Q, a warp that issues tcgen05.mma and two softmax
-// warpgroups, one for each of two slots of accumulators in tensor memory.
+// Structure (that of prefill_kernel.cuh, whose constants and helpers it uses): TMA warps for
+// K, V and Q, a warp that issues tcgen05.mma and two softmax warpgroups, one for each of two
+// slots of accumulators in tensor memory.
 //  * Work: the steps of all units (GroupWork) form one stream, cut into equal shares
-//    (stream-K): a long prefix is spread over all of these CTAs whatever the number of groups. A
-//    CTA's share is a list of segments, each a range of steps of one unit.
+//    whose bounds need not be those of units: a long prefix is spread over all of these CTAs
+//    whatever the number of groups. A CTA's share is a list of segments, each a range of
+//    steps of one unit.
 //  * A unit with two row tiles takes each key tile for both slots (one load, two products). A
 //    unit with one row tile would leave the second slot idle and its own chain of product,
 //    softmax, product exposed; it gives the slots alternate key tiles instead, and the two
@@ -96,6 +98,11 @@ constexpr size_t prefix_smem_bytes() {
   return 1023 + kPrefixCtlBytes + sizeof(PrefixTiles<D>);
 }
 
+// a / b, in 32 bits where both fit (a 64-bit division is a long subroutine).
+__device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
+  return ((a | b) >> 32) == 0 ? (uint64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Hands out a CTA's segments in order.
 struct PrefixWalk {
   int64_t x, x1;  // next step, end of the share
@@ -117,12 +124,12 @@ struct PrefixWalk {
         load_group(sh);
         w = GroupWork(sh, n, prefix, P);
       }
-      const uint32_t rel = (uint32_t)(x - gx);
-      const uint32_t per_pair = (uint32_t)Hk * (uint32_t)(kUnitSteps + w.nt);
-      const uint32_t pair = min(rel / per_pair, (uint32_t)w.full);
-      const uint32_t in_pair = rel - pair * per_pair;
+      const uint64_t rel = (uint64_t)(x - gx), per_pair = (uint64_t)Hk * (kUnitSteps + w.nt);
+      const uint64_t pair = min(quotient(rel, per_pair), (uint64_t)w.full);
+      const uint64_t in_pair = rel - pair * per_pair;
       const uint32_t us = (uint32_t)w.unit_steps((int)pair);
-      const int v0 = (int)(in_pair % us);
+      const uint64_t unit = quotient(in_pair, us);
+      const int v0 = (int)(in_pair - unit * us);
       const int v1 = (int)min((int64_t)us, (int64_t)v0 + (x1 - x));
       x += v1 - v0;
       if (v1 <= kUnitSteps) continue;  // nothing but the start's share
@@ -132,7 +139,7 @@ struct PrefixWalk {
       s.nt = w.nt;
       s.pair = (int)pair;
       s.two = (int)pair < w.full;
-      s.j = (int)(in_pair / us);
+      s.j = (int)unit;
       s.s0 = max(0, v0 - kUnitSteps);
       s.s1 = v1 - kUnitSteps;
       return true;
@@ -238,12 +245,15 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
   volatile int* abort_flag = &ctl.abort;
   PrefixSeg seg;
   int seg_n = 0;  // segments read
-  // The next segment into s (a whole warp calls it); false at the end. After a wait that ran
-  // out a role may read an old segment again, never one that was not written.
+  // The next segment into s (a whole warp calls it); false at the end, and after a wait that
+  // ran out: a slot is read only when it is full and (below) written only when it is empty.
   auto next_seg = [&](PrefixSeg& s) {
     const int slot = seg_n % kSegSlots;
-    if (!mbar_wait(&ctl.seg_full[slot], (uint32_t)((seg_n / kSegSlots) & 1), abort_flag))
+    const bool there = mbar_wait(&ctl.seg_full[slot], (uint32_t)((seg_n / kSegSlots) & 1), abort_flag);
+    if (!__all_sync(0xffffffffu, there)) {
       note_timeout(ctl, a.dev_err);
+      return false;
+    }
     ++seg_n;
     s = ctl.segs[slot];
     __syncwarp();
@@ -273,17 +283,20 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
         if (is_v) return next_seg(t);
         const bool more = walk.next(t, sh, Hk, P);
         if (!more) t.n = 0;
+        const int slot = pub % kSegSlots;
+        bool free = true;
         if (lane == 0) {
-          const int slot = pub % kSegSlots;
-          if (pub >= kSegSlots && !mbar_wait(&ctl.seg_empty[slot],
-                                             (uint32_t)(((pub / kSegSlots) - 1) & 1), abort_flag))
+          free = pub < kSegSlots || mbar_wait(&ctl.seg_empty[slot],
+                                              (uint32_t)(((pub / kSegSlots) - 1) & 1), abort_flag);
+          if (free) {
+            ctl.segs[slot] = t;
+            mbar_arrive(&ctl.seg_full[slot]);
+          } else {
             note_timeout(ctl, a.dev_err);
-          ctl.segs[slot] = t;
-          mbar_arrive(&ctl.seg_full[slot]);
+          }
         }
         ++pub;
-        __syncwarp();
-        return more;
+        return __all_sync(0xffffffffu, free) && more;
       };
       // this lane's block id of a key tile: -1 past the prefix, -2 out of the pool
       auto read_id = [&](const PrefixSeg& t, int tile) {

@@ -108,8 +108,8 @@ struct SharedPlan {
 // products and softmax or by what one SM takes from memory (57 to 61 GB/s, measured with 8
 // to 114 CTAs); a 64 KB tile of a rest; a rest's start and end. Side by side on the SMs instead
 // of one after the other, the two parts share one start-up, and the steps' products run
-// while the rests wait for memory: 50.7 -> TIME_PROMPT us for 64 sequences behind 8,192 keys,
-// 117.5 -> TIME_DOC us for 128 behind 32,768.
+// while the rests wait for memory: 50.7 -> 40 us for 64 sequences behind 8,192 keys, 117.5
+// -> 113 us for 128 behind 32,768.
 constexpr int kStepCost = 18, kTileCost = 11, kRestCost = 20;
 // A prefix CTA's start and end beyond a rest CTA's.
 constexpr int kPrefixCtaCost = 33;

@@ -2,7 +2,7 @@
 //
 // With normalised partial rows o_i and base-2 log-sum-exps l_i over disjoint sets of keys,
 //   o = sum_i 2^(l_i - m) o_i / sum_i 2^(l_i - m),  m = max_i l_i.
-// A row's parts are those of its group's prefix unit (one for each CTA that took steps of it),
+// A row's parts are those of its group's prefix unit (one for each CTA that took steps of it) and
 // the segments of its rest. They are summed in a fixed order in fp32: the result does not
 // depend on which CTA finished first.
 //
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     }
   }
   const float inv = den > 0.f ? 1.f / den : 0.f;
-  uint16_t* dst = static_cast<uint16_t*>(a.out) + row * D + lane * E;
+  uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)row * D + lane * E;
   if constexpr (E == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<F16>(acc[0] * inv, acc[1] * inv),
                                                 pack2<F16>(acc[2] * inv, acc[3] * inv));
