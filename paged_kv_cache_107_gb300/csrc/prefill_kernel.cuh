@@ -519,6 +519,32 @@ __device__ __forceinline__ void mod_tiles(PrefillCtl& ctl, PrefillTiles<D>& sm,
     if (!mbar_wait(&ctl.s_full[g], (uint32_t)(sc & 1), abort_flag)) note_timeout(ctl, a.dev_err);
     ++sc;
     umma::fence_after_sync();
+    if constexpr (kBias) {
+      if (a.mod.cap2 > 0.f) {  // a cap under the bias: the products are capped where they lie
+#pragma unroll 1
+        for (int k0 = 0; k0 < kKeys; k0 += 32) {
+          float y[32];
+          umma::tmem_ld32(s_addr + k0, y);
+          umma::tmem_ld_wait();
+          float x[32], zm[2] = {0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float2 v = make_float2(y[2 * c], y[2 * c + 1]);
+            const float2 z = umma::fmul2(v, v);
+            zm[c & 1] = fmaxf(zm[c & 1], fmaxf(z.x, z.y));
+            const float2 t = umma::fmul2(v, cap_poly2<5>(z, a.mod));
+            x[2 * c] = t.x;
+            x[2 * c + 1] = t.y;
+          }
+          if (!__all_sync(0xffffffffu, fmaxf(zm[0], zm[1]) < a.mod.z_lim)) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[c] = a.mod.cap2 * cap_tanh(y[c] * a.mod.cap_in);
+          }
+          umma::tmem_st32(s_addr + k0, x);
+        }
+        umma::tmem_st_wait();
+      }
+    }
     float sv[kKeys];
 #pragma unroll
     for (int c4 = 0; c4 < 4; ++c4) umma::tmem_ld32(s_addr + 32 * c4, sv + 32 * c4);
@@ -529,10 +555,6 @@ __device__ __forceinline__ void mod_tiles(PrefillCtl& ctl, PrefillTiles<D>& sm,
     }
 
     if constexpr (kBias) {
-      if (a.mod.cap2 > 0.f) {  // a cap under the bias
-#pragma unroll
-        for (int c = 0; c < kKeys; ++c) sv[c] = a.mod.cap2 * cap_tanh(sv[c] * a.mod.cap_in);
-      }
       const float pre = a.mod.cap2 > 0.f ? 1.f : a.scale_log2;
       const int dist = qpos - t0;             // from the tile's first key to the query
       if (t0 + kKeys - 1 <= pos0 + w0 / G) {  // every key at the warp's queries or before
