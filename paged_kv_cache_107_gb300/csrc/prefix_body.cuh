@@ -519,17 +519,26 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
         if (!mbar_wait(&ctl.s_full[g], (uint32_t)(sc & 1), abort_flag)) note_timeout(ctl, a.dev_err);
         ++sc;
         umma::fence_after_sync();
+        const int left = seg.len - seg.tile(g, it) * kKeys;  // keys of the tile that count
+        if (left < kKeys) {
+          // A prefix's last tile is masked where it lies. A branch that masks the row in registers
+          // lengthened every tile: 116 against 112 us for 128 sequences behind 32,768 keys.
+#pragma unroll 1
+          for (int k0 = 0; k0 < kKeys; k0 += 32) {
+            float y[32];
+            umma::tmem_ld32(lane_addr + col_s(g) + k0, y);
+            umma::tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (k0 + c >= left) y[c] = -INFINITY;
+            umma::tmem_st32(lane_addr + col_s(g) + k0, y);
+          }
+          umma::tmem_st_wait();
+        }
         float sv[kKeys];
 #pragma unroll
         for (int c4 = 0; c4 < 4; ++c4) umma::tmem_ld32(lane_addr + col_s(g) + 32 * c4, sv + 32 * c4);
         umma::tmem_ld_wait();
-
-        const int left = seg.len - seg.tile(g, it) * kKeys;  // keys of the tile that count
-        if (left < kKeys) {
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c)
-            if (c >= left) sv[c] = -INFINITY;
-        }
         float mx[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) mx[c] = sv[c];
