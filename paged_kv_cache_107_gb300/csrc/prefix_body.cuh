@@ -635,7 +635,10 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
           for (int e = 0; e < 32; ++e) ob[e] *= inv;
           if (row_ok) store32(dst + 32 * c4, ob);
         }
-        wait_o(1 - g);  // its phase ends about now; a later join waits for the one after
+        // The other slot's phase is counted without a wait: where the next segment has one step,
+        // its o_done can complete before a slower warpgroup here has looked, and the parity would
+        // have come round. (A join, below, comes after the other warpgroup's own wait for it.)
+        ++oc[1 - g];
       } else {
         // join the slots: warpgroup 1 hands over its maximum and sum, warpgroup 0 returns the
         // factors of both accumulators, and each takes half of the dims of both

@@ -335,3 +335,34 @@ def test_decoding_a_group_step_by_step():
                                   np.ones((1, pos + 1), bool))
             ar.assert_within(out[b:b + 1].float().cpu().double().numpy(), r,
                              ar.bound(r, A, dev, BF), f"step {i}")
+
+
+def test_shares_that_end_one_step_into_the_next_unit():
+    """Prefixes whose cut into equal shares leaves some CTAs a single step of a second unit: the
+    warps of one half may then be a segment behind the other's. No wait runs out and every call
+    gives the same bits."""
+    B, H, Hk, D, bs = 128, 32, 8, 128, 128
+    gen = torch.Generator("cuda").manual_seed(5000)
+    k, v = (torch.randn(64 + B, bs, Hk, D, dtype=BF, device="cuda", generator=gen)
+            for _ in range(2))
+    q = torch.randn(B, H, D, dtype=BF, device="cuda", generator=gen)
+    starts = torch.tensor([0, B], dtype=torch.int32, device="cuda")
+    for tiles in (16, 24, 31, 32, 40, 48, 63, 64):
+        table = torch.arange(tiles, dtype=torch.int32, device="cuda").repeat(B, 1)
+        table = torch.cat([table, 64 + torch.arange(B, dtype=torch.int32, device="cuda")[:, None]], 1)
+        ctx = tiles * bs + torch.arange(B, dtype=torch.int32, device="cuda") % 7
+        d = (q, k, v, table, ctx, starts, starts.new_tensor([tiles * bs]))
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        outs = [pk.pa_decode_shared(torch.empty_like(q), *d, dev_err=err) for _ in range(100)]
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0, f"device error bits {int(err.item())} at {tiles} tiles"
+        for o in outs[1:]:
+            assert torch.equal(o.view(torch.int16), outs[0].view(torch.int16))
+        for b in (0, 77):
+            n = int(ctx[b])
+            rows = [c[table[b].long()].reshape(-1, Hk, D)[:n].cpu().double().numpy()
+                    for c in (k, v)]
+            r, A, dev = ar.attend(q[b:b + 1].cpu().double().numpy(), *rows, [n - 1],
+                                  np.ones((1, n), bool))
+            ar.assert_within(outs[0][b:b + 1].float().cpu().double().numpy(), r,
+                             ar.bound(r, A, dev, BF), f"{tiles} tiles, {b}")
