@@ -12,7 +12,7 @@ namespace {
 
 constexpr int kPlanBytes = 4096;  // the scratch of the sums below; the plan's arrays follow
 
-// Sums the work and splits the CTAs (all threads of the block; ends with a barrier).
+// Sums the work and splits the CTAs (all threads of the block).
 template <int HS, int D>
 __device__ __forceinline__ SharedPlan make_plan(const DecodeSharedArgs& a, unsigned char* smem) {
   constexpr int kWarps = kPrefillThreads / 32;
@@ -80,8 +80,8 @@ __device__ __forceinline__ SharedPlan make_plan(const DecodeSharedArgs& a, unsig
   p.nt = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) p.nt += red_t[w];
-  split_shared(p, (int)gridDim.x, Hk / HS, a.min_tiles, B);
   __syncthreads();
+  split_shared(p, (int)gridDim.x, Hk / HS, a.min_tiles, B, common_pairs(p, sh, Hk, P));
   return p;
 }
 
@@ -98,12 +98,16 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   if (warp == kTmaWarp && lane < 5)
     umma::prefetch_tmap(lane == 0 ? &tm_k1 : lane == 1 ? &tm_v1 : lane == 2 ? &tm_q
                         : lane == 3 ? &tm_k : &tm_v);
-  pdl_launch_dependents();
   const SharedPlan plan = make_plan<HS, D>(a, shared_smem);
-  const int slabs = a.num_kv_heads / HS;
+  const int slabs = a.num_kv_heads / HS, active = plan.prefix_ctas + plan.rest_ctas * slabs;
+  // Where the call leaves SMs idle the join may be launched, and wait, there. Where it does not,
+  // the join's CTAs would crowd on the SMs that finish first, and those of the next call's two
+  // parts would lie on the SMs as they come free: the parts run best when they alternate, as a
+  // fresh launch lays them out (back to back, 106 -> 98
+  // us for 128 sequences behind 32,768 keys, 62 -> 56 for 257 in eight groups).
+  if (active < (int)gridDim.x) pdl_launch_dependents();
   if ((int)blockIdx.x < plan.prefix_ctas) {
-    prefix_body<D, F16>(tm_k1, tm_v1, tm_q, a, box_rows, shared_smem, plan,
-                        plan.prefix_ctas + plan.rest_ctas * slabs);
+    prefix_body<D, F16>(tm_k1, tm_v1, tm_q, a, box_rows, shared_smem, plan, active);
     return;
   }
   const int r = (int)blockIdx.x - plan.prefix_ctas;

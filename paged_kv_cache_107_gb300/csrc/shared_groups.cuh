@@ -109,14 +109,32 @@ struct SharedPlan {
 // to 114 CTAs); a 64 KB tile of a rest; a rest's start and end. Side by side on the SMs instead
 // of one after the other, the two parts share one start-up, and the steps' products run
 // while the rests wait for memory: 50.7 -> 40 us for 64 sequences behind 8,192 keys, 117.5
-// -> 113 us for 128 behind 32,768.
+// -> 113 us for 128 behind 32,768 (37 and 98 with the later steps).
 constexpr int kStepCost = 18, kTileCost = 11, kRestCost = 20;
 // A prefix CTA's start and end beyond a rest CTA's.
 constexpr int kPrefixCtaCost = 33;
 constexpr int kPrefixMinSteps = kUnitSteps + 2;
 
+// Where one group makes up the prefixes and its units all have two row tiles: their number per
+// KV head, else 1. The same share of every unit (a multiple of this many CTAs) lets the CTAs that
+// read the same keys for other rows go through them side by side, so that all but one find them
+// in L2 (128 sequences of 4 heads per KV head behind 32,768 keys: 528 -> 399 MB from memory, a
+// step 1.71 -> 1.49 us, the launch 107 -> 98 us).
+__device__ __forceinline__ int common_pairs(const SharedPlan& p, const SharedArgs& sh, int Hk,
+                                            int P) {
+  if (!p.ok || p.nx == 0) return 1;
+  int lo = 0, hi = sh.num_groups - 1;  // the first group with steps: the last that starts at 0
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.first_x[mid] == 0) lo = mid;
+    else hi = mid - 1;
+  }
+  const GroupWork w(sh, p.starts[lo + 1] - p.starts[lo], p.prefix[lo], P);
+  return w.steps(Hk) == p.nx && w.single == 0 ? w.full : 1;
+}
+
 __device__ __forceinline__ void split_shared(SharedPlan& p, int ctas, int slabs, int min_tiles,
-                                             int seqs) {
+                                             int seqs, int pairs) {
   const int64_t want1 = (p.nx + kPrefixMinSteps - 1) / kPrefixMinSteps;
   const int64_t want2 = max((int64_t)1, (p.nt + min_tiles - 1) / min_tiles);
   int64_t g1 = 0;
@@ -131,8 +149,11 @@ __device__ __forceinline__ void split_shared(SharedPlan& p, int ctas, int slabs,
                      c1 / (float)ctas);
     g1 = max((int64_t)1, min(min((int64_t)(g + 0.5f), want1), (int64_t)(ctas - slabs)));
   }
+  const bool level = pairs > 1 && g1 >= 4 * pairs;
+  if (level) g1 -= g1 % pairs;
   const int64_t g2 = max((int64_t)1, min(want2, (ctas - g1) / slabs));
   if (p.nx > 0) g1 = min(want1, ctas - g2 * slabs);  // what the rests leave
+  if (level) g1 -= g1 % pairs;
   p.prefix_ctas = (int)g1;
   p.rest_ctas = (int)g2;
 }

@@ -45,7 +45,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);  // b * H + h
   const int b = row / H, h = row % H;
-  pdl_launch_dependents();
+  // (a large grid's CTAs would still fill the SMs unevenly when the next call's arrive)
+  if ((int)gridDim.x <= a.grid_ctas) pdl_launch_dependents();
   if (b >= a.num_seqs) return;
   pdl_wait();
   const RestSegments rest = sh.rest[b];
