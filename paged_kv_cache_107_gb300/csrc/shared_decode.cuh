@@ -101,10 +101,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   const SharedPlan plan = make_plan<HS, D>(a, shared_smem);
   const int slabs = a.num_kv_heads / HS, active = plan.prefix_ctas + plan.rest_ctas * slabs;
   // Where the call leaves SMs idle the join may be launched, and wait, there. Where it does not,
-  // the join's CTAs would crowd on the SMs that finish first, and those of the next call's two
-  // parts would lie on the SMs as they come free: the parts run best when they alternate, as a
-  // fresh launch lays them out (back to back, 106 -> 98
-  // us for 128 sequences behind 32,768 keys, 62 -> 56 for 257 in eight groups).
+  // the join's CTAs would crowd on the SMs that finish first, and those of the next call would lie
+  // on the SMs as they come free. But a CTA of a prefix and one of the rests on the two SMs of a
+  // pair slow each other down (138 us instead of 98 for 128 sequences behind 32,768 keys with the
+  // parts alternating), and a fresh launch puts consecutive CTAs on pairs: 106 -> 98 us back to
+  // back, 62 -> 56 for 257 sequences in eight groups.
   if (active < (int)gridDim.x) pdl_launch_dependents();
   if ((int)blockIdx.x < plan.prefix_ctas) {
     prefix_body<D, F16>(tm_k1, tm_v1, tm_q, a, box_rows, shared_smem, plan, active);
