@@ -327,7 +327,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
         __syncwarp();
       };
       // a step of the stream: the key tiles of both slots (two: one for both) and this lane's
-      // block ids of them, read one step before the loads
+      // block ids of them (read while the ring has no free slot)
       struct Step {
         int n, j;
         int tile[2], id[2];
@@ -352,10 +352,9 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
       };
       Step cur = next_step();
       while (cur.n) {
-        const Step after = next_step();
         load(cur.j, cur.tile[0], cur.id[0]);
         if (cur.n == 2) load(cur.j, cur.tile[1], cur.id[1]);
-        cur = after;
+        cur = next_step();
       }
       if (lane == 0) {  // the last copies land before the CTA may exit
         for (int c = cnt > stages ? cnt - stages : 0; c < cnt; ++c)
