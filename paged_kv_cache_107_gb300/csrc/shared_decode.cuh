@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   // pair slow each other down (138 us instead of 98 for 128 sequences behind 32,768 keys with the
   // parts alternating), and a fresh launch puts consecutive CTAs on pairs: 106 -> 98 us back to
   // back, 62 -> 56 for 257 sequences in eight groups.
+  // (The rests' CTAs signal early in any case; the launch waits for the prefixes' too.)
   if (active < (int)gridDim.x) pdl_launch_dependents();
   if ((int)blockIdx.x < plan.prefix_ctas) {
     prefix_body<D, F16>(tm_k1, tm_v1, tm_q, a, box_rows, shared_smem, plan, active);
