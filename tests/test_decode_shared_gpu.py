@@ -366,3 +366,52 @@ def test_shares_that_end_one_step_into_the_next_unit():
                                   np.ones((1, n), bool))
             ar.assert_within(outs[0][b:b + 1].float().cpu().double().numpy(), r,
                              ar.bound(r, A, dev, BF), f"{tiles} tiles, {b}")
+
+
+@pytest.mark.parametrize("per_group,prefix", [(1, 200), (2, 130), (300, 144), (8192, 300)])
+def test_most_sequences(per_group, prefix):
+    """8192 sequences, in groups of one, two, a few hundred, or all together."""
+    B, H, Hk, D, bs = 8192, 2, 1, 64, 16
+    gen = torch.Generator("cuda").manual_seed(6000 + per_group)
+    starts = list(range(0, B, per_group)) + [B]
+    groups, lead = len(starts) - 1, -(-prefix // bs)
+    k, v = (torch.randn(groups * lead + B, bs, Hk, D, dtype=BF, device="cuda", generator=gen)
+            for _ in range(2))
+    q = torch.randn(B, H, D, dtype=BF, device="cuda", generator=gen) * 2
+    # whole blocks are shared; the block that holds the prefix's end is copied to each sequence
+    group = torch.arange(B, device="cuda") // per_group
+    table = group[:, None] * lead + torch.arange(lead, device="cuda")
+    own = groups * lead + torch.arange(B, device="cuda")
+    part = prefix % bs
+    if part:
+        for c in (k, v):
+            c[own, :part] = c[table[:, -1], :part]
+        table[:, -1] = own
+        first = torch.tensor(starts[:-1], device="cuda")
+        k[first * 0 + group[first] * lead + lead - 1] = float("nan")  # no table names it
+    else:
+        table = torch.cat([table, own[:, None]], 1)
+    ctx = (prefix + 1 + torch.arange(B, device="cuda") % (bs - part)).int()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    table = table.int().contiguous()
+    out = pk.pa_decode_shared(
+        torch.full_like(q, float("nan")), q, k, v, table, ctx,
+        torch.tensor(starts, dtype=torch.int32, device="cuda"),
+        torch.full((groups,), prefix, dtype=torch.int32, device="cuda"), dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0, f"device error bits {int(err.item())}"
+    assert torch.isfinite(out.float()).all()
+    for b in (0, 1, 299, 300, 4095, 4096, 8000, 8191):
+        n = int(ctx[b])
+        rows = [c[table[b].long()].reshape(-1, Hk, D)[:n].cpu().double().numpy() for c in (k, v)]
+        r, A, dev = ar.attend(q[b:b + 1].cpu().double().numpy(), *rows, [n - 1],
+                              np.ones((1, n), bool))
+        ar.assert_within(out[b:b + 1].float().cpu().double().numpy(), r, ar.bound(r, A, dev, BF),
+                         f"sequence {b}")
+
+
+@pytest.mark.parametrize("Hk", [155, 160])
+def test_more_kv_heads_than_sms(Hk):
+    """A CTA for every slab of KV heads, more than fit the SMs at once."""
+    Shared([5, 1], [400, 0], [3, 40, 1, 9, 100, 60], Hk, Hk, 64, 16, BF, seed=6100 + Hk).check(
+        rows=[0, 2, 4, 5])
