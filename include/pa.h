@@ -464,7 +464,8 @@ int pa_prefill_mod(void* out, const void* q, const void* k_cache, const void* v_
  *
  *   group_starts    device, int32 [num_groups + 1], non-decreasing from 0 to num_seqs: group
  *                   g is the sequences group_starts[g] .. group_starts[g+1] - 1. Groups may
- *                   be empty (a captured graph's spare ones) or hold one sequence.
+ *                   be empty (a captured graph's spare ones, whose prefix_lens do not
+ *                   matter) or hold one sequence.
  *   prefix_lens     device, int32 [num_groups], >= 0: the sequences of group g hold the same
  *                   keys and values at their first prefix_lens[g] positions. They are read
  *                   through the block table of the group's first sequence; the other tables'

@@ -34,7 +34,9 @@ __device__ __forceinline__ bool load_groups(const SharedArgs& sh, int B, int cap
   __syncthreads();
   bool bad = false;
   for (int i = threadIdx.x; i <= n; i += blockDim.x) {
-    if (i < n) bad = bad || starts[i] > starts[i + 1] || prefix[i] < 0 || prefix[i] > cap;
+    if (i < n)  // (the prefix of an empty group is not looked at)
+      bad = bad || starts[i] > starts[i + 1] ||
+            (starts[i] < starts[i + 1] && (prefix[i] < 0 || prefix[i] > cap));
     if (i == 0) bad = bad || starts[0] != 0;
     if (i == n) bad = bad || starts[n] != B;
   }

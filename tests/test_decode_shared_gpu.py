@@ -137,6 +137,13 @@ def test_many_groups_of_all_kinds():
     Shared(sizes, prefix, rest, 16, 8, 64, 16, BF, seed=501).check()
 
 
+def test_prefixes_of_empty_groups_do_not_matter():
+    c = Shared([0, 5, 0, 0, 2], [0, 300, 0, 0, 129], [1, 4, 70, 9, 2, 33, 1], 8, 2, 128, 16, BF,
+               seed=505)
+    c.prefix[[0, 2, 3]] = [1 << 30, -5, 100000]
+    c.check()
+
+
 def test_hundreds_of_small_groups():
     rng = np.random.default_rng(510)
     sizes = [2] * 400 + [3] * 30
