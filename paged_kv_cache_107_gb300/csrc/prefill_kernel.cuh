@@ -526,6 +526,9 @@ __device__ __forceinline__ void mod_tiles(PrefillCtl& ctl, PrefillTiles<D>& sm,
     auto below = [&](int end) { return (uint32_t)((1ull << min(max(end - t, 0), 32)) - 1); };
     return below(lim) & (~below(low) | below(u_keep));
   };
+  // keys from here on are seen by no query of the unit's two tiles
+  const int u_end =
+      max(causal ? min(kv_len, kv_len - u.n + u.i0 + 2 * P) : kv_len, min(kv_len, u.prefix));
   float slope2 = 0.f;
   if constexpr (kBias) slope2 = __ldg(a.mod.slopes + u.j * G + r % G) * 1.4426950408889634f;
   float m_run = -INFINITY, l_run = 0.f;
@@ -770,13 +773,13 @@ __device__ __forceinline__ void mod_tiles(PrefillCtl& ctl, PrefillTiles<D>& sm,
       }
     }
     // rows of the V tile beyond the sequence, and rows that no query of the unit sees: zero
-    // them (never multiply a stale row)
-    if (t0 + kKeys > kv_len || (t0 < u_low && t0 + kKeys > u_keep)) {
+    // them (they may be stale, and a NaN would not vanish against a zero probability)
+    if (t0 + kKeys > u_end || (t0 < u_low && t0 + kKeys > u_keep)) {
       const int vi = u.vbase + first_step<FORM>(u.nt, g) + it;
       const int st = vi % kVStages;
       if (!mbar_wait(&ctl.v_full[st], (uint32_t)((vi / kVStages) & 1), abort_flag))
         note_timeout(ctl, a.dev_err);
-      if (t0 + r >= kv_len || (t0 + r < u_low && t0 + r >= u_keep)) {
+      if (t0 + r >= u_end || (t0 + r < u_low && t0 + r >= u_keep)) {
 #pragma unroll
         for (int ch = 0; ch < D / 8; ++ch)
           *reinterpret_cast<uint4*>(sm.v[st] + (ch >> 3) * kHalf + r * 128 + (ch & 7) * 16) =
