@@ -518,7 +518,8 @@ __device__ __forceinline__ void mod_tiles(PrefillCtl& ctl, PrefillTiles<D>& sm,
     return max(causal ? min(kv_len, p + 1) : kv_len, min(kv_len, u.prefix));
   };
   const int lim = lim_of(qpos), lim_min = lim_of(pos0 + w0 / G);
-  const int low = a.mod.window > 0 ? qpos - a.mod.window + 1 : 0;
+  // (at least 0: low - t must not leave int32 for the keys after the query)
+  const int low = a.mod.window > 0 ? max(0, qpos - a.mod.window + 1) : 0;
   const int low_max = a.mod.window > 0 ? pos0 + (w0 + 31) / G - a.mod.window + 1 : 0;
   // Bit c: the row's query sees key t + c. One word of bits for 32 keys makes a test and a
   // select per key of a masked tile; comparisons with all three limits made up to five.

@@ -1,5 +1,5 @@
-"""What pa_prefill_mod must not look at, against the plain 64-bit attention within the bound that
-its arithmetic implies (attention_reference.py)."""
+"""What pa_prefill_mod must not look at, and windows so long that they hide nothing, against the
+plain 64-bit attention within the bound that its arithmetic implies (attention_reference.py)."""
 import numpy as np
 import pytest
 import torch
@@ -71,3 +71,19 @@ def test_keys_after_a_units_last_query_may_hold_anything(rule, H, Hk, D, bs, dty
             case.v_cache[blk, t % bs] = (float("nan"), float("inf"), -float("inf"))[i % 3]
         rows, ref, tol = expected(case, 0, np.arange(cached, cached + last), rule)
         ar.assert_within(run(case, rule)[rows], ref, tol, f"{rule}, first {last} queries")
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 100, 2 ** 31 - 400])
+@pytest.mark.parametrize("rule", ["none", "cap", "bias", "all"])
+@pytest.mark.parametrize("H,Hk,D,dtype", [(4, 2, 128, BF), (8, 1, 64, FP)])
+def test_the_longest_windows_hide_nothing_after_the_query(window, rule, H, Hk, D, dtype):
+    """Keys after the query, seen because the call is not causal or through the prefix, under a
+    window that reaches back past the start of every sequence."""
+    cached, new = [0, 50], [140, 300]
+    case = stored_case(cached, new, H, Hk, D, 16, dtype, seed=3100)
+    for causal, prefix in ((False, 0), (True, 120)):
+        r = dict(base.RULES[rule], window=window, sink=0, prefix=prefix)
+        got = run(case, r, causal)
+        for s, (c, n) in enumerate(zip(cached, new)):
+            rows, ref, tol = expected(case, s, np.arange(c, c + n), r, causal)
+            ar.assert_within(got[rows], ref, tol, f"{r} causal {causal}")
