@@ -541,6 +541,8 @@ class ScoreMod:
             self._array("prefix_lens", prefix, torch.int32, num_seqs)
         if not (self.softcap >= 0.0 and math.isfinite(self.softcap)):
             raise PagedAttentionError(f"softcap must be finite and >= 0, got {self.softcap}")
+        if self.softcap > 0.0 and ctypes.c_float(self.softcap).value == 0.0:
+            raise PagedAttentionError(f"softcap {self.softcap} is 0 in fp32, which means no cap")
         if not (0 <= self.window < 1 << 31 and 0 <= self.sink < 1 << 31):
             raise PagedAttentionError("window and sink must be >= 0 (32-bit)")
         return _PaScoreMod(self.softcap, self.window, self.sink,
