@@ -424,8 +424,10 @@ int pa_prefill_varlen(void* out, const void* q, const void* k_cache, const void*
  * may hold anything, NaN included. Rows that some query of such a unit sees must be finite.
  *
  * pa_decode_mod — pa_decode under these rules: arguments, workspace, launch and errors as
- * there (every shape runs on the tensor cores). Key tiles that lie wholly outside the window
- * are not read.
+ * there. Every shape runs on the tensor cores, so each probability is rounded to the element
+ * type before the P V product. Key tiles that lie wholly outside the window are not read.
+ * With a window, prefix_lens is read before the wait for the previous kernel too: pa_decode's
+ * rule on context_lens and block_tables holds for it. slopes is read after the wait.
  * pa_prefill_mod — pa_prefill_varlen under these rules: arguments, requirements and errors
  * as there.
  * Both: a softcap or window out of range is PA_ERR_SHAPE, mod == NULL is PA_ERR_NULL.

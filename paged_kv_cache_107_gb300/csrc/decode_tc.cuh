@@ -18,9 +18,10 @@
 //    boxes of tb tokens x HS heads x 64 dims (tb = the largest power of two dividing
 //    block_size, at most T), i.e. 2 * D/64 * T/tb copies per stage; a block size with no
 //    such tb >= 8 is filled with 16-byte cp.async copies into the same layout.
-//  * Launched as a programmatic dependent (decode_kernel.cuh's launch_dependent): the
-//    prologue reads only context_lens; before waiting for the previous grid the producer
-//    prefetches its first tiles' K/V runs into L2.
+//  * Launched as a programmatic dependent (launch_dependent): before waiting for the previous
+//    grid the prologue reads context_lens (the fused step slot_mapping too, a window with
+//    prefixes prefix_lens, the shared form the group arrays), and the producer reads its first
+//    tiles' block ids and prefetches their K/V runs into L2.
 //  * The fused step's new token: its K and V rows of the slab come from k_new / v_new into
 //    a side row of the stage; lanes whose token is the new one point ldmatrix there.
 //  * Q of a segment goes to its own slot (two where shared memory allows), loaded once per
@@ -203,9 +204,9 @@ __device__ __forceinline__ void decode_tc_body(const CUtensorMap& tm_k, const CU
   const int B = a.num_seqs;
   constexpr int T = TC::T;
   constexpr bool kHidden = FORM != kTcPlain;
-  // kTcShared: the plan's group arrays stay in shared memory until the first copies land; from
-  // then on the producer follows the groups in global memory
-  // leading keys of a group that its prefix part takes
+  // leading keys of a group that its prefix part takes (kTcShared: the plan's group arrays stay
+  // in shared memory until the first copies land; from then on the producer follows the groups
+  // in global memory)
   auto shared_of = [&](int n, int prefix) {
     if constexpr (FORM == kTcShared) return plan->ok ? shared_len(a.sh, n, prefix) : 0;
     else return 0;
@@ -356,8 +357,8 @@ __device__ __forceinline__ void decode_tc_body(const CUtensorMap& tm_k, const CU
       }
     }
   }
-  // everything above read only context_lens (an input no earlier kernel of the step
-  // writes); from here on the kernel reads q, the new rows and the caches and writes out
+  // everything above read only inputs that no earlier kernel of the step writes (the header
+  // names them); from here on the kernel reads q, the new rows and the caches and writes out
   // and the workspace, so the grids launched before it must be complete
   pdl_wait();
 
