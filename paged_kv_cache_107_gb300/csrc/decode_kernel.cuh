@@ -402,6 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl.pb0 = 0;
     fence_mbar_init();
   }
+  if (tid < C::STAGES) {  // a wait for a stage's first tile may run out: no keys, nothing to store
+    ctl.meta[tid] = StageMeta{};
+    ctl.meta[tid].new_row = -1;
+  }
 
   // the next kernel on the stream may be scheduled onto SMs as this grid's CTAs leave (it
   // waits for this grid before touching its results)

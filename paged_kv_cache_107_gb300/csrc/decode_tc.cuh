@@ -241,6 +241,10 @@ __device__ __forceinline__ void decode_tc_body(const CUtensorMap& tm_k, const CU
     ctl.pb0 = 0;
     fence_mbar_init();
   }
+  if (tid < S) {  // a wait for a stage's first tile may run out: no keys, nothing to store
+    ctl.meta[tid] = Meta{};
+    ctl.meta[tid].new_row = -1;
+  }
   // the next kernel on the stream may be scheduled onto SMs as this grid's CTAs leave (it
   // waits for this grid before touching its results)
   pdl_launch_dependents();
@@ -498,6 +502,14 @@ __device__ __forceinline__ void decode_tc_body(const CUtensorMap& tm_k, const CU
           }
         }
       }
+#ifdef PA_TEST_DELAY_LAST_TILE_CYCLES
+      // test build only (decode_kernel.cuh): the consumers' wait for the last tile runs out
+      if (it == n_tiles - 1) {
+        const long long t_hold = clock64();
+        while (clock64() - t_hold < (long long)(PA_TEST_DELAY_LAST_TILE_CYCLES)) {
+        }
+      }
+#endif
       unsigned char* st = smem + (size_t)s * TC::STAGE_BYTES;
       unsigned char* side = st + 2 * TC::KV_BYTES;
       if (lane == 0) {
