@@ -544,6 +544,23 @@ __device__ __forceinline__ void mod_tiles(PrefillCtl& ctl, PrefillTiles<D>& sm,
     if (!mbar_wait(&ctl.s_full[g], (uint32_t)(sc & 1), abort_flag)) note_timeout(ctl, a.dev_err);
     ++sc;
     umma::fence_after_sync();
+    // Rows of the V tile beyond the sequence, and rows that no query of the unit sees: zero them
+    // (they may be stale, and a NaN would not vanish against a zero probability). Not before the
+    // products are here: these tell that the V ring has come to this tile, where its parity
+    // alone could be that of an earlier one (a tile of rows sits out the units without it).
+    // All rows start in the same banks, so each goes through its chunks in an order of its own.
+    if (t0 + r >= u_end || (t0 + r < u_low && t0 + r >= u_keep)) {
+      const int vi = u.vbase + first_step<FORM>(u.nt, g) + it;
+      const int st = vi % kVStages;
+      if (!mbar_wait(&ctl.v_full[st], (uint32_t)((vi / kVStages) & 1), abort_flag))
+        note_timeout(ctl, a.dev_err);
+#pragma unroll
+      for (int ch = 0; ch < D / 8; ++ch)
+        *reinterpret_cast<uint4*>(sm.v[st] + (ch >> 3) * kHalf + r * 128 + (((ch ^ r) & 7) << 4)) =
+            make_uint4(0u, 0u, 0u, 0u);
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
     if constexpr (kBias) {
       if (a.mod.cap2 > 0.f) {  // a cap under the bias: the products are capped where they lie
 #pragma unroll 1
@@ -772,21 +789,6 @@ __device__ __forceinline__ void mod_tiles(PrefillCtl& ctl, PrefillTiles<D>& sm,
         umma::tmem_st32(lane_addr + col_o(g) + 64 * c4, ob);
         umma::tmem_st32(lane_addr + col_o(g) + 64 * c4 + 32, ob + 32);
       }
-    }
-    // rows of the V tile beyond the sequence, and rows that no query of the unit sees: zero
-    // them (they may be stale, and a NaN would not vanish against a zero probability)
-    if (t0 + kKeys > u_end || (t0 < u_low && t0 + kKeys > u_keep)) {
-      const int vi = u.vbase + first_step<FORM>(u.nt, g) + it;
-      const int st = vi % kVStages;
-      if (!mbar_wait(&ctl.v_full[st], (uint32_t)((vi / kVStages) & 1), abort_flag))
-        note_timeout(ctl, a.dev_err);
-      if (t0 + r >= u_end || (t0 + r < u_low && t0 + r >= u_keep)) {
-#pragma unroll
-        for (int ch = 0; ch < D / 8; ++ch)
-          *reinterpret_cast<uint4*>(sm.v[st] + (ch >> 3) * kHalf + r * 128 + (ch & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_proxy_async_smem();
     }
     umma::tmem_st_wait();
     umma::fence_before_sync();

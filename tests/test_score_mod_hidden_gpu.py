@@ -87,3 +87,21 @@ def test_the_longest_windows_hide_nothing_after_the_query(window, rule, H, Hk, D
         for s, (c, n) in enumerate(zip(cached, new)):
             rows, ref, tol = expected(case, s, np.arange(c, c + n), r, causal)
             ar.assert_within(got[rows], ref, tol, f"{r} causal {causal}")
+
+
+@pytest.mark.parametrize("rule", ["none", "cap", "bias", "sink", "prefix", "all"])
+@pytest.mark.parametrize("D,dtype", [(128, BF), (64, FP)])
+def test_short_units_after_long_ones_with_one_row_tile(rule, D, dtype):
+    """Several units for each CTA, the heaviest first: 16 key tiles for the first row tile alone, so
+    that the second one's rows sit out many phases of the V ring, then units of both row tiles
+    whose first key tile already holds rows to be left out."""
+    H, Hk, bs, rule = 16, 8, 16, base.RULES[rule]
+    rng = np.random.default_rng(3200)
+    n = 30
+    new = rng.integers(1, 6, n).tolist() + rng.integers(65, 128, n).tolist()
+    case = stored_case([2000] * n + [0] * n, new, H, Hk, D, bs, dtype, seed=3201)
+    got = run(case, rule)
+    for s in [0, 7, n - 1] + list(range(n, 2 * n)):
+        total = int(np.diff(case.cu_seqlens_k)[s])
+        rows, ref, tol = expected(case, s, np.arange(total - new[s], total), rule)
+        ar.assert_within(got[rows], ref, tol, f"{rule} sequence {s}")
