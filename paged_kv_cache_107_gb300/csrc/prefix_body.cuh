@@ -352,6 +352,15 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tm_k, const CUten
       };
       Step cur = next_step();
       while (cur.n) {
+#ifdef PA_TEST_DELAY_LAST_TILE_CYCLES
+        // test build only: the wait for the K tiles of the CTA's last step runs out (the copies
+        // are still issued, late, and awaited below)
+        if (!is_v && !more) {
+          const long long t_hold = clock64();
+          while (clock64() - t_hold < (long long)(PA_TEST_DELAY_LAST_TILE_CYCLES)) {
+          }
+        }
+#endif
         load(cur.j, cur.tile[0], cur.id[0]);
         if (cur.n == 2) load(cur.j, cur.tile[1], cur.id[1]);
         cur = next_step();
