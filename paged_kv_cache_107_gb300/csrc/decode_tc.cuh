@@ -17,7 +17,9 @@
 //    rows an ldmatrix reads sit in 8 different bank groups. The producer fills it with TMA
 //    boxes of tb tokens x HS heads x 64 dims (tb = the largest power of two dividing
 //    block_size, at most T), i.e. 2 * D/64 * T/tb copies per stage; a block size with no
-//    such tb >= 8 is filled with 16-byte cp.async copies into the same layout.
+//    such tb >= 8 is filled with 16-byte cp.async copies into the same layout, each with a
+//    table read and divisions of its own: 1,530 us against 85 at block size 20 and 16 (128
+//    sequences of 100 to 2,048, 32 / 8 heads, head_dim 128; 1,810 with modified scores).
 //  * Launched as a programmatic dependent (launch_dependent): before waiting for the previous
 //    grid the prologue reads context_lens (the fused step slot_mapping too, a window with
 //    prefixes prefix_lens, the shared form the group arrays), and the producer reads its first
@@ -258,39 +260,39 @@ __device__ __forceinline__ void decode_tc_body(const CUtensorMap& tm_k, const CU
       ctl.x1 = plan->nt > 0 ? tile_begin(c + 1, plan->nt, nctas) : 0;
     }
   } else {
-  int64_t local = 0;
-  for (int b = tid; b < B; b += kThreads) {
-    const int raw = __ldg(a.context_lens + b);
-    if (raw < 0 || raw > cap) {
-      if ((b % nctas) == c && slab == 0) set_dev_err(a.dev_err, PA_DEV_ERR_CONTEXT);
+    int64_t local = 0;
+    for (int b = tid; b < B; b += kThreads) {
+      const int raw = __ldg(a.context_lens + b);
+      if (raw < 0 || raw > cap) {
+        if ((b % nctas) == c && slab == 0) set_dev_err(a.dev_err, PA_DEV_ERR_CONTEXT);
+      }
+      // FUSED: a token of an empty sequence has no position to be stored at
+      if (FUSED && (raw <= 0 || raw > cap) && __ldg(a.slot_mapping + b) != -1) {
+        if ((b % nctas) == c && slab == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SLOT);
+      }
+      local += span_of(b).tiles(T);
     }
-    // FUSED: a token of an empty sequence has no position to be stored at
-    if (FUSED && (raw <= 0 || raw > cap) && __ldg(a.slot_mapping + b) != -1) {
-      if ((b % nctas) == c && slab == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SLOT);
-    }
-    local += span_of(b).tiles(T);
-  }
 #pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) local += __shfl_xor_sync(0xffffffffu, local, m);
-  if (lane == 0) ctl.red[warp] = local;
-  __syncthreads();
-  if (tid == 0) {
-    int64_t nt = 0;
-    for (int w = 0; w < kThreads / 32; ++w) nt += ctl.red[w];
-    ctl.nt = nt;
-    // CTAs that own tiles: every CTA of the grid, unless the stream is too short to give
-    // each at least min_tiles
-    const int64_t mt = a.min_tiles > 1 ? a.min_tiles : 1;
-    const int64_t want = (nt + mt - 1) / mt;
-    const int g_eff = (int)(want < (int64_t)nctas ? want : (int64_t)nctas);
-    ctl.g_eff = g_eff;
-    if (c < g_eff) {
-      ctl.x0 = tile_begin(c, nt, g_eff);
-      ctl.x1 = tile_begin(c + 1, nt, g_eff);
-    } else {
-      ctl.x0 = ctl.x1 = 0;
+    for (int m = 16; m >= 1; m >>= 1) local += __shfl_xor_sync(0xffffffffu, local, m);
+    if (lane == 0) ctl.red[warp] = local;
+    __syncthreads();
+    if (tid == 0) {
+      int64_t nt = 0;
+      for (int w = 0; w < kThreads / 32; ++w) nt += ctl.red[w];
+      ctl.nt = nt;
+      // CTAs that own tiles: every CTA of the grid, unless the stream is too short to give
+      // each at least min_tiles
+      const int64_t mt = a.min_tiles > 1 ? a.min_tiles : 1;
+      const int64_t want = (nt + mt - 1) / mt;
+      const int g_eff = (int)(want < (int64_t)nctas ? want : (int64_t)nctas);
+      ctl.g_eff = g_eff;
+      if (c < g_eff) {
+        ctl.x0 = tile_begin(c, nt, g_eff);
+        ctl.x1 = tile_begin(c + 1, nt, g_eff);
+      } else {
+        ctl.x0 = ctl.x1 = 0;
+      }
     }
-  }
   }
   __syncthreads();
   const int64_t NT = ctl.nt;

@@ -170,7 +170,8 @@ struct PrefillTiles {
 
 constexpr int kCtlBytes = 256;
 constexpr int kRecBytes = 1792;  // fills the opt-in limit at head_dim 128 with the slack below
-// (56 records; 40 with modified scores)
+// (56 records; 40 with modified scores, whose batches go to one unit per CTA above 39 units per
+// SM, 5,928 on 152 SMs, and the plain form's above 55, 8,360)
 template <int FORM>
 constexpr int kMaxUnitRecs = kRecBytes / (int)sizeof(RecT<FORM>);
 static_assert(sizeof(PrefillCtl) <= kCtlBytes, "control block");
@@ -253,7 +254,8 @@ __device__ __forceinline__ KeySpan<FORM != kFormPlain> tile_span(const ArgsT<FOR
 // Estimated time of a unit (the longest-first order's key), given its first new token i0:
 // a key-tile step that both tiles take costs about 2.1 us on GB300, a step of one tile
 // alone about 1.8 us, and a unit's start and end about 5 us (measured per unit with clock
-// traces of this kernel on the chunked-prefill workload); in units of 0.1 us.
+// traces of this kernel on the chunked-prefill workload); in units of 0.1 us. The modified
+// forms, whose steps take 1.3 to 1.5 times as long, are sorted by the same weights.
 template <int P, int FORM>
 __device__ __forceinline__ uint32_t pair_cost(const ArgsT<FORM>& a, int s, int n, int kv_len,
                                               int i0) {

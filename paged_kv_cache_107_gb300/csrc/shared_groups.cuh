@@ -14,8 +14,13 @@ namespace pa {
 constexpr int kPrefixRows = 128;  // query rows per tile of the prefix part
 constexpr int kPrefixKeys = 128;  // keys per tile
 
-// Leading positions that a group of n sequences computes once: the prefix, where there is
-// something to save. A lone sequence reads its keys once either way.
+// Leading positions that a group of n sequences computes once: the prefix, where there are
+// bytes to save. A lone sequence reads its keys once either way, and below a key tile there is
+// nothing to multiply. The rule does not weigh time: a lone row tile of few rows costs its
+// steps whatever n. 64 groups of n behind a prefix, together / each for itself (16 / 8 heads,
+// head_dim 128): n = 2 42 / 27 us at 128 positions, 64 / 47 at 512, 78 / 89 at 1,024; n = 4
+// 43 / 37, 64 / 96, 83 / 172; n = 16 73 / 103, 96 / 325, 133 / 637. (32 / 8 heads, head_dim 64:
+// n = 2 36 / 21, 43 / 32, 63 / 48; n = 4 38 / 27, 49 / 51, 75 / 93.)
 __device__ __forceinline__ int shared_len(const SharedArgs& sh, int n, int prefix) {
   return sh.boxes && n >= 2 && prefix >= kPrefixKeys ? prefix : 0;
 }
