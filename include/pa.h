@@ -67,7 +67,8 @@ enum pa_dev_error {
   PA_DEV_ERR_CONTEXT = 4,  /* context length above max_blocks_per_seq*block_size, or negative */
   PA_DEV_ERR_TIMEOUT = 8,  /* a bounded pipeline wait gave up (the kernel returned early) */
   PA_DEV_ERR_SEQLENS = 16, /* cu_seqlens not non-decreasing, or a sequence shape out of range */
-  PA_DEV_ERR_STAGED = 32   /* a staged run outside the tensor, or run offsets that decrease */
+  PA_DEV_ERR_STAGED = 32,  /* a staged run outside the tensor, or run offsets that decrease */
+  PA_DEV_ERR_AXIS = 64     /* a rotary frequency's axis outside [0, num_axes) */
 };
 
 /* Element types: the sampler's logits (F32 or BF16) and the attention calls' q, caches
@@ -511,6 +512,154 @@ int pa_decode_shared(void* out, const void* q, const void* k_cache, const void* 
                      int num_kv_heads, int head_dim, int dtype, int block_size,
                      int64_t num_blocks, float scale, void* workspace, size_t workspace_bytes,
                      int* dev_err, void* stream);
+
+/*
+ * 8-bit caches: the paged caches with one byte an element and one fp32 scale for each row, that
+ * is for each (token, KV head) of K and of V. An element stands for code * scale.
+ *
+ *   k, v            device, 1-byte codes [num_blocks, block_size, num_kv_heads, head_dim],
+ *                   16-byte aligned.
+ *   k_scale,v_scale device, fp32 [num_blocks, num_kv_heads, block_size], 16-byte aligned: the
+ *                   tokens of a block side by side, so that an attention kernel reads the
+ *                   scales of one head's tokens as one run.
+ *   format          PA_Q8_E4M3: codes are 8-bit floats (4 exponent, 3 mantissa bits, largest
+ *                   448, no infinities), the scale a power of two, so that a value keeps 4
+ *                   significant bits wherever it lies below its row's largest by less than a
+ *                   factor of about 2^14. PA_Q8_INT8: two's complement -127..127, steps of
+ *                   1/127 of the row's largest value.
+ *
+ * Rows are quantised alone (top = the row's largest magnitude):
+ *   E4M3   scale = 2^e, the least e >= -126 with top <= 448 * 2^e; code = x / scale rounded to
+ *          the nearest code, ties to the even one.
+ *   INT8   t = max(top, 127 * 2^-126); scale = t / 127 (rounded to fp32); code = 127 x / t
+ *          rounded to the nearest integer, ties to the even one (exactly: the quotient is not
+ *          rounded before).
+ *   top = 0: scale 0, codes 0. A row that holds a NaN or an infinity: scale NaN, codes 0, so
+ *   that the whole row reads back as NaN.
+ */
+enum pa_q8_format { PA_Q8_E4M3 = 1, PA_Q8_INT8 = 2 };
+
+typedef struct pa_q8_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t format;
+} pa_q8_cache;
+
+/*
+ * pa_store_kvcache_q8 — pa_store_kvcache into an 8-bit cache: each row is quantised as it is
+ * written. Slots, strides, races and errors as there; k and v are of type `dtype`
+ * (PA_DTYPE_BF16 or PA_DTYPE_F16), any alignment and token stride of whole elements.
+ * Launched as a programmatic dependent: everything is read and written after the wait for the
+ * previous kernel, and the next kernel may start (and wait) early.
+ */
+int pa_store_kvcache_q8(const void* k, const void* v, int64_t k_tok_stride, int64_t v_tok_stride,
+                        int dtype, const pa_q8_cache* cache, const int32_t* slot_mapping,
+                        int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                        int64_t num_blocks, int* dev_err, void* stream);
+
+/*
+ * pa_load_kvcache_q8 — blocks of an 8-bit cache as blocks of 16-bit elements: block i of k_out
+ * and v_out receives code * scale (rounded once, to the nearest) of block blocks[i] of the
+ * cache. So a prefill over a cached prefix reads the sequences' blocks back into a scratch
+ * cache and attends there (pa_prefill_varlen with tables that number the scratch's blocks).
+ *
+ *   k_out, v_out    device, [num_listed, block_size, num_kv_heads, head_dim] of type `dtype`
+ *                   (PA_DTYPE_BF16 or PA_DTYPE_F16), 16-byte aligned. fp16 values above 65504
+ *                   become infinite.
+ *   blocks          device, int32 [num_listed]; -1 leaves its output block as it is (a block
+ *                   table's padding), any other id outside [0, num_blocks) does so too and
+ *                   sets PA_DEV_ERR_BLOCK_ID. A block may be listed more than once.
+ * Whole blocks are read, rows that no token was stored in included. Launched as
+ * pa_store_kvcache_q8.
+ */
+int pa_load_kvcache_q8(void* k_out, void* v_out, int dtype, const pa_q8_cache* cache,
+                       const int32_t* blocks, int num_listed, int num_kv_heads, int head_dim,
+                       int block_size, int64_t num_blocks, int* dev_err, void* stream);
+
+/*
+ * pa_decode_q8 — pa_decode over an 8-bit cache: q and out are 16-bit floats of type `dtype`, keys
+ * and values code * scale. Arguments, workspace (pa_decode_workspace_size), launch and errors
+ * as there.
+ *
+ * Arithmetic: codes are widened exactly; a bf16 query row is scaled by a power of two into
+ * fp16's range (elements below the row's largest by a factor of 2^28 or more lose bits); fp32
+ * products, softmax and accumulation; each probability times its key's value scale is rounded
+ * to fp16 (2^-11 relative, or 2^-39 of the largest value scale met so far where that is more)
+ * before the second product; one rounding of the output.
+ * Block sizes that no power of two from 8 up divides are much slower than others.
+ */
+int pa_decode_q8(void* out, const void* q, const pa_q8_cache* cache, const int32_t* block_tables,
+                 int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                 int num_heads, int num_kv_heads, int head_dim, int dtype, int block_size,
+                 int64_t num_blocks, float scale, int grid_ctas, void* workspace,
+                 size_t workspace_bytes, int* dev_err, void* stream);
+
+/*
+ * Rotary positions. Frequency i of rotary_dim / 2 turns one pair of dims (a, b) of every query
+ * and key head by the angle p * f_i, p the token's position along axis axes[i]:
+ *   a' = amplitude * (a cos - b sin),  b' = amplitude * (b cos + a sin)
+ * One axis is plain text; three (time, height, width) place image and video tokens.
+ *
+ *   turns           device, uint64 [rotary_dim / 2]: f_i / (2 pi) modulo 1 as a 64-bit fraction
+ *                   (pa_rotary_turns). A position times it, modulo 2^64, is the angle in turns
+ *                   without its whole turns: exact to 2^-33 of a turn at any 32-bit position.
+ *   axes            device, int32 [rotary_dim / 2], each in [0, num_axes). An entry outside
+ *                   sets PA_DEV_ERR_AXIS and turns its pair by axis 0's position.
+ *   rotary_dim      a multiple of 16, 16 .. head_dim: the first dims of each head; the rest pass
+ *                   through.
+ *   num_axes        1 .. 16.
+ *   adjacent        0: frequency i turns dims (i, i + rotary_dim/2); otherwise (2i, 2i + 1).
+ *   amplitude       finite factor of the turned dims (1; context extensions use others).
+ *
+ * pa_rotary_turns — the 64-bit fraction of a frequency in radians per position (host code; of
+ * either sign, at most 2^40 in magnitude; 0 for others), off by at most 2^-64 of a turn.
+ *
+ * pa_rotary_store — turns the new queries and keys and writes keys and values to the cache.
+ *
+ *   q_out           device, rows of num_heads*head_dim elements at q_out + i*q_out_tok_stride.
+ *                   May be q itself (same pointer and stride), otherwise must not overlap q.
+ *   q, k, v         device, type `dtype` (PA_DTYPE_BF16 or PA_DTYPE_F16); token i's row starts
+ *                   at q + i*q_tok_stride and so on; any alignment and stride of whole elements
+ *                   (at least a row's), so that the three may be parts of one projection.
+ *   positions       device, int32; token i's position along axis x is
+ *                   positions[x*pos_axis_stride + i].
+ *   slot_mapping    as pa_store_kvcache; a padding row (-1) still has its queries turned.
+ *   k_cache,v_cache 16-bit caches as pa_store_kvcache, of type `dtype`.
+ *   num_heads       >= 1, num_kv_heads >= 1; neither has to divide the other.
+ * Arithmetic: cos and sin in fp32 of the angle above, products in fp32, one rounding.
+ * Launched as pa_store_kvcache_q8.
+ *
+ * pa_rotary_store_q8 — the same into an 8-bit cache: bit for bit what pa_rotary_store followed by
+ * pa_store_kvcache_q8 of the keys and values gives.
+ */
+typedef struct pa_rotary {
+  const uint64_t* turns;
+  const int32_t* axes;
+  int32_t rotary_dim;
+  int32_t num_axes;
+  int32_t adjacent;
+  float amplitude;
+} pa_rotary;
+
+uint64_t pa_rotary_turns(double inv_freq);
+
+int pa_rotary_store(void* q_out, const void* q, const void* k, const void* v,
+                    int64_t q_out_tok_stride, int64_t q_tok_stride, int64_t k_tok_stride,
+                    int64_t v_tok_stride, int dtype, const int32_t* positions,
+                    int64_t pos_axis_stride, const pa_rotary* rotary, void* k_cache,
+                    void* v_cache, const int32_t* slot_mapping, int num_tokens, int num_heads,
+                    int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                    int* dev_err, void* stream);
+
+int pa_rotary_store_q8(void* q_out, const void* q, const void* k, const void* v,
+                       int64_t q_out_tok_stride, int64_t q_tok_stride, int64_t k_tok_stride,
+                       int64_t v_tok_stride, int dtype, const int32_t* positions,
+                       int64_t pos_axis_stride, const pa_rotary* rotary,
+                       const pa_q8_cache* cache, const int32_t* slot_mapping, int num_tokens,
+                       int num_heads, int num_kv_heads, int head_dim, int block_size,
+                       int64_t num_blocks, int* dev_err, void* stream);
 
 #ifdef __cplusplus
 }

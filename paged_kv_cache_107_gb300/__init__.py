@@ -22,7 +22,9 @@ from . import build as _build
 __all__ = ["pa_store_kvcache", "pa_decode", "pa_decode_step", "pa_decode_workspace_size",
            "pa_prefill_varlen", "pa_decode_noalloc", "pa_decode_mod", "pa_prefill_mod",
            "ScoreMod", "pa_decode_shared", "pa_decode_shared_workspace_size",
-           "SharedDecodeWorkspace", "pa_staged_write_apply",
+           "SharedDecodeWorkspace", "Q8Cache", "pa_store_kvcache_q8", "pa_load_kvcache_q8",
+           "pa_decode_q8", "Rotary", "pa_rotary_turns", "pa_rotary_store", "pa_rotary_store_q8",
+           "pa_staged_write_apply",
            "pa_staged_pack", "pa_staged_pack_bound", "pa_staged_upload_apply",
            "PaStagedLayout", "pa_sample_workspace_size", "pa_gumbel_sample",
            "SampleWorkspace",
@@ -30,7 +32,7 @@ __all__ = ["pa_store_kvcache", "pa_decode", "pa_decode_step", "pa_decode_workspa
            "PA_DEV_ERR"]
 
 PA_DEV_ERR = {"block_id": 1, "slot": 2, "context": 4, "timeout": 8, "seqlens": 16,
-              "staged": 32}
+              "staged": 32, "axis": 64}
 
 PA_ERR_WORKSPACE_CODE = 4
 
@@ -767,3 +769,323 @@ def pa_decode_shared(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
     if rc:
         _check(rc, "pa_decode_shared")
     return out
+
+
+# ---------------------------------------------------------------- 8-bit caches
+class _PaQ8Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int32)]
+
+
+_Q8_FORMATS = {torch.float8_e4m3fn: 1, torch.int8: 2}
+
+
+class Q8Cache:
+    """An 8-bit paged cache (pa_q8_cache in pa.h): codes k, v [num_blocks, block_size, Hk, D] of
+    torch.float8_e4m3fn or torch.int8, scales k_scale, v_scale fp32 [num_blocks, Hk, block_size].
+    A new one holds zeros."""
+
+    def __init__(self, num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int = 128,
+                 dtype: torch.dtype = torch.float8_e4m3fn, device=None):
+        shape, device = (num_blocks, block_size, num_kv_heads, head_dim), device or "cuda"
+        codes = [torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype)
+                 for _ in range(2)]
+        scales = [torch.zeros(num_blocks, num_kv_heads, block_size, device=device)
+                  for _ in range(2)]
+        self._set(*codes, *scales)
+
+    @classmethod
+    def of(cls, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
+           v_scale: torch.Tensor) -> "Q8Cache":
+        """A cache over tensors that the caller has."""
+        cache = cls.__new__(cls)
+        cache._set(k, v, k_scale, v_scale)
+        return cache
+
+    def _set(self, k, v, k_scale, v_scale):
+        if k.dtype not in _Q8_FORMATS or v.dtype != k.dtype:
+            raise PagedAttentionError("codes must be float8_e4m3fn or int8, K and V alike, got "
+                                      f"{k.dtype} and {v.dtype}")
+        if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+            raise PagedAttentionError("scales must be float32")
+        if k.dim() != 4 or v.shape != k.shape:
+            raise PagedAttentionError("codes must be [num_blocks, block_size, Hk, D], K and V alike")
+        nb, bs, hk, _ = k.shape
+        if k_scale.shape != (nb, hk, bs) or v_scale.shape != (nb, hk, bs):
+            raise PagedAttentionError("scales must be [num_blocks, Hk, block_size]")
+        if not all(t.is_contiguous() for t in (k, v, k_scale, v_scale)):
+            raise PagedAttentionError("codes and scales must be contiguous")
+        if len({t.device for t in (k, v, k_scale, v_scale)}) != 1:
+            raise PagedAttentionError("codes and scales on several devices")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._shape = tuple(k.shape)
+        self._format = _Q8_FORMATS[k.dtype]
+
+    def _struct(self) -> _PaQ8Cache:
+        return _PaQ8Cache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
+                          self.v_scale.data_ptr(), self._format)
+
+
+def _on_device(anchor: torch.Tensor, tensors, stream) -> None:
+    """_one_device for `anchor` and `tensors`, quick where all is well."""
+    device = anchor.device
+    if (device.type == "cuda" and device.index == torch.cuda.current_device()
+            and (stream is None or stream.device == device)):
+        for t in tensors:
+            if t is not None and t.device != device:
+                break
+        else:
+            return
+    _one_device(anchor, *tensors, stream=stream)
+
+
+def _q8_cache(cache) -> "Q8Cache":
+    if not isinstance(cache, Q8Cache):
+        raise PagedAttentionError("cache must be a Q8Cache")
+    return cache
+
+
+def _rows(name: str, t: torch.Tensor, dtype, heads: int, d: int) -> int:
+    """The token stride of t [N, heads, d]: rows contiguous, tokens at any stride of at least a
+    row (a stride of 0 or less, or overlapping rows, are refused)."""
+    if t.dtype != dtype or dtype not in _ATTN_TYPES:
+        raise PagedAttentionError(f"{name} must be bf16 or fp16, all alike, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise PagedAttentionError(f"{name} must be [N, {heads}, {d}], got {tuple(t.shape)}")
+    st = t.stride()
+    if (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
+        raise PagedAttentionError(f"{name} rows must be [{heads}, {d}] contiguous")
+    if t.shape[0] <= 1:
+        return max(st[0], heads * d)
+    if st[0] < heads * d:
+        raise PagedAttentionError(f"{name}: tokens overlap (stride {st[0]})")
+    return st[0]
+
+
+def _slots(slot_mapping: torch.Tensor, n: int) -> None:
+    if slot_mapping.dtype != torch.int32 or slot_mapping.dim() != 1:
+        raise PagedAttentionError("slot_mapping must be int32 [N]")
+    if slot_mapping.shape[0] != n or not slot_mapping.is_contiguous():
+        raise PagedAttentionError(f"slot_mapping must be contiguous with {n} entries")
+
+
+def pa_store_kvcache_q8(k: torch.Tensor, v: torch.Tensor, cache: Q8Cache,
+                        slot_mapping: torch.Tensor, dev_err: Optional[torch.Tensor] = None,
+                        stream=None) -> None:
+    """pa_store_kvcache into an 8-bit cache, each row quantised as it is written: k, v [N, Hk, D]
+    bf16 or fp16 (any token stride), slot_mapping [N] int32."""
+    nb, bs, hk, d = _q8_cache(cache)._shape
+    _on_device(cache.k, (k, v, slot_mapping, dev_err), stream)
+    dt = k.dtype
+    ks, vs = _rows("k", k, dt, hk, d), _rows("v", v, dt, hk, d)
+    n = k.shape[0]
+    if v.shape[0] != n:
+        raise PagedAttentionError("k / v token counts differ")
+    _slots(slot_mapping, n)
+    fn = _fns.get("pa_store_kvcache_q8") or _typed(
+        "pa_store_kvcache_q8", [_VP, _VP, _I64, _I64, _I32, _VP, _VP, _I32, _I32, _I32, _I32, _I64,
+                                _VP, _VP])
+    rc = fn(k.data_ptr(), v.data_ptr(), ks, vs, PA_DTYPE[dt], ctypes.byref(cache._struct()),
+            slot_mapping.data_ptr(), n, hk, d, bs, nb,
+            None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, k.device))
+    if rc:
+        _check(rc, "pa_store_kvcache_q8")
+
+
+def pa_load_kvcache_q8(k_out: torch.Tensor, v_out: torch.Tensor, cache: Q8Cache,
+                       blocks: torch.Tensor, dev_err: Optional[torch.Tensor] = None,
+                       stream=None) -> None:
+    """Blocks of an 8-bit cache as 16-bit blocks: k_out, v_out [n, block_size, Hk, D] bf16 or fp16,
+    block i from block blocks[i] (int32 [n]; -1 leaves it as it is)."""
+    nb, bs, hk, d = _q8_cache(cache)._shape
+    _on_device(cache.k, (k_out, v_out, blocks, dev_err), stream)
+    dt = k_out.dtype
+    if dt not in _ATTN_TYPES or v_out.dtype != dt:
+        raise PagedAttentionError("k_out and v_out must be bf16 or fp16, both alike")
+    if blocks.dtype != torch.int32 or blocks.dim() != 1 or not blocks.is_contiguous():
+        raise PagedAttentionError("blocks must be contiguous int32 [n]")
+    n = blocks.shape[0]
+    shape = (n, bs, hk, d)
+    if tuple(k_out.shape) != shape or tuple(v_out.shape) != shape:
+        raise PagedAttentionError(f"k_out and v_out must be {shape}")
+    if not (k_out.is_contiguous() and v_out.is_contiguous()):
+        raise PagedAttentionError("k_out and v_out must be contiguous")
+    fn = _fns.get("pa_load_kvcache_q8") or _typed(
+        "pa_load_kvcache_q8", [_VP, _VP, _I32, _VP, _VP, _I32, _I32, _I32, _I32, _I64, _VP, _VP])
+    rc = fn(k_out.data_ptr(), v_out.data_ptr(), PA_DTYPE[dt], ctypes.byref(cache._struct()),
+            blocks.data_ptr(), n, hk, d, bs, nb,
+            None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, blocks.device))
+    if rc:
+        _check(rc, "pa_load_kvcache_q8")
+
+
+def pa_decode_q8(out: torch.Tensor, q: torch.Tensor, cache: Q8Cache, block_tables: torch.Tensor,
+                 context_lens: torch.Tensor, scale: Optional[float] = None, grid_ctas: int = 0,
+                 workspace: Optional[DecodeWorkspace] = None,
+                 dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_decode over an 8-bit cache: out, q [B, H, D] bf16 or fp16; the same tables, lengths and
+    workspace."""
+    nb, bs, hk, d2 = _q8_cache(cache)._shape
+    dt = q.dtype
+    if dt not in _ATTN_TYPES:
+        _need16(q, "q", 3)
+    _ready((("q", q, dt, 3), ("out", out, dt, 3), ("block_tables", block_tables, torch.int32, 2),
+            ("context_lens", context_lens, torch.int32, 1)),
+           (cache.k, None if workspace is None else workspace.buffer, dev_err), stream)
+    B, H, D = q.shape
+    if out.shape != q.shape or d2 != D:
+        raise PagedAttentionError("shape mismatch")
+    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise PagedAttentionError("block_tables / context_lens batch mismatch")
+    if workspace is None:
+        workspace = _stream_workspace(("decode", H, hk, D),
+                                      lambda: DecodeWorkspace(max(B, 1), H, hk, D, q.device),
+                                      lambda w: w.fits(B, H, hk, D), q.device, stream)
+    fn = _fns.get("pa_decode_q8") or _typed(
+        "pa_decode_q8", [_VP, _VP, _VP, _VP, _I32, _VP, _I32, _I32, _I32, _I32, _I32, _I32, _I64,
+                         _F32, _I32, _VP, _SZ, _VP, _VP])
+    rc = fn(out.data_ptr(), q.data_ptr(), ctypes.byref(cache._struct()), block_tables.data_ptr(),
+            block_tables.shape[1], context_lens.data_ptr(), B, H, hk, D, PA_DTYPE[dt], bs, nb,
+            _scale(scale), int(grid_ctas), workspace.buffer.data_ptr(), workspace.nbytes,
+            None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, q.device))
+    if rc:
+        _check(rc, "pa_decode_q8")
+    return out
+
+
+# ---------------------------------------------------------------- rotary positions
+class _PaRotary(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("axes", ctypes.c_void_p),
+                ("rotary_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("adjacent", ctypes.c_int32), ("amplitude", ctypes.c_float)]
+
+
+def pa_rotary_turns(inv_freq: float) -> int:
+    """A frequency in radians per position as the 64-bit fraction of a turn (host code)."""
+    fn = _fns.get("pa_rotary_turns") or _typed("pa_rotary_turns", [ctypes.c_double],
+                                               ctypes.c_uint64)
+    return int(fn(float(inv_freq)))
+
+
+class Rotary:
+    """The frequencies of pa_rotary_store (pa_rotary in pa.h), kept on the device.
+
+    inv_freq     radians per position of each pair; by default base ** (-2 i / rotary_dim) for
+                 the rotary_dim / 2 pairs (rotary_dim: head_dim unless given).
+    axes         the axis whose position turns each pair. Either `sections` (pairs of axis 0,
+                 then of axis 1, ...) or `axes` (one entry for each pair); all 0 by default.
+    adjacent     pairs are dims (2i, 2i+1) instead of (i, i + rotary_dim/2).
+    amplitude    factor of the turned dims."""
+
+    def __init__(self, head_dim: int = 128, rotary_dim: Optional[int] = None,
+                 base: float = 10000.0, inv_freq=None, sections=None, axes=None,
+                 adjacent: bool = False, amplitude: float = 1.0, device=None):
+        if inv_freq is None:
+            rotary_dim = head_dim if rotary_dim is None else rotary_dim
+            if not (base > 0.0 and math.isfinite(base)):
+                raise PagedAttentionError(f"base must be positive and finite, got {base}")
+            inv_freq = [base ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
+        inv_freq = [float(f) for f in inv_freq]
+        if rotary_dim is None:
+            rotary_dim = 2 * len(inv_freq)
+        if rotary_dim % 16 or not 16 <= rotary_dim <= head_dim or 2 * len(inv_freq) != rotary_dim:
+            raise PagedAttentionError(
+                f"rotary_dim must be a multiple of 16 up to head_dim {head_dim} with a frequency "
+                f"for each pair, got {rotary_dim} and {len(inv_freq)}")
+        if not all(abs(f) <= 2.0 ** 40 for f in inv_freq):
+            raise PagedAttentionError("frequencies must be finite, at most 2^40")
+        if sections is not None and axes is not None:
+            raise PagedAttentionError("pass sections or axes, not both")
+        if sections is not None:
+            axes = [a for a, n in enumerate(sections) for _ in range(int(n))]
+        axes = [0] * len(inv_freq) if axes is None else [int(a) for a in axes]
+        if len(axes) != len(inv_freq) or min(axes) < 0:
+            raise PagedAttentionError(f"{len(inv_freq)} pairs need as many axes, got {len(axes)}")
+        num_axes = max(axes) + 1 if sections is None else max(len(sections), 1)
+        if num_axes > 16:
+            raise PagedAttentionError("at most 16 axes")
+        if not math.isfinite(amplitude):
+            raise PagedAttentionError("amplitude must be finite")
+        device = torch.device(device or "cuda")
+        turns = [pa_rotary_turns(f) for f in inv_freq]
+        self.turns = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns],
+                                  dtype=torch.int64, device=device)
+        self.axes = torch.tensor(axes, dtype=torch.int32, device=device)
+        self.head_dim, self.rotary_dim, self.num_axes = head_dim, rotary_dim, num_axes
+        self.adjacent, self.amplitude = bool(adjacent), float(amplitude)
+
+    def _struct(self) -> _PaRotary:
+        return _PaRotary(self.turns.data_ptr(), self.axes.data_ptr(), self.rotary_dim,
+                         self.num_axes, int(self.adjacent), self.amplitude)
+
+
+def _rotary_store(name, q_out, q, k, v, positions, rotary, hk, d, slot_mapping, caches, bs, nb,
+                  anchor, v_cache, dev_err, stream):
+    if not isinstance(rotary, Rotary):
+        raise PagedAttentionError("rotary must be a Rotary")
+    _on_device(anchor, (q_out, q, k, v, positions, rotary.turns, slot_mapping, v_cache, dev_err),
+               stream)
+    if rotary.head_dim != d:
+        raise PagedAttentionError(f"rotary is for head_dim {rotary.head_dim}, the cache has {d}")
+    dt = q.dtype
+    if q.dim() != 3:
+        raise PagedAttentionError(f"q must be [N, H, D], got {tuple(q.shape)}")
+    n, h = q.shape[0], q.shape[1]
+    strides = (_rows("q_out", q_out, dt, h, d), _rows("q", q, dt, h, d), _rows("k", k, dt, hk, d),
+               _rows("v", v, dt, hk, d))
+    if q_out.shape[0] != n or k.shape[0] != n or v.shape[0] != n:
+        raise PagedAttentionError("q_out / q / k / v token counts differ")
+    if positions.dtype != torch.int32 or positions.dim() not in (1, 2):
+        raise PagedAttentionError("positions must be int32 [axes, N] (or [N] for one axis)")
+    if positions.dim() == 1:
+        axes, pos_stride = 1, 0
+    else:
+        axes, pos_stride = positions.shape[0], positions.stride(0)
+    if axes != rotary.num_axes or positions.shape[-1] != n:
+        raise PagedAttentionError(f"positions must be [{rotary.num_axes}, {n}], got "
+                                  f"{tuple(positions.shape)}")
+    if n > 1 and positions.stride(-1) != 1:
+        raise PagedAttentionError("positions of one axis must be contiguous")
+    _slots(slot_mapping, n)
+    fn = _fns.get(name) or _typed(
+        name, [_VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I32, _VP, _I64, _VP]
+        + [_VP] * len(caches) + [_VP, _I32, _I32, _I32, _I32, _I32, _I64, _VP, _VP])
+    rc = fn(q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, PA_DTYPE[dt],
+            positions.data_ptr(), pos_stride, ctypes.byref(rotary._struct()), *caches,
+            slot_mapping.data_ptr(), n, h, hk, d, bs, nb,
+            None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, anchor.device))
+    if rc:
+        _check(rc, name)
+
+
+def pa_rotary_store(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    positions: torch.Tensor, rotary: Rotary, k_cache: torch.Tensor,
+                    v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                    dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Turns new queries and keys by their positions and writes keys and values to the cache:
+    q_out, q [N, H, D], k, v [N, Hk, D] bf16 or fp16 (any token stride; q_out may be q);
+    positions int32 [axes, N] ([N] for one axis); caches [nb, bs, Hk, D] of the same type;
+    slot_mapping [N] int32 (-1: only the query is turned)."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise PagedAttentionError("caches must be [num_blocks, block_size, Hk, D], both alike")
+    if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
+        raise PagedAttentionError("caches must be of q's type")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise PagedAttentionError("caches must be contiguous")
+    nb, bs, hk, d = k_cache.shape
+    _rotary_store("pa_rotary_store", q_out, q, k, v, positions, rotary, hk, d, slot_mapping,
+                  (k_cache.data_ptr(), v_cache.data_ptr()), bs, nb, k_cache, v_cache, dev_err,
+                  stream)
+    return q_out
+
+
+def pa_rotary_store_q8(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       positions: torch.Tensor, rotary: Rotary, cache: Q8Cache,
+                       slot_mapping: torch.Tensor, dev_err: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """pa_rotary_store into an 8-bit cache: bit for bit pa_rotary_store, then
+    pa_store_kvcache_q8."""
+    nb, bs, hk, d = _q8_cache(cache)._shape
+    _rotary_store("pa_rotary_store_q8", q_out, q, k, v, positions, rotary, hk, d, slot_mapping,
+                  (ctypes.byref(cache._struct()),), bs, nb, cache.k, None, dev_err, stream)
+    return q_out

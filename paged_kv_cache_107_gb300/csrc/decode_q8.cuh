@@ -1,0 +1,712 @@
+// decode_q8.cuh — paged decode attention over an 8-bit cache (pa_q8_cache) on the tensor cores:
+// warp-level mma.sync m16n8k16 with fp16 operands and fp32 accumulators.
+//
+// With codes kc, vc and scales ks, vs of key t, query row q and c = softmax scale * log2 e:
+//   x_t = c ks_t (q . kc_t),  m = max x,  l = sum 2^(x_t - m),  o = sum (2^(x_t - m) vs_t) vc_t / l
+// The work split (stream-K over key tiles), the partial results and their combine are those of
+// decode_kernel.cuh and decode_tc.cuh. What differs:
+//
+//  * A code is half as many bytes, so a stage of 64 KB holds twice the tokens, and every byte has
+//    to be widened: e4m3 by the hardware's conversion to fp16 (exact), int8 by placing the byte
+//    in an fp16 number (q8.cuh). Nothing is widened in shared memory: a register of four codes
+//    becomes the two fp16 words of one MMA operand.
+//    K: the operand's columns are tokens and its rows dims. ldmatrix gives a lane four
+//    consecutive dims of a token; the lane's two words take dims 4i, 4i+1 and 4i+2, 4i+3, so the
+//    products pair with queries loaded in the same order.
+//    V: rows are tokens, columns dims. The transposing ldmatrix moves 16-bit pieces, so a
+//    register holds dims 2i, 2i+1 of two tokens; its even and its odd bytes are the operands
+//    of two products, one for the even dims, one for the odd ones.
+//  * The K scale multiplies the score column. The V scale is taken into the probability, which
+//    is then rounded to fp16: w_t = p_t vs_t 2^(14-E), E the exponent of the largest vs met so
+//    far by the warp (when it grows the accumulators are rescaled), so that w < 2^15 and what is
+//    rounded off lies 2^-39 below the largest scale or 2^-11 below w itself.
+//  * bf16 queries go to fp16 with a power of two for each row (row_to_f16 below).
+//  * A warp takes 32 tokens at a time: the maximum, the exponentials and the shuffles are spread
+//    over twice the bytes of the 16-bit kernel's.
+//  * Scales come beside the codes, [head][token] of each box, by TMA; their slots are padded to
+//    128 bytes (a TMA destination's alignment).
+#pragma once
+
+#include "decode_tc.cuh"
+#include "q8.cuh"
+
+namespace pa {
+namespace {
+
+template <int HS, int D>
+struct Q8Cfg {
+  static constexpr int SUB = D == 64 ? 2 : 1;       // steps of 32 tokens per warp and stage
+  static constexpr int T = 256 * SUB / HS;          // tokens per stage
+  static constexpr int WPH = kConsumerWarps / HS;   // warps per KV head (token split)
+  static constexpr int KV_BYTES = HS * T * D;
+  static constexpr int SC_BYTES = T * (4 * HS > 16 ? 4 * HS : 16);  // boxes of 8 tokens, padded
+  static constexpr int STAGE_BYTES = (2 * (KV_BYTES + SC_BYTES) + 1023) / 1024 * 1024;
+  static constexpr int Q_BYTES = HS * kTcGMax * D * 2;
+  static constexpr int CTRL_BYTES = 1024;
+  static constexpr int BUDGET = 227 * 1024 - 1024 - CTRL_BYTES;  // less the alignment slack
+  static constexpr int QS = (3 * STAGE_BYTES + 2 * Q_BYTES <= BUDGET) ? 2 : 1;
+  static constexpr int STAGES = (BUDGET - QS * Q_BYTES) / STAGE_BYTES;
+  static constexpr int MERGE_FLOATS = kTcGMax * (D + 2);
+  static constexpr size_t SMEM =
+      1024 + (size_t)STAGES * STAGE_BYTES + (size_t)QS * Q_BYTES + CTRL_BYTES;
+  static_assert(STAGES >= 2, "at least two stages");
+  static_assert(sizeof(TcCtrl<STAGES>) <= CTRL_BYTES, "control block");
+  static_assert(HS * (WPH - 1) * MERGE_FLOATS * 4 <= 2 * KV_BYTES, "merge scratch");
+  static_assert(SMEM <= 227 * 1024, "shared memory budget");
+};
+
+// One 3-D TMA box into shared memory.
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, int c0, int c1,
+                                                 int c2, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)),
+      "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+
+struct Q8Maps {
+  CUtensorMap k, v, ks, vs;
+};
+
+// A lane's part of a query row, dims 16c + 4 tig .. + 3 of every chunk c, as fp16. bf16 rows are
+// scaled by 2^(14-e), e the exponent of the row's largest magnitude (at least -112): exact but for
+// elements 2^28 and more below that largest. The row sits in the four lanes of a quad. Returns
+// the factor that undoes it.
+template <int KC>
+__device__ __forceinline__ float row_to_f16(uint32_t (&qa)[KC][2], bool f16) {
+  if (f16) return 1.f;
+  uint32_t top = 0u;
+#pragma unroll
+  for (int c = 0; c < KC; ++c)
+    top = __vmaxu2(top, __vmaxu2(qa[c][0] & 0x7fff7fffu, qa[c][1] & 0x7fff7fffu));
+  top = max(top & 0xffffu, top >> 16);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const int e = max((int)(top >> 7) - 127, -112);
+  const float up = pow2f(14 - e);
+#pragma unroll
+  for (int c = 0; c < KC; ++c)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float lo, hi;
+      bf16x2_to_f32(qa[c][i], lo, hi);
+      qa[c][i] = f2_elt2<true>(lo * up, hi * up);
+    }
+  return pow2f(e - 14);
+}
+
+template <int HS, int D, int FMT>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_decode_q8_kernel(const __grid_constant__ Q8Maps tm, const DecodeQ8Args a, const int tb) {
+  using C = Q8Cfg<HS, D>;
+  using Ctl = TcCtrl<C::STAGES>;
+  constexpr int S = C::STAGES, T = C::T;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* qbuf = smem + (size_t)S * C::STAGE_BYTES;
+  Ctl& ctl = *reinterpret_cast<Ctl*>(qbuf + (size_t)C::QS * C::Q_BYTES);
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const int c = (int)blockIdx.x, slab = (int)blockIdx.y, nctas = (int)gridDim.x;
+  const int H = a.num_heads;
+  const int Hk = a.num_kv_heads;
+  const int G = H / Hk;  // 1..8
+  const int cap = a.max_blocks * a.block_size;
+  const int B = a.num_seqs;
+  auto tiles_of = [&](int b) { return (load_ctx(a.context_lens, b, cap) + T - 1) / T; };
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&ctl.full[s], 1);
+      mbar_init(&ctl.empty[s], kConsumerWarps);
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&ctl.q_full[q], 1);
+      mbar_init(&ctl.q_empty[q], kConsumerWarps);
+    }
+    mbar_init(&ctl.seg_bar, kConsumerWarps);
+    if (C::WPH > 1)
+      for (int j = 0; j < HS; ++j) mbar_init(&ctl.merge_bar[j], C::WPH - 1);
+    ctl.found = 0;
+    ctl.abort = 0;
+    ctl.b0 = 0;
+    ctl.pb0 = 0;
+    fence_mbar_init();
+  }
+  if (tid < S) ctl.meta[tid] = StageMeta{};  // a first wait may run out: no keys
+  pdl_launch_dependents();
+
+  // ---- prologue: total tiles, then the sequence that holds this CTA's first tile -----
+  {
+    int64_t local = 0;
+    for (int b = tid; b < B; b += kThreads) {
+      const int raw = __ldg(a.context_lens + b);
+      if ((raw < 0 || raw > cap) && (b % nctas) == c && slab == 0)
+        set_dev_err(a.dev_err, PA_DEV_ERR_CONTEXT);
+      local += tiles_of(b);
+    }
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) local += __shfl_xor_sync(0xffffffffu, local, m);
+    if (lane == 0) ctl.red[warp] = local;
+    __syncthreads();
+    if (tid == 0) {
+      int64_t nt = 0;
+      for (int w = 0; w < kThreads / 32; ++w) nt += ctl.red[w];
+      ctl.nt = nt;
+      const int64_t mt = a.min_tiles > 1 ? a.min_tiles : 1;
+      const int64_t want = (nt + mt - 1) / mt;
+      const int g = (int)(want < (int64_t)nctas ? want : (int64_t)nctas);
+      ctl.g_eff = g;
+      ctl.x0 = c < g ? tile_begin(c, nt, g) : 0;
+      ctl.x1 = c < g ? tile_begin(c + 1, nt, g) : 0;
+    }
+  }
+  __syncthreads();
+  const int64_t NT = ctl.nt;
+  const int g_eff = ctl.g_eff;
+  const int64_t x0 = ctl.x0, x1 = ctl.x1;
+
+  if (x0 < x1) {
+    int64_t running = 0;
+    for (int base = 0; base < B; base += kConsumerWarps * 32) {
+      int n = 0;
+      const int b = base + tid;
+      if (tid < kConsumerWarps * 32 && b < B) n = tiles_of(b);
+      int incl = n;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, m);
+        if (lane >= m) incl += y;
+      }
+      if (lane == 31) ctl.red[warp] = incl;
+      __syncthreads();
+      int64_t before = 0, chunk = 0;
+      for (int w = 0; w < kConsumerWarps; ++w) {
+        if (w < warp) before += ctl.red[w];
+        chunk += ctl.red[w];
+      }
+      if (n > 0) {
+        const int64_t p = running + before + incl - n;
+        if (p <= x0 && x0 < p + n) {
+          ctl.b0 = b;
+          ctl.pb0 = p;
+          ctl.found = 1;
+        }
+      }
+      running += chunk;
+      __syncthreads();
+      if (ctl.found) break;
+    }
+  }
+  __syncthreads();
+  // what came before reads only context_lens, which no earlier kernel of the step writes
+  pdl_wait();
+
+  {  // zero rows of empty (or invalid) sequences assigned to this CTA: one warp per row
+    const int heads = HS * G;
+    for (int b = c + warp * nctas; b < B; b += (kThreads / 32) * nctas) {
+      if (load_ctx(a.context_lens, b, cap) != 0) continue;
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                            ((int64_t)b * H + slab * heads) * D);
+      for (int i = lane; i < heads * D / 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  if (x0 >= x1) return;
+  if (!ctl.found) {  // context_lens changed under the kernel
+    if (tid == 0) set_dev_err(a.dev_err, PA_DEV_ERR_CONTEXT);
+    return;
+  }
+  const int64_t n_tiles = x1 - x0;
+  volatile int* abort_flag = &ctl.abort;
+  auto gave_up = [&]() {
+    if (lane == 0) {
+      ctl.abort = 1;
+      set_dev_err(a.dev_err, PA_DEV_ERR_TIMEOUT);
+    }
+  };
+  // boxes of tbl tokens: codes [head][token][D], scales [head][token]
+  const int tbl = tb > 0 ? tb : T;
+  const int lg_tbl = __ffs(tbl) - 1;
+  const int sc_slot = max(HS * tbl * 4, 128);
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------------ producer
+    const uint64_t policy = policy_evict_first();
+    if (tb > 0 && lane == 0) {
+      prefetch_tensor_map(&tm.k);
+      prefetch_tensor_map(&tm.v);
+      prefetch_tensor_map(&tm.ks);
+      prefetch_tensor_map(&tm.vs);
+    }
+    const int nbx = tb > 0 ? T / tb : 0;  // boxes of a full tile
+    const int box_bytes = HS * tb * (D + 4);
+    int b = ctl.b0;
+    int64_t pb = ctl.pb0;
+    int hi = load_ctx(a.context_lens, b, cap);
+    int nb = (hi + T - 1) / T;
+    int q_n = 0;  // segments whose Q has been issued
+    for (int64_t it = 0; it < n_tiles; ++it) {
+      const int64_t x = x0 + it;
+      while (x >= pb + nb && b + 1 < B) {
+        pb += nb;
+        ++b;
+        hi = load_ctx(a.context_lens, b, cap);
+        nb = (hi + T - 1) / T;
+      }
+      const int s = (int)(it % S);
+      const int lt = (int)(x - pb);
+      const int tok0 = lt * T;
+      const int count = min(T, hi - tok0);
+      const int32_t* table = a.block_tables + (int64_t)b * a.max_blocks;
+      int flags = 0;
+      if (x == x0 || lt == 0) flags |= kFlagFirst;
+      if (x == x1 - 1 || lt == nb - 1) flags |= kFlagLast;
+      if (pb >= x0 && pb + nb <= x1) flags |= kFlagWhole;
+      // this lane's boxes: tokens tok0 + i * tb .. + tb - 1 for i = lane, lane + 32, inside one
+      // block each
+      constexpr int kBoxes = T / 8 > 32 ? 2 : 1;
+      int blk[kBoxes], off[kBoxes], nbox = 0;
+#pragma unroll
+      for (int r = 0; r < kBoxes; ++r) {
+        const int i = lane + 32 * r;
+        blk[r] = -1;
+        off[r] = 0;
+        if (i < nbx && i * tb < count) {
+          const int pos = tok0 + i * tb;
+          const int id = __ldg(table + pos / a.block_size);
+          off[r] = pos % a.block_size;
+          if (id >= 0 && (int64_t)id < a.num_blocks) blk[r] = id;
+          else set_dev_err(a.dev_err, PA_DEV_ERR_BLOCK_ID);
+        }
+        nbox += __popc(__ballot_sync(0xffffffffu, blk[r] >= 0));
+      }
+      if (it >= S && !mbar_wait(&ctl.empty[s], (uint32_t)(((it / S) - 1) & 1), abort_flag))
+        gave_up();
+#ifdef PA_TEST_DELAY_LAST_TILE_CYCLES
+      // test build only (decode_kernel.cuh): the consumers' wait for the last tile runs out
+      if (it == n_tiles - 1) {
+        const long long t_hold = clock64();
+        while (clock64() - t_hold < (long long)(PA_TEST_DELAY_LAST_TILE_CYCLES)) {
+        }
+      }
+#endif
+      unsigned char* st = smem + (size_t)s * C::STAGE_BYTES;
+      unsigned char* st_sc = st + 2 * C::KV_BYTES;
+      if (lane == 0) {
+        StageMeta& m = ctl.meta[s];
+        m.pb = pb;
+        m.b = b;
+        m.tok0 = tok0;
+        m.count = count;
+        m.nb = nb;
+        m.flags = flags;
+        if (tb > 0) mbar_arrive_expect_tx(&ctl.full[s], (uint32_t)(nbox * 2 * box_bytes));
+      }
+      __syncwarp();
+      if (tb > 0) {
+#pragma unroll
+        for (int r = 0; r < kBoxes; ++r) {
+          if (blk[r] < 0) continue;
+          const int i = lane + 32 * r;
+          tma_load_4d_hint(st + i * HS * tb * D, &tm.k, 0, off[r], slab * HS, blk[r],
+                           &ctl.full[s], policy);
+          tma_load_3d_hint(st_sc + i * sc_slot, &tm.ks, off[r], slab * HS, blk[r], &ctl.full[s],
+                           policy);
+          tma_load_4d_hint(st + C::KV_BYTES + i * HS * tb * D, &tm.v, 0, off[r], slab * HS, blk[r],
+                           &ctl.full[s], policy);
+          tma_load_3d_hint(st_sc + C::SC_BYTES + i * sc_slot, &tm.vs, off[r], slab * HS, blk[r],
+                           &ctl.full[s], policy);
+        }
+      } else {
+        // 16-byte copies into the same swizzled layout, one box of T tokens, a token at a time
+        constexpr int CH = D / 16;  // 16-byte chunks of one head's row
+        for (int t = 0; t < count; ++t) {
+          const int pos = tok0 + t;
+          const int id = __ldg(table + pos / a.block_size);
+          const int in = pos % a.block_size;
+          if (id < 0 || (int64_t)id >= a.num_blocks) {
+            if (lane == 0) set_dev_err(a.dev_err, PA_DEV_ERR_BLOCK_ID);
+            continue;
+          }
+          const int64_t row =
+              (((int64_t)id * a.block_size + in) * Hk + slab * HS) * D;  // HS * D bytes
+          for (int i = lane; i < 2 * HS * CH; i += 32) {
+            const int kv = i / (HS * CH), jj = i / CH % HS, ch = i % CH;
+            const int sw = D == 128 ? t & 7 : (t >> 1) & 3;
+            const unsigned char* src =
+                static_cast<const unsigned char*>(kv ? a.v_cache : a.k_cache) + row + jj * D + ch * 16;
+            cp_async16(st + kv * C::KV_BYTES + (jj * T + t) * D + ((ch ^ sw) << 4), src);
+          }
+          if (lane < 2 * HS) {
+            const int kv = lane / HS, jj = lane % HS;
+            const float* src = (kv ? a.v_scale : a.k_scale) +
+                               ((int64_t)id * Hk + slab * HS + jj) * a.block_size + in;
+            cp_async4(st_sc + kv * C::SC_BYTES + (jj * T + t) * 4, src);
+          }
+        }
+        cp_async_arrive(&ctl.full[s]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.full[s]);
+      }
+      if (flags & kFlagFirst) {
+        // Q of the segment (HS*G rows of D, contiguous) into its slot
+        const int qs = q_n % C::QS;
+        if (q_n >= C::QS &&
+            !mbar_wait(&ctl.q_empty[qs], (uint32_t)(((q_n / C::QS) - 1) & 1), abort_flag))
+          gave_up();
+        if (lane == 0) {
+          const uint32_t q_bytes = (uint32_t)(HS * G * D * 2);
+          mbar_arrive_expect_tx(&ctl.q_full[qs], q_bytes);
+          bulk_g2s(qbuf + (size_t)qs * C::Q_BYTES,
+                   static_cast<const uint16_t*>(a.q) + ((int64_t)b * H + (int64_t)slab * HS * G) * D,
+                   q_bytes, &ctl.q_full[qs]);
+        }
+        ++q_n;
+      }
+    }
+    // copies still in flight land before the producer leaves
+    for (int64_t it = n_tiles > S ? n_tiles - S : 0; it < n_tiles; ++it)
+      mbar_wait_copies(&ctl.full[it % S], (uint32_t)((it / S) & 1));
+    for (int n = q_n > C::QS ? q_n - C::QS : 0; n < q_n; ++n)
+      mbar_wait_copies(&ctl.q_full[n % C::QS], (uint32_t)((n / C::QS) & 1));
+    return;
+  }
+
+  // -------------------------------------------------------------------- consumers
+  const int j = warp / C::WPH;    // KV head within the slab
+  const int w = warp % C::WPH;    // token group within the tile
+  const int kvh = slab * HS + j;  // global KV head
+  const int gid = lane >> 2, tig = lane & 3;
+  const bool row_ok = gid < G;
+  constexpr int KC = D / 16;      // chunks of 16 dims
+  uint32_t qa[KC][2];             // Q of row gid: dims 16 kc + 4 tig, +1 and +2, +3
+  float o[KC][4];                 // O of row gid: dims 16 kc + 4 tig .. + 3
+  float2 z = make_float2(0.f, 0.f);  // accumulators of the padding rows (never read)
+  float m_run = -INFINITY, l_part = 0.f;  // row gid: running max (log2 units), partial sum
+  float cq = 0.f;                 // row gid: c over the power of two in its fp16 queries
+  constexpr int kE0 = -112;
+  int e_run = kE0;                // exponent of the largest value scale so far
+#pragma unroll
+  for (int n = 0; n < KC; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+
+  // row (token t of head j) of a code tile, and its scale
+  auto row_off = [&](int t) -> int {
+    return ((((t >> lg_tbl) * HS + j) << lg_tbl) + (t & (tbl - 1))) * D;
+  };
+  auto sc_off = [&](int t) -> int {
+    return (t >> lg_tbl) * sc_slot + ((j << lg_tbl) + (t & (tbl - 1))) * 4;
+  };
+  // chunk ch of a row sits at chunk ch ^ sw; a lane's ldmatrix row has the same sw everywhere
+  const int sw = D == 128 ? lane & 7 : (lane >> 1) & 3;
+  const uint32_t sw_hi = (uint32_t)(sw & 6) << 4;
+  const int k_hi = (lane >> 3) & 1, v_hi = lane >> 4;  // which of a pair of chunks
+  const uint32_t smem_base = smem_u32(smem);
+
+  int seg_count = 0;
+  int q_n = 0;
+  for (int64_t it = 0; it < n_tiles; ++it) {
+    const int s = (int)(it % S);
+    if (!mbar_wait(&ctl.full[s], (uint32_t)((it / S) & 1), abort_flag)) gave_up();
+    const StageMeta meta = ctl.meta[s];
+    unsigned char* Kst = smem + (size_t)s * C::STAGE_BYTES;
+    unsigned char* Vst = Kst + C::KV_BYTES;
+    const unsigned char* ksc = Kst + 2 * C::KV_BYTES;
+    const unsigned char* vsc = ksc + C::SC_BYTES;
+    const int count = meta.count;
+
+    if (meta.flags & kFlagFirst) {
+      const int qs = q_n % C::QS;
+      if (!mbar_wait(&ctl.q_full[qs], (uint32_t)((q_n / C::QS) & 1), abort_flag)) gave_up();
+      const unsigned char* Qst = qbuf + (size_t)qs * C::Q_BYTES;
+#pragma unroll
+      for (int kc = 0; kc < KC; ++kc) {
+        uint2 x = make_uint2(0u, 0u);
+        if (row_ok)
+          x = *reinterpret_cast<const uint2*>(Qst + ((j * G + gid) * D + kc * 16 + 4 * tig) * 2);
+        qa[kc][0] = x.x;
+        qa[kc][1] = x.y;
+      }
+      // order these reads before the next segment's bulk copy (async proxy) into the slot
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.q_empty[qs]);
+      ++q_n;
+      cq = row_to_f16<KC>(qa, a.f16 != 0) * a.scale_log2;
+#pragma unroll
+      for (int n = 0; n < KC; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+      m_run = -INFINITY;
+      l_part = 0.f;
+      e_run = kE0;
+    }
+
+#pragma unroll
+    for (int u = 0; u < C::SUB; ++u) {
+      const int tw0 = (w * C::SUB + u) * 32;  // first token of these 32
+      if (tw0 >= count) continue;
+      // e4m3 rows past the context may hold NaN codes, which a zero weight does not remove
+      if (FMT == PA_Q8_E4M3 && tw0 + 32 > count) {
+        constexpr int CH = D / 16;
+        for (int i = lane; i < 32 * CH; i += 32) {
+          const int t = tw0 + i / CH;
+          if (t >= count)
+            *reinterpret_cast<uint4*>(Vst + row_off(t) + (i % CH) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      const uint32_t st_u = smem_base + (uint32_t)s * C::STAGE_BYTES;
+
+      // ---- S = Q K^T: four column tiles of 8 tokens --------------------------------------
+      float sc[4][2] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = tw0 + 16 * h + (lane & 7) + ((lane >> 4) << 3);
+        const uint32_t base = st_u + (uint32_t)row_off(t) + ((uint32_t)(k_hi ^ (sw & 1)) << 4);
+#pragma unroll
+        for (int p = 0; p < KC / 2; ++p) {
+          uint32_t r[4];
+          ldsm_x4(r, base + (((uint32_t)p << 5) ^ sw_hi));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // token tile 2h + i / 2, chunk 2p + i % 2
+            uint32_t b0, b1;
+            widen4<FMT, false>(r[i], b0, b1);
+            float* acc = sc[2 * h + (i >> 1)];
+            const uint32_t* q = qa[2 * p + (i & 1)];
+            mma16816<true>(acc[0], acc[1], z, q[0], q[1], b0, b1);
+          }
+        }
+      }
+      // ---- online softmax ---------------------------------------------------------------
+      float wv[4][2];  // value scales, then the weights
+      float tmax = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int t = tw0 + 8 * n + 2 * tig;
+        const float2 kf = *reinterpret_cast<const float2*>(ksc + sc_off(t));
+        const float2 vf = *reinterpret_cast<const float2*>(vsc + sc_off(t));
+        sc[n][0] = t < count ? sc[n][0] * (kf.x * cq) : -INFINITY;
+        sc[n][1] = t + 1 < count ? sc[n][1] * (kf.y * cq) : -INFINITY;
+        wv[n][0] = t < count ? vf.x : 0.f;
+        wv[n][1] = t + 1 < count ? vf.y : 0.f;
+        tmax = fmaxf(tmax, fmaxf(sc[n][0], sc[n][1]));
+      }
+      tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
+      tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
+      uint32_t vtop = 0u;  // largest value scale of the 32 tokens, as bits
+      {
+        const int t = tw0 + lane;
+        if (t < count) vtop = *reinterpret_cast<const uint32_t*>(vsc + sc_off(t)) & 0x7fffffffu;
+        vtop = __reduce_max_sync(0xffffffffu, vtop);
+      }
+      const float m_new = fmaxf(m_run, tmax);
+      // (-inf only where every score so far is -inf or NaN: a NaN then stays one)
+      const float m_ref = m_new == -INFINITY ? 0.f : m_new;
+      float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m_run - m_new);
+      m_run = m_new;
+      l_part *= alpha;
+      const int e_new = max((int)(vtop >> 23) - 127, e_run);
+      if (e_new > e_run) {
+        alpha *= e_run - e_new < -126 ? 0.f : pow2f(e_run - e_new);
+        e_run = e_new;
+      }
+      const float nu = pow2f(14 - e_run);
+      uint32_t pa[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float p0 = fast_exp2(sc[n][0] - m_ref), p1 = fast_exp2(sc[n][1] - m_ref);
+        l_part += p0 + p1;
+        pa[n] = f2_elt2<true>(p0 * (wv[n][0] * nu), p1 * (wv[n][1] * nu));
+      }
+      if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+        for (int n = 0; n < KC; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][e] *= alpha;
+      }
+      // ---- O += W V: two blocks of 16 tokens ----------------------------------------------
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = tw0 + 16 * h + (lane & 7) + (((lane >> 3) & 1) << 3);
+        const uint32_t base =
+            st_u + C::KV_BYTES + (uint32_t)row_off(t) + ((uint32_t)(v_hi ^ (sw & 1)) << 4);
+#pragma unroll
+        for (int p = 0; p < KC / 2; ++p) {
+          uint32_t r[4];
+          ldsm_x4_t(r, base + (((uint32_t)p << 5) ^ sw_hi));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {  // chunk 2p + i: tokens 0..7 in r[2i], 8..15 in r[2i + 1]
+            uint32_t e0, o0, e1, o1;
+            widen4<FMT, true>(r[2 * i], e0, o0);
+            widen4<FMT, true>(r[2 * i + 1], e1, o1);
+            float* acc = o[2 * p + i];
+            mma16816<true>(acc[0], acc[2], z, pa[2 * h], pa[2 * h + 1], e0, e1);
+            mma16816<true>(acc[1], acc[3], z, pa[2 * h], pa[2 * h + 1], o0, o1);
+          }
+        }
+      }
+    }
+
+    if (meta.flags & kFlagLast) {
+      // ---- finalize the segment: from the warp's reference scale back to the values' ------
+      const float back = pow2f(e_run - 14);
+#pragma unroll
+      for (int n = 0; n < KC; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][e] *= back;
+      float l_all = l_part;
+      l_all += __shfl_xor_sync(0xffffffffu, l_all, 1);
+      l_all += __shfl_xor_sync(0xffffffffu, l_all, 2);
+      // several warps per KV head: merge their softmax states through the stage's K/V
+      // shared memory once every consumer warp is done with it
+      if constexpr (C::WPH > 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.seg_bar);
+        if (!mbar_wait(&ctl.seg_bar, (uint32_t)(seg_count & 1), abort_flag)) gave_up();
+      }
+      float* merge = reinterpret_cast<float*>(Kst) + (size_t)j * (C::WPH - 1) * C::MERGE_FLOATS;
+      if (w != 0) {
+        float* mine = merge + (size_t)(w - 1) * C::MERGE_FLOATS;
+        if (row_ok) {
+#pragma unroll
+          for (int n = 0; n < KC; ++n)
+            *reinterpret_cast<float4*>(mine + gid * D + n * 16 + 4 * tig) =
+                make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
+          if (tig == 0) {
+            mine[kTcGMax * D + gid] = m_run;
+            mine[kTcGMax * D + kTcGMax + gid] = l_all;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.merge_bar[j]);
+      } else {
+        if constexpr (C::WPH > 1) {
+          if (!mbar_wait(&ctl.merge_bar[j], (uint32_t)(seg_count & 1), abort_flag)) gave_up();
+        }
+        for (int w2 = 1; w2 < C::WPH; ++w2) {
+          const float* other = merge + (size_t)(w2 - 1) * C::MERGE_FLOATS;
+          if (row_ok) {
+            const float m2 = other[kTcGMax * D + gid];
+            const float l2 = other[kTcGMax * D + kTcGMax + gid];
+            const float mm = fmaxf(m_run, m2);
+            // (a state without scores, or with NaN alone, keeps what it has: 0 or NaN)
+            const float a1 = m_run == mm ? 1.f : fast_exp2(m_run - mm);
+            const float a2 = m2 == mm ? 1.f : fast_exp2(m2 - mm);
+#pragma unroll
+            for (int n = 0; n < KC; ++n) {
+              const float4 ov = *reinterpret_cast<const float4*>(other + gid * D + n * 16 + 4 * tig);
+              o[n][0] = o[n][0] * a1 + ov.x * a2;
+              o[n][1] = o[n][1] * a1 + ov.y * a2;
+              o[n][2] = o[n][2] * a1 + ov.z * a2;
+              o[n][3] = o[n][3] * a1 + ov.w * a2;
+            }
+            l_all = l_all * a1 + l2 * a2;
+            m_run = mm;
+          }
+        }
+        // normalise and write the rows, or the partials for the combine (a NaN sum stays NaN)
+        const int b = meta.b;
+        const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
+        if (meta.flags & kFlagWhole) {
+          if (row_ok) {
+            uint16_t* dst = static_cast<uint16_t*>(a.out) + ((int64_t)b * H + kvh * G + gid) * D;
+#pragma unroll
+            for (int n = 0; n < KC; ++n) {
+              const float r[4] = {o[n][0] * inv, o[n][1] * inv, o[n][2] * inv, o[n][3] * inv};
+              *reinterpret_cast<uint2*>(dst + n * 16 + 4 * tig) =
+                  a.f16 ? make_uint2(f2_elt2<true>(r[0], r[1]), f2_elt2<true>(r[2], r[3]))
+                        : make_uint2(f2_elt2<false>(r[0], r[1]), f2_elt2<false>(r[2], r[3]));
+            }
+          }
+        } else {
+          const int slot = (x0 < meta.pb) ? 1 : 0;
+          if (row_ok) {
+            const int hg = kvh * G + gid;
+            float* dst = a.part_o + (((int64_t)c * 2 + slot) * H + hg) * D;
+#pragma unroll
+            for (int n = 0; n < KC; ++n)
+              *reinterpret_cast<float4*>(dst + n * 16 + 4 * tig) =
+                  make_float4(o[n][0] * inv, o[n][1] * inv, o[n][2] * inv, o[n][3] * inv);
+            if (tig == 0)
+              a.part_lse[((int64_t)c * 2 + slot) * H + hg] =
+                  l_all == 0.f ? -INFINITY : m_run + fast_log2(l_all);
+          }
+          __threadfence();
+          __syncwarp();
+          int old = 0;
+          int* counter = a.counters + (int64_t)b * Hk + kvh;
+          if (lane == 0) old = atomicAdd(counter, 1);
+          old = __shfl_sync(0xffffffffu, old, 0);
+          const int64_t c_lo = cta_of(meta.pb, NT, g_eff);
+          const int64_t c_hi = cta_of(meta.pb + meta.nb - 1, NT, g_eff);
+          const int nseg = (int)(c_hi - c_lo + 1);
+          if (old == nseg - 1) {  // last arrival: combine the partials of sequence b in CTA order
+            __threadfence();
+            if (a.f16)
+              combine_partials<D, true, kTcGMax>(a, b, kvh, G, c_lo, nseg, NT, g_eff, meta.pb, lane);
+            else
+              combine_partials<D, false, kTcGMax>(a, b, kvh, G, c_lo, nseg, NT, g_eff, meta.pb, lane);
+            if (lane == 0) *counter = 0;  // leave the counter zero for the next call
+          }
+        }
+      }
+      ++seg_count;
+      fence_proxy_async_smem();
+    }
+    // order this tile's shared-memory reads before the producer's next copy into the stage
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl.empty[s]);
+  }
+}
+
+template <int HS, int D, int FMT>
+int launch_decode_q8_t(DecodeQ8Args a, const DeviceInfo& info, cudaStream_t stream) {
+  using C = Q8Cfg<HS, D>;
+  static std::atomic<bool> attr_done[64];  // zero-initialised: false
+  const int dev = info.device;
+  if (dev < 0 || dev >= 64) return PA_ERR_CUDA;
+  if (!attr_done[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(paged_decode_q8_kernel<HS, D, FMT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
+      return PA_ERR_CUDA;
+    attr_done[dev].store(true, std::memory_order_release);
+  }
+  int tb = tc_box_tokens(a.block_size, C::T);
+  if (tb > 256) tb = 256;  // a box's largest extent
+  Q8Maps tm;
+  memset(&tm, 0, sizeof(tm));
+  if (tb > 0 &&
+      (!make_codes_map(&tm.k, a.k_cache, a.num_kv_heads, D, a.block_size, a.num_blocks, tb, HS) ||
+       !make_codes_map(&tm.v, a.v_cache, a.num_kv_heads, D, a.block_size, a.num_blocks, tb, HS) ||
+       !make_scales_map(&tm.ks, a.k_scale, a.num_kv_heads, a.block_size, a.num_blocks, tb, HS) ||
+       !make_scales_map(&tm.vs, a.v_scale, a.num_kv_heads, a.block_size, a.num_blocks, tb, HS)))
+    return PA_ERR_CUDA;
+  const dim3 grid((unsigned)a.grid_ctas, (unsigned)(a.num_kv_heads / HS));
+  if (launch_dependent(paged_decode_q8_kernel<HS, D, FMT>, grid, dim3(kThreads), C::SMEM, stream,
+                       tm, a, tb) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+template <int D, int FMT>
+int dispatch_slab_q8(const DecodeQ8Args& a, const DeviceInfo& info, cudaStream_t stream) {
+  switch (decode_head_slab(a.num_kv_heads)) {
+    case 8: return launch_decode_q8_t<8, D, FMT>(a, info, stream);
+    case 4: return launch_decode_q8_t<4, D, FMT>(a, info, stream);
+    case 2: return launch_decode_q8_t<2, D, FMT>(a, info, stream);
+    default: return launch_decode_q8_t<1, D, FMT>(a, info, stream);
+  }
+}
+
+}  // namespace
+}  // namespace pa

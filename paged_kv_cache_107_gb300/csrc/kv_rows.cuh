@@ -1,0 +1,286 @@
+// kv_rows.cuh — the rows of new tokens on their way into a cache: rotary positions, 8-bit
+// quantisation, the scatter by slot. store_q8.cu and rotary_store_*.cu instantiate it.
+//
+// A head's D dims are D/16 units of 16, one for each of the lanes that hold the head: a unit is
+// two vectors of 8 elements, chosen so that both dims of a rotated pair lie in one lane (vectors
+// u and u + R/16 for pairs R/2 apart, 2u and 2u + 1 for neighbours and for what passes
+// through). A warp moves 32 / (D/16) heads of one token at a time and loads kRowsUnroll such
+// groups before it uses the first: one work item, up to 16 heads at head_dim 128, 32 at 64. The
+// items of all tokens are dealt to the warps in turn. The kernel moves bytes: 16 in flight for
+// each lane and vector.
+//
+// Angles: position times the frequency's 64-bit fraction of a turn, modulo 2^64, is the angle
+// without its whole turns; its top 32 bits go to sincospi in fp32. Far positions cost no
+// accuracy. A lane computes two frequencies and the unit's eight come by shuffles.
+//
+// Quantisation: the row's largest magnitude from the 16-bit patterns, whose order without the
+// sign is that of the magnitudes (infinities and NaN above all), two at a time.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dependent_launch.cuh"
+#include "pa_device.cuh"
+#include "pa_launch.h"
+#include "q8.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kRowsUnroll = 4;   // head groups a warp loads before it uses the first
+constexpr int kRowsThreads = 256;
+constexpr int kRowsBlocksPerSM = 3;  // resident blocks per SM (register budget)
+
+// Eight 16-bit elements, by one 16-byte access or by elements. (Plain loads: q may be turned in
+// place.)
+__device__ __forceinline__ uint4 ld_vec8(const uint16_t* p, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4*>(p);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void st_vec8(uint16_t* p, const uint4& v, bool vec) {
+  if (vec) {
+    *reinterpret_cast<uint4*>(p) = v;
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    p[2 * i] = (uint16_t)(w[i] & 0xffffu);
+    p[2 * i + 1] = (uint16_t)(w[i] >> 16);
+  }
+}
+
+template <bool F16>
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+  if constexpr (F16) {
+    return f16x2_f2(w);
+  } else {
+    float2 f;
+    bf16x2_to_f32(w, f.x, f.y);
+    return f;
+  }
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+  if constexpr (F16) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  } else {
+    return f32x2_to_bf16x2(lo, hi);
+  }
+}
+
+// The unit's pairs (vectors a and b of 8 elements) turned by cos, sin of its eight frequencies.
+template <bool F16, bool ADJ>
+__device__ __forceinline__ void turn_unit(uint4& va, uint4& vb, const float (&c)[8],
+                                          const float (&s)[8]) {
+  uint32_t* a = reinterpret_cast<uint32_t*>(&va);
+  uint32_t* b = reinterpret_cast<uint32_t*>(&vb);
+  if constexpr (ADJ) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t& w = i < 4 ? a[i & 3] : b[i & 3];
+      const float2 x = widen2<F16>(w);
+      w = narrow2<F16>(x.x * c[i] - x.y * s[i], x.y * c[i] + x.x * s[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = widen2<F16>(a[i]), y = widen2<F16>(b[i]);
+      a[i] = narrow2<F16>(x.x * c[2 * i] - y.x * s[2 * i],
+                          x.y * c[2 * i + 1] - y.y * s[2 * i + 1]);
+      b[i] = narrow2<F16>(y.x * c[2 * i] + x.x * s[2 * i],
+                          y.y * c[2 * i + 1] + x.y * s[2 * i + 1]);
+    }
+  }
+}
+
+// cos and sin of the token's angles: this lane's unit u holds frequencies 8u .. 8u + 7.
+template <int D>
+__device__ __forceinline__ void unit_angles(const RowsArgs& a, int64_t tok, int lane, int u,
+                                            float (&c)[8], float (&s)[8]) {
+  float cs[2], sn[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int f = 2 * lane + i;
+    cs[i] = sn[i] = 0.f;
+    if (f < a.rot.rotary_dim / 2) {
+      int axis = __ldg(a.rot.axes + f);
+      if (axis < 0 || axis >= a.rot.num_axes) {
+        set_dev_err(a.dev_err, PA_DEV_ERR_AXIS);
+        axis = 0;
+      }
+      const int64_t p = __ldg(a.positions + axis * a.pos_stride + tok);
+      const uint64_t turn = (uint64_t)p * __ldg(a.rot.turns + f);
+      float sv, cv;
+      sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &sv, &cv);  // 2^-31
+      cs[i] = cv * a.rot.amplitude;
+      sn[i] = sv * a.rot.amplitude;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    c[e] = __shfl_sync(0xffffffffu, cs[e & 1], 4 * u + (e >> 1));
+    s[e] = __shfl_sync(0xffffffffu, sn[e & 1], 4 * u + (e >> 1));
+  }
+}
+
+// FMT: 0 = 16-bit cache, else a pa_q8_format.
+template <int D, bool F16, int FMT, bool ROT, bool ADJ>
+__global__ void __launch_bounds__(kRowsThreads, kRowsBlocksPerSM) kv_rows_kernel(const RowsArgs a) {
+  constexpr int UNITS = D / 16;         // lanes of one head
+  constexpr int HPW = 32 / UNITS;       // heads a warp moves at a time
+  constexpr int U = kRowsUnroll;
+  const int lane = threadIdx.x & 31;
+  const int u = lane % UNITS, hl = lane / UNITS;
+  const int H = ROT ? a.num_heads : 0, Hk = a.num_kv_heads;
+  const int heads = H + 2 * Hk;         // q, k, v in turn
+  const int half = a.rot.rotary_dim / 16;  // vectors, and units, that hold turned dims
+  const bool turned = ROT && u < half;
+  const int va = (ROT && !ADJ && turned) ? u : 2 * u;
+  const int vb = (ROT && !ADJ && turned) ? u + half : 2 * u + 1;
+  const uint32_t chunks = (uint32_t)a.chunks;
+  const uint32_t items = (uint32_t)a.num_tokens * chunks;  // below 2^31 (the launcher)
+  const uint32_t warps = gridDim.x * (kRowsThreads / 32);
+  const bool vec = a.vec != 0;
+
+  pdl_launch_dependents();
+  pdl_wait();
+  for (uint32_t item = blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5); item < items;
+       item += warps) {
+    const int64_t tok = item / chunks;
+    const int hw = (int)(item % chunks) * (HPW * U);  // the warp's first head
+    const int h0 = hw + hl;
+    const int64_t slot = __ldg(a.slots + tok);
+    uint4 xa[U], xb[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int h = h0 + i * HPW;
+      if (h < heads) {
+        const uint16_t* row;
+        if (ROT && h < H)
+          row = static_cast<const uint16_t*>(a.q) + tok * a.q_stride + (int64_t)h * D;
+        else if (h < H + Hk)
+          row = static_cast<const uint16_t*>(a.k) + tok * a.k_stride + (int64_t)(h - H) * D;
+        else
+          row = static_cast<const uint16_t*>(a.v) + tok * a.v_stride + (int64_t)(h - H - Hk) * D;
+        xa[i] = ld_vec8(row + va * 8, vec);
+        xb[i] = ld_vec8(row + vb * 8, vec);
+      } else {
+        xa[i] = xb[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    float c[8], s[8];
+    if constexpr (ROT) {
+      // (an item of values only turns nothing)
+      if (hw < H + Hk) unit_angles<D>(a, tok, lane, u, c, s);
+    }
+    bool keep = slot != -1;
+    if (keep && (slot < 0 || slot >= a.num_slots)) {
+      if (lane == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SLOT);
+      keep = false;
+    }
+    // (slots are 32-bit numbers)
+    const uint32_t blk = keep ? (uint32_t)slot / (uint32_t)a.block_size : 0u;
+    const uint32_t off = keep ? (uint32_t)slot % (uint32_t)a.block_size : 0u;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int h = h0 + i * HPW;
+      const bool is_q = ROT && h < H, is_k = h < H + Hk;
+      if constexpr (ROT) {
+        if (turned && is_k) turn_unit<F16, ADJ>(xa[i], xb[i], c, s);
+        if (is_q) {
+          uint16_t* row = static_cast<uint16_t*>(a.q_out) + tok * a.q_out_stride + (int64_t)h * D;
+          st_vec8(row + va * 8, xa[i], vec);
+          st_vec8(row + vb * 8, xb[i], vec);
+        }
+      }
+      const int kh = is_k ? h - H : h - H - Hk;  // KV head
+      const bool write = !is_q && h < heads && keep;
+      if constexpr (FMT == 0) {
+        if (write) {
+          uint16_t* row = static_cast<uint16_t*>(is_k ? a.k_cache : a.v_cache) +
+                          (slot * Hk + kh) * D;
+          st_vec8(row + va * 8, xa[i], true);
+          st_vec8(row + vb * 8, xb[i], true);
+        }
+      } else {
+        const uint32_t* wa = reinterpret_cast<const uint32_t*>(&xa[i]);
+        const uint32_t* wb = reinterpret_cast<const uint32_t*>(&xb[i]);
+        uint32_t top = 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          top = __vmaxu2(top, wa[e] & 0x7fff7fffu);
+          top = __vmaxu2(top, wb[e] & 0x7fff7fffu);
+        }
+#pragma unroll
+        for (int m = 1; m < UNITS; m <<= 1)
+          top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, m));
+        top = max(top & 0xffffu, top >> 16);
+        const RowScale r = row_scale<FMT>(widen2<F16>(top).x);
+        const bool finite = r.scale == r.scale;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t* p = e < 2 ? wa + 2 * e : wb + 2 * (e - 2);
+          const float2 lo = widen2<F16>(p[0]), hi = widen2<F16>(p[1]);
+          w[e] = finite ? quantise4<FMT>(r, lo.x, lo.y, hi.x, hi.y) : 0u;
+        }
+        if (write) {
+          unsigned char* row = static_cast<unsigned char*>(is_k ? a.k_cache : a.v_cache) +
+                               (slot * Hk + kh) * D;
+          if (vb == va + 1) {
+            *reinterpret_cast<uint4*>(row + va * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+            *reinterpret_cast<uint2*>(row + va * 8) = make_uint2(w[0], w[1]);
+            *reinterpret_cast<uint2*>(row + vb * 8) = make_uint2(w[2], w[3]);
+          }
+          if (u == 0)
+            (is_k ? a.k_scale : a.v_scale)[((int64_t)blk * Hk + kh) * a.block_size + off] = r.scale;
+        }
+      }
+    }
+  }
+}
+
+template <int D, bool F16, int FMT, bool ROT, bool ADJ>
+int launch_rows_t(RowsArgs a, const DeviceInfo& info, cudaStream_t stream) {
+  constexpr int per_item = 32 / (D / 16) * kRowsUnroll;
+  const int64_t heads = (ROT ? a.num_heads : 0) + 2 * (int64_t)a.num_kv_heads;
+  a.chunks = (int)((heads + per_item - 1) / per_item);
+  const int64_t items = (int64_t)a.num_tokens * a.chunks;
+  if (heads > INT32_MAX - per_item || items > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  int64_t blocks = (items + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
+  const int64_t cap = (int64_t)info.num_sms * kRowsBlocksPerSM;  // one resident wave
+  if (blocks > cap) blocks = cap;
+  if (launch_dependent(kv_rows_kernel<D, F16, FMT, ROT, ADJ>, dim3((unsigned)blocks),
+                       dim3(kRowsThreads), 0, stream, a) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// Every rotary form of one head_dim and element type.
+template <int D, bool F16>
+int launch_rotary_rows_t(const RowsArgs& a, int fmt, const DeviceInfo& info, cudaStream_t stream) {
+  const bool adj = a.rot.adjacent != 0;
+  switch (fmt) {
+    case 0:
+      return adj ? launch_rows_t<D, F16, 0, true, true>(a, info, stream)
+                 : launch_rows_t<D, F16, 0, true, false>(a, info, stream);
+    case PA_Q8_E4M3:
+      return adj ? launch_rows_t<D, F16, PA_Q8_E4M3, true, true>(a, info, stream)
+                 : launch_rows_t<D, F16, PA_Q8_E4M3, true, false>(a, info, stream);
+    default:
+      return adj ? launch_rows_t<D, F16, PA_Q8_INT8, true, true>(a, info, stream)
+                 : launch_rows_t<D, F16, PA_Q8_INT8, true, false>(a, info, stream);
+  }
+}
+
+}  // namespace
+}  // namespace pa

@@ -532,3 +532,233 @@ int pa_decode_shared(void* out, const void* q, const void* k_cache, const void* 
 }
 
 }  // extern "C"
+
+namespace pa {
+
+static bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1) == 0; }
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+static int check_q8_cache(const pa_q8_cache* c) {
+  if (!c) return PA_ERR_NULL;
+  if (c->format != PA_Q8_E4M3 && c->format != PA_Q8_INT8) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+static int check_q8_pointers(const pa_q8_cache* c) {
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return PA_ERR_NULL;
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale))
+    return PA_ERR_ALIGN;
+  return PA_OK;
+}
+
+// Sizes of the paged cache that a call writes or reads by slot or block.
+static int check_cache_shape(int num_kv_heads, int head_dim, int block_size, int64_t num_blocks) {
+  if (num_kv_heads <= 0 || block_size <= 0 || num_blocks <= 0) return PA_ERR_SHAPE;
+  if (!head_dim_supported(head_dim)) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+static int check_rotary(const pa_rotary* r, int head_dim) {
+  if (!r) return PA_ERR_NULL;
+  if (r->rotary_dim < 16 || r->rotary_dim > head_dim || r->rotary_dim % 16 || r->num_axes < 1 ||
+      r->num_axes > 16 || !isfinite(r->amplitude))
+    return PA_ERR_SHAPE;
+  return PA_OK;
+}
+
+// The new tokens' rows: k and v, and with rotary q too.
+struct RowTensors {
+  void* q_out;
+  const void *q, *k, *v;
+  int64_t q_out_stride, q_stride, k_stride, v_stride;
+  int dtype;
+  const int32_t* positions;
+  int64_t pos_stride;
+  const pa_rotary* rotary;  // null: keys and values only
+  int num_heads;
+};
+
+// pa_store_kvcache_q8, pa_rotary_store (k_cache, v_cache) and pa_rotary_store_q8 (q8).
+static int rows_entry(const RowTensors& t, void* k_cache, void* v_cache, const pa_q8_cache* q8,
+                      bool to_q8, const int32_t* slot_mapping, int num_tokens, int num_kv_heads,
+                      int head_dim, int block_size, int64_t num_blocks, int* dev_err,
+                      void* stream, bool rotary) {
+  int rc = check_cache_shape(num_kv_heads, head_dim, block_size, num_blocks);
+  if (rc != PA_OK) return rc;
+  if (num_tokens < 0 || (rotary && t.num_heads <= 0)) return PA_ERR_SHAPE;
+  if (t.dtype != PA_DTYPE_BF16 && t.dtype != PA_DTYPE_F16) return PA_ERR_UNSUPPORTED;
+  if (to_q8 && (rc = check_q8_cache(q8)) != PA_OK) return rc;
+  if (rotary && (rc = check_rotary(t.rotary, head_dim)) != PA_OK) return rc;
+  const int64_t row = (int64_t)num_kv_heads * head_dim;
+  const int64_t q_row = (int64_t)t.num_heads * head_dim;
+  if (t.k_stride < row || t.v_stride < row) return PA_ERR_SHAPE;
+  if (rotary && (t.q_stride < q_row || t.q_out_stride < q_row)) return PA_ERR_SHAPE;
+  if (num_tokens == 0) return PA_OK;
+  if (!t.k || !t.v || !slot_mapping) return PA_ERR_NULL;
+  if (rotary && (!t.q || !t.q_out || !t.positions || !t.rotary->turns || !t.rotary->axes))
+    return PA_ERR_NULL;
+  if (to_q8) {
+    if ((rc = check_q8_pointers(q8)) != PA_OK) return rc;
+  } else {
+    if (!k_cache || !v_cache) return PA_ERR_NULL;
+    if (!aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_ALIGN;
+  }
+  if (!aligned2(t.k) || !aligned2(t.v) || !aligned4(slot_mapping)) return PA_ERR_ALIGN;
+  if (rotary && (!aligned2(t.q) || !aligned2(t.q_out) || !aligned4(t.positions) ||
+                 !aligned4(t.rotary->axes) ||
+                 (reinterpret_cast<uintptr_t>(t.rotary->turns) & 7)))
+    return PA_ERR_ALIGN;
+  DeviceInfo info;
+  if (!current_device_info(&info)) return PA_ERR_CUDA;
+  RowsArgs a{};
+  a.k = t.k;
+  a.v = t.v;
+  a.k_stride = t.k_stride;
+  a.v_stride = t.v_stride;
+  bool vec = aligned16(t.k) && aligned16(t.v) && t.k_stride % 8 == 0 && t.v_stride % 8 == 0;
+  if (rotary) {
+    a.q_out = t.q_out;
+    a.q = t.q;
+    a.q_out_stride = t.q_out_stride;
+    a.q_stride = t.q_stride;
+    a.positions = t.positions;
+    a.pos_stride = t.pos_stride;
+    a.rot = *t.rotary;
+    a.num_heads = t.num_heads;
+    vec = vec && aligned16(t.q) && aligned16(t.q_out) && t.q_stride % 8 == 0 &&
+          t.q_out_stride % 8 == 0;
+  }
+  a.k_cache = to_q8 ? q8->k : k_cache;
+  a.v_cache = to_q8 ? q8->v : v_cache;
+  a.k_scale = to_q8 ? q8->k_scale : nullptr;
+  a.v_scale = to_q8 ? q8->v_scale : nullptr;
+  a.slots = slot_mapping;
+  a.num_tokens = num_tokens;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_slots = num_blocks * (int64_t)block_size;
+  a.dev_err = dev_err;
+  a.vec = vec;
+  const int fmt = to_q8 ? q8->format : 0;
+  const bool f16 = t.dtype == PA_DTYPE_F16;
+  return rotary
+             ? launch_rotary_rows(a, fmt, head_dim, f16, info, static_cast<cudaStream_t>(stream))
+             : launch_store_rows(a, fmt, head_dim, f16, info, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace pa
+
+extern "C" {
+
+int pa_store_kvcache_q8(const void* k, const void* v, int64_t k_tok_stride, int64_t v_tok_stride,
+                        int dtype, const pa_q8_cache* cache, const int32_t* slot_mapping,
+                        int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                        int64_t num_blocks, int* dev_err, void* stream) {
+  pa::RowTensors t{};
+  t.k = k;
+  t.v = v;
+  t.k_stride = k_tok_stride;
+  t.v_stride = v_tok_stride;
+  t.dtype = dtype;
+  return pa::rows_entry(t, nullptr, nullptr, cache, true, slot_mapping, num_tokens, num_kv_heads,
+                        head_dim, block_size, num_blocks, dev_err, stream, false);
+}
+
+int pa_rotary_store(void* q_out, const void* q, const void* k, const void* v,
+                    int64_t q_out_tok_stride, int64_t q_tok_stride, int64_t k_tok_stride,
+                    int64_t v_tok_stride, int dtype, const int32_t* positions,
+                    int64_t pos_axis_stride, const pa_rotary* rotary, void* k_cache,
+                    void* v_cache, const int32_t* slot_mapping, int num_tokens, int num_heads,
+                    int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                    int* dev_err, void* stream) {
+  const pa::RowTensors t{q_out,        q,            k,     v,         q_out_tok_stride,
+                         q_tok_stride, k_tok_stride, v_tok_stride,
+                         dtype,        positions,    pos_axis_stride,  rotary, num_heads};
+  return pa::rows_entry(t, k_cache, v_cache, nullptr, false, slot_mapping, num_tokens,
+                        num_kv_heads, head_dim, block_size, num_blocks, dev_err, stream, true);
+}
+
+int pa_rotary_store_q8(void* q_out, const void* q, const void* k, const void* v,
+                       int64_t q_out_tok_stride, int64_t q_tok_stride, int64_t k_tok_stride,
+                       int64_t v_tok_stride, int dtype, const int32_t* positions,
+                       int64_t pos_axis_stride, const pa_rotary* rotary,
+                       const pa_q8_cache* cache, const int32_t* slot_mapping, int num_tokens,
+                       int num_heads, int num_kv_heads, int head_dim, int block_size,
+                       int64_t num_blocks, int* dev_err, void* stream) {
+  const pa::RowTensors t{q_out,        q,            k,     v,         q_out_tok_stride,
+                         q_tok_stride, k_tok_stride, v_tok_stride,
+                         dtype,        positions,    pos_axis_stride,  rotary, num_heads};
+  return pa::rows_entry(t, nullptr, nullptr, cache, true, slot_mapping, num_tokens, num_kv_heads,
+                        head_dim, block_size, num_blocks, dev_err, stream, true);
+}
+
+uint64_t pa_rotary_turns(double inv_freq) {
+  // 1 / (2 pi) in 192 binary places, most significant word first
+  constexpr uint64_t kInv2Pi[3] = {0x28be60db9391054aull, 0x7f09d5f47d4d3770ull,
+                                   0x36d8a5664f10e410ull};
+  if (!isfinite(inv_freq) || fabs(inv_freq) > 0x1p40) return 0;
+  int x = 0;
+  const uint64_t m = (uint64_t)ldexp(frexp(fabs(inv_freq), &x), 53);  // |inv_freq| = m 2^(x-53)
+  // m / (2 pi) with 192 places, least significant word first
+  uint64_t p[4];
+  unsigned __int128 carry = 0;
+  for (int i = 0; i < 3; ++i) {
+    carry += (unsigned __int128)m * kInv2Pi[2 - i];
+    p[i] = (uint64_t)carry;
+    carry >>= 64;
+  }
+  p[3] = (uint64_t)carry;
+  // times 2^(x-53), 64 places kept: shift right by 192 - 64 - (x - 53), at least 140
+  const int shift = 181 - x;
+  if (shift >= 256) return 0;
+  auto bit = [&](int i) { return i < 256 ? p[i >> 6] >> (i & 63) & 1 : 0; };
+  uint64_t r = bit(shift - 1);  // rounds
+  for (int i = 0; i < 64; ++i) r += bit(shift + i) << i;
+  return inv_freq < 0 ? 0 - r : r;
+}
+
+int pa_load_kvcache_q8(void* k_out, void* v_out, int dtype, const pa_q8_cache* cache,
+                       const int32_t* blocks, int num_listed, int num_kv_heads, int head_dim,
+                       int block_size, int64_t num_blocks, int* dev_err, void* stream) {
+  int rc = pa::check_cache_shape(num_kv_heads, head_dim, block_size, num_blocks);
+  if (rc != PA_OK) return rc;
+  if (num_listed < 0) return PA_ERR_SHAPE;
+  if (dtype != PA_DTYPE_BF16 && dtype != PA_DTYPE_F16) return PA_ERR_UNSUPPORTED;
+  if ((rc = pa::check_q8_cache(cache)) != PA_OK) return rc;
+  if ((int64_t)block_size * num_kv_heads > INT32_MAX / 2) return PA_ERR_UNSUPPORTED;
+  if (num_listed == 0) return PA_OK;
+  if (!k_out || !v_out || !blocks) return PA_ERR_NULL;
+  if ((rc = pa::check_q8_pointers(cache)) != PA_OK) return rc;
+  if (!pa::aligned16(k_out) || !pa::aligned16(v_out) || !pa::aligned4(blocks)) return PA_ERR_ALIGN;
+  pa::DeviceInfo info;
+  if (!pa::current_device_info(&info)) return PA_ERR_CUDA;
+  const pa::LoadQ8Args a{k_out,          v_out,  cache->k,   cache->v,     cache->k_scale,
+                         cache->v_scale, blocks, num_listed, num_kv_heads, block_size,
+                         num_blocks,     dev_err};
+  return pa::launch_load_q8(a, cache->format, head_dim, dtype == PA_DTYPE_F16, info,
+                            static_cast<cudaStream_t>(stream));
+}
+
+int pa_decode_q8(void* out, const void* q, const pa_q8_cache* cache, const int32_t* block_tables,
+                 int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                 int num_heads, int num_kv_heads, int head_dim, int dtype, int block_size,
+                 int64_t num_blocks, float scale, int grid_ctas, void* workspace,
+                 size_t workspace_bytes, int* dev_err, void* stream) {
+  int rc = pa::check_q8_cache(cache);
+  if (rc != PA_OK) return rc;
+  pa::DecodeQ8Args a;
+  pa::DeviceInfo info;
+  bool nothing = false;
+  if (num_seqs > 0 && (rc = pa::check_q8_pointers(cache)) != PA_OK) return rc;
+  rc = pa::decode_prepare(out, q, cache->k, cache->v, block_tables, max_blocks_per_seq,
+                          context_lens, num_seqs, num_heads, num_kv_heads, head_dim, dtype,
+                          block_size, num_blocks, scale, grid_ctas, dev_err, nullptr, &a, &info,
+                          &nothing);
+  if (rc != PA_OK || nothing) return rc;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  rc = pa::decode_check_workspace(&a, info, workspace, workspace_bytes);
+  if (rc != PA_OK) return rc;
+  return pa::launch_decode_q8(a, cache->format, info, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

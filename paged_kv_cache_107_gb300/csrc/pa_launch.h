@@ -262,6 +262,59 @@ struct PrefillModArgs : PrefillArgs {
   ScoreModArgs mod;
 };
 
+// pa_store_kvcache_q8, pa_rotary_store, pa_rotary_store_q8: the rows of new tokens on their way
+// into a cache.
+struct RowsArgs {
+  void* q_out;  // rotary calls only, as q
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_out_stride, q_stride, k_stride, v_stride;  // elements between tokens
+  const int32_t* positions;
+  int64_t pos_stride;  // elements between axes
+  pa_rotary rot;
+  void* k_cache;  // 16-bit rows or codes
+  void* v_cache;
+  float* k_scale;  // 8-bit caches
+  float* v_scale;
+  const int32_t* slots;
+  int num_tokens;
+  int num_heads;  // of q; 0 = no rotation
+  int num_kv_heads;
+  int block_size;
+  int64_t num_slots;
+  int* dev_err;
+  int vec;     // 1: q, q_out, k, v and their strides allow 16-byte vectors
+  int chunks;  // warps that share a token's heads (set by the launcher)
+};
+// fmt: 0 = 16-bit cache, else a pa_q8_format.
+int launch_store_rows(const RowsArgs& a, int fmt, int head_dim, bool f16, const DeviceInfo& info,
+                      cudaStream_t stream);
+int launch_rotary_rows(const RowsArgs& a, int fmt, int head_dim, bool f16, const DeviceInfo& info,
+                       cudaStream_t stream);
+
+struct LoadQ8Args {
+  void *k_out, *v_out;
+  const void *k_codes, *v_codes;
+  const float *k_scale, *v_scale;
+  const int32_t* blocks;
+  int num_listed;
+  int num_kv_heads;
+  int block_size;
+  int64_t num_blocks;
+  int* dev_err;
+};
+int launch_load_q8(const LoadQ8Args& a, int fmt, int head_dim, bool f16, const DeviceInfo& info,
+                   cudaStream_t stream);
+
+// pa_decode_q8: the decode over an 8-bit cache (k_cache, v_cache: codes; f16 is the type of q
+// and out).
+struct DecodeQ8Args : DecodeArgs {
+  const float* k_scale;
+  const float* v_scale;
+};
+int launch_decode_q8(const DecodeQ8Args& a, int fmt, const DeviceInfo& info, cudaStream_t stream);
+
 bool prefill_supported(int num_heads, int num_kv_heads, int block_size);
 int launch_prefill(const PrefillArgs& a, const DeviceInfo& info, cudaStream_t stream);
 int launch_prefill_mod(const PrefillModArgs& a, const DeviceInfo& info, cudaStream_t stream);

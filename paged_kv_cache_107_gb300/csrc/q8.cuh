@@ -1,0 +1,107 @@
+// q8.cuh — 8-bit codes (pa_q8_format): widening, and the quantisation of a row.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pa_device.cuh"
+
+namespace pa {
+
+// Four codes of a word to fp16, exactly: codes (0, 1) and (2, 3), or (0, 2) and (1, 3) with
+// STRIDED. E4M3 converts in hardware; an int8 code x sits in the low byte of the fp16 number
+// 1024 + (x + 128), 1152 is taken off.
+template <int FMT, bool STRIDED>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
+  if constexpr (FMT == PA_Q8_E4M3) {
+    if constexpr (STRIDED) w = __byte_perm(w, 0u, 0x3120);
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(w));
+  } else {
+    w ^= 0x80808080u;
+    a = __byte_perm(w, 0x64646464u, STRIDED ? 0x4240 : 0x4140);
+    b = __byte_perm(w, 0x64646464u, STRIDED ? 0x4341 : 0x4342);
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(a) : "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(b) : "r"(0x64806480u));
+  }
+}
+
+// fp16 pair to fp32, exactly.
+__device__ __forceinline__ float2 f16x2_f2(uint32_t w) {
+  float2 f;
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(w));
+  return f;
+}
+
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+
+// A row's scale, and what its elements are multiplied with, from the row's largest magnitude.
+// E4M3: mul = 1 / scale, both powers of two. INT8: with 2^E the exponent of t, mul = 127 * 2^-E
+// and inv = 1 / (t * 2^-E), so that 127 x / t = (x mul) / (t 2^-E) stays in range for every t.
+struct RowScale {
+  float scale, mul, t, inv;
+};
+
+template <int FMT>
+__device__ __forceinline__ RowScale row_scale(float top) {
+  RowScale r{0.f, 0.f, 1.f, 1.f};
+  const uint32_t u = __float_as_uint(top);
+  if (u >= 0x7f800000u) {  // a NaN or an infinity in the row: codes 0, scale NaN
+    r.scale = __uint_as_float(0x7fc00000u);
+    return r;
+  }
+  if (u == 0u) return r;
+  if constexpr (FMT == PA_Q8_E4M3) {
+    // 448 = 1.75 * 2^8
+    const int e = max((int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
+    r.scale = pow2f(e);
+    r.mul = pow2f(-e);
+  } else {
+    const float t = fmaxf(top, 127.f * 1.17549435e-38f);
+    const int e = (int)(__float_as_uint(t) >> 23) - 127;  // -120 .. 127
+    r.scale = __fdiv_rn(t, 127.f);
+    r.mul = __int_as_float(((133 - e) << 23) | 0x7e0000);  // 127 / 64 * 2^(6 - e)
+    r.t = __uint_as_float((__float_as_uint(t) & 0x7fffffu) | 0x3f800000u);
+    r.inv = __frcp_rn(r.t);
+  }
+  return r;
+}
+
+// Four codes of a row, packed. A row with a NaN or an infinity has mul = 0 and gets codes 0 by
+// the caller (0 * infinity would be NaN).
+//
+// INT8: n = x mul is exact (7 bits by 11 at most), q0 = n inv has a relative error of 2^-23, and
+// the remainder n - q0 t, exact in one multiply-add, corrects it to 2^-46 before the last
+// rounding. Where the quotient is a tie (an integer and a half, a number of fp32) that rounding
+// gives it exactly; where it is none, it lies at least 2^-21 of itself from the next tie (a
+// quotient of two 11-bit numbers, times 127), which one rounding of 2^-24 does not cross. So the
+// integer rounding after it, an addition of 1.5 * 2^23, goes the way of the exact quotient.
+template <int FMT>
+__device__ __forceinline__ uint32_t quantise4(const RowScale& r, float x0, float x1, float x2,
+                                              float x3) {
+  if constexpr (FMT == PA_Q8_E4M3) {
+    uint32_t w;
+    asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(w)
+        : "f"(x0 * r.mul), "f"(x1 * r.mul), "f"(x2 * r.mul), "f"(x3 * r.mul));
+    return w;
+  } else {
+    uint32_t c[4];
+    const float x[4] = {x0, x1, x2, x3};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float n = x[i] * r.mul;
+      const float q0 = n * r.inv;
+      const float q = fmaf(fmaf(-q0, r.t, n), r.inv, q0);
+      c[i] = __float_as_uint(q + 12582912.f);
+    }
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+  }
+}
+
+}  // namespace pa

@@ -19,6 +19,17 @@ PFN_cuTensorMapEncodeTiled_v12000 tmap_encode_fn();
 bool make_slab_map(CUtensorMap* map, const void* base, int num_kv_heads, int head_dim, bool f16,
                    int block_size, int64_t num_blocks, int box_tokens, int box_heads);
 
+// The same over a cache of 1-byte codes: a box of head_dim bytes x box_tokens tokens x box_heads
+// heads lands as [head][token][head_dim bytes], 128-byte rows with the 128-byte swizzle, or
+// 64-byte rows with the 64-byte one (chunk c of row r at chunk c ^ (r / 2 % 4)).
+bool make_codes_map(CUtensorMap* map, const void* base, int num_kv_heads, int head_dim,
+                    int block_size, int64_t num_blocks, int box_tokens, int box_heads);
+
+// A 3-D map over the scales [num_blocks, num_kv_heads, block_size] in fp32 of such a cache,
+// walked as (token in block, KV head, block): a box lands as [head][token].
+bool make_scales_map(CUtensorMap* map, const float* base, int num_kv_heads, int block_size,
+                     int64_t num_blocks, int box_tokens, int box_heads);
+
 // A 3-D map over a [rows, num_heads, head_dim] tensor of 16-bit elements (q or out of the
 // prefill), walked as (dim, head, row): a box of 64 dims x box_heads heads x box_rows rows
 // lands in shared memory as [row][head][64 dims], 128-byte rows with the 128-byte swizzle.
