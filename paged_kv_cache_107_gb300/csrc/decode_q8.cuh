@@ -9,20 +9,24 @@
 //  * A code is half as many bytes, so a stage of 64 KB holds twice the tokens, and every byte has
 //    to be widened: e4m3 by the hardware's conversion to fp16 (exact), int8 by placing the byte
 //    in an fp16 number (q8.cuh). Nothing is widened in shared memory: a register of four codes
-//    becomes the two fp16 words of one MMA operand.
-//    K: the operand's columns are tokens and its rows dims. ldmatrix gives a lane four
-//    consecutive dims of a token; the lane's two words take dims 4i, 4i+1 and 4i+2, 4i+3, so the
-//    products pair with queries loaded in the same order.
-//    V: rows are tokens, columns dims. The transposing ldmatrix moves 16-bit pieces, so a
-//    register holds dims 2i, 2i+1 of two tokens; its even and its odd bytes are the operands
-//    of two products, one for the even dims, one for the odd ones.
-//  * The K scale multiplies the score column. The V scale is taken into the probability, which
-//    is then rounded to fp16: w_t = p_t vs_t 2^(14-E), E the exponent of the largest vs met so
-//    far by the warp (when it grows the accumulators are rescaled), so that w < 2^15 and what is
-//    rounded off lies 2^-39 below the largest scale or 2^-11 below w itself.
-//  * bf16 queries go to fp16 with a power of two for each row (row_to_f16 below).
-//  * A warp takes 32 tokens at a time: the maximum, the exponentials and the shuffles are spread
-//    over twice the bytes of the 16-bit kernel's.
+//    becomes two fp16 words of an MMA operand.
+//  * Both products are taken transposed, S^T = K Q^T and O^T = V^T W^T: 16 tokens, or 16 dims, are
+//    the 16 rows of an MMA and the up to 8 heads of a group its 8 columns, so that no row is
+//    padding (with the heads as rows half of them are, and every byte is multiplied twice).
+//    K: ldmatrix gives a lane four consecutive dims of a token; its two words stand for dims 4i,
+//    4i+1 and 4i+2, 4i+3, and the queries are loaded in the same order.
+//    V: the transposing ldmatrix moves 16-bit pieces, so a register holds dims 2i, 2i+1 of two
+//    tokens. Its even bytes are a word of row i, its odd bytes of row i + 8: row r of a chunk
+//    of 16 dims is dim 2 (r mod 8) + r / 8.
+//    W: a warp's weights (token by head) become the second product's operand (head by token)
+//    with movmatrix.
+//  * A lane holds four tokens' scores of two heads. The running maximum is moved only when some
+//    score of the 32 tokens exceeds it (one vote): most steps need no shuffle and no rescaling.
+//  * The K scale multiplies the score. The V scale is taken into the weight, which is then rounded
+//    to fp16: w_t = p_t vs_t 2^(14-E), E the exponent of the largest vs met so far by the warp
+//    (when it grows the accumulators are rescaled), so that w < 2^15 and what is rounded off
+//    lies 2^-39 below the largest scale or 2^-11 below w itself.
+//  * bf16 queries go to fp16 with a power of two for each head (row_to_f16 below).
 //  * Scales come beside the codes, [head][token] of each box, by TMA; their slots are padded to
 //    128 bytes (a TMA destination's alignment).
 #pragma once
@@ -55,6 +59,28 @@ struct Q8Cfg {
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 
+// D (16x8) += A (16x16) B (16x8), fp16 operands, fp32 accumulators.
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// An 8x8 matrix of 16-bit elements held by the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// The combine of decode_kernel.cuh, out of line: its registers are not the main loop's.
+template <int D, bool F16>
+__device__ __noinline__ void combine_q8(const DecodeArgs& a, int b, int kvh, int G, int64_t c_lo,
+                                        int nseg, int64_t NT, int g_eff, int64_t pb, int lane) {
+  combine_partials<D, F16, kTcGMax>(a, b, kvh, G, c_lo, nseg, NT, g_eff, pb, lane);
+}
+
 // One 3-D TMA box into shared memory.
 __device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, int c0, int c1,
                                                  int c2, uint64_t* bar, uint64_t policy) {
@@ -74,10 +100,10 @@ struct Q8Maps {
   CUtensorMap k, v, ks, vs;
 };
 
-// A lane's part of a query row, dims 16c + 4 tig .. + 3 of every chunk c, as fp16. bf16 rows are
-// scaled by 2^(14-e), e the exponent of the row's largest magnitude (at least -112): exact but for
-// elements 2^28 and more below that largest. The row sits in the four lanes of a quad. Returns
-// the factor that undoes it.
+// A lane's part of a query, dims 16c + 4 tig .. + 3 of every chunk c, as fp16. bf16 queries are
+// scaled by 2^(14-e), e the exponent of the query's largest magnitude (at least -112): exact but
+// for elements 2^28 and more below that largest. The query sits in the four lanes of a quad.
+// Returns the factor that undoes it.
 template <int KC>
 __device__ __forceinline__ float row_to_f16(uint32_t (&qa)[KC][2], bool f16) {
   if (f16) return 1.f;
@@ -386,17 +412,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int w = warp % C::WPH;    // token group within the tile
   const int kvh = slab * HS + j;  // global KV head
   const int gid = lane >> 2, tig = lane & 3;
-  const bool row_ok = gid < G;
   constexpr int KC = D / 16;      // chunks of 16 dims
-  uint32_t qa[KC][2];             // Q of row gid: dims 16 kc + 4 tig, +1 and +2, +3
-  float o[KC][4];                 // O of row gid: dims 16 kc + 4 tig .. + 3
-  float2 z = make_float2(0.f, 0.f);  // accumulators of the padding rows (never read)
-  float m_run = -INFINITY, l_part = 0.f;  // row gid: running max (log2 units), partial sum
-  float cq = 0.f;                 // row gid: c over the power of two in its fp16 queries
+  uint32_t qa[KC][2];             // Q of head gid: dims 16 kc + 4 tig, +1 and +2, +3
+  // O of heads 2 tig, 2 tig + 1: dims 16 kc + 2 gid (elements 0, 1), 16 kc + 2 gid + 1 (2, 3)
+  float o[KC][4];
+  // of heads 2 tig, + 1: running max (log2 units), the same but 0 while it is -inf, this lane's
+  // part of the sum, c over the power of two in the fp16 queries
+  float m_run[2], m_ref[2], l_part[2], cq[2];
   constexpr int kE0 = -112;
   int e_run = kE0;                // exponent of the largest value scale so far
+  auto reset = [&]() {
 #pragma unroll
-  for (int n = 0; n < KC; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    for (int n = 0; n < KC; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      m_run[i] = -INFINITY;
+      m_ref[i] = l_part[i] = 0.f;
+    }
+    e_run = kE0;
+  };
+  cq[0] = cq[1] = 0.f;
+  reset();
 
   // row (token t of head j) of a code tile, and its scale
   auto row_off = [&](int t) -> int {
@@ -408,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // chunk ch of a row sits at chunk ch ^ sw; a lane's ldmatrix row has the same sw everywhere
   const int sw = D == 128 ? lane & 7 : (lane >> 1) & 3;
   const uint32_t sw_hi = (uint32_t)(sw & 6) << 4;
-  const int k_hi = (lane >> 3) & 1, v_hi = lane >> 4;  // which of a pair of chunks
+  const int hi = lane >> 4;  // which of a pair of chunks this lane's ldmatrix row is of
   const uint32_t smem_base = smem_u32(smem);
 
   int seg_count = 0;
@@ -430,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int kc = 0; kc < KC; ++kc) {
         uint2 x = make_uint2(0u, 0u);
-        if (row_ok)
+        if (gid < G)
           x = *reinterpret_cast<const uint2*>(Qst + ((j * G + gid) * D + kc * 16 + 4 * tig) * 2);
         qa[kc][0] = x.x;
         qa[kc][1] = x.y;
@@ -440,12 +476,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.q_empty[qs]);
       ++q_n;
-      cq = row_to_f16<KC>(qa, a.f16 != 0) * a.scale_log2;
-#pragma unroll
-      for (int n = 0; n < KC; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-      m_run = -INFINITY;
-      l_part = 0.f;
-      e_run = kE0;
+      // (not 0: masked scores are -inf)
+      const float c_gid = fmaxf(row_to_f16<KC>(qa, a.f16 != 0) * a.scale_log2, 1.4e-45f);
+      cq[0] = __shfl_sync(0xffffffffu, c_gid, 8 * tig);
+      cq[1] = __shfl_sync(0xffffffffu, c_gid, 8 * tig + 4);
+      reset();
     }
 
 #pragma unroll
@@ -465,91 +500,113 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t st_u = smem_base + (uint32_t)s * C::STAGE_BYTES;
 
-      // ---- S = Q K^T: four column tiles of 8 tokens --------------------------------------
-      float sc[4][2] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+      // scales of this lane's tokens tw0 + 8 i + gid, asked for before the product
+      float kf[4], vf[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = sc_off(tw0 + 8 * i + gid);
+        kf[i] = *reinterpret_cast<const float*>(ksc + at);
+        vf[i] = *reinterpret_cast<const float*>(vsc + at);
+      }
+      // ---- S^T = K Q^T: two row tiles of 16 tokens; element 2 i + e: token 8 i + gid of the
+      // tile, head 2 tig + e
+      float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int t = tw0 + 16 * h + (lane & 7) + ((lane >> 4) << 3);
-        const uint32_t base = st_u + (uint32_t)row_off(t) + ((uint32_t)(k_hi ^ (sw & 1)) << 4);
+        const int t = tw0 + 16 * h + (lane & 7) + (((lane >> 3) & 1) << 3);
+        const uint32_t base = st_u + (uint32_t)row_off(t) + ((uint32_t)(hi ^ (sw & 1)) << 4);
 #pragma unroll
         for (int p = 0; p < KC / 2; ++p) {
-          uint32_t r[4];
+          uint32_t r[4];  // chunk 2p: tokens 0..7, 8..15; chunk 2p + 1
           ldsm_x4(r, base + (((uint32_t)p << 5) ^ sw_hi));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // token tile 2h + i / 2, chunk 2p + i % 2
-            uint32_t b0, b1;
-            widen4<FMT, false>(r[i], b0, b1);
-            float* acc = sc[2 * h + (i >> 1)];
-            const uint32_t* q = qa[2 * p + (i & 1)];
-            mma16816<true>(acc[0], acc[1], z, q[0], q[1], b0, b1);
+          for (int i = 0; i < 2; ++i) {
+            uint32_t a0, a1, a2, a3;
+            widen4<FMT, false>(r[2 * i], a0, a2);
+            widen4<FMT, false>(r[2 * i + 1], a1, a3);
+            mma_f16(sc[h], a0, a1, a2, a3, qa[2 * p + i][0], qa[2 * p + i][1]);
           }
         }
       }
       // ---- online softmax ---------------------------------------------------------------
-      float wv[4][2];  // value scales, then the weights
-      float tmax = -INFINITY;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int t = tw0 + 8 * n + 2 * tig;
-        const float2 kf = *reinterpret_cast<const float2*>(ksc + sc_off(t));
-        const float2 vf = *reinterpret_cast<const float2*>(vsc + sc_off(t));
-        sc[n][0] = t < count ? sc[n][0] * (kf.x * cq) : -INFINITY;
-        sc[n][1] = t + 1 < count ? sc[n][1] * (kf.y * cq) : -INFINITY;
-        wv[n][0] = t < count ? vf.x : 0.f;
-        wv[n][1] = t + 1 < count ? vf.y : 0.f;
-        tmax = fmaxf(tmax, fmaxf(sc[n][0], sc[n][1]));
+      for (int i = 0; i < 4; ++i) {
+        sc[i >> 1][2 * (i & 1)] *= kf[i];
+        sc[i >> 1][2 * (i & 1) + 1] *= kf[i];
       }
-      tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
-      tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
-      uint32_t vtop = 0u;  // largest value scale of the 32 tokens, as bits
-      {
-        const int t = tw0 + lane;
-        if (t < count) vtop = *reinterpret_cast<const uint32_t*>(vsc + sc_off(t)) & 0x7fffffffu;
-        vtop = __reduce_max_sync(0xffffffffu, vtop);
+      if (tw0 + 32 > count) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (tw0 + 8 * i + gid >= count) {
+            sc[i >> 1][2 * (i & 1)] = sc[i >> 1][2 * (i & 1) + 1] = -INFINITY;
+            vf[i] = 0.f;
+          }
       }
-      const float m_new = fmaxf(m_run, tmax);
-      // (-inf only where every score so far is -inf or NaN: a NaN then stays one)
-      const float m_ref = m_new == -INFINITY ? 0.f : m_new;
-      float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m_run - m_new);
-      m_run = m_new;
-      l_part *= alpha;
-      const int e_new = max((int)(vtop >> 23) - 127, e_run);
-      if (e_new > e_run) {
-        alpha *= e_run - e_new < -126 ? 0.f : pow2f(e_run - e_new);
-        e_run = e_new;
+      float top[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        top[e] = cq[e] * fmaxf(fmaxf(sc[0][e], sc[0][2 + e]), fmaxf(sc[1][e], sc[1][2 + e]));
+      const uint32_t vtop = __reduce_max_sync(
+          0xffffffffu, max(max(__float_as_uint(vf[0]) & 0x7fffffffu,
+                               __float_as_uint(vf[1]) & 0x7fffffffu),
+                           max(__float_as_uint(vf[2]) & 0x7fffffffu,
+                               __float_as_uint(vf[3]) & 0x7fffffffu)));
+      const int e_new = (int)(vtop >> 23) - 127;
+      if (__any_sync(0xffffffffu, top[0] > m_run[0] || top[1] > m_run[1]) || e_new > e_run) {
+        float grow = 1.f;
+        if (e_new > e_run) {
+          grow = e_run - e_new < -126 ? 0.f : pow2f(e_run - e_new);
+          e_run = e_new;
+        }
+        float alpha[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int m = 4; m < 32; m <<= 1)
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], m));
+          const float m_new = fmaxf(m_run[e], top[e]);
+          // (-inf only where every score so far is NaN)
+          alpha[e] = m_new == m_run[e] ? 1.f : fast_exp2(m_run[e] - m_new);
+          m_run[e] = m_new;
+          m_ref[e] = m_new == -INFINITY ? 0.f : m_new;
+          l_part[e] *= alpha[e];
+          alpha[e] *= grow;
+        }
+#pragma unroll
+        for (int n = 0; n < KC; ++n) {
+          o[n][0] *= alpha[0];
+          o[n][1] *= alpha[1];
+          o[n][2] *= alpha[0];
+          o[n][3] *= alpha[1];
+        }
       }
       const float nu = pow2f(14 - e_run);
-      uint32_t pa[4];
+      uint32_t wt[4];  // the operand's words: head gid, tokens 8 i + 2 tig, + 1
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float p0 = fast_exp2(sc[n][0] - m_ref), p1 = fast_exp2(sc[n][1] - m_ref);
-        l_part += p0 + p1;
-        pa[n] = f2_elt2<true>(p0 * (wv[n][0] * nu), p1 * (wv[n][1] * nu));
+      for (int i = 0; i < 4; ++i) {
+        const float p0 = fast_exp2(fmaf(sc[i >> 1][2 * (i & 1)], cq[0], -m_ref[0]));
+        const float p1 = fast_exp2(fmaf(sc[i >> 1][2 * (i & 1) + 1], cq[1], -m_ref[1]));
+        l_part[0] += p0;
+        l_part[1] += p1;
+        vf[i] *= nu;
+        wt[i] = transpose8(f2_elt2<true>(p0 * vf[i], p1 * vf[i]));
       }
-      if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
-        for (int n = 0; n < KC; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][e] *= alpha;
-      }
-      // ---- O += W V: two blocks of 16 tokens ----------------------------------------------
+      // ---- O^T += V^T W^T: two blocks of 16 tokens ----------------------------------------
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int t = tw0 + 16 * h + (lane & 7) + (((lane >> 3) & 1) << 3);
         const uint32_t base =
-            st_u + C::KV_BYTES + (uint32_t)row_off(t) + ((uint32_t)(v_hi ^ (sw & 1)) << 4);
+            st_u + C::KV_BYTES + (uint32_t)row_off(t) + ((uint32_t)(hi ^ (sw & 1)) << 4);
 #pragma unroll
         for (int p = 0; p < KC / 2; ++p) {
-          uint32_t r[4];
+          uint32_t r[4];  // chunk 2p: tokens 0..7, 8..15; chunk 2p + 1
           ldsm_x4_t(r, base + (((uint32_t)p << 5) ^ sw_hi));
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {  // chunk 2p + i: tokens 0..7 in r[2i], 8..15 in r[2i + 1]
-            uint32_t e0, o0, e1, o1;
-            widen4<FMT, true>(r[2 * i], e0, o0);
-            widen4<FMT, true>(r[2 * i + 1], e1, o1);
-            float* acc = o[2 * p + i];
-            mma16816<true>(acc[0], acc[2], z, pa[2 * h], pa[2 * h + 1], e0, e1);
-            mma16816<true>(acc[1], acc[3], z, pa[2 * h], pa[2 * h + 1], o0, o1);
+          for (int i = 0; i < 2; ++i) {
+            uint32_t a0, a1, a2, a3;
+            widen4<FMT, true>(r[2 * i], a0, a1);
+            widen4<FMT, true>(r[2 * i + 1], a2, a3);
+            mma_f16(o[2 * p + i], a0, a1, a2, a3, wt[2 * h], wt[2 * h + 1]);
           }
         }
       }
@@ -562,9 +619,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = 0; n < KC; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][e] *= back;
-      float l_all = l_part;
-      l_all += __shfl_xor_sync(0xffffffffu, l_all, 1);
-      l_all += __shfl_xor_sync(0xffffffffu, l_all, 2);
+      float l_all[2] = {l_part[0], l_part[1]};
+#pragma unroll
+      for (int m = 4; m < 32; m <<= 1) {
+        l_all[0] += __shfl_xor_sync(0xffffffffu, l_all[0], m);
+        l_all[1] += __shfl_xor_sync(0xffffffffu, l_all[1], m);
+      }
       // several warps per KV head: merge their softmax states through the stage's K/V
       // shared memory once every consumer warp is done with it
       if constexpr (C::WPH > 1) {
@@ -575,14 +635,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* merge = reinterpret_cast<float*>(Kst) + (size_t)j * (C::WPH - 1) * C::MERGE_FLOATS;
       if (w != 0) {
         float* mine = merge + (size_t)(w - 1) * C::MERGE_FLOATS;
-        if (row_ok) {
 #pragma unroll
-          for (int n = 0; n < KC; ++n)
-            *reinterpret_cast<float4*>(mine + gid * D + n * 16 + 4 * tig) =
-                make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
-          if (tig == 0) {
-            mine[kTcGMax * D + gid] = m_run;
-            mine[kTcGMax * D + kTcGMax + gid] = l_all;
+        for (int e = 0; e < 2; ++e) {
+          const int head = 2 * tig + e;
+          if (head < G) {
+#pragma unroll
+            for (int n = 0; n < KC; ++n)
+              *reinterpret_cast<float2*>(mine + head * D + n * 16 + 2 * gid) =
+                  make_float2(o[n][e], o[n][2 + e]);
+            if (gid == 0) {
+              mine[kTcGMax * D + head] = m_run[e];
+              mine[kTcGMax * D + kTcGMax + head] = l_all[e];
+            }
           }
         }
         fence_proxy_async_smem();
@@ -594,52 +658,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int w2 = 1; w2 < C::WPH; ++w2) {
           const float* other = merge + (size_t)(w2 - 1) * C::MERGE_FLOATS;
-          if (row_ok) {
-            const float m2 = other[kTcGMax * D + gid];
-            const float l2 = other[kTcGMax * D + kTcGMax + gid];
-            const float mm = fmaxf(m_run, m2);
-            // (a state without scores, or with NaN alone, keeps what it has: 0 or NaN)
-            const float a1 = m_run == mm ? 1.f : fast_exp2(m_run - mm);
-            const float a2 = m2 == mm ? 1.f : fast_exp2(m2 - mm);
 #pragma unroll
-            for (int n = 0; n < KC; ++n) {
-              const float4 ov = *reinterpret_cast<const float4*>(other + gid * D + n * 16 + 4 * tig);
-              o[n][0] = o[n][0] * a1 + ov.x * a2;
-              o[n][1] = o[n][1] * a1 + ov.y * a2;
-              o[n][2] = o[n][2] * a1 + ov.z * a2;
-              o[n][3] = o[n][3] * a1 + ov.w * a2;
+          for (int e = 0; e < 2; ++e) {
+            const int head = 2 * tig + e;
+            if (head < G) {
+              const float m2 = other[kTcGMax * D + head];
+              const float l2 = other[kTcGMax * D + kTcGMax + head];
+              const float mm = fmaxf(m_run[e], m2);
+              // (a state without scores, or with NaN alone, keeps what it has: 0 or NaN)
+              const float a1 = m_run[e] == mm ? 1.f : fast_exp2(m_run[e] - mm);
+              const float a2 = m2 == mm ? 1.f : fast_exp2(m2 - mm);
+#pragma unroll
+              for (int n = 0; n < KC; ++n) {
+                const float2 ov =
+                    *reinterpret_cast<const float2*>(other + head * D + n * 16 + 2 * gid);
+                o[n][e] = o[n][e] * a1 + ov.x * a2;
+                o[n][2 + e] = o[n][2 + e] * a1 + ov.y * a2;
+              }
+              l_all[e] = l_all[e] * a1 + l2 * a2;
+              m_run[e] = mm;
             }
-            l_all = l_all * a1 + l2 * a2;
-            m_run = mm;
           }
         }
         // normalise and write the rows, or the partials for the combine (a NaN sum stays NaN)
         const int b = meta.b;
-        const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
-        if (meta.flags & kFlagWhole) {
-          if (row_ok) {
-            uint16_t* dst = static_cast<uint16_t*>(a.out) + ((int64_t)b * H + kvh * G + gid) * D;
+        const bool whole = (meta.flags & kFlagWhole) != 0;
+        const int slot = (x0 < meta.pb) ? 1 : 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int head = 2 * tig + e;
+          if (head >= G) continue;
+          const int hg = kvh * G + head;
+          const float inv = l_all[e] == 0.f ? 0.f : 1.f / l_all[e];
+          if (whole) {
+            uint16_t* dst = static_cast<uint16_t*>(a.out) + ((int64_t)b * H + hg) * D + 2 * gid;
 #pragma unroll
             for (int n = 0; n < KC; ++n) {
-              const float r[4] = {o[n][0] * inv, o[n][1] * inv, o[n][2] * inv, o[n][3] * inv};
-              *reinterpret_cast<uint2*>(dst + n * 16 + 4 * tig) =
-                  a.f16 ? make_uint2(f2_elt2<true>(r[0], r[1]), f2_elt2<true>(r[2], r[3]))
-                        : make_uint2(f2_elt2<false>(r[0], r[1]), f2_elt2<false>(r[2], r[3]));
+              const float r0 = o[n][e] * inv, r1 = o[n][2 + e] * inv;
+              *reinterpret_cast<uint32_t*>(dst + n * 16) =
+                  a.f16 ? f2_elt2<true>(r0, r1) : f2_elt2<false>(r0, r1);
             }
-          }
-        } else {
-          const int slot = (x0 < meta.pb) ? 1 : 0;
-          if (row_ok) {
-            const int hg = kvh * G + gid;
-            float* dst = a.part_o + (((int64_t)c * 2 + slot) * H + hg) * D;
+          } else {
+            float* dst = a.part_o + (((int64_t)c * 2 + slot) * H + hg) * D + 2 * gid;
 #pragma unroll
             for (int n = 0; n < KC; ++n)
-              *reinterpret_cast<float4*>(dst + n * 16 + 4 * tig) =
-                  make_float4(o[n][0] * inv, o[n][1] * inv, o[n][2] * inv, o[n][3] * inv);
-            if (tig == 0)
+              *reinterpret_cast<float2*>(dst + n * 16) = make_float2(o[n][e] * inv, o[n][2 + e] * inv);
+            if (gid == 0)
               a.part_lse[((int64_t)c * 2 + slot) * H + hg] =
-                  l_all == 0.f ? -INFINITY : m_run + fast_log2(l_all);
+                  l_all[e] == 0.f ? -INFINITY : m_run[e] + fast_log2(l_all[e]);
           }
+        }
+        if (!whole) {
           __threadfence();
           __syncwarp();
           int old = 0;
@@ -652,9 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (old == nseg - 1) {  // last arrival: combine the partials of sequence b in CTA order
             __threadfence();
             if (a.f16)
-              combine_partials<D, true, kTcGMax>(a, b, kvh, G, c_lo, nseg, NT, g_eff, meta.pb, lane);
+              combine_q8<D, true>(a, b, kvh, G, c_lo, nseg, NT, g_eff, meta.pb, lane);
             else
-              combine_partials<D, false, kTcGMax>(a, b, kvh, G, c_lo, nseg, NT, g_eff, meta.pb, lane);
+              combine_q8<D, false>(a, b, kvh, G, c_lo, nseg, NT, g_eff, meta.pb, lane);
             if (lane == 0) *counter = 0;  // leave the counter zero for the next call
           }
         }
