@@ -74,11 +74,98 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// The combine of decode_kernel.cuh, out of line: its registers are not the main loop's.
+// The last arrival for (sequence, KV head): joins the partials of its nseg CTAs c_lo.. in CTA order
+// and writes the G rows from head hg0 on. One warp; lane s holds the weights of segment s of a
+// chunk of 32, and the partial rows of two heads and eight segments are asked for together.
+// (combine_partials of decode_kernel.cuh takes a round trip to memory for each segment here,
+// within the registers that its kernel leaves it: 8 segments cost 5 us. Out of line, this one has
+// the registers to itself.)
 template <int D, bool F16>
-__device__ __noinline__ void combine_q8(const DecodeArgs& a, int b, int kvh, int G, int64_t c_lo,
-                                        int nseg, int64_t NT, int g_eff, int64_t pb, int lane) {
-  combine_partials<D, F16, kTcGMax>(a, b, kvh, G, c_lo, nseg, NT, g_eff, pb, lane);
+__device__ __noinline__ void combine_q8(const float* part_o, const float* part_lse, uint16_t* out,
+                                        int H, int hg0, int G, int c_lo, int nseg,
+                                        bool first_slot, int lane) {
+  constexpr int CPL = D / 32, SU = 8;
+#pragma unroll 1
+  for (int h0 = 0; h0 < G; h0 += 2) {
+    const int two = h0 + 1 < G ? 1 : 0;  // 0: the second of the pair repeats the first
+    float acc[2][CPL], m_h[2], den[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      m_h[q] = -INFINITY;
+      den[q] = 0.f;
+#pragma unroll
+      for (int e = 0; e < CPL; ++e) acc[q][e] = 0.f;
+    }
+#pragma unroll 1
+    for (int s0 = 0; s0 < nseg; s0 += 32) {
+      const int nb = min(32, nseg - s0);
+      // row of a segment's partials: a CTA's slot 1 where the sequence is not its first
+      auto row = [&](int seg, int q) {
+        return ((int64_t)(c_lo + seg) * 2 + (seg == 0 && first_slot ? 1 : 0)) * H + hg0 + h0 + q * two;
+      };
+      float w[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        w[q] = lane < nb ? __ldcg(part_lse + row(s0 + lane, q)) : -INFINITY;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float bm = w[q];
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, m));
+        const float nm = fmaxf(m_h[q], bm);
+        const float al = m_h[q] == nm ? 1.f : fast_exp2(m_h[q] - nm);
+        m_h[q] = nm;
+        // (a segment without keys weighs nothing; a NaN stays one)
+        w[q] = w[q] == -INFINITY ? 0.f : fast_exp2(w[q] - nm);
+        float sum = w[q];
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        den[q] = den[q] * al + sum;
+#pragma unroll
+        for (int e = 0; e < CPL; ++e) acc[q][e] *= al;
+      }
+#pragma unroll 1
+      for (int j0 = 0; j0 < nb; j0 += SU) {
+        float po[SU][2][CPL];
+#pragma unroll
+        for (int u = 0; u < SU; ++u)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            // (past the last segment: the last one again, with no weight)
+            const float* src = part_o + row(s0 + min(j0 + u, nb - 1), q) * D + lane * CPL;
+            if constexpr (CPL == 4) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+              po[u][q][0] = v.x, po[u][q][1] = v.y, po[u][q][2] = v.z, po[u][q][3] = v.w;
+            } else {
+              const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+              po[u][q][0] = v.x, po[u][q][1] = v.y;
+            }
+          }
+#pragma unroll
+        for (int u = 0; u < SU; ++u)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float wj = __shfl_sync(0xffffffffu, w[q], (j0 + u) & 31);
+            if (j0 + u < nb) {
+#pragma unroll
+              for (int e = 0; e < CPL; ++e) acc[q][e] = fmaf(wj, po[u][q][e], acc[q][e]);
+            }
+          }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (q == 1 && !two) break;
+      const float inv = den[q] == 0.f ? 0.f : 1.f / den[q];
+      uint16_t* dst = out + (int64_t)(h0 + q) * D + lane * CPL;
+      if constexpr (CPL == 4) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(f2_elt2<F16>(acc[q][0] * inv, acc[q][1] * inv),
+                                                    f2_elt2<F16>(acc[q][2] * inv, acc[q][3] * inv));
+      } else {
+        *reinterpret_cast<uint32_t*>(dst) = f2_elt2<F16>(acc[q][0] * inv, acc[q][1] * inv);
+      }
+    }
+  }
 }
 
 // One 3-D TMA box into shared memory.
@@ -90,6 +177,20 @@ __device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)),
       "l"(policy)
       : "memory");
+}
+// The same boxes into L2 only.
+__device__ __forceinline__ void prefetch_box_4d(const CUtensorMap* map, int c0, int c1, int c2,
+                                                int c3) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+__device__ __forceinline__ void prefetch_box_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
 }
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
@@ -172,69 +273,107 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   // ---- prologue: total tiles, then the sequence that holds this CTA's first tile -----
-  {
-    int64_t local = 0;
-    for (int b = tid; b < B; b += kThreads) {
-      const int raw = __ldg(a.context_lens + b);
-      if ((raw < 0 || raw > cap) && (b % nctas) == c && slab == 0)
-        set_dev_err(a.dev_err, PA_DEV_ERR_CONTEXT);
-      local += tiles_of(b);
-    }
+  constexpr int kScan = kConsumerWarps * 32;  // sequences scanned at a time
+  int64_t NT = 0, x0 = 0, x1 = 0;
+  int g_eff = 0;
+  // a chunk of kScan sequences: tiles of sequence base + tid, of those before it, of all
+  auto scan = [&](int base, int64_t* before, int64_t* all) {
+    const int b = base + tid;
+    const int n = tid < kScan && b < B ? tiles_of(b) : 0;
+    int64_t incl = n;
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) local += __shfl_xor_sync(0xffffffffu, local, m);
-    if (lane == 0) ctl.red[warp] = local;
+    for (int m = 1; m < 32; m <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, m);
+      if (lane >= m) incl += y;
+    }
+    if (lane == 31) ctl.red[warp] = incl;
     __syncthreads();
-    if (tid == 0) {
-      int64_t nt = 0;
-      for (int w = 0; w < kThreads / 32; ++w) nt += ctl.red[w];
-      ctl.nt = nt;
-      const int64_t mt = a.min_tiles > 1 ? a.min_tiles : 1;
-      const int64_t want = (nt + mt - 1) / mt;
-      const int g = (int)(want < (int64_t)nctas ? want : (int64_t)nctas);
-      ctl.g_eff = g;
-      ctl.x0 = c < g ? tile_begin(c, nt, g) : 0;
-      ctl.x1 = c < g ? tile_begin(c + 1, nt, g) : 0;
-    }
-  }
-  __syncthreads();
-  const int64_t NT = ctl.nt;
-  const int g_eff = ctl.g_eff;
-  const int64_t x0 = ctl.x0, x1 = ctl.x1;
-
-  if (x0 < x1) {
-    int64_t running = 0;
-    for (int base = 0; base < B; base += kConsumerWarps * 32) {
-      int n = 0;
-      const int b = base + tid;
-      if (tid < kConsumerWarps * 32 && b < B) n = tiles_of(b);
-      int incl = n;
+    *before = incl - n;
+    *all = 0;
 #pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, m);
-        if (lane >= m) incl += y;
-      }
-      if (lane == 31) ctl.red[warp] = incl;
+    for (int w = 0; w < kConsumerWarps; ++w) {
+      const int64_t r = ctl.red[w];
+      if (w < warp) *before += r;
+      *all += r;
+    }
+    return n;
+  };
+  auto split = [&]() {  // this CTA's share of NT tiles
+    const int64_t mt = a.min_tiles > 1 ? a.min_tiles : 1;
+    const int64_t want = (NT + mt - 1) / mt;
+    g_eff = (int)(want < (int64_t)nctas ? want : (int64_t)nctas);
+    if (c < g_eff) {
+      x0 = tile_begin(c, NT, g_eff);
+      x1 = tile_begin(c + 1, NT, g_eff);
+    }
+  };
+  auto holds = [&](int b, int64_t p, int n) {  // tiles p .. p + n - 1 are those of sequence b
+    if (n > 0 && x0 < x1 && p <= x0 && x0 < p + n) {
+      ctl.b0 = b;
+      ctl.pb0 = p;
+      ctl.found = 1;
+    }
+  };
+  for (int b = tid; b < B; b += kThreads) {
+    const int raw = __ldg(a.context_lens + b);
+    if ((raw < 0 || raw > cap) && (b % nctas) == c && slab == 0)
+      set_dev_err(a.dev_err, PA_DEV_ERR_CONTEXT);
+  }
+  if (B <= kScan) {
+    int64_t p;
+    const int n = scan(0, &p, &NT);
+    split();
+    holds(tid, p, n);
+  } else {
+    for (int base = 0; base < B; base += kScan) {
+      int64_t p, all;
+      scan(base, &p, &all);
+      NT += all;
       __syncthreads();
-      int64_t before = 0, chunk = 0;
-      for (int w = 0; w < kConsumerWarps; ++w) {
-        if (w < warp) before += ctl.red[w];
-        chunk += ctl.red[w];
-      }
-      if (n > 0) {
-        const int64_t p = running + before + incl - n;
-        if (p <= x0 && x0 < p + n) {
-          ctl.b0 = b;
-          ctl.pb0 = p;
-          ctl.found = 1;
-        }
-      }
-      running += chunk;
+    }
+    split();
+    int64_t running = 0;
+    for (int base = 0; base < B && running <= x0; base += kScan) {
+      int64_t p, all;
+      const int n = scan(base, &p, &all);
+      holds(base + tid, running + p, n);
+      running += all;
       __syncthreads();
-      if (ctl.found) break;
     }
   }
   __syncthreads();
-  // what came before reads only context_lens, which no earlier kernel of the step writes
+
+  const bool boxes = tb > 0;
+  const int nbx = boxes ? T / tb : 0;  // boxes of a full tile
+  // Before the wait the producer warms L2 with what its first tiles read: the codes, the scales
+  // and the block ids, which no earlier kernel of the step writes but for the new tokens' rows
+  // (a line warmed too early is the one that the store then updates).
+  if (warp == kProducerWarp && boxes && x0 < x1 && ctl.found) {
+    int b = ctl.b0;
+    int64_t pb = ctl.pb0;
+    int hi = load_ctx(a.context_lens, b, cap);
+    int nb = (hi + T - 1) / T;
+    for (int64_t x = x0; x < x1 && x < x0 + S; ++x) {
+      while (x >= pb + nb && b + 1 < B) {
+        pb += nb;
+        ++b;
+        hi = load_ctx(a.context_lens, b, cap);
+        nb = (hi + T - 1) / T;
+      }
+      const int tok0 = (int)(x - pb) * T;
+      const int count = min(T, hi - tok0);
+      for (int i = lane; i < nbx && i * tb < count; i += 32) {
+        const int pos = tok0 + i * tb;
+        const int id = __ldg(a.block_tables + (int64_t)b * a.max_blocks + pos / a.block_size);
+        if (id < 0 || (int64_t)id >= a.num_blocks) continue;
+        const int off = pos % a.block_size;
+        prefetch_box_4d(&tm.k, 0, off, slab * HS, id);
+        prefetch_box_4d(&tm.v, 0, off, slab * HS, id);
+        prefetch_box_3d(&tm.ks, off, slab * HS, id);
+        prefetch_box_3d(&tm.vs, off, slab * HS, id);
+      }
+    }
+  }
   pdl_wait();
 
   {  // zero rows of empty (or invalid) sequences assigned to this CTA: one warp per row
@@ -251,7 +390,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) set_dev_err(a.dev_err, PA_DEV_ERR_CONTEXT);
     return;
   }
-  const int64_t n_tiles = x1 - x0;
+  // the end of a segment reads these again: nothing of the split stays in registers meanwhile
+  if (tid == 0) {
+    ctl.nt = NT;
+    ctl.x0 = x0;
+    ctl.g_eff = g_eff;
+  }
+  __syncthreads();
+  const int n_tiles = (int)(x1 - x0);
   volatile int* abort_flag = &ctl.abort;
   auto gave_up = [&]() {
     if (lane == 0) {
@@ -273,14 +419,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tensor_map(&tm.ks);
       prefetch_tensor_map(&tm.vs);
     }
-    const int nbx = tb > 0 ? T / tb : 0;  // boxes of a full tile
     const int box_bytes = HS * tb * (D + 4);
     int b = ctl.b0;
     int64_t pb = ctl.pb0;
     int hi = load_ctx(a.context_lens, b, cap);
     int nb = (hi + T - 1) / T;
     int q_n = 0;  // segments whose Q has been issued
-    for (int64_t it = 0; it < n_tiles; ++it) {
+    int s = 0;
+    uint32_t phase = 0;  // of the stage's uses
+    for (int it = 0; it < n_tiles; ++it, s = s + 1 == S ? 0 : s + 1, phase ^= (s == 0)) {
       const int64_t x = x0 + it;
       while (x >= pb + nb && b + 1 < B) {
         pb += nb;
@@ -288,7 +435,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         hi = load_ctx(a.context_lens, b, cap);
         nb = (hi + T - 1) / T;
       }
-      const int s = (int)(it % S);
       const int lt = (int)(x - pb);
       const int tok0 = lt * T;
       const int count = min(T, hi - tok0);
@@ -315,8 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         nbox += __popc(__ballot_sync(0xffffffffu, blk[r] >= 0));
       }
-      if (it >= S && !mbar_wait(&ctl.empty[s], (uint32_t)(((it / S) - 1) & 1), abort_flag))
-        gave_up();
+      if (it >= S && !mbar_wait(&ctl.empty[s], phase ^ 1u, abort_flag)) gave_up();
 #ifdef PA_TEST_DELAY_LAST_TILE_CYCLES
       // test build only (decode_kernel.cuh): the consumers' wait for the last tile runs out
       if (it == n_tiles - 1) {
@@ -400,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // copies still in flight land before the producer leaves
-    for (int64_t it = n_tiles > S ? n_tiles - S : 0; it < n_tiles; ++it)
+    for (int it = n_tiles > S ? n_tiles - S : 0; it < n_tiles; ++it)
       mbar_wait_copies(&ctl.full[it % S], (uint32_t)((it / S) & 1));
     for (int n = q_n > C::QS ? q_n - C::QS : 0; n < q_n; ++n)
       mbar_wait_copies(&ctl.q_full[n % C::QS], (uint32_t)((n / C::QS) & 1));
@@ -430,8 +575,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       m_ref[i] = l_part[i] = 0.f;
     }
     e_run = kE0;
+    cq[0] = cq[1] = 0.f;
+#pragma unroll
+    for (int kc = 0; kc < KC; ++kc) qa[kc][0] = qa[kc][1] = 0u;
   };
-  cq[0] = cq[1] = 0.f;
   reset();
 
   // row (token t of head j) of a code tile, and its scale
@@ -449,17 +596,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   int seg_count = 0;
   int q_n = 0;
-  for (int64_t it = 0; it < n_tiles; ++it) {
-    const int s = (int)(it % S);
-    if (!mbar_wait(&ctl.full[s], (uint32_t)((it / S) & 1), abort_flag)) gave_up();
-    const StageMeta meta = ctl.meta[s];
+  int s = 0;
+  uint32_t phase = 0;
+  for (int it = 0; it < n_tiles; ++it, s = s + 1 == S ? 0 : s + 1, phase ^= (s == 0)) {
+    if (!mbar_wait(&ctl.full[s], phase, abort_flag)) gave_up();
+    const StageMeta& meta = ctl.meta[s];
+    const int count = meta.count, flags = meta.flags;
     unsigned char* Kst = smem + (size_t)s * C::STAGE_BYTES;
     unsigned char* Vst = Kst + C::KV_BYTES;
     const unsigned char* ksc = Kst + 2 * C::KV_BYTES;
     const unsigned char* vsc = ksc + C::SC_BYTES;
-    const int count = meta.count;
 
-    if (meta.flags & kFlagFirst) {
+    if (flags & kFlagFirst) {
       const int qs = q_n % C::QS;
       if (!mbar_wait(&ctl.q_full[qs], (uint32_t)((q_n / C::QS) & 1), abort_flag)) gave_up();
       const unsigned char* Qst = qbuf + (size_t)qs * C::Q_BYTES;
@@ -480,7 +628,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float c_gid = fmaxf(row_to_f16<KC>(qa, a.f16 != 0) * a.scale_log2, 1.4e-45f);
       cq[0] = __shfl_sync(0xffffffffu, c_gid, 8 * tig);
       cq[1] = __shfl_sync(0xffffffffu, c_gid, 8 * tig + 4);
-      reset();
     }
 
 #pragma unroll
@@ -612,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
 
-    if (meta.flags & kFlagLast) {
+    if (flags & kFlagLast) {
       // ---- finalize the segment: from the warp's reference scale back to the values' ------
       const float back = pow2f(e_run - 14);
 #pragma unroll
@@ -682,8 +829,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // normalise and write the rows, or the partials for the combine (a NaN sum stays NaN)
         const int b = meta.b;
-        const bool whole = (meta.flags & kFlagWhole) != 0;
-        const int slot = (x0 < meta.pb) ? 1 : 0;
+        const bool whole = (flags & kFlagWhole) != 0;
+        const int slot = (ctl.x0 < meta.pb) ? 1 : 0;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int head = 2 * tig + e;
@@ -715,20 +862,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           int* counter = a.counters + (int64_t)b * Hk + kvh;
           if (lane == 0) old = atomicAdd(counter, 1);
           old = __shfl_sync(0xffffffffu, old, 0);
-          const int64_t c_lo = cta_of(meta.pb, NT, g_eff);
-          const int64_t c_hi = cta_of(meta.pb + meta.nb - 1, NT, g_eff);
+          const int64_t nt = ctl.nt, pb = meta.pb;
+          const int g = ctl.g_eff;
+          const int64_t c_lo = cta_of(pb, nt, g);
+          const int64_t c_hi = cta_of(pb + meta.nb - 1, nt, g);
           const int nseg = (int)(c_hi - c_lo + 1);
           if (old == nseg - 1) {  // last arrival: combine the partials of sequence b in CTA order
             __threadfence();
+            const bool first_slot = tile_begin(c_lo, nt, g) < pb;
+            uint16_t* dst = static_cast<uint16_t*>(a.out) + ((int64_t)b * H + kvh * G) * D;
             if (a.f16)
-              combine_q8<D, true>(a, b, kvh, G, c_lo, nseg, NT, g_eff, meta.pb, lane);
+              combine_q8<D, true>(a.part_o, a.part_lse, dst, H, kvh * G, G, (int)c_lo, nseg,
+                                  first_slot, lane);
             else
-              combine_q8<D, false>(a, b, kvh, G, c_lo, nseg, NT, g_eff, meta.pb, lane);
+              combine_q8<D, false>(a.part_o, a.part_lse, dst, H, kvh * G, G, (int)c_lo, nseg,
+                                   first_slot, lane);
             if (lane == 0) *counter = 0;  // leave the counter zero for the next call
           }
         }
       }
       ++seg_count;
+      reset();  // here, so that none of it is kept across the combine
       fence_proxy_async_smem();
     }
     // order this tile's shared-memory reads before the producer's next copy into the stage
@@ -760,7 +914,10 @@ int launch_decode_q8_t(DecodeQ8Args a, const DeviceInfo& info, cudaStream_t stre
        !make_scales_map(&tm.ks, a.k_scale, a.num_kv_heads, a.block_size, a.num_blocks, tb, HS) ||
        !make_scales_map(&tm.vs, a.v_scale, a.num_kv_heads, a.block_size, a.num_blocks, tb, HS)))
     return PA_ERR_CUDA;
-  const dim3 grid((unsigned)a.grid_ctas, (unsigned)(a.num_kv_heads / HS));
+  // the automatic grid: one resident wave over all slabs
+  const int slabs = a.num_kv_heads / HS;
+  if (a.auto_grid) a.grid_ctas = slabs < info.num_sms ? info.num_sms / slabs : 1;
+  const dim3 grid((unsigned)a.grid_ctas, (unsigned)slabs);
   if (launch_dependent(paged_decode_q8_kernel<HS, D, FMT>, grid, dim3(kThreads), C::SMEM, stream,
                        tm, a, tb) != cudaSuccess)
     return PA_ERR_CUDA;

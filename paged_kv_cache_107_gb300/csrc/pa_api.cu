@@ -756,6 +756,7 @@ int pa_decode_q8(void* out, const void* q, const pa_q8_cache* cache, const int32
   if (rc != PA_OK || nothing) return rc;
   a.k_scale = cache->k_scale;
   a.v_scale = cache->v_scale;
+  a.auto_grid = grid_ctas == 0;
   rc = pa::decode_check_workspace(&a, info, workspace, workspace_bytes);
   if (rc != PA_OK) return rc;
   return pa::launch_decode_q8(a, cache->format, info, static_cast<cudaStream_t>(stream));

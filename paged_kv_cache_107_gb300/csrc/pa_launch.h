@@ -312,6 +312,7 @@ int launch_load_q8(const LoadQ8Args& a, int fmt, int head_dim, bool f16, const D
 struct DecodeQ8Args : DecodeArgs {
   const float* k_scale;
   const float* v_scale;
+  bool auto_grid;  // the caller left the grid to the library
 };
 int launch_decode_q8(const DecodeQ8Args& a, int fmt, const DeviceInfo& info, cudaStream_t stream);
 
