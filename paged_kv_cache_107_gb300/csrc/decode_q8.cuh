@@ -20,15 +20,21 @@
 //    of 16 dims is dim 2 (r mod 8) + r / 8.
 //    W: a warp's weights (token by head) become the second product's operand (head by token)
 //    with movmatrix.
-//  * A lane holds four tokens' scores of two heads. The running maximum is moved only when some
-//    score of the 32 tokens exceeds it (one vote): most steps need no shuffle and no rescaling.
+//  * A warp takes 32 tokens of a stage (64 with heads of 64), a lane two heads' scores of four
+//    (eight) of them. The running maximum is moved only when one of these scores exceeds it (one
+//    vote): most tiles need no shuffle and no rescaling.
 //  * The K scale multiplies the score. The V scale is taken into the weight, which is then rounded
 //    to fp16: w_t = p_t vs_t 2^(14-E), E the exponent of the largest vs met so far by the warp
 //    (when it grows the accumulators are rescaled), so that w < 2^15 and what is rounded off
 //    lies 2^-39 below the largest scale or 2^-11 below w itself.
 //  * bf16 queries go to fp16 with a power of two for each head (row_to_f16 below).
+//  * Rows of shared memory are 128 bytes with the 128-byte swizzle: a head of 128 dims, or two
+//    heads of 64, which lie side by side in the cache (half as many rows for the copies: 72.8 ->
+//    66.0 us for 200 sequences of up to 4,096 positions, 32 / 8 heads of 64, block size 16). A single head of 64 has
+//    64-byte rows and the 64-byte swizzle.
 //  * Scales come beside the codes, [head][token] of each box, by TMA; their slots are padded to
-//    128 bytes (a TMA destination's alignment).
+//    128 bytes (a TMA destination's alignment). Fetched by the producer's lanes instead, 16 bytes
+//    at a time, the same batches take 2 to 4 % longer.
 #pragma once
 
 #include "decode_tc.cuh"
@@ -39,10 +45,12 @@ namespace {
 
 template <int HS, int D>
 struct Q8Cfg {
-  static constexpr int SUB = D == 64 ? 2 : 1;       // steps of 32 tokens per warp and stage
+  static constexpr int SUB = D == 64 ? 2 : 1;       // a warp takes 32 * SUB tokens of a stage
   static constexpr int T = 256 * SUB / HS;          // tokens per stage
   static constexpr int WPH = kConsumerWarps / HS;   // warps per KV head (token split)
   static constexpr int KV_BYTES = HS * T * D;
+  static constexpr int HPR = D == 64 && HS > 1 ? 2 : 1;  // heads of one shared-memory row
+  static constexpr int ROW = HPR * D;               // 128 bytes, or 64 for a single head of 64
   static constexpr int SC_BYTES = T * (4 * HS > 16 ? 4 * HS : 16);  // boxes of 8 tokens, padded
   static constexpr int STAGE_BYTES = (2 * (KV_BYTES + SC_BYTES) + 1023) / 1024 * 1024;
   static constexpr int Q_BYTES = HS * kTcGMax * D * 2;
@@ -275,11 +283,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- prologue: total tiles, then the sequence that holds this CTA's first tile -----
   constexpr int kScan = kConsumerWarps * 32;  // sequences scanned at a time
   int64_t NT = 0, x0 = 0, x1 = 0;
-  int g_eff = 0;
+  int g_eff = 0, held = 0;  // CTAs that own tiles; sequences that hold keys
   // a chunk of kScan sequences: tiles of sequence base + tid, of those before it, of all
   auto scan = [&](int base, int64_t* before, int64_t* all) {
     const int b = base + tid;
     const int n = tid < kScan && b < B ? tiles_of(b) : 0;
+    held += __syncthreads_count(n > 0);
     int64_t incl = n;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -299,8 +308,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     return n;
   };
   auto split = [&]() {  // this CTA's share of NT tiles
-    const int64_t mt = a.min_tiles > 1 ? a.min_tiles : 1;
-    const int64_t want = (NT + mt - 1) / mt;
+    int64_t want = NT;
+    if (a.auto_grid) {
+      // A tile takes a CTA 0.95 us, each segment of a sequence its combine 0.11 us for every pair
+      // of heads: with g CTAs NT / g of the one and g / held of the other, least at this g (one
+      // sequence of 200, 1,000, 30,000 keys 7.7, 10.0, 27 us; with at least four tiles for each
+      // CTA 10.5, 10.6, 32; of 1,000 with 8 heads a group 14.8, with a tile for each CTA 21.5).
+      // Then as few CTAs as keep the longest share (16 of 1,000: 11.9 us, 13.9 without).
+      want = (int64_t)sqrtf((float)NT * (float)held * (8.6f / (float)((G + 1) / 2)));
+      want = want < 1 ? 1 : want;
+      if (want > nctas) want = nctas;
+      if (want < NT) {
+        const int64_t share = (NT + want - 1) / want;
+        want = (NT + share - 1) / share;
+      } else {
+        want = NT;
+      }
+    }
     g_eff = (int)(want < (int64_t)nctas ? want : (int64_t)nctas);
     if (c < g_eff) {
       x0 = tile_begin(c, NT, g_eff);
@@ -345,8 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const bool boxes = tb > 0;
   const int nbx = boxes ? T / tb : 0;  // boxes of a full tile
-  // Before the wait the producer warms L2 with what its first tiles read: the codes, the scales
-  // and the block ids, which no earlier kernel of the step writes but for the new tokens' rows
+  // Before the wait the producer warms L2 with what its first tiles read: the codes and the
+  // block ids, which no earlier kernel of the step writes but for the new tokens' rows
   // (a line warmed too early is the one that the store then updates).
   if (warp == kProducerWarp && boxes && x0 < x1 && ctl.found) {
     int b = ctl.b0;
@@ -367,8 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int id = __ldg(a.block_tables + (int64_t)b * a.max_blocks + pos / a.block_size);
         if (id < 0 || (int64_t)id >= a.num_blocks) continue;
         const int off = pos % a.block_size;
-        prefetch_box_4d(&tm.k, 0, off, slab * HS, id);
-        prefetch_box_4d(&tm.v, 0, off, slab * HS, id);
+        prefetch_box_4d(&tm.k, 0, off, slab * (HS / C::HPR), id);
+        prefetch_box_4d(&tm.v, 0, off, slab * (HS / C::HPR), id);
         prefetch_box_3d(&tm.ks, off, slab * HS, id);
         prefetch_box_3d(&tm.vs, off, slab * HS, id);
       }
@@ -405,7 +429,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       set_dev_err(a.dev_err, PA_DEV_ERR_TIMEOUT);
     }
   };
-  // boxes of tbl tokens: codes [head][token][D], scales [head][token]
+  // boxes of tbl tokens, [heads of a row][token][row]; 16-byte chunk ch of token t's row sits at
+  // chunk ch ^ swizzle(t)
+  auto swizzle = [](int t) { return C::ROW == 128 ? t & 7 : (t >> 1) & 3; };
   const int tbl = tb > 0 ? tb : T;
   const int lg_tbl = __ffs(tbl) - 1;
   const int sc_slot = max(HS * tbl * 4, 128);
@@ -488,12 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int r = 0; r < kBoxes; ++r) {
           if (blk[r] < 0) continue;
           const int i = lane + 32 * r;
-          tma_load_4d_hint(st + i * HS * tb * D, &tm.k, 0, off[r], slab * HS, blk[r],
+          tma_load_4d_hint(st + i * HS * tb * D, &tm.k, 0, off[r], slab * (HS / C::HPR), blk[r],
                            &ctl.full[s], policy);
           tma_load_3d_hint(st_sc + i * sc_slot, &tm.ks, off[r], slab * HS, blk[r], &ctl.full[s],
                            policy);
-          tma_load_4d_hint(st + C::KV_BYTES + i * HS * tb * D, &tm.v, 0, off[r], slab * HS, blk[r],
-                           &ctl.full[s], policy);
+          tma_load_4d_hint(st + C::KV_BYTES + i * HS * tb * D, &tm.v, 0, off[r],
+                           slab * (HS / C::HPR), blk[r], &ctl.full[s], policy);
           tma_load_3d_hint(st_sc + C::SC_BYTES + i * sc_slot, &tm.vs, off[r], slab * HS, blk[r],
                            &ctl.full[s], policy);
         }
@@ -512,10 +538,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               (((int64_t)id * a.block_size + in) * Hk + slab * HS) * D;  // HS * D bytes
           for (int i = lane; i < 2 * HS * CH; i += 32) {
             const int kv = i / (HS * CH), jj = i / CH % HS, ch = i % CH;
-            const int sw = D == 128 ? t & 7 : (t >> 1) & 3;
             const unsigned char* src =
                 static_cast<const unsigned char*>(kv ? a.v_cache : a.k_cache) + row + jj * D + ch * 16;
-            cp_async16(st + kv * C::KV_BYTES + (jj * T + t) * D + ((ch ^ sw) << 4), src);
+            cp_async16(st + kv * C::KV_BYTES + ((jj / C::HPR) * T + t) * C::ROW +
+                           (((jj % C::HPR * CH + ch) ^ swizzle(t)) << 4),
+                       src);
           }
           if (lane < 2 * HS) {
             const int kv = lane / HS, jj = lane % HS;
@@ -581,16 +608,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   reset();
 
-  // row (token t of head j) of a code tile, and its scale
+  // row that holds token t of head j in a code tile, and the token's scale
   auto row_off = [&](int t) -> int {
-    return ((((t >> lg_tbl) * HS + j) << lg_tbl) + (t & (tbl - 1))) * D;
+    return ((((t >> lg_tbl) * (HS / C::HPR) + j / C::HPR) << lg_tbl) + (t & (tbl - 1))) * C::ROW;
   };
   auto sc_off = [&](int t) -> int {
     return (t >> lg_tbl) * sc_slot + ((j << lg_tbl) + (t & (tbl - 1))) * 4;
   };
-  // chunk ch of a row sits at chunk ch ^ sw; a lane's ldmatrix row has the same sw everywhere
-  const int sw = D == 128 ? lane & 7 : (lane >> 1) & 3;
-  const uint32_t sw_hi = (uint32_t)(sw & 6) << 4;
+  // chunk 2p + hi of the head sits at chunk (ch0 + 2p + hi) ^ sw of the row, ch0 the head's first;
+  // a lane's ldmatrix rows all have the same sw
+  const int ch0 = (j % C::HPR) * (D / 16);
+  const int sw = swizzle(lane & 7);
+  const uint32_t sw_hi = (uint32_t)((sw & 6) ^ ch0) << 4;
   const int hi = lane >> 4;  // which of a pair of chunks this lane's ldmatrix row is of
   const uint32_t smem_base = smem_u32(smem);
 
@@ -630,17 +659,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       cq[1] = __shfl_sync(0xffffffffu, c_gid, 8 * tig + 4);
     }
 
-#pragma unroll
-    for (int u = 0; u < C::SUB; ++u) {
-      const int tw0 = (w * C::SUB + u) * 32;  // first token of these 32
-      if (tw0 >= count) continue;
+    constexpr int TW = 32 * C::SUB;   // tokens of a warp
+    constexpr int NI = TW / 8;        // of a lane
+    const int tw0 = w * TW;           // the warp's first
+    if (tw0 < count) {
       // e4m3 rows past the context may hold NaN codes, which a zero weight does not remove
-      if (FMT == PA_Q8_E4M3 && tw0 + 32 > count) {
+      if (FMT == PA_Q8_E4M3 && tw0 + TW > count) {
         constexpr int CH = D / 16;
-        for (int i = lane; i < 32 * CH; i += 32) {
+        for (int i = lane; i < TW * CH; i += 32) {
           const int t = tw0 + i / CH;
           if (t >= count)
-            *reinterpret_cast<uint4*>(Vst + row_off(t) + (i % CH) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(Vst + row_off(t) + (((ch0 + i % CH) ^ swizzle(t)) << 4)) =
+                make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -648,18 +678,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t st_u = smem_base + (uint32_t)s * C::STAGE_BYTES;
 
       // scales of this lane's tokens tw0 + 8 i + gid, asked for before the product
-      float kf[4], vf[4];
+      float kf[NI], vf[NI];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < NI; ++i) {
         const int at = sc_off(tw0 + 8 * i + gid);
         kf[i] = *reinterpret_cast<const float*>(ksc + at);
         vf[i] = *reinterpret_cast<const float*>(vsc + at);
       }
-      // ---- S^T = K Q^T: two row tiles of 16 tokens; element 2 i + e: token 8 i + gid of the
+      // ---- S^T = K Q^T: row tiles of 16 tokens; element 2 i + e: token 8 i + gid of the
       // tile, head 2 tig + e
-      float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      float sc[TW / 16][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < TW / 16; ++h) {
+        sc[h][0] = sc[h][1] = sc[h][2] = sc[h][3] = 0.f;
         const int t = tw0 + 16 * h + (lane & 7) + (((lane >> 3) & 1) << 3);
         const uint32_t base = st_u + (uint32_t)row_off(t) + ((uint32_t)(hi ^ (sw & 1)) << 4);
 #pragma unroll
@@ -677,27 +708,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- online softmax ---------------------------------------------------------------
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < NI; ++i) {
         sc[i >> 1][2 * (i & 1)] *= kf[i];
         sc[i >> 1][2 * (i & 1) + 1] *= kf[i];
       }
-      if (tw0 + 32 > count) {
+      if (tw0 + TW > count) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < NI; ++i)
           if (tw0 + 8 * i + gid >= count) {
             sc[i >> 1][2 * (i & 1)] = sc[i >> 1][2 * (i & 1) + 1] = -INFINITY;
             vf[i] = 0.f;
           }
       }
-      float top[2];
+      float top[2] = {-INFINITY, -INFINITY};
+      uint32_t vtop = 0u;
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        top[e] = cq[e] * fmaxf(fmaxf(sc[0][e], sc[0][2 + e]), fmaxf(sc[1][e], sc[1][2 + e]));
-      const uint32_t vtop = __reduce_max_sync(
-          0xffffffffu, max(max(__float_as_uint(vf[0]) & 0x7fffffffu,
-                               __float_as_uint(vf[1]) & 0x7fffffffu),
-                           max(__float_as_uint(vf[2]) & 0x7fffffffu,
-                               __float_as_uint(vf[3]) & 0x7fffffffu)));
+      for (int h = 0; h < TW / 16; ++h) {
+        top[0] = fmaxf(top[0], fmaxf(sc[h][0], sc[h][2]));
+        top[1] = fmaxf(top[1], fmaxf(sc[h][1], sc[h][3]));
+        vtop = max(vtop, max(__float_as_uint(vf[2 * h]) & 0x7fffffffu,
+                             __float_as_uint(vf[2 * h + 1]) & 0x7fffffffu));
+      }
+      top[0] *= cq[0];
+      top[1] *= cq[1];
+      vtop = __reduce_max_sync(0xffffffffu, vtop);
       const int e_new = (int)(vtop >> 23) - 127;
       if (__any_sync(0xffffffffu, top[0] > m_run[0] || top[1] > m_run[1]) || e_new > e_run) {
         float grow = 1.f;
@@ -728,9 +762,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float nu = pow2f(14 - e_run);
-      uint32_t wt[4];  // the operand's words: head gid, tokens 8 i + 2 tig, + 1
+      uint32_t wt[NI];  // the operand's words: head gid, tokens 8 i + 2 tig, + 1
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < NI; ++i) {
         const float p0 = fast_exp2(fmaf(sc[i >> 1][2 * (i & 1)], cq[0], -m_ref[0]));
         const float p1 = fast_exp2(fmaf(sc[i >> 1][2 * (i & 1) + 1], cq[1], -m_ref[1]));
         l_part[0] += p0;
@@ -738,9 +772,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         vf[i] *= nu;
         wt[i] = transpose8(f2_elt2<true>(p0 * vf[i], p1 * vf[i]));
       }
-      // ---- O^T += V^T W^T: two blocks of 16 tokens ----------------------------------------
+      // ---- O^T += V^T W^T: blocks of 16 tokens ----------------------------------------
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < TW / 16; ++h) {
         const int t = tw0 + 16 * h + (lane & 7) + (((lane >> 3) & 1) << 3);
         const uint32_t base =
             st_u + C::KV_BYTES + (uint32_t)row_off(t) + ((uint32_t)(hi ^ (sw & 1)) << 4);
@@ -909,8 +943,10 @@ int launch_decode_q8_t(DecodeQ8Args a, const DeviceInfo& info, cudaStream_t stre
   Q8Maps tm;
   memset(&tm, 0, sizeof(tm));
   if (tb > 0 &&
-      (!make_codes_map(&tm.k, a.k_cache, a.num_kv_heads, D, a.block_size, a.num_blocks, tb, HS) ||
-       !make_codes_map(&tm.v, a.v_cache, a.num_kv_heads, D, a.block_size, a.num_blocks, tb, HS) ||
+      (!make_codes_map(&tm.k, a.k_cache, a.num_kv_heads / C::HPR, C::ROW, a.block_size,
+                       a.num_blocks, tb, HS / C::HPR) ||
+       !make_codes_map(&tm.v, a.v_cache, a.num_kv_heads / C::HPR, C::ROW, a.block_size,
+                       a.num_blocks, tb, HS / C::HPR) ||
        !make_scales_map(&tm.ks, a.k_scale, a.num_kv_heads, a.block_size, a.num_blocks, tb, HS) ||
        !make_scales_map(&tm.vs, a.v_scale, a.num_kv_heads, a.block_size, a.num_blocks, tb, HS)))
     return PA_ERR_CUDA;

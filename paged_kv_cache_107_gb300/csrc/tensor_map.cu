@@ -39,20 +39,20 @@ bool make_slab_map(CUtensorMap* map, const void* base, int num_kv_heads, int hea
   return rc == CUDA_SUCCESS;
 }
 
-bool make_codes_map(CUtensorMap* map, const void* base, int num_kv_heads, int head_dim,
-                    int block_size, int64_t num_blocks, int box_tokens, int box_heads) {
+bool make_codes_map(CUtensorMap* map, const void* base, int num_pieces, int piece_bytes,
+                    int block_size, int64_t num_blocks, int box_tokens, int box_pieces) {
   auto encode = tmap_encode_fn();
   if (!encode) return false;
-  const cuuint64_t row = (cuuint64_t)num_kv_heads * head_dim;
-  cuuint64_t dims[4] = {(cuuint64_t)head_dim, (cuuint64_t)block_size, (cuuint64_t)num_kv_heads,
+  const cuuint64_t row = (cuuint64_t)num_pieces * piece_bytes;
+  cuuint64_t dims[4] = {(cuuint64_t)piece_bytes, (cuuint64_t)block_size, (cuuint64_t)num_pieces,
                         (cuuint64_t)num_blocks};
-  cuuint64_t strides[3] = {row, (cuuint64_t)head_dim, row * (cuuint64_t)block_size};
-  cuuint32_t box[4] = {(cuuint32_t)head_dim, (cuuint32_t)box_tokens, (cuuint32_t)box_heads, 1};
+  cuuint64_t strides[3] = {row, (cuuint64_t)piece_bytes, row * (cuuint64_t)block_size};
+  cuuint32_t box[4] = {(cuuint32_t)piece_bytes, (cuuint32_t)box_tokens, (cuuint32_t)box_pieces, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult rc =
       encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             piece_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return rc == CUDA_SUCCESS;
 }

@@ -19,11 +19,12 @@ PFN_cuTensorMapEncodeTiled_v12000 tmap_encode_fn();
 bool make_slab_map(CUtensorMap* map, const void* base, int num_kv_heads, int head_dim, bool f16,
                    int block_size, int64_t num_blocks, int box_tokens, int box_heads);
 
-// The same over a cache of 1-byte codes: a box of head_dim bytes x box_tokens tokens x box_heads
-// heads lands as [head][token][head_dim bytes], 128-byte rows with the 128-byte swizzle, or
-// 64-byte rows with the 64-byte one (chunk c of row r at chunk c ^ (r / 2 % 4)).
-bool make_codes_map(CUtensorMap* map, const void* base, int num_kv_heads, int head_dim,
-                    int block_size, int64_t num_blocks, int box_tokens, int box_heads);
+// The same over a cache of 1-byte codes, whose token rows are num_pieces pieces of piece_bytes
+// (a head, or two): a box of box_tokens tokens x box_pieces pieces lands as [piece][token], rows of
+// 128 bytes with the 128-byte swizzle, or of 64 with the 64-byte one (chunk c of row r at
+// chunk c ^ (r / 2 % 4)).
+bool make_codes_map(CUtensorMap* map, const void* base, int num_pieces, int piece_bytes,
+                    int block_size, int64_t num_blocks, int box_tokens, int box_pieces);
 
 // A 3-D map over the scales [num_blocks, num_kv_heads, block_size] in fp32 of such a cache,
 // walked as (token in block, KV head, block): a box lands as [head][token].
