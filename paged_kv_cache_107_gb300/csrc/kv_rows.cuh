@@ -13,8 +13,8 @@
 // without its whole turns; its top 32 bits go to sincospi in fp32. Far positions cost no
 // accuracy. A lane computes two frequencies and the unit's eight come by shuffles.
 //
-// Quantisation: the row's largest magnitude from the 16-bit patterns, whose order without the
-// sign is that of the magnitudes (infinities and NaN above all), two at a time.
+// Quantisation: the row's largest magnitude from the 16-bit elements, two at a time (a NaN wins:
+// its pattern, like infinity's, is above every finite number's).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -102,7 +102,6 @@ __device__ __forceinline__ void turn_unit(uint4& va, uint4& vb, const float (&c)
 }
 
 // cos and sin of the token's angles: this lane's unit u holds frequencies 8u .. 8u + 7.
-template <int D>
 __device__ __forceinline__ void unit_angles(const RowsArgs& a, int64_t tok, int lane, int u,
                                             float (&c)[8], float (&s)[8]) {
   float cs[2], sn[2];
@@ -112,12 +111,13 @@ __device__ __forceinline__ void unit_angles(const RowsArgs& a, int64_t tok, int 
     cs[i] = sn[i] = 0.f;
     if (f < a.rot.rotary_dim / 2) {
       int axis = __ldg(a.rot.axes + f);
+      const uint64_t per_position = __ldg(a.rot.turns + f);
       if (axis < 0 || axis >= a.rot.num_axes) {
         set_dev_err(a.dev_err, PA_DEV_ERR_AXIS);
         axis = 0;
       }
       const int64_t p = __ldg(a.positions + axis * a.pos_stride + tok);
-      const uint64_t turn = (uint64_t)p * __ldg(a.rot.turns + f);
+      const uint64_t turn = (uint64_t)p * per_position;
       float sv, cv;
       sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &sv, &cv);  // 2^-31
       cs[i] = cv * a.rot.amplitude;
@@ -129,6 +129,21 @@ __device__ __forceinline__ void unit_angles(const RowsArgs& a, int64_t tok, int 
     c[e] = __shfl_sync(0xffffffffu, cs[e & 1], 4 * u + (e >> 1));
     s[e] = __shfl_sync(0xffffffffu, sn[e & 1], 4 * u + (e >> 1));
   }
+}
+
+// The larger magnitudes of two pairs of elements; NaN wins.
+template <bool F16>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (F16)
+    asm("{\n\t.reg .b32 x, y;\n\tabs.f16x2 x, %1;\n\tabs.f16x2 y, %2;\n\tmax.NaN.f16x2 %0, x, y;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+  else
+    asm("{\n\t.reg .b32 x, y;\n\tabs.bf16x2 x, %1;\n\tabs.bf16x2 y, %2;\n\tmax.NaN.bf16x2 %0, x, y;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+  return r;
 }
 
 // FMT: 0 = 16-bit cache, else a pa_q8_format.
@@ -147,17 +162,17 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsBlocksPerSM) kv_rows_kernel
   const int vb = (ROT && !ADJ && turned) ? u + half : 2 * u + 1;
   const uint32_t chunks = (uint32_t)a.chunks;
   const uint32_t items = (uint32_t)a.num_tokens * chunks;  // below 2^31 (the launcher)
-  const uint32_t warps = gridDim.x * (kRowsThreads / 32);
   const bool vec = a.vec != 0;
 
   pdl_launch_dependents();
   pdl_wait();
-  for (uint32_t item = blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5); item < items;
-       item += warps) {
+  const uint32_t item = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+  if (item >= items) return;
+  {
     const int64_t tok = item / chunks;
+    const int64_t slot = __ldg(a.slots + tok);
     const int hw = (int)(item % chunks) * (HPW * U);  // the warp's first head
     const int h0 = hw + hl;
-    const int64_t slot = __ldg(a.slots + tok);
     uint4 xa[U], xb[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -179,7 +194,7 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsBlocksPerSM) kv_rows_kernel
     float c[8], s[8];
     if constexpr (ROT) {
       // (an item of values only turns nothing)
-      if (hw < H + Hk) unit_angles<D>(a, tok, lane, u, c, s);
+      if (hw < H + Hk) unit_angles(a, tok, lane, u, c, s);
     }
     bool keep = slot != -1;
     if (keep && (slot < 0 || slot >= a.num_slots)) {
@@ -213,15 +228,13 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsBlocksPerSM) kv_rows_kernel
       } else {
         const uint32_t* wa = reinterpret_cast<const uint32_t*>(&xa[i]);
         const uint32_t* wb = reinterpret_cast<const uint32_t*>(&xb[i]);
-        uint32_t top = 0u;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          top = __vmaxu2(top, wa[e] & 0x7fff7fffu);
-          top = __vmaxu2(top, wb[e] & 0x7fff7fffu);
-        }
+        uint32_t top = max_abs2<F16>(max_abs2<F16>(max_abs2<F16>(wa[0], wa[1]),
+                                                   max_abs2<F16>(wa[2], wa[3])),
+                                     max_abs2<F16>(max_abs2<F16>(wb[0], wb[1]),
+                                                   max_abs2<F16>(wb[2], wb[3])));
 #pragma unroll
         for (int m = 1; m < UNITS; m <<= 1)
-          top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, m));
+          top = max_abs2<F16>(top, __shfl_xor_sync(0xffffffffu, top, m));
         top = max(top & 0xffffu, top >> 16);
         const RowScale r = row_scale<FMT>(widen2<F16>(top).x);
         const bool finite = r.scale == r.scale;
@@ -256,11 +269,11 @@ int launch_rows_t(RowsArgs a, const DeviceInfo& info, cudaStream_t stream) {
   a.chunks = (int)((heads + per_item - 1) / per_item);
   const int64_t items = (int64_t)a.num_tokens * a.chunks;
   if (heads > INT32_MAX - per_item || items > INT32_MAX) return PA_ERR_UNSUPPORTED;
-  int64_t blocks = (items + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
-  const int64_t cap = (int64_t)info.num_sms * kRowsBlocksPerSM;  // one resident wave
-  if (blocks > cap) blocks = cap;
+  // few items are spread over the SMs in blocks of two warps
+  const int threads = items < (int64_t)info.num_sms * 8 ? 64 : kRowsThreads;
+  const int64_t blocks = (items + threads / 32 - 1) / (threads / 32);
   if (launch_dependent(kv_rows_kernel<D, F16, FMT, ROT, ADJ>, dim3((unsigned)blocks),
-                       dim3(kRowsThreads), 0, stream, a) != cudaSuccess)
+                       dim3((unsigned)threads), 0, stream, a) != cudaSuccess)
     return PA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

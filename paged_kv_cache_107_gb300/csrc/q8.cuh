@@ -37,6 +37,22 @@ __device__ __forceinline__ float2 f16x2_f2(uint32_t w) {
   return f;
 }
 
+// Four codes of a word to fp32, exactly: an int8 code x is the low byte of 2^23 + (x + 128).
+template <int FMT>
+__device__ __forceinline__ void widen4_f32(uint32_t w, float (&x)[4]) {
+  if constexpr (FMT == PA_Q8_E4M3) {
+    uint32_t a, b;
+    widen4<FMT, false>(w, a, b);
+    const float2 lo = f16x2_f2(a), hi = f16x2_f2(b);
+    x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
+  } else {
+    w ^= 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7650 + i)) - 8388736.f;
+  }
+}
+
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
 
 // A row's scale, and what its elements are multiplied with, from the row's largest magnitude.
@@ -71,6 +87,28 @@ __device__ __forceinline__ RowScale row_scale(float top) {
   return r;
 }
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Four codes of a row, packed. A row with a NaN or an infinity has mul = 0 and gets codes 0 by
 // the caller (0 * infinity would be NaN).
 //
@@ -84,21 +122,27 @@ template <int FMT>
 __device__ __forceinline__ uint32_t quantise4(const RowScale& r, float x0, float x1, float x2,
                                               float x3) {
   if constexpr (FMT == PA_Q8_E4M3) {
+    const uint64_t mul = pair2(r.mul, r.mul);
+    const uint64_t lo = pair_mul(pair2(x0, x1), mul), hi = pair_mul(pair2(x2, x3), mul);
     uint32_t w;
     asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
         "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
         : "=r"(w)
-        : "f"(x0 * r.mul), "f"(x1 * r.mul), "f"(x2 * r.mul), "f"(x3 * r.mul));
+        : "f"(__uint_as_float((uint32_t)lo)), "f"(__uint_as_float((uint32_t)(lo >> 32))),
+          "f"(__uint_as_float((uint32_t)hi)), "f"(__uint_as_float((uint32_t)(hi >> 32))));
     return w;
   } else {
+    const uint64_t mul = pair2(r.mul, r.mul), inv = pair2(r.inv, r.inv), t = pair2(-r.t, -r.t);
+    const uint64_t magic = pair2(12582912.f, 12582912.f);
     uint32_t c[4];
-    const float x[4] = {x0, x1, x2, x3};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float n = x[i] * r.mul;
-      const float q0 = n * r.inv;
-      const float q = fmaf(fmaf(-q0, r.t, n), r.inv, q0);
-      c[i] = __float_as_uint(q + 12582912.f);
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t n = pair_mul(i ? pair2(x2, x3) : pair2(x0, x1), mul);
+      const uint64_t q0 = pair_mul(n, inv);
+      const uint64_t q = pair_fma(pair_fma(q0, t, n), inv, q0);
+      const uint64_t k = pair_add(q, magic);
+      c[2 * i] = (uint32_t)k;
+      c[2 * i + 1] = (uint32_t)(k >> 32);
     }
     return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
   }

@@ -38,81 +38,78 @@ int launch_rotary_rows(const RowsArgs& a, int fmt, int head_dim, bool f16, const
 namespace {
 
 constexpr int kLoadThreads = 256;
-constexpr int kLoadUnroll = 4;       // row groups a warp loads before it uses the first
-constexpr int kLoadBlocksPerSM = 4;  // resident blocks per SM (register budget)
+constexpr int kLoadUnroll = 4;  // row groups a warp loads before it uses the first
 
-// A block's rows (token, KV head) are consecutive; a lane holds 16 codes, D/16 lanes a row. A
-// warp takes kLoadUnroll consecutive groups of 32 / (D/16) rows of K or V of one listed block:
-// 512 bytes of codes in and 1,024 of elements out for each group.
+// A block's rows (token, KV head) are consecutive; a lane holds 8 codes, D/8 lanes a row, so that
+// every store of the warp covers 512 consecutive bytes (with 16 codes a lane writes half a
+// sector at a time: 1.3 times as long). A warp takes kLoadUnroll consecutive groups of
+// 32 / (D/8) rows of K or V of one listed block.
 template <int D, bool F16, int FMT>
-__global__ void __launch_bounds__(kLoadThreads, kLoadBlocksPerSM)
-    load_q8_kernel(const LoadQ8Args a, const int parts) {
-  constexpr int UNITS = D / 16, RPW = 32 / UNITS, U = kLoadUnroll;
+__global__ void __launch_bounds__(kLoadThreads)
+    load_q8_kernel(const LoadQ8Args a, const int parts, const uint64_t per_head) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, U = kLoadUnroll;
   const int lane = threadIdx.x & 31;
-  const int u = lane % UNITS, rl = lane / UNITS;
   const int rows = a.block_size * a.num_kv_heads;
-  const int64_t items = (int64_t)a.num_listed * 2 * parts;
-  const int64_t warps = (int64_t)gridDim.x * (kLoadThreads / 32);
+  const int64_t item = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
   pdl_launch_dependents();
   pdl_wait();
-  for (int64_t item = (int64_t)blockIdx.x * (kLoadThreads / 32) + (threadIdx.x >> 5);
-       item < items; item += warps) {
-    const int part = (int)(item % parts);
-    const int kv = (int)(item / parts & 1);
-    const int64_t at = item / parts >> 1;
-    const int blk = __ldg(a.blocks + at);
-    if (blk < 0 || blk >= a.num_blocks) {
-      if (blk != -1 && lane == 0) set_dev_err(a.dev_err, PA_DEV_ERR_BLOCK_ID);
-      continue;
-    }
-    const unsigned char* src =
-        static_cast<const unsigned char*>(kv ? a.v_codes : a.k_codes) + (int64_t)blk * rows * D;
-    uint16_t* dst = static_cast<uint16_t*>(kv ? a.v_out : a.k_out) + at * rows * D;
-    const float* scales = (kv ? a.v_scale : a.k_scale) + (int64_t)blk * rows;
-    const int r0 = part * (RPW * U) + rl;
-    uint4 w[U];
-    float sc[U];
+  if (item >= (int64_t)a.num_listed * 2 * parts) return;
+  const int64_t which = item / parts;  // 2 i: K of listed block i, 2 i + 1: its V
+  const int r0 = (int)(item - which * parts) * (RPW * U) + lane / LPR;
+  const bool v = (which & 1) != 0;
+  const int blk = __ldg(a.blocks + (which >> 1));
+  if (blk < 0 || blk >= a.num_blocks) {
+    if (blk != -1 && lane == 0) set_dev_err(a.dev_err, PA_DEV_ERR_BLOCK_ID);
+    return;
+  }
+  const unsigned char* src = static_cast<const unsigned char*>(v ? a.v_codes : a.k_codes) +
+                             (int64_t)blk * rows * D + lane % LPR * 8;
+  uint16_t* dst = static_cast<uint16_t*>(v ? a.v_out : a.k_out) + (which >> 1) * rows * D +
+                  lane % LPR * 8;
+  const float* scales = (v ? a.v_scale : a.k_scale) + (int64_t)blk * rows;
+  uint2 w[U];
+  float sc[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int r = r0 + i * RPW;
-      if (r < rows) {
-        w[i] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)r * D + u * 16));
-        const uint32_t t = (uint32_t)r / (uint32_t)a.num_kv_heads;
-        sc[i] = __ldg(scales + (r - t * a.num_kv_heads) * a.block_size + t);
+  for (int i = 0; i < U; ++i) {
+    const int r = min(r0 + i * RPW, rows - 1);
+    w[i] = __ldg(reinterpret_cast<const uint2*>(src + (int64_t)r * D));
+    // r / num_kv_heads
+    const uint32_t t = per_head ? (uint32_t)__umul64hi((uint64_t)r, per_head) : (uint32_t)r;
+    sc[i] = __ldg(scales + (r - t * a.num_kv_heads) * a.block_size + t);
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int r = r0 + i * RPW;
+    if (r < rows) {
+      const uint32_t p[2] = {w[i].x, w[i].y};
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x[4];
+        widen4_f32<FMT>(p[e], x);
+        o[2 * e] = narrow2<F16>(x[0] * sc[i], x[1] * sc[i]);
+        o[2 * e + 1] = narrow2<F16>(x[2] * sc[i], x[3] * sc[i]);
       }
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int r = r0 + i * RPW;
-      if (r < rows) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(&w[i]);
-        uint32_t o[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t lo, hi;
-          widen4<FMT, false>(p[e], lo, hi);
-          const float2 x = f16x2_f2(lo), y = f16x2_f2(hi);
-          o[2 * e] = narrow2<F16>(x.x * sc[i], x.y * sc[i]);
-          o[2 * e + 1] = narrow2<F16>(y.x * sc[i], y.y * sc[i]);
-        }
-        uint4* q = reinterpret_cast<uint4*>(dst + (int64_t)r * D + u * 16);
-        q[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        q[1] = make_uint4(o[4], o[5], o[6], o[7]);
-      }
+      *reinterpret_cast<uint4*>(dst + (int64_t)r * D) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
 
 template <int D, bool F16, int FMT>
 int launch_load_t(const LoadQ8Args& a, const DeviceInfo& info, cudaStream_t stream) {
-  constexpr int per_item = 32 / (D / 16) * kLoadUnroll;
+  constexpr int per_item = 32 / (D / 8) * kLoadUnroll;
   const int parts = (a.block_size * a.num_kv_heads + per_item - 1) / per_item;
   const int64_t items = (int64_t)a.num_listed * 2 * parts;
-  int64_t blocks = (items + kLoadThreads / 32 - 1) / (kLoadThreads / 32);
-  const int64_t cap = (int64_t)info.num_sms * kLoadBlocksPerSM;  // one resident wave
-  if (blocks > cap) blocks = cap;
-  if (launch_dependent(load_q8_kernel<D, F16, FMT>, dim3((unsigned)blocks), dim3(kLoadThreads), 0,
-                       stream, a, parts) != cudaSuccess)
+  // ceil(2^64 / heads): the high half of its product with r is r / heads for every 32-bit r and
+  // heads > 1 (0 for one head)
+  const uint64_t heads = (uint64_t)a.num_kv_heads;
+  const uint64_t per_head = heads > 1 ? UINT64_MAX / heads + 1 : 0;
+  // few items are spread over the SMs in blocks of two warps
+  const int threads = items < (int64_t)info.num_sms * 8 ? 64 : kLoadThreads;
+  const int64_t blocks = (items + threads / 32 - 1) / (threads / 32);
+  if (blocks > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (launch_dependent(load_q8_kernel<D, F16, FMT>, dim3((unsigned)blocks), dim3((unsigned)threads),
+                       0, stream, a, parts, per_head) != cudaSuccess)
     return PA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
