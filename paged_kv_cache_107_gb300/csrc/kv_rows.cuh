@@ -4,10 +4,8 @@
 // A head's D dims are D/16 units of 16, one for each of the lanes that hold the head: a unit is
 // two vectors of 8 elements, chosen so that both dims of a rotated pair lie in one lane (vectors
 // u and u + R/16 for pairs R/2 apart, 2u and 2u + 1 for neighbours and for what passes
-// through). A warp moves 32 / (D/16) heads of one token at a time and loads kRowsUnroll such
-// groups before it uses the first: one work item, up to 16 heads at head_dim 128, 32 at 64. The
-// items of all tokens are dealt to the warps in turn. The kernel moves bytes: 16 in flight for
-// each lane and vector.
+// through). A warp has one work item: up to kRowsUnroll groups of 32 / (D/16) heads of a token's
+// queries, keys or values, all loaded before the first is used.
 //
 // Angles: position times the frequency's 64-bit fraction of a turn, modulo 2^64, is the angle
 // without its whole turns; its top 32 bits go to sincospi in fp32. Far positions cost no
@@ -28,9 +26,8 @@
 namespace pa {
 namespace {
 
-constexpr int kRowsUnroll = 4;   // head groups a warp loads before it uses the first
+constexpr int kRowsUnroll = 2;   // head groups of a work item
 constexpr int kRowsThreads = 256;
-constexpr int kRowsBlocksPerSM = 3;  // resident blocks per SM (register budget)
 
 // Eight 16-bit elements, by one 16-byte access or by elements. (Plain loads: q may be turned in
 // place.)
@@ -148,115 +145,117 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
 
 // FMT: 0 = 16-bit cache, else a pa_q8_format.
 template <int D, bool F16, int FMT, bool ROT, bool ADJ>
-__global__ void __launch_bounds__(kRowsThreads, kRowsBlocksPerSM) kv_rows_kernel(const RowsArgs a) {
-  constexpr int UNITS = D / 16;         // lanes of one head
-  constexpr int HPW = 32 / UNITS;       // heads a warp moves at a time
+__global__ void __launch_bounds__(kRowsThreads) kv_rows_kernel(const RowsArgs a) {
+  constexpr int UNITS = D / 16;    // lanes of one head
+  constexpr int HPW = 32 / UNITS;  // heads a warp moves at a time
   constexpr int U = kRowsUnroll;
   const int lane = threadIdx.x & 31;
-  const int u = lane % UNITS, hl = lane / UNITS;
-  const int H = ROT ? a.num_heads : 0, Hk = a.num_kv_heads;
-  const int heads = H + 2 * Hk;         // q, k, v in turn
-  const int half = a.rot.rotary_dim / 16;  // vectors, and units, that hold turned dims
-  const bool turned = ROT && u < half;
-  const int va = (ROT && !ADJ && turned) ? u : 2 * u;
-  const int vb = (ROT && !ADJ && turned) ? u + half : 2 * u + 1;
-  const uint32_t chunks = (uint32_t)a.chunks;
-  const uint32_t items = (uint32_t)a.num_tokens * chunks;  // below 2^31 (the launcher)
-  const bool vec = a.vec != 0;
+  const int u = lane % UNITS;
+  const uint32_t chunks = (uint32_t)(a.q_chunks + 2 * a.kv_chunks);
+  const uint32_t item = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
 
   pdl_launch_dependents();
   pdl_wait();
-  const uint32_t item = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-  if (item >= items) return;
-  {
-    const int64_t tok = item / chunks;
-    const int64_t slot = __ldg(a.slots + tok);
-    const int hw = (int)(item % chunks) * (HPW * U);  // the warp's first head
-    const int h0 = hw + hl;
-    uint4 xa[U], xb[U];
+  if (item >= (uint32_t)a.num_tokens * chunks) return;  // (below 2^31: the launcher)
+  const int64_t tok = item / chunks;
+  int chunk = (int)(item % chunks);
+  const bool is_q = ROT && chunk < a.q_chunks;
+  if (!is_q) chunk -= a.q_chunks;
+  const bool is_v = !is_q && chunk >= a.kv_chunks;
+  if (is_v) chunk -= a.kv_chunks;
+  const int heads = is_q ? a.num_heads : a.num_kv_heads;
+  const int h0 = chunk * (HPW * U) + lane / UNITS;
+
+  // the vectors of this lane's unit: a pair's two dims lie in them
+  const int half = a.rot.rotary_dim / 16;  // vectors, and units, that hold turned dims
+  const bool turned = ROT && !is_v && u < half;
+  const int va = 8 * ((!ADJ && turned) ? u : 2 * u);
+  const int vb = 8 * ((!ADJ && turned) ? u + half : 2 * u + 1);
+  const uint16_t* src = is_q ? static_cast<const uint16_t*>(a.q) + tok * a.q_stride
+                        : is_v ? static_cast<const uint16_t*>(a.v) + tok * a.v_stride
+                               : static_cast<const uint16_t*>(a.k) + tok * a.k_stride;
+  const bool vec = a.vec != 0;
+  const int64_t slot = __ldg(a.slots + tok);
+  uint4 xa[U], xb[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    // (not under a condition, which would put each load next to its use)
+    const uint16_t* row = src + min(h0 + i * HPW, heads - 1) * D;
+    xa[i] = ld_vec8(row + va, vec);
+    xb[i] = ld_vec8(row + vb, vec);
+  }
+  if constexpr (ROT) {
+    if (!is_v) {
+      float c[8], s[8];
+      unit_angles(a, tok, lane, u, c, s);
+      if (turned) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) turn_unit<F16, ADJ>(xa[i], xb[i], c, s);
+      }
+    }
+    if (is_q) {
+      uint16_t* dst = static_cast<uint16_t*>(a.q_out) + tok * a.q_out_stride;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int h = h0 + i * HPW;
+        if (h < heads) {
+          st_vec8(dst + h * D + va, xa[i], vec);
+          st_vec8(dst + h * D + vb, xb[i], vec);
+        }
+      }
+      return;
+    }
+  }
+  if (slot == -1) return;
+  if (slot < 0 || slot >= a.num_slots) {
+    if (lane == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SLOT);
+    return;
+  }
+  if constexpr (FMT == 0) {
+    uint16_t* dst = static_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) + slot * heads * D;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int h = h0 + i * HPW;
       if (h < heads) {
-        const uint16_t* row;
-        if (ROT && h < H)
-          row = static_cast<const uint16_t*>(a.q) + tok * a.q_stride + (int64_t)h * D;
-        else if (h < H + Hk)
-          row = static_cast<const uint16_t*>(a.k) + tok * a.k_stride + (int64_t)(h - H) * D;
-        else
-          row = static_cast<const uint16_t*>(a.v) + tok * a.v_stride + (int64_t)(h - H - Hk) * D;
-        xa[i] = ld_vec8(row + va * 8, vec);
-        xb[i] = ld_vec8(row + vb * 8, vec);
-      } else {
-        xa[i] = xb[i] = make_uint4(0u, 0u, 0u, 0u);
+        st_vec8(dst + h * D + va, xa[i], true);
+        st_vec8(dst + h * D + vb, xb[i], true);
       }
     }
-    float c[8], s[8];
-    if constexpr (ROT) {
-      // (an item of values only turns nothing)
-      if (hw < H + Hk) unit_angles(a, tok, lane, u, c, s);
-    }
-    bool keep = slot != -1;
-    if (keep && (slot < 0 || slot >= a.num_slots)) {
-      if (lane == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SLOT);
-      keep = false;
-    }
+  } else {
+    unsigned char* dst = static_cast<unsigned char*>(is_v ? a.v_cache : a.k_cache) + slot * heads * D;
     // (slots are 32-bit numbers)
-    const uint32_t blk = keep ? (uint32_t)slot / (uint32_t)a.block_size : 0u;
-    const uint32_t off = keep ? (uint32_t)slot % (uint32_t)a.block_size : 0u;
+    const uint32_t blk = (uint32_t)slot / (uint32_t)a.block_size;
+    float* scales = (is_v ? a.v_scale : a.k_scale) + (int64_t)blk * heads * a.block_size +
+                    ((uint32_t)slot - blk * a.block_size);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int h = h0 + i * HPW;
-      const bool is_q = ROT && h < H, is_k = h < H + Hk;
-      if constexpr (ROT) {
-        if (turned && is_k) turn_unit<F16, ADJ>(xa[i], xb[i], c, s);
-        if (is_q) {
-          uint16_t* row = static_cast<uint16_t*>(a.q_out) + tok * a.q_out_stride + (int64_t)h * D;
-          st_vec8(row + va * 8, xa[i], vec);
-          st_vec8(row + vb * 8, xb[i], vec);
-        }
+      const uint32_t* wa = reinterpret_cast<const uint32_t*>(&xa[i]);
+      const uint32_t* wb = reinterpret_cast<const uint32_t*>(&xb[i]);
+      uint32_t top = max_abs2<F16>(
+          max_abs2<F16>(max_abs2<F16>(wa[0], wa[1]), max_abs2<F16>(wa[2], wa[3])),
+          max_abs2<F16>(max_abs2<F16>(wb[0], wb[1]), max_abs2<F16>(wb[2], wb[3])));
+#pragma unroll
+      for (int m = 1; m < UNITS; m <<= 1)
+        top = max_abs2<F16>(top, __shfl_xor_sync(0xffffffffu, top, m));
+      top = max(top & 0xffffu, top >> 16);
+      const RowScale r = row_scale<FMT>(widen2<F16>(top).x);
+      const bool finite = r.scale == r.scale;
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t* p = e < 2 ? wa + 2 * e : wb + 2 * (e - 2);
+        const float2 lo = widen2<F16>(p[0]), hi = widen2<F16>(p[1]);
+        w[e] = finite ? quantise4<FMT>(r, lo.x, lo.y, hi.x, hi.y) : 0u;
       }
-      const int kh = is_k ? h - H : h - H - Hk;  // KV head
-      const bool write = !is_q && h < heads && keep;
-      if constexpr (FMT == 0) {
-        if (write) {
-          uint16_t* row = static_cast<uint16_t*>(is_k ? a.k_cache : a.v_cache) +
-                          (slot * Hk + kh) * D;
-          st_vec8(row + va * 8, xa[i], true);
-          st_vec8(row + vb * 8, xb[i], true);
+      if (h < heads) {
+        if (vb == va + 8) {
+          *reinterpret_cast<uint4*>(dst + h * D + va) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          *reinterpret_cast<uint2*>(dst + h * D + va) = make_uint2(w[0], w[1]);
+          *reinterpret_cast<uint2*>(dst + h * D + vb) = make_uint2(w[2], w[3]);
         }
-      } else {
-        const uint32_t* wa = reinterpret_cast<const uint32_t*>(&xa[i]);
-        const uint32_t* wb = reinterpret_cast<const uint32_t*>(&xb[i]);
-        uint32_t top = max_abs2<F16>(max_abs2<F16>(max_abs2<F16>(wa[0], wa[1]),
-                                                   max_abs2<F16>(wa[2], wa[3])),
-                                     max_abs2<F16>(max_abs2<F16>(wb[0], wb[1]),
-                                                   max_abs2<F16>(wb[2], wb[3])));
-#pragma unroll
-        for (int m = 1; m < UNITS; m <<= 1)
-          top = max_abs2<F16>(top, __shfl_xor_sync(0xffffffffu, top, m));
-        top = max(top & 0xffffu, top >> 16);
-        const RowScale r = row_scale<FMT>(widen2<F16>(top).x);
-        const bool finite = r.scale == r.scale;
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t* p = e < 2 ? wa + 2 * e : wb + 2 * (e - 2);
-          const float2 lo = widen2<F16>(p[0]), hi = widen2<F16>(p[1]);
-          w[e] = finite ? quantise4<FMT>(r, lo.x, lo.y, hi.x, hi.y) : 0u;
-        }
-        if (write) {
-          unsigned char* row = static_cast<unsigned char*>(is_k ? a.k_cache : a.v_cache) +
-                               (slot * Hk + kh) * D;
-          if (vb == va + 1) {
-            *reinterpret_cast<uint4*>(row + va * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-          } else {
-            *reinterpret_cast<uint2*>(row + va * 8) = make_uint2(w[0], w[1]);
-            *reinterpret_cast<uint2*>(row + vb * 8) = make_uint2(w[2], w[3]);
-          }
-          if (u == 0)
-            (is_k ? a.k_scale : a.v_scale)[((int64_t)blk * Hk + kh) * a.block_size + off] = r.scale;
-        }
+        if (u == 0) scales[(int64_t)h * a.block_size] = r.scale;
       }
     }
   }
@@ -265,10 +264,13 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsBlocksPerSM) kv_rows_kernel
 template <int D, bool F16, int FMT, bool ROT, bool ADJ>
 int launch_rows_t(RowsArgs a, const DeviceInfo& info, cudaStream_t stream) {
   constexpr int per_item = 32 / (D / 16) * kRowsUnroll;
-  const int64_t heads = (ROT ? a.num_heads : 0) + 2 * (int64_t)a.num_kv_heads;
-  a.chunks = (int)((heads + per_item - 1) / per_item);
-  const int64_t items = (int64_t)a.num_tokens * a.chunks;
-  if (heads > INT32_MAX - per_item || items > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  a.q_chunks = ROT ? (int)(((int64_t)a.num_heads + per_item - 1) / per_item) : 0;
+  a.kv_chunks = (int)(((int64_t)a.num_kv_heads + per_item - 1) / per_item);
+  const int64_t items = (int64_t)a.num_tokens * (a.q_chunks + 2 * (int64_t)a.kv_chunks);
+  // (a row of 2^31 elements is not memory that anyone has)
+  if (items > INT32_MAX || ((int64_t)a.num_heads + per_item) * D > INT32_MAX ||
+      ((int64_t)a.num_kv_heads + per_item) * D > INT32_MAX)
+    return PA_ERR_UNSUPPORTED;
   // few items are spread over the SMs in blocks of two warps
   const int threads = items < (int64_t)info.num_sms * 8 ? 64 : kRowsThreads;
   const int64_t blocks = (items + threads / 32 - 1) / (threads / 32);

@@ -285,7 +285,7 @@ struct RowsArgs {
   int64_t num_slots;
   int* dev_err;
   int vec;     // 1: q, q_out, k, v and their strides allow 16-byte vectors
-  int chunks;  // warps that share a token's heads (set by the launcher)
+  int q_chunks, kv_chunks;  // work items of a token's queries, keys, values (set by the launcher)
 };
 // fmt: 0 = 16-bit cache, else a pa_q8_format.
 int launch_store_rows(const RowsArgs& a, int fmt, int head_dim, bool f16, const DeviceInfo& info,

@@ -79,10 +79,13 @@ __device__ __forceinline__ RowScale row_scale(float top) {
   } else {
     const float t = fmaxf(top, 127.f * 1.17549435e-38f);
     const int e = (int)(__float_as_uint(t) >> 23) - 127;  // -120 .. 127
-    r.scale = __fdiv_rn(t, 127.f);
+    // t / 127: the remainder of the rounded product, exact, corrects it; equal to the rounded
+    // quotient for every t of 11 bits (all of them tried)
+    const float s0 = t * (1.f / 127.f);
+    r.scale = fmaf(fmaf(-s0, 127.f, t), 1.f / 127.f, s0);
     r.mul = __int_as_float(((133 - e) << 23) | 0x7e0000);  // 127 / 64 * 2^(6 - e)
     r.t = __uint_as_float((__float_as_uint(t) & 0x7fffffu) | 0x3f800000u);
-    r.inv = __frcp_rn(r.t);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.inv) : "f"(r.t));
   }
   return r;
 }
@@ -112,9 +115,9 @@ __device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
 // Four codes of a row, packed. A row with a NaN or an infinity has mul = 0 and gets codes 0 by
 // the caller (0 * infinity would be NaN).
 //
-// INT8: n = x mul is exact (7 bits by 11 at most), q0 = n inv has a relative error of 2^-23, and
-// the remainder n - q0 t, exact in one multiply-add, corrects it to 2^-46 before the last
-// rounding. Where the quotient is a tie (an integer and a half, a number of fp32) that rounding
+// INT8: n = x mul is exact (7 bits by 11 at most), q0 = n inv has a relative error of 2^-22 (inv is
+// the hardware's approximation), and the remainder n - q0 t, exact in one multiply-add (t has
+// 11 bits), corrects it to 2^-44 before the last rounding. Where the quotient is a tie (an integer and a half, a number of fp32) that rounding
 // gives it exactly; where it is none, it lies at least 2^-21 of itself from the next tie (a
 // quotient of two 11-bit numbers, times 127), which one rounding of 2^-24 does not cross. So the
 // integer rounding after it, an addition of 1.5 * 2^23, goes the way of the exact quotient.
