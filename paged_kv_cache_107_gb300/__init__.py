@@ -783,7 +783,7 @@ _Q8_FORMATS = {torch.float8_e4m3fn: 1, torch.int8: 2}
 class Q8Cache:
     """An 8-bit paged cache (pa_q8_cache in pa.h): codes k, v [num_blocks, block_size, Hk, D] of
     torch.float8_e4m3fn or torch.int8, scales k_scale, v_scale fp32 [num_blocks, Hk, block_size].
-    A new one holds zeros."""
+    A new one holds zeros. The tensors stay the cache's own (their contents may change)."""
 
     def __init__(self, num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int = 128,
                  dtype: torch.dtype = torch.float8_e4m3fn, device=None):
@@ -817,26 +817,25 @@ class Q8Cache:
             raise PagedAttentionError("codes and scales must be contiguous")
         if len({t.device for t in (k, v, k_scale, v_scale)}) != 1:
             raise PagedAttentionError("codes and scales on several devices")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self._shape = tuple(k.shape)
-        self._format = _Q8_FORMATS[k.dtype]
+        self._tensors = k, v, k_scale, v_scale
+        self._shape, self._index = tuple(k.shape), k.get_device()
+        self._arg = ctypes.byref(_PaQ8Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                                            v_scale.data_ptr(), _Q8_FORMATS[k.dtype]))
 
-    def _struct(self) -> _PaQ8Cache:
-        return _PaQ8Cache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
-                          self.v_scale.data_ptr(), self._format)
+    k = property(lambda self: self._tensors[0], doc="codes of K")
+    v = property(lambda self: self._tensors[1], doc="codes of V")
+    k_scale = property(lambda self: self._tensors[2], doc="scales of K")
+    v_scale = property(lambda self: self._tensors[3], doc="scales of V")
 
 
-def _on_device(anchor: torch.Tensor, tensors, stream) -> None:
-    """_one_device for `anchor` and `tensors`, quick where all is well."""
-    device = anchor.device
-    if (device.type == "cuda" and device.index == torch.cuda.current_device()
-            and (stream is None or stream.device == device)):
-        for t in tensors:
-            if t is not None and t.device != device:
-                break
-        else:
-            return
-    _one_device(anchor, *tensors, stream=stream)
+def _all_on(index: int, *tensors) -> bool:
+    """`index` is the current device's and every tensor (or None) lies there."""
+    if index < 0 or index != torch._C._cuda_getDevice():
+        return False
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            return False
+    return True
 
 
 def _q8_cache(cache) -> "Q8Cache":
@@ -845,28 +844,33 @@ def _q8_cache(cache) -> "Q8Cache":
     return cache
 
 
-def _rows(name: str, t: torch.Tensor, dtype, heads: int, d: int) -> int:
-    """The token stride of t [N, heads, d]: rows contiguous, tokens at any stride of at least a
-    row (a stride of 0 or less, or overlapping rows, are refused)."""
+def _rows(name: str, t: torch.Tensor, dtype, n: int, heads: int, d: int) -> int:
+    """The token stride of t [n, heads, d] of a 16-bit type `dtype`: rows contiguous, tokens at any
+    stride that keeps them apart."""
+    st = t.stride()
+    if (t.shape == (n, heads, d) and t.dtype is dtype and dtype in _ATTN_TYPES and st[2] == 1
+            and st[1] == d and st[0] >= heads * d):
+        return st[0]
     if t.dtype != dtype or dtype not in _ATTN_TYPES:
         raise PagedAttentionError(f"{name} must be bf16 or fp16, all alike, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise PagedAttentionError(f"{name} must be [N, {heads}, {d}], got {tuple(t.shape)}")
-    st = t.stride()
+    if t.shape != (n, heads, d):
+        raise PagedAttentionError(f"{name} must be [{n}, {heads}, {d}], got {tuple(t.shape)}")
     if (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
         raise PagedAttentionError(f"{name} rows must be [{heads}, {d}] contiguous")
-    if t.shape[0] <= 1:
-        return max(st[0], heads * d)
-    if st[0] < heads * d:
+    if n > 1 and st[0] < heads * d:
         raise PagedAttentionError(f"{name}: tokens overlap (stride {st[0]})")
-    return st[0]
+    return max(st[0], heads * d)
 
 
 def _slots(slot_mapping: torch.Tensor, n: int) -> None:
-    if slot_mapping.dtype != torch.int32 or slot_mapping.dim() != 1:
-        raise PagedAttentionError("slot_mapping must be int32 [N]")
-    if slot_mapping.shape[0] != n or not slot_mapping.is_contiguous():
-        raise PagedAttentionError(f"slot_mapping must be contiguous with {n} entries")
+    if (slot_mapping.dtype is not torch.int32 or slot_mapping.shape != (n,)
+            or not slot_mapping.is_contiguous()):
+        raise PagedAttentionError(f"slot_mapping must be contiguous int32 [{n}], got "
+                                  f"{slot_mapping.dtype} {tuple(slot_mapping.shape)}")
+
+
+def _stream_of(stream, index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def pa_store_kvcache_q8(k: torch.Tensor, v: torch.Tensor, cache: Q8Cache,
@@ -875,19 +879,17 @@ def pa_store_kvcache_q8(k: torch.Tensor, v: torch.Tensor, cache: Q8Cache,
     """pa_store_kvcache into an 8-bit cache, each row quantised as it is written: k, v [N, Hk, D]
     bf16 or fp16 (any token stride), slot_mapping [N] int32."""
     nb, bs, hk, d = _q8_cache(cache)._shape
-    _on_device(cache.k, (k, v, slot_mapping, dev_err), stream)
-    dt = k.dtype
-    ks, vs = _rows("k", k, dt, hk, d), _rows("v", v, dt, hk, d)
-    n = k.shape[0]
-    if v.shape[0] != n:
-        raise PagedAttentionError("k / v token counts differ")
+    if stream is not None or not _all_on(cache._index, k, v, slot_mapping, dev_err):
+        _one_device(cache.k, k, v, slot_mapping, dev_err, stream=stream)
+    dt, n = k.dtype, k.shape[0] if k.dim() == 3 else -1
+    ks, vs = _rows("k", k, dt, n, hk, d), _rows("v", v, dt, n, hk, d)
     _slots(slot_mapping, n)
     fn = _fns.get("pa_store_kvcache_q8") or _typed(
         "pa_store_kvcache_q8", [_VP, _VP, _I64, _I64, _I32, _VP, _VP, _I32, _I32, _I32, _I32, _I64,
                                 _VP, _VP])
-    rc = fn(k.data_ptr(), v.data_ptr(), ks, vs, PA_DTYPE[dt], ctypes.byref(cache._struct()),
-            slot_mapping.data_ptr(), n, hk, d, bs, nb,
-            None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, k.device))
+    rc = fn(k.data_ptr(), v.data_ptr(), ks, vs, PA_DTYPE[dt], cache._arg, slot_mapping.data_ptr(), n,
+            hk, d, bs, nb, None if dev_err is None else dev_err.data_ptr(),
+            _stream_of(stream, cache._index))
     if rc:
         _check(rc, "pa_store_kvcache_q8")
 
@@ -898,7 +900,8 @@ def pa_load_kvcache_q8(k_out: torch.Tensor, v_out: torch.Tensor, cache: Q8Cache,
     """Blocks of an 8-bit cache as 16-bit blocks: k_out, v_out [n, block_size, Hk, D] bf16 or fp16,
     block i from block blocks[i] (int32 [n]; -1 leaves it as it is)."""
     nb, bs, hk, d = _q8_cache(cache)._shape
-    _on_device(cache.k, (k_out, v_out, blocks, dev_err), stream)
+    if stream is not None or not _all_on(cache._index, k_out, v_out, blocks, dev_err):
+        _one_device(cache.k, k_out, v_out, blocks, dev_err, stream=stream)
     dt = k_out.dtype
     if dt not in _ATTN_TYPES or v_out.dtype != dt:
         raise PagedAttentionError("k_out and v_out must be bf16 or fp16, both alike")
@@ -906,15 +909,15 @@ def pa_load_kvcache_q8(k_out: torch.Tensor, v_out: torch.Tensor, cache: Q8Cache,
         raise PagedAttentionError("blocks must be contiguous int32 [n]")
     n = blocks.shape[0]
     shape = (n, bs, hk, d)
-    if tuple(k_out.shape) != shape or tuple(v_out.shape) != shape:
+    if k_out.shape != shape or v_out.shape != shape:
         raise PagedAttentionError(f"k_out and v_out must be {shape}")
     if not (k_out.is_contiguous() and v_out.is_contiguous()):
         raise PagedAttentionError("k_out and v_out must be contiguous")
     fn = _fns.get("pa_load_kvcache_q8") or _typed(
         "pa_load_kvcache_q8", [_VP, _VP, _I32, _VP, _VP, _I32, _I32, _I32, _I32, _I64, _VP, _VP])
-    rc = fn(k_out.data_ptr(), v_out.data_ptr(), PA_DTYPE[dt], ctypes.byref(cache._struct()),
-            blocks.data_ptr(), n, hk, d, bs, nb,
-            None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, blocks.device))
+    rc = fn(k_out.data_ptr(), v_out.data_ptr(), PA_DTYPE[dt], cache._arg, blocks.data_ptr(), n, hk,
+            d, bs, nb, None if dev_err is None else dev_err.data_ptr(),
+            _stream_of(stream, cache._index))
     if rc:
         _check(rc, "pa_load_kvcache_q8")
 
@@ -927,11 +930,18 @@ def pa_decode_q8(out: torch.Tensor, q: torch.Tensor, cache: Q8Cache, block_table
     workspace."""
     nb, bs, hk, d2 = _q8_cache(cache)._shape
     dt = q.dtype
-    if dt not in _ATTN_TYPES:
-        _need16(q, "q", 3)
-    _ready((("q", q, dt, 3), ("out", out, dt, 3), ("block_tables", block_tables, torch.int32, 2),
-            ("context_lens", context_lens, torch.int32, 1)),
-           (cache.k, None if workspace is None else workspace.buffer, dev_err), stream)
+    if not (stream is None and dt in _ATTN_TYPES and out.dtype is dt and q.dim() == 3
+            and block_tables.dtype is torch.int32 and block_tables.dim() == 2
+            and context_lens.dtype is torch.int32 and context_lens.dim() == 1
+            and q.is_contiguous() and out.is_contiguous() and block_tables.is_contiguous()
+            and context_lens.is_contiguous()
+            and _all_on(cache._index, q, out, block_tables, context_lens, dev_err,
+                        None if workspace is None else workspace.buffer)):
+        if dt not in _ATTN_TYPES:
+            _need16(q, "q", 3)
+        _ready((("q", q, dt, 3), ("out", out, dt, 3), ("block_tables", block_tables, torch.int32, 2),
+                ("context_lens", context_lens, torch.int32, 1)),
+               (cache.k, None if workspace is None else workspace.buffer, dev_err), stream)
     B, H, D = q.shape
     if out.shape != q.shape or d2 != D:
         raise PagedAttentionError("shape mismatch")
@@ -944,10 +954,10 @@ def pa_decode_q8(out: torch.Tensor, q: torch.Tensor, cache: Q8Cache, block_table
     fn = _fns.get("pa_decode_q8") or _typed(
         "pa_decode_q8", [_VP, _VP, _VP, _VP, _I32, _VP, _I32, _I32, _I32, _I32, _I32, _I32, _I64,
                          _F32, _I32, _VP, _SZ, _VP, _VP])
-    rc = fn(out.data_ptr(), q.data_ptr(), ctypes.byref(cache._struct()), block_tables.data_ptr(),
+    rc = fn(out.data_ptr(), q.data_ptr(), cache._arg, block_tables.data_ptr(),
             block_tables.shape[1], context_lens.data_ptr(), B, H, hk, D, PA_DTYPE[dt], bs, nb,
             _scale(scale), int(grid_ctas), workspace.buffer.data_ptr(), workspace.nbytes,
-            None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, q.device))
+            None if dev_err is None else dev_err.data_ptr(), _stream_of(stream, cache._index))
     if rc:
         _check(rc, "pa_decode_q8")
     return out
@@ -1008,52 +1018,60 @@ class Rotary:
             raise PagedAttentionError("amplitude must be finite")
         device = torch.device(device or "cuda")
         turns = [pa_rotary_turns(f) for f in inv_freq]
-        self.turns = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns],
-                                  dtype=torch.int64, device=device)
-        self.axes = torch.tensor(axes, dtype=torch.int32, device=device)
-        self.head_dim, self.rotary_dim, self.num_axes = head_dim, rotary_dim, num_axes
-        self.adjacent, self.amplitude = bool(adjacent), float(amplitude)
+        self._tensors = (torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns],
+                                      dtype=torch.int64, device=device),
+                         torch.tensor(axes, dtype=torch.int32, device=device))
+        self._form = head_dim, rotary_dim, num_axes, bool(adjacent), float(amplitude)
+        self._index = self.turns.get_device()
+        self._arg = ctypes.byref(_PaRotary(self.turns.data_ptr(), self.axes.data_ptr(), rotary_dim,
+                                           num_axes, int(self.adjacent), self.amplitude))
 
-    def _struct(self) -> _PaRotary:
-        return _PaRotary(self.turns.data_ptr(), self.axes.data_ptr(), self.rotary_dim,
-                         self.num_axes, int(self.adjacent), self.amplitude)
+    turns = property(lambda self: self._tensors[0], doc="fractions of a turn, int64 read as uint64")
+    axes = property(lambda self: self._tensors[1], doc="axis of each pair, int32")
+    head_dim = property(lambda self: self._form[0])
+    rotary_dim = property(lambda self: self._form[1])
+    num_axes = property(lambda self: self._form[2])
+    adjacent = property(lambda self: self._form[3])
+    amplitude = property(lambda self: self._form[4])
 
 
-def _rotary_store(name, q_out, q, k, v, positions, rotary, hk, d, slot_mapping, caches, bs, nb,
-                  anchor, v_cache, dev_err, stream):
+_ROTARY_ARGS = [_VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I32, _VP, _I64, _VP]
+_ROTARY_TAIL = [_VP, _I32, _I32, _I32, _I32, _I32, _I64, _VP, _VP]
+
+
+def _rotary_store(name, q_out, q, k, v, positions, rotary, shape, slot_mapping, caches, k_cache,
+                  v_cache, dev_err, stream):
+    """The calls' checks and launch; `caches` is what the library takes in the caches' place."""
+    nb, bs, hk, d = shape
     if not isinstance(rotary, Rotary):
         raise PagedAttentionError("rotary must be a Rotary")
-    _on_device(anchor, (q_out, q, k, v, positions, rotary.turns, slot_mapping, v_cache, dev_err),
-               stream)
-    if rotary.head_dim != d:
-        raise PagedAttentionError(f"rotary is for head_dim {rotary.head_dim}, the cache has {d}")
-    dt = q.dtype
+    index = rotary._index
+    if stream is not None or not _all_on(index, q, q_out, k, v, positions, slot_mapping, k_cache,
+                                         v_cache, dev_err):
+        _one_device(k_cache, v_cache, q_out, q, k, v, positions, rotary.turns, slot_mapping, dev_err,
+                    stream=stream)
+    form = rotary._form
+    if form[0] != d:
+        raise PagedAttentionError(f"rotary is for head_dim {form[0]}, the cache has {d}")
     if q.dim() != 3:
         raise PagedAttentionError(f"q must be [N, H, D], got {tuple(q.shape)}")
-    n, h = q.shape[0], q.shape[1]
-    strides = (_rows("q_out", q_out, dt, h, d), _rows("q", q, dt, h, d), _rows("k", k, dt, hk, d),
-               _rows("v", v, dt, hk, d))
-    if q_out.shape[0] != n or k.shape[0] != n or v.shape[0] != n:
-        raise PagedAttentionError("q_out / q / k / v token counts differ")
-    if positions.dtype != torch.int32 or positions.dim() not in (1, 2):
-        raise PagedAttentionError("positions must be int32 [axes, N] (or [N] for one axis)")
-    if positions.dim() == 1:
-        axes, pos_stride = 1, 0
-    else:
-        axes, pos_stride = positions.shape[0], positions.stride(0)
-    if axes != rotary.num_axes or positions.shape[-1] != n:
-        raise PagedAttentionError(f"positions must be [{rotary.num_axes}, {n}], got "
-                                  f"{tuple(positions.shape)}")
-    if n > 1 and positions.stride(-1) != 1:
+    dt, (n, h, _) = q.dtype, q.shape
+    q_stride, out_stride = _rows("q", q, dt, n, h, d), _rows("q_out", q_out, dt, n, h, d)
+    k_stride, v_stride = _rows("k", k, dt, n, hk, d), _rows("v", v, dt, n, hk, d)
+    pos_shape = positions.shape
+    if positions.dtype is not torch.int32 or not (pos_shape == (form[2], n)
+                                                  or (form[2] == 1 and pos_shape == (n,))):
+        raise PagedAttentionError(f"positions must be int32 [{form[2]}, {n}], got "
+                                  f"{positions.dtype} {tuple(pos_shape)}")
+    pos_stride = positions.stride()
+    if pos_stride[-1] != 1 and n > 1:
         raise PagedAttentionError("positions of one axis must be contiguous")
     _slots(slot_mapping, n)
-    fn = _fns.get(name) or _typed(
-        name, [_VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I32, _VP, _I64, _VP]
-        + [_VP] * len(caches) + [_VP, _I32, _I32, _I32, _I32, _I32, _I64, _VP, _VP])
-    rc = fn(q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, PA_DTYPE[dt],
-            positions.data_ptr(), pos_stride, ctypes.byref(rotary._struct()), *caches,
-            slot_mapping.data_ptr(), n, h, hk, d, bs, nb,
-            None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, anchor.device))
+    fn = _fns.get(name) or _typed(name, _ROTARY_ARGS + [_VP] * len(caches) + _ROTARY_TAIL)
+    rc = fn(q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out_stride, q_stride,
+            k_stride, v_stride, PA_DTYPE[dt], positions.data_ptr(), pos_stride[0], rotary._arg,
+            *caches, slot_mapping.data_ptr(), n, h, hk, d, bs, nb,
+            None if dev_err is None else dev_err.data_ptr(), _stream_of(stream, index))
     if rc:
         _check(rc, name)
 
@@ -1066,16 +1084,15 @@ def pa_rotary_store(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     q_out, q [N, H, D], k, v [N, Hk, D] bf16 or fp16 (any token stride; q_out may be q);
     positions int32 [axes, N] ([N] for one axis); caches [nb, bs, Hk, D] of the same type;
     slot_mapping [N] int32 (-1: only the query is turned)."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    shape, dt = k_cache.shape, q.dtype
+    if len(shape) != 4 or v_cache.shape != shape:
         raise PagedAttentionError("caches must be [num_blocks, block_size, Hk, D], both alike")
-    if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
+    if k_cache.dtype is not dt or v_cache.dtype is not dt:
         raise PagedAttentionError("caches must be of q's type")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise PagedAttentionError("caches must be contiguous")
-    nb, bs, hk, d = k_cache.shape
-    _rotary_store("pa_rotary_store", q_out, q, k, v, positions, rotary, hk, d, slot_mapping,
-                  (k_cache.data_ptr(), v_cache.data_ptr()), bs, nb, k_cache, v_cache, dev_err,
-                  stream)
+    _rotary_store("pa_rotary_store", q_out, q, k, v, positions, rotary, shape, slot_mapping,
+                  (k_cache.data_ptr(), v_cache.data_ptr()), k_cache, v_cache, dev_err, stream)
     return q_out
 
 
@@ -1085,7 +1102,7 @@ def pa_rotary_store_q8(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
                        stream=None) -> torch.Tensor:
     """pa_rotary_store into an 8-bit cache: bit for bit pa_rotary_store, then
     pa_store_kvcache_q8."""
-    nb, bs, hk, d = _q8_cache(cache)._shape
-    _rotary_store("pa_rotary_store_q8", q_out, q, k, v, positions, rotary, hk, d, slot_mapping,
-                  (ctypes.byref(cache._struct()),), bs, nb, cache.k, None, dev_err, stream)
+    shape = _q8_cache(cache)._shape
+    _rotary_store("pa_rotary_store_q8", q_out, q, k, v, positions, rotary, shape, slot_mapping,
+                  (cache._arg,), cache.k, None, dev_err, stream)
     return q_out

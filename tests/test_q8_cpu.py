@@ -206,13 +206,15 @@ def test_binding_wants_a_q8_cache(make):
 
 def test_row_strides():
     x = torch.zeros(6, 24, 64, dtype=torch.bfloat16)
-    assert pk._rows("k", x[:, 16:20], torch.bfloat16, 4, 64) == 24 * 64
-    assert pk._rows("k", x[:1, 16:20], torch.bfloat16, 4, 64) == 24 * 64
-    assert pk._rows("k", x[:0, :4], torch.bfloat16, 4, 64) == 24 * 64
+    assert pk._rows("k", x[:, 16:20], torch.bfloat16, 6, 4, 64) == 24 * 64
+    assert pk._rows("k", x[:1, 16:20], torch.bfloat16, 1, 4, 64) == 24 * 64
+    assert pk._rows("k", x[:0, :4], torch.bfloat16, 0, 4, 64) == 24 * 64
+    one = x.as_strided((1, 24, 64), (7, 64, 1))  # a single token's stride does not matter
+    assert pk._rows("k", one, torch.bfloat16, 1, 24, 64) == 24 * 64
     for bad in (x[:, ::2], x[..., :32], x.transpose(0, 1), x[:1].expand(6, 24, 64), x.float(),
                 x[:, :3], x.as_strided((2, 24, 64), (64, 64, 1))):
         with pytest.raises(pk.PagedAttentionError):
-            pk._rows("k", bad, torch.bfloat16, 24, 64)
+            pk._rows("k", bad, torch.bfloat16, bad.shape[0], 24, 64)
 
 
 @pytest.mark.parametrize("kw", [
