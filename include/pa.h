@@ -269,8 +269,8 @@ size_t pa_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, i
  * slot_mapping); everything else is read and every output written after the wait. So
  * context_lens, block_tables and slot_mapping must not be written by a preceding kernel
  * that releases its dependents before it has written them (host copies and ordinary
- * kernels are fine; of this library's kernels only the decode kernels release early, and
- * they write none of these).
+ * kernels are fine; of this library's kernels the decode kernels, the rotary calls and those that
+ * store to or load from an 8-bit cache release early, and they write none of these).
  */
 int pa_decode(void* out, const void* q, const void* k_cache, const void* v_cache,
               const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
@@ -626,7 +626,7 @@ int pa_decode_q8(void* out, const void* q, const pa_q8_cache* cache, const int32
  *   positions       device, int32; token i's position along axis x is
  *                   positions[x*pos_axis_stride + i].
  *   slot_mapping    as pa_store_kvcache; a padding row (-1) still has its queries turned.
- *   k_cache,v_cache 16-bit caches as pa_store_kvcache, of type `dtype`.
+ *   k_cache,v_cache 16-bit caches as pa_store_kvcache, of type `dtype`, 16-byte aligned.
  *   num_heads       >= 1, num_kv_heads >= 1; neither has to divide the other.
  * Arithmetic: cos and sin in fp32 of the angle above, products in fp32, one rounding.
  * Launched as pa_store_kvcache_q8.

@@ -992,8 +992,8 @@ class Rotary:
                  adjacent: bool = False, amplitude: float = 1.0, device=None):
         if inv_freq is None:
             rotary_dim = head_dim if rotary_dim is None else rotary_dim
-            if not (base > 0.0 and math.isfinite(base)):
-                raise PagedAttentionError(f"base must be positive and finite, got {base}")
+            if not (base >= 1.0 and math.isfinite(base)):
+                raise PagedAttentionError(f"base must be finite and at least 1, got {base}")
             inv_freq = [base ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
         inv_freq = [float(f) for f in inv_freq]
         if rotary_dim is None:
@@ -1007,6 +1007,8 @@ class Rotary:
         if sections is not None and axes is not None:
             raise PagedAttentionError("pass sections or axes, not both")
         if sections is not None:
+            if min(sections, default=0) < 0:
+                raise PagedAttentionError("sections must be >= 0")
             axes = [a for a, n in enumerate(sections) for _ in range(int(n))]
         axes = [0] * len(inv_freq) if axes is None else [int(a) for a in axes]
         if len(axes) != len(inv_freq) or min(axes) < 0:

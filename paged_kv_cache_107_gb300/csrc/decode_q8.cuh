@@ -257,7 +257,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = H / Hk;  // 1..8
   const int cap = a.max_blocks * a.block_size;
   const int B = a.num_seqs;
-  auto tiles_of = [&](int b) { return (load_ctx(a.context_lens, b, cap) + T - 1) / T; };
+  // (unsigned: a context may end near 2^31)
+  auto tiles_in = [](int n) { return (int)(((unsigned)n + T - 1) / T); };
+  auto tiles_of = [&](int b) { return tiles_in(load_ctx(a.context_lens, b, cap)); };
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -376,13 +378,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int b = ctl.b0;
     int64_t pb = ctl.pb0;
     int hi = load_ctx(a.context_lens, b, cap);
-    int nb = (hi + T - 1) / T;
+    int nb = tiles_in(hi);
     for (int64_t x = x0; x < x1 && x < x0 + S; ++x) {
       while (x >= pb + nb && b + 1 < B) {
         pb += nb;
         ++b;
         hi = load_ctx(a.context_lens, b, cap);
-        nb = (hi + T - 1) / T;
+        nb = tiles_in(hi);
       }
       const int tok0 = (int)(x - pb) * T;
       const int count = min(T, hi - tok0);
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int b = ctl.b0;
     int64_t pb = ctl.pb0;
     int hi = load_ctx(a.context_lens, b, cap);
-    int nb = (hi + T - 1) / T;
+    int nb = tiles_in(hi);
     int q_n = 0;  // segments whose Q has been issued
     int s = 0;
     uint32_t phase = 0;  // of the stage's uses
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         pb += nb;
         ++b;
         hi = load_ctx(a.context_lens, b, cap);
-        nb = (hi + T - 1) / T;
+        nb = tiles_in(hi);
       }
       const int lt = (int)(x - pb);
       const int tok0 = lt * T;

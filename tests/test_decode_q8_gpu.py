@@ -166,6 +166,26 @@ def test_grids_and_repeats(fmt, D):
     assert torch.equal(case.run(workspace=big), first)
 
 
+@pytest.mark.parametrize("B", [255, 256, 257, 513, 900])
+def test_many_sequences(B):
+    """More sequences than the prologue scans at once, some of them empty."""
+    rng = np.random.default_rng(B)
+    lens = [int(n) if n % 7 else 0 for n in rng.integers(0, 90, B)]
+    lens[0], lens[-1] = 0, 33
+    case = Case(lens, 8, 4, 64, "int8", "bf16", 16, seed=B)
+    case.check()
+    case.check("one CTA", grid_ctas=1)
+    case = Case([0] * (B - 1) + [200], 2, 1, 64, "e4m3", "fp16", 16, seed=B)  # the last alone
+    case.check()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_heads(D):
+    """More slabs (of one head) than SMs, and twenty slabs of eight."""
+    Case([70, 0, 300], 153, 153, D, "e4m3", "bf16", 16, seed=153).check()
+    Case([70, 1], 320, 160, D, "int8", "fp16", 16, seed=160).check()
+
+
 def test_nan_in_a_held_row_reaches_its_sequence_only():
     case = Case([40, 600, 50], 16, 8, 128, "e4m3", "bf16", 16, seed=10)
     clean = case.run()

@@ -218,8 +218,8 @@ def test_row_strides():
 
 
 @pytest.mark.parametrize("kw", [
-    dict(rotary_dim=24), dict(rotary_dim=8), dict(rotary_dim=256), dict(base=0.0),
-    dict(base=math.nan), dict(inv_freq=[1.0] * 7), dict(inv_freq=[math.inf] * 8),
+    dict(rotary_dim=24), dict(rotary_dim=8), dict(rotary_dim=256), dict(base=0.0), dict(base=0.5),
+    dict(base=math.nan), dict(base=math.inf), dict(sections=(64, -5)), dict(rotary_dim=0), dict(rotary_dim=-16), dict(inv_freq=[1.0] * 7), dict(inv_freq=[math.inf] * 8),
     dict(inv_freq=[2.0 ** 41] * 8), dict(sections=(16, 24)), dict(sections=(16, 24, 25)),
     dict(axes=[0] * 63), dict(axes=[-1] + [0] * 63), dict(axes=[16] + [0] * 63),
     dict(sections=(16, 24, 24), axes=[0] * 64), dict(amplitude=math.inf),
