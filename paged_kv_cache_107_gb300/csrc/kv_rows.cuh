@@ -145,7 +145,7 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
 
 // FMT: 0 = 16-bit cache, else a pa_q8_format.
 template <int D, bool F16, int FMT, bool ROT, bool ADJ>
-__global__ void __launch_bounds__(kRowsThreads) kv_rows_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(kRowsThreads, ROT ? 5 : 8) kv_rows_kernel(const RowsArgs a) {
   constexpr int UNITS = D / 16;    // lanes of one head
   constexpr int HPW = 32 / UNITS;  // heads a warp moves at a time
   constexpr int U = kRowsUnroll;
@@ -185,13 +185,17 @@ __global__ void __launch_bounds__(kRowsThreads) kv_rows_kernel(const RowsArgs a)
   const bool vec = a.vec != 0;
   const int64_t slot = live ? __ldg(a.slots + tok) : -1;
   uint4 xa[U], xb[U];
+  auto load = [&](bool v) {
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    // (not under a condition, which would put each load next to its use)
-    const uint16_t* row = src + min(h0 + i * HPW, heads - 1) * D;
-    xa[i] = ld_vec8(row + va, vec);
-    xb[i] = ld_vec8(row + vb, vec);
-  }
+    for (int i = 0; i < U; ++i) {
+      // (not under a condition of its own, which would put each load next to its use)
+      const uint16_t* row = src + min(h0 + i * HPW, heads - 1) * D;
+      xa[i] = ld_vec8(row + va, v);
+      xb[i] = ld_vec8(row + vb, v);
+    }
+  };
+  if (vec) load(true);
+  else load(false);
   if constexpr (ROT) {
     if (!is_v) {
       float c[8], s[8];
@@ -267,11 +271,13 @@ __global__ void __launch_bounds__(kRowsThreads) kv_rows_kernel(const RowsArgs a)
     // together, 8 tokens fill a sector. (Four bytes at a time from every warp they cost 15 % of
     // the call: 66.8 us against 57.4 without them for 64,000 tokens of 8 heads of 128.)
     __syncthreads();
-    const int tokens = blockDim.x / 32;
-    const int t = threadIdx.x % tokens, hh = threadIdx.x / tokens;  // HPW U <= 32
+    const int lg_tokens = blockDim.x == kRowsThreads ? 3 : 1;  // warps of the block
+    static_assert(kRowsThreads == 256, "eight warps, or two");
+    if (threadIdx.x >= (HPW * U) << lg_tokens) return;
+    const int t = threadIdx.x & ((1 << lg_tokens) - 1), hh = threadIdx.x >> lg_tokens;
     const int32_t s = tok_slot[t];
     const int h = chunk * (HPW * U) + hh;
-    if (hh < HPW * U && h < heads && s >= 0) {
+    if (h < heads && s >= 0) {
       const uint32_t blk = (uint32_t)s / (uint32_t)a.block_size;
       (is_v ? a.v_scale : a.k_scale)[((int64_t)blk * heads + h) * a.block_size +
                                      ((uint32_t)s - blk * a.block_size)] = tok_scale[t][hh];

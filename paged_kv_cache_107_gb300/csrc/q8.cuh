@@ -64,29 +64,29 @@ struct RowScale {
 
 template <int FMT>
 __device__ __forceinline__ RowScale row_scale(float top) {
-  RowScale r{0.f, 0.f, 1.f, 1.f};
+  RowScale r;
   const uint32_t u = __float_as_uint(top);
-  if (u >= 0x7f800000u) {  // a NaN or an infinity in the row: codes 0, scale NaN
-    r.scale = __uint_as_float(0x7fc00000u);
-    return r;
-  }
-  if (u == 0u) return r;
   if constexpr (FMT == PA_Q8_E4M3) {
     // 448 = 1.75 * 2^8
     const int e = max((int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
     r.scale = pow2f(e);
     r.mul = pow2f(-e);
+    r.t = r.inv = 1.f;
   } else {
     const float t = fmaxf(top, 127.f * 1.17549435e-38f);
-    const int e = (int)(__float_as_uint(t) >> 23) - 127;  // -120 .. 127
+    const uint32_t ut = __float_as_uint(t);
     // t / 127: the remainder of the rounded product, exact, corrects it; equal to the rounded
     // quotient for every t of 11 bits (all of them tried)
     const float s0 = t * (1.f / 127.f);
     r.scale = fmaf(fmaf(-s0, 127.f, t), 1.f / 127.f, s0);
-    r.mul = __int_as_float(((133 - e) << 23) | 0x7e0000);  // 127 / 64 * 2^(6 - e)
-    r.t = __uint_as_float((__float_as_uint(t) & 0x7fffffu) | 0x3f800000u);
+    // 127 / 64 * 2^(6 - E), E of -120 .. 127
+    r.mul = __int_as_float(((133 + 127 - (int)(ut >> 23)) << 23) | 0x7e0000);
+    r.t = __uint_as_float((ut & 0x7fffffu) | 0x3f800000u);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.inv) : "f"(r.t));
   }
+  if (u == 0u) r.scale = 0.f;  // (its codes are 0 anyway)
+  // a NaN or an infinity in the row: scale NaN, and the caller writes codes 0
+  if (u >= 0x7f800000u) r.scale = __uint_as_float(0x7fc00000u);
   return r;
 }
 
@@ -112,8 +112,7 @@ __device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Four codes of a row, packed. A row with a NaN or an infinity has mul = 0 and gets codes 0 by
-// the caller (0 * infinity would be NaN).
+// Four codes of a row, packed.
 //
 // INT8: n = x mul is exact (7 bits by 11 at most), q0 = n inv has a relative error of 2^-22 (inv is
 // the hardware's approximation), and the remainder n - q0 t, exact in one multiply-add (t has
