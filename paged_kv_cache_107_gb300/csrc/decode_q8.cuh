@@ -84,18 +84,39 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 // The last arrival for (sequence, KV head): joins the partials of its nseg CTAs c_lo.. in CTA order
 // and writes the G rows from head hg0 on. One warp; lane s holds the weights of segment s of a
-// chunk of 32, and the partial rows of two heads and eight segments are asked for together.
-// (combine_partials of decode_kernel.cuh takes a round trip to memory for each segment here,
+// chunk of 32. The partial rows of two heads and 8 segments (16 of 64 dims) are asked for together, beside the
+// log-sum-exps that will weigh them, so that up to as many segments cost one round trip to memory
+// for each pair of heads. (combine_partials of decode_kernel.cuh takes one for each segment here,
 // within the registers that its kernel leaves it: 8 segments cost 5 us. Out of line, this one has
 // the registers to itself.)
 template <int D, bool F16>
 __device__ __noinline__ void combine_q8(const float* part_o, const float* part_lse, uint16_t* out,
                                         int H, int hg0, int G, int c_lo, int nseg,
                                         bool first_slot, int lane) {
-  constexpr int CPL = D / 32, SU = 8;
+  constexpr int CPL = D / 32, SU = 32 / CPL;
 #pragma unroll 1
   for (int h0 = 0; h0 < G; h0 += 2) {
     const int two = h0 + 1 < G ? 1 : 0;  // 0: the second of the pair repeats the first
+    // row of a segment's partials: a CTA's slot 1 where the sequence is not its first
+    auto row = [&](int seg, int q) {
+      return ((int64_t)(c_lo + seg) * 2 + (seg == 0 && first_slot ? 1 : 0)) * H + hg0 + h0 + q * two;
+    };
+    float po[SU][2][CPL];
+    auto ask = [&](int s0) {  // (past the last segment: the last one again, with no weight)
+#pragma unroll
+      for (int u = 0; u < SU; ++u)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float* src = part_o + row(min(s0 + u, nseg - 1), q) * D + lane * CPL;
+          if constexpr (CPL == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+            po[u][q][0] = v.x, po[u][q][1] = v.y, po[u][q][2] = v.z, po[u][q][3] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+            po[u][q][0] = v.x, po[u][q][1] = v.y;
+          }
+        }
+    };
     float acc[2][CPL], m_h[2], den[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -107,14 +128,11 @@ __device__ __noinline__ void combine_q8(const float* part_o, const float* part_l
 #pragma unroll 1
     for (int s0 = 0; s0 < nseg; s0 += 32) {
       const int nb = min(32, nseg - s0);
-      // row of a segment's partials: a CTA's slot 1 where the sequence is not its first
-      auto row = [&](int seg, int q) {
-        return ((int64_t)(c_lo + seg) * 2 + (seg == 0 && first_slot ? 1 : 0)) * H + hg0 + h0 + q * two;
-      };
       float w[2];
 #pragma unroll
       for (int q = 0; q < 2; ++q)
         w[q] = lane < nb ? __ldcg(part_lse + row(s0 + lane, q)) : -INFINITY;
+      ask(s0);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         float bm = w[q];
@@ -134,21 +152,7 @@ __device__ __noinline__ void combine_q8(const float* part_o, const float* part_l
       }
 #pragma unroll 1
       for (int j0 = 0; j0 < nb; j0 += SU) {
-        float po[SU][2][CPL];
-#pragma unroll
-        for (int u = 0; u < SU; ++u)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            // (past the last segment: the last one again, with no weight)
-            const float* src = part_o + row(s0 + min(j0 + u, nb - 1), q) * D + lane * CPL;
-            if constexpr (CPL == 4) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-              po[u][q][0] = v.x, po[u][q][1] = v.y, po[u][q][2] = v.z, po[u][q][3] = v.w;
-            } else {
-              const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-              po[u][q][0] = v.x, po[u][q][1] = v.y;
-            }
-          }
+        if (j0 > 0) ask(s0 + j0);
 #pragma unroll
         for (int u = 0; u < SU; ++u)
 #pragma unroll
@@ -313,11 +317,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t want = NT;
     if (a.auto_grid) {
       // A tile takes a CTA 0.95 us, each segment of a sequence its combine 0.11 us for every pair
-      // of heads: with g CTAs NT / g of the one and g / held of the other, least at this g (one
-      // sequence of 200, 1,000, 30,000 keys 7.7, 10.0, 27 us; with at least four tiles for each
-      // CTA 10.5, 10.6, 32; of 1,000 with 8 heads a group 14.8, with a tile for each CTA 21.5).
-      // Then as few CTAs as keep the longest share (16 of 1,000: 11.9 us, 13.9 without).
-      want = (int64_t)sqrtf((float)NT * (float)held * (8.6f / (float)((G + 1) / 2)));
+      // of heads of 128: with g CTAs NT / g of the one and g / held of the other, least at this g
+      // (one sequence of 200, 1,000, 30,000 keys 7.7, 9.1, 24.6 us; with at least four tiles for
+      // each CTA 10.5, 10.6, 32; of 1,000 with 8 heads a group 14.5, with a tile for each CTA
+      // 20.8). Rows of 64 are joined in a quarter of the time. Then as few CTAs as keep the longest
+      // share (16 of 1,000: 11.8 us, 13.9 without).
+      constexpr float kRatio = D == 128 ? 8.6f : 34.f;
+      want = (int64_t)sqrtf((float)NT * (float)held * (kRatio / (float)((G + 1) / 2)));
       want = want < 1 ? 1 : want;
       if (want > nctas) want = nctas;
       if (want < NT) {
