@@ -4,8 +4,9 @@
 // A head's D dims are D/16 units of 16, one for each of the lanes that hold the head: a unit is
 // two vectors of 8 elements, chosen so that both dims of a rotated pair lie in one lane (vectors
 // u and u + R/16 for pairs R/2 apart, 2u and 2u + 1 for neighbours and for what passes
-// through). A warp has one work item: up to kRowsUnroll groups of 32 / (D/16) heads of a token's
-// queries, keys or values, all loaded before the first is used.
+// through). A warp has one work item: kRowsUnroll groups of 32 / (D/16) heads, of a token's
+// queries, keys or values, or of consecutive rows of several tokens, all loaded before the first
+// is used.
 //
 // Angles: position times the frequency's 64-bit fraction of a turn, modulo 2^64, is the angle
 // without its whole turns; its top 32 bits go to sincospi in fp32. Far positions cost no
@@ -98,6 +99,16 @@ __device__ __forceinline__ void turn_unit(uint4& va, uint4& vb, const float (&c)
   }
 }
 
+// cos and sin, times the amplitude, of a frequency's angle at a position.
+__device__ __forceinline__ void turn_angle(int32_t position, uint64_t per_position,
+                                           float amplitude, float* c, float* s) {
+  const uint64_t turn = (uint64_t)(int64_t)position * per_position;
+  float sv, cv;
+  sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &sv, &cv);  // 2^-31
+  *c = cv * amplitude;
+  *s = sv * amplitude;
+}
+
 // cos and sin of the token's angles: this lane's unit u holds frequencies 8u .. 8u + 7.
 __device__ __forceinline__ void unit_angles(const RowsArgs& a, int64_t tok, int lane, int u,
                                             float (&c)[8], float (&s)[8]) {
@@ -113,12 +124,8 @@ __device__ __forceinline__ void unit_angles(const RowsArgs& a, int64_t tok, int 
         set_dev_err(a.dev_err, PA_DEV_ERR_AXIS);
         axis = 0;
       }
-      const int64_t p = __ldg(a.positions + axis * a.pos_stride + tok);
-      const uint64_t turn = (uint64_t)p * per_position;
-      float sv, cv;
-      sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &sv, &cv);  // 2^-31
-      cs[i] = cv * a.rot.amplitude;
-      sn[i] = sv * a.rot.amplitude;
+      turn_angle(__ldg(a.positions + axis * a.pos_stride + tok), per_position, a.rot.amplitude,
+                 &cs[i], &sn[i]);
     }
   }
 #pragma unroll
@@ -143,15 +150,76 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// FMT: 0 = 16-bit cache, else a pa_q8_format.
+template <int D>
+struct RowsCfg {
+  static constexpr int UNITS = D / 16;           // lanes of one head
+  static constexpr int HPW = 32 / UNITS;         // heads a warp moves at a time
+  static constexpr int R = HPW * kRowsUnroll;    // heads of a work item
+  static constexpr int WARPS = kRowsThreads / 32;
+};
+
+// The two vectors of a lane's unit, by offset in a row, and whether they hold turned dims.
+struct UnitPlace {
+  int va, vb;
+  bool turned;
+};
+template <bool ROT, bool ADJ>
+__device__ __forceinline__ UnitPlace unit_place(const RowsArgs& a, int u, bool is_v) {
+  const int half = a.rot.rotary_dim / 16;  // vectors, and units, that hold turned dims
+  UnitPlace p;
+  p.turned = ROT && !is_v && u < half;
+  p.va = 8 * ((!ADJ && p.turned) ? u : 2 * u);
+  p.vb = 8 * ((!ADJ && p.turned) ? u + half : 2 * u + 1);
+  return p;
+}
+
+// Quantises the row whose units xa, xb its lanes hold; writes this lane's codes where `write`.
+// Returns the row's scale.
+template <int D, bool F16, int FMT>
+__device__ __forceinline__ float quantise_unit(const uint4& xa, const uint4& xb,
+                                               const UnitPlace& p, unsigned char* row, bool write) {
+  const uint32_t* wa = reinterpret_cast<const uint32_t*>(&xa);
+  const uint32_t* wb = reinterpret_cast<const uint32_t*>(&xb);
+  uint32_t top =
+      max_abs2<F16>(max_abs2<F16>(max_abs2<F16>(wa[0], wa[1]), max_abs2<F16>(wa[2], wa[3])),
+                    max_abs2<F16>(max_abs2<F16>(wb[0], wb[1]), max_abs2<F16>(wb[2], wb[3])));
+#pragma unroll
+  for (int m = 1; m < RowsCfg<D>::UNITS; m <<= 1)
+    top = max_abs2<F16>(top, __shfl_xor_sync(0xffffffffu, top, m));
+  top = max(top & 0xffffu, top >> 16);
+  const RowScale r = row_scale<FMT>(widen2<F16>(top).x);
+  const bool finite = r.scale == r.scale;
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t* q = e < 2 ? wa + 2 * e : wb + 2 * (e - 2);
+    const float2 lo = widen2<F16>(q[0]), hi = widen2<F16>(q[1]);
+    w[e] = finite ? quantise4<FMT>(r, lo.x, lo.y, hi.x, hi.y) : 0u;
+  }
+  if (write) {
+    if (p.vb == p.va + 8) {
+      *reinterpret_cast<uint4*>(row + p.va) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      *reinterpret_cast<uint2*>(row + p.va) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(row + p.vb) = make_uint2(w[2], w[3]);
+    }
+  }
+  return r.scale;
+}
+
+__device__ __forceinline__ void write_scale(float* scales, int32_t slot, int64_t heads, int h,
+                                            int block_size, float scale) {
+  const uint32_t blk = (uint32_t)slot / (uint32_t)block_size;
+  scales[(blk * heads + h) * block_size + ((uint32_t)slot - blk * block_size)] = scale;
+}
+
+// Work items of one token each: every lane of the warp needs the same token's angles.
 template <int D, bool F16, int FMT, bool ROT, bool ADJ>
-__global__ void __launch_bounds__(kRowsThreads, ROT ? 5 : 8) kv_rows_kernel(const RowsArgs a) {
-  constexpr int UNITS = D / 16;    // lanes of one head
-  constexpr int HPW = 32 / UNITS;  // heads a warp moves at a time
+__device__ __forceinline__ void wide_rows(const RowsArgs& a) {
+  using C = RowsCfg<D>;
   constexpr int U = kRowsUnroll;
-  const int lane = threadIdx.x & 31;
-  const int u = lane % UNITS;
-  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int u = lane % C::UNITS;
   // The warp's token and chunk of heads. 16-bit caches: a token's chunks follow each other. 8-bit
   // ones: a block takes one chunk of as many consecutive tokens as it has warps, whose scales it
   // writes together (without that need the first order is 4 % faster).
@@ -161,9 +229,6 @@ __global__ void __launch_bounds__(kRowsThreads, ROT ? 5 : 8) kv_rows_kernel(cons
   const uint32_t group = item / chunks;
   int chunk = (int)(item - group * chunks);
   const int64_t my_tok = kTogether ? (int64_t)group * (blockDim.x / 32) + warp : (int64_t)group;
-
-  pdl_launch_dependents();
-  pdl_wait();
   const bool live = my_tok < a.num_tokens;
   if (!kTogether && !live) return;
   const int64_t tok = live ? my_tok : a.num_tokens - 1;
@@ -172,16 +237,11 @@ __global__ void __launch_bounds__(kRowsThreads, ROT ? 5 : 8) kv_rows_kernel(cons
   const bool is_v = !is_q && chunk >= a.kv_chunks;
   if (is_v) chunk -= a.kv_chunks;
   const int heads = is_q ? a.num_heads : a.num_kv_heads;
-  const int h0 = chunk * (HPW * U) + lane / UNITS;
-
-  // the vectors of this lane's unit: a pair's two dims lie in them
-  const int half = a.rot.rotary_dim / 16;  // vectors, and units, that hold turned dims
-  const bool turned = ROT && !is_v && u < half;
-  const int va = 8 * ((!ADJ && turned) ? u : 2 * u);
-  const int vb = 8 * ((!ADJ && turned) ? u + half : 2 * u + 1);
-  const uint16_t* src = is_q ? static_cast<const uint16_t*>(a.q) + tok * a.q_stride
-                        : is_v ? static_cast<const uint16_t*>(a.v) + tok * a.v_stride
-                               : static_cast<const uint16_t*>(a.k) + tok * a.k_stride;
+  const int h0 = chunk * C::R + lane / C::UNITS;
+  const UnitPlace p = unit_place<ROT, ADJ>(a, u, is_v);
+  const uint16_t* src = (is_q ? static_cast<const uint16_t*>(a.q) + tok * a.q_stride
+                         : is_v ? static_cast<const uint16_t*>(a.v) + tok * a.v_stride
+                                : static_cast<const uint16_t*>(a.k) + tok * a.k_stride);
   const bool vec = a.vec != 0;
   const int64_t slot = live ? __ldg(a.slots + tok) : -1;
   uint4 xa[U], xb[U];
@@ -189,9 +249,9 @@ __global__ void __launch_bounds__(kRowsThreads, ROT ? 5 : 8) kv_rows_kernel(cons
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       // (not under a condition of its own, which would put each load next to its use)
-      const uint16_t* row = src + min(h0 + i * HPW, heads - 1) * D;
-      xa[i] = ld_vec8(row + va, v);
-      xb[i] = ld_vec8(row + vb, v);
+      const uint16_t* row = src + min(h0 + i * C::HPW, heads - 1) * D;
+      xa[i] = ld_vec8(row + p.va, v);
+      xb[i] = ld_vec8(row + p.vb, v);
     }
   };
   if (vec) load(true);
@@ -200,7 +260,7 @@ __global__ void __launch_bounds__(kRowsThreads, ROT ? 5 : 8) kv_rows_kernel(cons
     if (!is_v) {
       float c[8], s[8];
       unit_angles(a, tok, lane, u, c, s);
-      if (turned) {
+      if (p.turned) {
 #pragma unroll
         for (int i = 0; i < U; ++i) turn_unit<F16, ADJ>(xa[i], xb[i], c, s);
       }
@@ -209,10 +269,10 @@ __global__ void __launch_bounds__(kRowsThreads, ROT ? 5 : 8) kv_rows_kernel(cons
       uint16_t* dst = static_cast<uint16_t*>(a.q_out) + tok * a.q_out_stride;
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int h = h0 + i * HPW;
+        const int h = h0 + i * C::HPW;
         if (h < heads && live) {
-          st_vec8(dst + h * D + va, xa[i], vec);
-          st_vec8(dst + h * D + vb, xb[i], vec);
+          st_vec8(dst + h * D + p.va, xa[i], vec);
+          st_vec8(dst + h * D + p.vb, xb[i], vec);
         }
       }
       return;
@@ -220,89 +280,232 @@ __global__ void __launch_bounds__(kRowsThreads, ROT ? 5 : 8) kv_rows_kernel(cons
   }
   const bool keep = slot >= 0 && slot < a.num_slots;
   if (!keep && slot != -1 && lane == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SLOT);
+  const int64_t at = slot * heads * D;
   if constexpr (FMT == 0) {
-    uint16_t* dst = static_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) + slot * heads * D;
+    uint16_t* dst = static_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) + at;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int h = h0 + i * HPW;
+      const int h = h0 + i * C::HPW;
       if (h < heads && keep) {
-        st_vec8(dst + h * D + va, xa[i], true);
-        st_vec8(dst + h * D + vb, xb[i], true);
+        st_vec8(dst + h * D + p.va, xa[i], true);
+        st_vec8(dst + h * D + p.vb, xb[i], true);
       }
     }
   } else {
-    unsigned char* dst = static_cast<unsigned char*>(is_v ? a.v_cache : a.k_cache) + slot * heads * D;
-    // the block's scales, and its slots (-1: nothing is written)
-    __shared__ float tok_scale[kRowsThreads / 32][HPW * U];
-    __shared__ int32_t tok_slot[kRowsThreads / 32];
-    if (lane == 0) tok_slot[warp] = keep ? (int32_t)slot : -1;
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int h = h0 + i * HPW;
-      const uint32_t* wa = reinterpret_cast<const uint32_t*>(&xa[i]);
-      const uint32_t* wb = reinterpret_cast<const uint32_t*>(&xb[i]);
-      uint32_t top = max_abs2<F16>(
-          max_abs2<F16>(max_abs2<F16>(wa[0], wa[1]), max_abs2<F16>(wa[2], wa[3])),
-          max_abs2<F16>(max_abs2<F16>(wb[0], wb[1]), max_abs2<F16>(wb[2], wb[3])));
-#pragma unroll
-      for (int m = 1; m < UNITS; m <<= 1)
-        top = max_abs2<F16>(top, __shfl_xor_sync(0xffffffffu, top, m));
-      top = max(top & 0xffffu, top >> 16);
-      const RowScale r = row_scale<FMT>(widen2<F16>(top).x);
-      const bool finite = r.scale == r.scale;
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t* p = e < 2 ? wa + 2 * e : wb + 2 * (e - 2);
-        const float2 lo = widen2<F16>(p[0]), hi = widen2<F16>(p[1]);
-        w[e] = finite ? quantise4<FMT>(r, lo.x, lo.y, hi.x, hi.y) : 0u;
-      }
-      if (u == 0) tok_scale[warp][i * HPW + lane / UNITS] = r.scale;
-      if (h < heads && keep) {
-        if (vb == va + 8) {
-          *reinterpret_cast<uint4*>(dst + h * D + va) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-          *reinterpret_cast<uint2*>(dst + h * D + va) = make_uint2(w[0], w[1]);
-          *reinterpret_cast<uint2*>(dst + h * D + vb) = make_uint2(w[2], w[3]);
-        }
-      }
-    }
+    unsigned char* dst = static_cast<unsigned char*>(is_v ? a.v_cache : a.k_cache) + at;
     // The scales of a head's consecutive tokens lie side by side where their slots do: written
     // together, 8 tokens fill a sector. (Four bytes at a time from every warp they cost 15 % of
     // the call: 66.8 us against 57.4 without them for 64,000 tokens of 8 heads of 128.)
+    // The block's scales, and its slots (-1: nothing is written):
+    __shared__ float tok_scale[C::WARPS][C::R];
+    __shared__ int32_t tok_slot[C::WARPS];
+    if (lane == 0) tok_slot[warp] = keep ? (int32_t)slot : -1;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int h = h0 + i * C::HPW;
+      const float scale =
+          quantise_unit<D, F16, FMT>(xa[i], xb[i], p, dst + h * D, h < heads && keep);
+      if (u == 0) tok_scale[warp][i * C::HPW + lane / C::UNITS] = scale;
+    }
     __syncthreads();
     const int lg_tokens = blockDim.x == kRowsThreads ? 3 : 1;  // warps of the block
-    static_assert(kRowsThreads == 256, "eight warps, or two");
-    if (threadIdx.x >= (HPW * U) << lg_tokens) return;
+    static_assert(C::WARPS == 8, "eight warps, or two");
+    if (threadIdx.x >= C::R << lg_tokens) return;
     const int t = threadIdx.x & ((1 << lg_tokens) - 1), hh = threadIdx.x >> lg_tokens;
-    const int32_t s = tok_slot[t];
-    const int h = chunk * (HPW * U) + hh;
-    if (h < heads && s >= 0) {
-      const uint32_t blk = (uint32_t)s / (uint32_t)a.block_size;
-      (is_v ? a.v_scale : a.k_scale)[((int64_t)blk * heads + h) * a.block_size +
-                                     ((uint32_t)s - blk * a.block_size)] = tok_scale[t][hh];
+    if (tok_slot[t] >= 0 && chunk * C::R + hh < heads)
+      write_scale(is_v ? a.v_scale : a.k_scale, tok_slot[t], heads, chunk * C::R + hh,
+                  a.block_size, tok_scale[t][hh]);
+  }
+}
+
+// Blocks of consecutive rows (token, head) of the queries, the keys or the values, whatever the
+// head count: a warp's rows may be of several tokens. The angles of the block's tokens are worked
+// out once, in shared memory. (With an item for each token, 1 to 3 heads of 128 leave most lanes
+// without a row: 32,000 tokens of 1 / 1 heads took 35.7 us.)
+template <int D, bool F16, int FMT, bool ROT, bool ADJ>
+__device__ __forceinline__ void flat_rows(const RowsArgs& a, uint32_t blk, bool is_q, bool is_v) {
+  using C = RowsCfg<D>;
+  constexpr int U = kRowsUnroll;
+  constexpr int F = D / 2;  // most frequencies
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int u = lane % C::UNITS;
+  const uint32_t heads = (uint32_t)(is_q ? a.num_heads : a.num_kv_heads);
+  const uint64_t per_head = is_q ? a.q_magic : a.kv_magic;
+  const uint32_t total = (uint32_t)a.num_tokens * heads;  // below 2^31 (the launcher)
+  const uint32_t rows = C::R * (blockDim.x / 32);
+  const uint32_t row0 = blk * rows;
+  auto token_of = [&](uint32_t r) {
+    return per_head ? (uint32_t)__umul64hi((uint64_t)r, per_head) : r;
+  };
+  const uint32_t tok0 = token_of(row0);
+  const UnitPlace p = unit_place<ROT, ADJ>(a, u, is_v);
+  const uint16_t* src = static_cast<const uint16_t*>(is_q ? a.q : is_v ? a.v : a.k);
+  const int64_t stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
+  const bool vec = a.vec != 0;
+  const uint32_t r0 = row0 + warp * C::R + lane / C::UNITS;  // this lane's rows: + i HPW
+  uint32_t tok[U], head[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const uint32_t r = min(r0 + i * C::HPW, total - 1);
+    tok[i] = token_of(r);
+    head[i] = r - tok[i] * heads;
+  }
+  uint4 xa[U], xb[U];
+  auto load = [&](bool v) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint16_t* row = src + tok[i] * stride + head[i] * D;
+      xa[i] = ld_vec8(row + p.va, v);
+      xb[i] = ld_vec8(row + p.vb, v);
+    }
+  };
+  if (vec) load(true);
+  else load(false);
+  int64_t slot[U];
+  if (!is_q) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      slot[i] = r0 + i * C::HPW < total ? __ldg(a.slots + tok[i]) : -1;
+  }
+  const uint32_t tokens = token_of(min(row0 + rows, total) - 1) - tok0 + 1;  // of the block
+  if constexpr (ROT) {
+    if (!is_v) {
+      // at most as many tokens as rows
+      __shared__ __align__(16) float cs[C::R * C::WARPS][F], sn[C::R * C::WARPS][F];
+      const int f = threadIdx.x % F;
+      if (f < a.rot.rotary_dim / 2) {
+        int axis = __ldg(a.rot.axes + f);
+        const uint64_t per_position = __ldg(a.rot.turns + f);
+        if (axis < 0 || axis >= a.rot.num_axes) {
+          set_dev_err(a.dev_err, PA_DEV_ERR_AXIS);
+          axis = 0;
+        }
+        const int32_t* pos = a.positions + axis * a.pos_stride + tok0;
+        for (uint32_t t = threadIdx.x / F; t < tokens; t += blockDim.x / F)
+          turn_angle(__ldg(pos + t), per_position, a.rot.amplitude, &cs[t][f], &sn[t][f]);
+      }
+      __syncthreads();
+      if (p.turned) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const float4* cp = reinterpret_cast<const float4*>(&cs[tok[i] - tok0][8 * u]);
+          const float4* sp = reinterpret_cast<const float4*>(&sn[tok[i] - tok0][8 * u]);
+          const float4 c0 = cp[0], c1 = cp[1], s0 = sp[0], s1 = sp[1];
+          const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+          const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+          turn_unit<F16, ADJ>(xa[i], xb[i], c, s);
+        }
+      }
+    }
+    if (is_q) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (r0 + i * C::HPW < total) {
+          uint16_t* row =
+              static_cast<uint16_t*>(a.q_out) + tok[i] * a.q_out_stride + head[i] * D;
+          st_vec8(row + p.va, xa[i], vec);
+          st_vec8(row + p.vb, xb[i], vec);
+        }
+      }
+      return;
+    }
+  }
+  void* cache = is_v ? a.v_cache : a.k_cache;
+  __shared__ float row_scales[FMT != 0 ? C::R * C::WARPS : 1];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const bool keep = slot[i] >= 0 && slot[i] < a.num_slots;
+    if (!keep && slot[i] != -1 && u == 0 && head[i] == 0) set_dev_err(a.dev_err, PA_DEV_ERR_SLOT);
+    const int64_t at = (slot[i] * heads + head[i]) * D;
+    if constexpr (FMT == 0) {
+      if (keep) {
+        uint16_t* row = static_cast<uint16_t*>(cache) + at;
+        st_vec8(row + p.va, xa[i], true);
+        st_vec8(row + p.vb, xb[i], true);
+      }
+    } else {
+      const float scale = quantise_unit<D, F16, FMT>(
+          xa[i], xb[i], p, static_cast<unsigned char*>(cache) + at, keep);
+      if (u == 0) row_scales[warp * C::R + i * C::HPW + lane / C::UNITS] = scale;
+    }
+  }
+  if constexpr (FMT != 0) {
+    // scales together, as above
+    __syncthreads();
+    for (uint32_t n = threadIdx.x; n < tokens * heads; n += blockDim.x) {
+      const uint32_t h = n / tokens, t = tok0 + (n - h * tokens);
+      const uint32_t r = t * heads + h - row0;  // (wraps below the block's first row)
+      if (r >= rows || r >= total - row0) continue;
+      const int32_t s = __ldg(a.slots + t);
+      if (s >= 0 && s < a.num_slots)
+        write_scale(is_v ? a.v_scale : a.k_scale, s, heads, (int)h, a.block_size, row_scales[r]);
     }
   }
 }
 
+// FMT: 0 = 16-bit cache, else a pa_q8_format. Blocks of wide items come first, then (FLAT) flat
+// blocks of queries, keys and values (RowsArgs). The form without flat blocks has no shared
+// memory for their angles and fewer registers.
+template <int D, bool F16, int FMT, bool ROT, bool ADJ, bool FLAT>
+__global__ void __launch_bounds__(kRowsThreads, ROT ? 5 : FLAT ? 6 : 8)
+    kv_rows_kernel(const RowsArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  if constexpr (FLAT) {
+    uint32_t blk = blockIdx.x;
+    if (blk >= a.wide_blocks) {
+      blk -= a.wide_blocks;
+      const bool is_q = ROT && blk < a.q_blocks;
+      if (ROT && !is_q) blk -= a.q_blocks;
+      const bool is_v = !is_q && blk >= a.kv_blocks;
+      if (is_v) blk -= a.kv_blocks;
+      flat_rows<D, F16, FMT, ROT, ADJ>(a, blk, is_q, is_v);
+      return;
+    }
+  }
+  if constexpr (ROT || !FLAT) wide_rows<D, F16, FMT, ROT, ADJ>(a);
+}
+
 template <int D, bool F16, int FMT, bool ROT, bool ADJ>
 int launch_rows_t(RowsArgs a, const DeviceInfo& info, cudaStream_t stream) {
-  constexpr int per_item = 32 / (D / 16) * kRowsUnroll;
-  a.q_chunks = ROT ? (int)(((int64_t)a.num_heads + per_item - 1) / per_item) : 0;
-  a.kv_chunks = (int)(((int64_t)a.num_kv_heads + per_item - 1) / per_item);
-  const int64_t chunks = a.q_chunks + 2 * (int64_t)a.kv_chunks;
-  // few items are spread over the SMs in blocks of two warps
-  const int threads = a.num_tokens * chunks < (int64_t)info.num_sms * 8 ? 64 : kRowsThreads;
-  const int warps = threads / 32;
-  const int64_t blocks = FMT == 0 ? (a.num_tokens * chunks + warps - 1) / warps
-                                  : ((int64_t)a.num_tokens + warps - 1) / warps * chunks;
-  // (a row of 2^31 elements is not memory that anyone has)
-  if (a.num_tokens * chunks > INT32_MAX || blocks > INT32_MAX || ((int64_t)a.num_heads + per_item) * D > INT32_MAX ||
-      ((int64_t)a.num_kv_heads + per_item) * D > INT32_MAX)
+  constexpr int64_t R = RowsCfg<D>::R;
+  auto over = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  const int64_t n = a.num_tokens, q_heads = ROT ? a.num_heads : 0, kv_heads = a.num_kv_heads;
+  // (memory that nobody has)
+  if (n * over(q_heads, R) * R > INT32_MAX || n * over(kv_heads, R) * R > INT32_MAX ||
+      (q_heads + R) * D > INT32_MAX || (kv_heads + R) * D > INT32_MAX)
     return PA_ERR_UNSUPPORTED;
-  if (launch_dependent(kv_rows_kernel<D, F16, FMT, ROT, ADJ>, dim3((unsigned)blocks),
-                       dim3((unsigned)threads), 0, stream, a) != cudaSuccess)
-    return PA_ERR_CUDA;
+  // half full items at least; queries three quarters where keys and values take flat blocks anyway
+  // (32,000 tokens of 4 / 2 heads of 128: 26.1 us flat, 30.4 wide; 9 / 3: 42.8 and 50.6)
+  const bool kv_wide = 2 * kv_heads >= R;
+  const bool q_wide = kv_wide ? 2 * q_heads >= R : 4 * q_heads >= 3 * over(q_heads, R) * R;
+  a.q_chunks = q_wide ? (int)over(q_heads, R) : 0;
+  a.kv_chunks = kv_wide ? (int)over(kv_heads, R) : 0;
+  const int64_t chunks = a.q_chunks + 2 * (int64_t)a.kv_chunks;
+  const int64_t q_items = q_wide ? 0 : over(n * q_heads, R);
+  const int64_t kv_items = kv_wide ? 0 : over(n * kv_heads, R);
+  // few items are spread over the SMs in blocks of two warps
+  const int threads =
+      n * chunks + q_items + 2 * kv_items < (int64_t)info.num_sms * 8 ? 64 : kRowsThreads;
+  const int warps = threads / 32;
+  const int64_t wide = FMT == 0 ? over(n * chunks, warps) : over(n, warps) * chunks;
+  const int64_t q_flat = over(q_items, warps), kv_flat = over(kv_items, warps);
+  const int64_t blocks = wide + q_flat + 2 * kv_flat;
+  if (blocks > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  a.wide_blocks = (uint32_t)wide;
+  a.q_blocks = (uint32_t)q_flat;
+  a.kv_blocks = (uint32_t)kv_flat;
+  // ceil(2^64 / heads): the high half of its product with r is r / heads (0 for one head)
+  auto magic = [](int64_t heads) { return heads > 1 ? UINT64_MAX / (uint64_t)heads + 1 : 0; };
+  a.q_magic = magic(q_heads);
+  a.kv_magic = magic(kv_heads);
+  const bool flat = q_flat + kv_flat > 0;
+  const cudaError_t rc =
+      flat ? launch_dependent(kv_rows_kernel<D, F16, FMT, ROT, ADJ, true>, dim3((unsigned)blocks),
+                              dim3((unsigned)threads), 0, stream, a)
+           : launch_dependent(kv_rows_kernel<D, F16, FMT, ROT, ADJ, false>, dim3((unsigned)blocks),
+                              dim3((unsigned)threads), 0, stream, a);
+  if (rc != cudaSuccess) return PA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

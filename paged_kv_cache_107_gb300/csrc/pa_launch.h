@@ -285,7 +285,11 @@ struct RowsArgs {
   int64_t num_slots;
   int* dev_err;
   int vec;     // 1: q, q_out, k, v and their strides allow 16-byte vectors
-  int q_chunks, kv_chunks;  // work items of a token's queries, keys, values (set by the launcher)
+  // set by the launcher: wide work items of a token's queries, and of its keys or values (0: they
+  // are taken by flat blocks), the blocks of each, and 2^64 / heads for the flat ones
+  int q_chunks, kv_chunks;
+  uint32_t wide_blocks, q_blocks, kv_blocks;
+  uint64_t q_magic, kv_magic;
 };
 // fmt: 0 = 16-bit cache, else a pa_q8_format.
 int launch_store_rows(const RowsArgs& a, int fmt, int head_dim, bool f16, const DeviceInfo& info,

@@ -42,7 +42,9 @@ def check_store(cache, k, v, slots, fmt):
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("d,hk,bs,n", [(128, 8, 16, 1), (128, 8, 256, 700), (64, 8, 16, 333),
                                        (128, 1, 20, 67), (64, 1, 1, 5), (64, 3, 32, 100),
-                                       (128, 5, 8, 41), (128, 16, 48, 129), (64, 40, 16, 9)])
+                                       (128, 5, 8, 41), (128, 16, 48, 129), (64, 40, 16, 9),
+                                       (128, 2, 16, 500), (128, 3, 8, 1), (64, 7, 16, 1031),
+                                       (128, 4, 32, 77), (64, 2, 256, 3000), (128, 1, 64, 2000)])
 def test_store_matches_the_definition(fmt, dtype, d, hk, bs, n):
     g = torch.Generator(device=DEV).manual_seed(n * hk)
     # rows of very different sizes

@@ -110,6 +110,20 @@ def test_shapes(n, h, hk, bs, d):
     run(n, h, hk, d, "bf16", bs, d, (d // 4, d // 4), False)
 
 
+@pytest.mark.parametrize("n", [1, 7, 64, 129, 1500])
+@pytest.mark.parametrize("h,hk", [(1, 1), (2, 1), (3, 3), (8, 1), (9, 2), (16, 3), (7, 5), (40, 2),
+                                  (12, 7), (2, 8), (1, 16)])
+@pytest.mark.parametrize("d,adjacent", [(64, True), (128, False)])
+def test_few_heads(n, h, hk, d, adjacent):
+    """Head counts below, at and above a work item's, for queries and for keys."""
+    run(n, h, hk, d, "fp16" if adjacent else "bf16", 16, d // 2, (3, d // 4 - 3), adjacent)
+
+
+def test_few_heads_packed_in_place():
+    run(300, 3, 2, 64, "bf16", 16, 64, (32,), False, packed=True, shift=1, in_place=True)
+    run(300, 1, 1, 128, "fp16", 16, 128, (30, 34), True, packed=True, shift=0, in_place=True)
+
+
 @pytest.mark.parametrize("adjacent", [False, True])
 @pytest.mark.parametrize("shift,d", [(0, 128), (8, 64), (1, 128), (3, 64)])
 @pytest.mark.parametrize("in_place", [False, True])
