@@ -3,8 +3,12 @@
 //
 // With codes kc, vc and scales ks, vs of key t, query row q and c = softmax scale * log2 e:
 //   x_t = c ks_t (q . kc_t),  m = max x,  l = sum 2^(x_t - m),  o = sum (2^(x_t - m) vs_t) vc_t / l
-// The work split (stream-K over key tiles), the partial results and their combine are those of
-// decode_kernel.cuh and decode_tc.cuh. What differs:
+// The work split (stream-K over key tiles), the partial results and their order are those of
+// decode_kernel.cuh and decode_tc.cuh. Bound by the bytes of codes and scales: 256 sequences of
+// 100 to 2,048 positions (16 / 8 heads of 128) take 84 us, 6.7 TB/s or 0.99 of the copy rate; 8 of
+// 32k to 131k with 32 / 8 heads 217, 7.0 TB/s; 200 of up to 4,096 with heads of 64 66 us at block
+// size 32 and more (6.2 TB/s) and 71 at 16, whose 8 KB runs the memory serves more slowly. Without
+// any products these take 83.6, 218, 63 and 67. What differs from the 16-bit kernels:
 //
 //  * A code is half as many bytes, so a stage of 64 KB holds twice the tokens, and every byte has
 //    to be widened: e4m3 by the hardware's conversion to fp16 (exact), int8 by placing the byte
@@ -12,7 +16,7 @@
 //    becomes two fp16 words of an MMA operand.
 //  * Both products are taken transposed, S^T = K Q^T and O^T = V^T W^T: 16 tokens, or 16 dims, are
 //    the 16 rows of an MMA and the up to 8 heads of a group its 8 columns, so that no row is
-//    padding (with the heads as rows half of them are, and every byte is multiplied twice).
+//    padding (with the heads as rows half of them are: 114 us against 89 for the 256 sequences).
 //    K: ldmatrix gives a lane four consecutive dims of a token; its two words stand for dims 4i,
 //    4i+1 and 4i+2, 4i+3, and the queries are loaded in the same order.
 //    V: the transposing ldmatrix moves 16-bit pieces, so a register holds dims 2i, 2i+1 of two
@@ -29,9 +33,11 @@
 //    lies 2^-39 below the largest scale or 2^-11 below w itself.
 //  * bf16 queries go to fp16 with a power of two for each head (row_to_f16 below).
 //  * Rows of shared memory are 128 bytes with the 128-byte swizzle: a head of 128 dims, or two
-//    heads of 64, which lie side by side in the cache (half as many rows for the copies: 72.8 ->
-//    66.0 us for 200 sequences of up to 4,096 positions, 32 / 8 heads of 64, block size 16). A single head of 64 has
-//    64-byte rows and the 64-byte swizzle.
+//    heads of 64, which lie side by side in the cache (half as many rows for the copies, 72.8 us
+//    against 70.9 for the 200 sequences at block size 16). A single head of 64 has 64-byte rows
+//    and the 64-byte swizzle.
+//  * Stages of 64 KB, as elsewhere: with half as many tokens of 64 dims in each the same 200
+//    sequences take 78 us (88 at block size 16).
 //  * Scales come beside the codes, [head][token] of each box, by TMA; their slots are padded to
 //    128 bytes (a TMA destination's alignment). Fetched by the producer's lanes instead, 16 bytes
 //    at a time, the same batches take 2 to 4 % longer.

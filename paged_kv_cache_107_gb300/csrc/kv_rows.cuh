@@ -14,6 +14,13 @@
 //
 // Quantisation: the row's largest magnitude from the 16-bit elements, two at a time (a NaN wins:
 // its pattern, like infinity's, is above every finite number's).
+//
+// Bound by bytes: 17,556 tokens of 16 / 8 heads of 128 are turned and stored in 43.4 us, 6.6 TB/s
+// or 0.98 of the copy rate; their keys and values quantised in 17.7 us (e4m3) and 18.5 (int8,
+// whose instructions take 80 % of the issue slots), 64,000 tokens in 57 and 59 (1.02, 0.99). Each
+// warp has one item and the grid as many blocks as that takes: one resident wave of blocks that
+// stride over the tokens was slower (49.8 us, 24.3), and so were items of 4 (46.8, 31.3) or of one
+// (50.2, 24.0) groups.
 #pragma once
 
 #include <cuda_runtime.h>
