@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl.g_eff = g_eff;
   }
   __syncthreads();
-  const int n_tiles = (int)(x1 - x0);
+  const int64_t n_tiles = x1 - x0;
   volatile int* abort_flag = &ctl.abort;
   auto gave_up = [&]() {
     if (lane == 0) {
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int q_n = 0;  // segments whose Q has been issued
     int s = 0;
     uint32_t phase = 0;  // of the stage's uses
-    for (int it = 0; it < n_tiles; ++it, s = s + 1 == S ? 0 : s + 1, phase ^= (s == 0)) {
+    for (int64_t it = 0; it < n_tiles; ++it, s = s + 1 == S ? 0 : s + 1, phase ^= (s == 0)) {
       const int64_t x = x0 + it;
       while (x >= pb + nb && b + 1 < B) {
         pb += nb;
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // copies still in flight land before the producer leaves
-    for (int it = n_tiles > S ? n_tiles - S : 0; it < n_tiles; ++it)
+    for (int64_t it = n_tiles > S ? n_tiles - S : 0; it < n_tiles; ++it)
       mbar_wait_copies(&ctl.full[it % S], (uint32_t)((it / S) & 1));
     for (int n = q_n > C::QS ? q_n - C::QS : 0; n < q_n; ++n)
       mbar_wait_copies(&ctl.q_full[n % C::QS], (uint32_t)((n / C::QS) & 1));
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int q_n = 0;
   int s = 0;
   uint32_t phase = 0;
-  for (int it = 0; it < n_tiles; ++it, s = s + 1 == S ? 0 : s + 1, phase ^= (s == 0)) {
+  for (int64_t it = 0; it < n_tiles; ++it, s = s + 1 == S ? 0 : s + 1, phase ^= (s == 0)) {
     if (!mbar_wait(&ctl.full[s], phase, abort_flag)) gave_up();
     const StageMeta& meta = ctl.meta[s];
     const int count = meta.count, flags = meta.flags;
