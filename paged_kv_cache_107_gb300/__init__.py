@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import importlib.util
 import math
 import os
 import threading
@@ -772,6 +773,29 @@ def pa_decode_shared(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
 
 
 # ---------------------------------------------------------------- 8-bit caches
+_CALLS = ("pa_store_kvcache_q8", "pa_load_kvcache_q8", "pa_decode_q8", "pa_rotary_store",
+          "pa_rotary_store_q8")
+_call_module = None
+
+
+def _calls():
+    """lib/_pa_call.so (csrc/py_call.c), bound to the loaded library."""
+    global _call_module
+    if _call_module is None:
+        lib = load_library()
+        with _lock:
+            if not os.path.exists(_build.CALL_PATH):
+                raise PagedAttentionError(f"{_build.CALL_PATH} not found; build it first "
+                                          "(python -m paged_kv_cache_107_gb300.build)")
+            spec = importlib.util.spec_from_file_location("_pa_call", _build.CALL_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                          for name in _CALLS))
+            _call_module = module
+    return _call_module
+
+
 class _PaQ8Cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int32)]
@@ -819,8 +843,9 @@ class Q8Cache:
             raise PagedAttentionError("codes and scales on several devices")
         self._tensors = k, v, k_scale, v_scale
         self._shape, self._index = tuple(k.shape), k.get_device()
-        self._arg = ctypes.byref(_PaQ8Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
-                                            v_scale.data_ptr(), _Q8_FORMATS[k.dtype]))
+        self._struct = _PaQ8Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                                  v_scale.data_ptr(), _Q8_FORMATS[k.dtype])
+        self._arg = ctypes.addressof(self._struct)
 
     k = property(lambda self: self._tensors[0], doc="codes of K")
     v = property(lambda self: self._tensors[1], doc="codes of V")
@@ -884,12 +909,10 @@ def pa_store_kvcache_q8(k: torch.Tensor, v: torch.Tensor, cache: Q8Cache,
     dt, n = k.dtype, k.shape[0] if k.dim() == 3 else -1
     ks, vs = _rows("k", k, dt, n, hk, d), _rows("v", v, dt, n, hk, d)
     _slots(slot_mapping, n)
-    fn = _fns.get("pa_store_kvcache_q8") or _typed(
-        "pa_store_kvcache_q8", [_VP, _VP, _I64, _I64, _I32, _VP, _VP, _I32, _I32, _I32, _I32, _I64,
-                                _VP, _VP])
-    rc = fn(k.data_ptr(), v.data_ptr(), ks, vs, PA_DTYPE[dt], cache._arg, slot_mapping.data_ptr(), n,
-            hk, d, bs, nb, None if dev_err is None else dev_err.data_ptr(),
-            _stream_of(stream, cache._index))
+    rc = (_call_module or _calls()).pa_store_kvcache_q8(
+        k.data_ptr(), v.data_ptr(), ks, vs, PA_DTYPE[dt], cache._arg, slot_mapping.data_ptr(), n, hk,
+        d, bs, nb, None if dev_err is None else dev_err.data_ptr(),
+        _stream_of(stream, cache._index))
     if rc:
         _check(rc, "pa_store_kvcache_q8")
 
@@ -913,11 +936,9 @@ def pa_load_kvcache_q8(k_out: torch.Tensor, v_out: torch.Tensor, cache: Q8Cache,
         raise PagedAttentionError(f"k_out and v_out must be {shape}")
     if not (k_out.is_contiguous() and v_out.is_contiguous()):
         raise PagedAttentionError("k_out and v_out must be contiguous")
-    fn = _fns.get("pa_load_kvcache_q8") or _typed(
-        "pa_load_kvcache_q8", [_VP, _VP, _I32, _VP, _VP, _I32, _I32, _I32, _I32, _I64, _VP, _VP])
-    rc = fn(k_out.data_ptr(), v_out.data_ptr(), PA_DTYPE[dt], cache._arg, blocks.data_ptr(), n, hk,
-            d, bs, nb, None if dev_err is None else dev_err.data_ptr(),
-            _stream_of(stream, cache._index))
+    rc = (_call_module or _calls()).pa_load_kvcache_q8(
+        k_out.data_ptr(), v_out.data_ptr(), PA_DTYPE[dt], cache._arg, blocks.data_ptr(), n, hk, d, bs,
+        nb, None if dev_err is None else dev_err.data_ptr(), _stream_of(stream, cache._index))
     if rc:
         _check(rc, "pa_load_kvcache_q8")
 
@@ -951,13 +972,11 @@ def pa_decode_q8(out: torch.Tensor, q: torch.Tensor, cache: Q8Cache, block_table
         workspace = _stream_workspace(("decode", H, hk, D),
                                       lambda: DecodeWorkspace(max(B, 1), H, hk, D, q.device),
                                       lambda w: w.fits(B, H, hk, D), q.device, stream)
-    fn = _fns.get("pa_decode_q8") or _typed(
-        "pa_decode_q8", [_VP, _VP, _VP, _VP, _I32, _VP, _I32, _I32, _I32, _I32, _I32, _I32, _I64,
-                         _F32, _I32, _VP, _SZ, _VP, _VP])
-    rc = fn(out.data_ptr(), q.data_ptr(), cache._arg, block_tables.data_ptr(),
-            block_tables.shape[1], context_lens.data_ptr(), B, H, hk, D, PA_DTYPE[dt], bs, nb,
-            _scale(scale), int(grid_ctas), workspace.buffer.data_ptr(), workspace.nbytes,
-            None if dev_err is None else dev_err.data_ptr(), _stream_of(stream, cache._index))
+    rc = (_call_module or _calls()).pa_decode_q8(
+        out.data_ptr(), q.data_ptr(), cache._arg, block_tables.data_ptr(), block_tables.shape[1],
+        context_lens.data_ptr(), B, H, hk, D, PA_DTYPE[dt], bs, nb, _scale(scale), int(grid_ctas),
+        workspace.buffer.data_ptr(), workspace.nbytes,
+        None if dev_err is None else dev_err.data_ptr(), _stream_of(stream, cache._index))
     if rc:
         _check(rc, "pa_decode_q8")
     return out
@@ -1025,8 +1044,9 @@ class Rotary:
                          torch.tensor(axes, dtype=torch.int32, device=device))
         self._form = head_dim, rotary_dim, num_axes, bool(adjacent), float(amplitude)
         self._index = self.turns.get_device()
-        self._arg = ctypes.byref(_PaRotary(self.turns.data_ptr(), self.axes.data_ptr(), rotary_dim,
-                                           num_axes, int(self.adjacent), self.amplitude))
+        self._struct = _PaRotary(self.turns.data_ptr(), self.axes.data_ptr(), rotary_dim, num_axes,
+                                 int(self.adjacent), self.amplitude)
+        self._arg = ctypes.addressof(self._struct)
 
     turns = property(lambda self: self._tensors[0], doc="fractions of a turn, int64 read as uint64")
     axes = property(lambda self: self._tensors[1], doc="axis of each pair, int32")
@@ -1035,10 +1055,6 @@ class Rotary:
     num_axes = property(lambda self: self._form[2])
     adjacent = property(lambda self: self._form[3])
     amplitude = property(lambda self: self._form[4])
-
-
-_ROTARY_ARGS = [_VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _I32, _VP, _I64, _VP]
-_ROTARY_TAIL = [_VP, _I32, _I32, _I32, _I32, _I32, _I64, _VP, _VP]
 
 
 def _rotary_store(name, q_out, q, k, v, positions, rotary, shape, slot_mapping, caches, k_cache,
@@ -1069,11 +1085,11 @@ def _rotary_store(name, q_out, q, k, v, positions, rotary, shape, slot_mapping, 
     if pos_stride[-1] != 1 and n > 1:
         raise PagedAttentionError("positions of one axis must be contiguous")
     _slots(slot_mapping, n)
-    fn = _fns.get(name) or _typed(name, _ROTARY_ARGS + [_VP] * len(caches) + _ROTARY_TAIL)
-    rc = fn(q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out_stride, q_stride,
-            k_stride, v_stride, PA_DTYPE[dt], positions.data_ptr(), pos_stride[0], rotary._arg,
-            *caches, slot_mapping.data_ptr(), n, h, hk, d, bs, nb,
-            None if dev_err is None else dev_err.data_ptr(), _stream_of(stream, index))
+    rc = getattr(_call_module or _calls(), name)(
+        q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out_stride, q_stride, k_stride,
+        v_stride, PA_DTYPE[dt], positions.data_ptr(), pos_stride[0], rotary._arg, *caches,
+        slot_mapping.data_ptr(), n, h, hk, d, bs, nb,
+        None if dev_err is None else dev_err.data_ptr(), _stream_of(stream, index))
     if rc:
         _check(rc, name)
 

@@ -2,7 +2,8 @@
 
 Every .cu file under csrc/ is compiled for sm_103a only (one -gencode), in parallel, then
 linked into one shared library with a plain C ABI (include/pa.h). No torch headers are
-involved; the CUDA runtime is linked statically.
+involved; the CUDA runtime is linked statically. Beside it goes lib/_pa_call.so, the Python
+module of csrc/py_call.c.
 """
 from __future__ import annotations
 
@@ -12,11 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libpagedkv.so")
+CALL_SRC = os.path.join(CSRC, "py_call.c")
+CALL_PATH = os.path.join(LIB_DIR, "_pa_call.so")
 OBJ_DIR = os.path.join(LIB_DIR, "obj")
 GENCODE = "arch=compute_103a,code=sm_103a"
 
@@ -47,10 +51,34 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not (os.path.exists(LIB_PATH) and _call_up_to_date()):
         return False
     t = os.path.getmtime(LIB_PATH)
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _call_up_to_date() -> bool:
+    if not os.path.exists(CALL_PATH):
+        return False
+    header = os.path.join(os.path.dirname(HERE), "include", "pa.h")
+    t = os.path.getmtime(CALL_PATH)
+    return all(os.path.getmtime(p) <= t for p in (CALL_SRC, header))
+
+
+def build_call() -> str:
+    """Compile csrc/py_call.c for the running interpreter. Returns lib/_pa_call.so's path."""
+    os.makedirs(LIB_DIR, exist_ok=True)
+    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+    if not cc:
+        raise RuntimeError("no C compiler: set CC")
+    tmp = CALL_PATH + f".tmp{os.getpid()}"
+    cmd = [cc, "-O2", "-std=gnu11", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+           CALL_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed for {CALL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL_PATH)
+    return CALL_PATH
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: str = None) -> str:
@@ -63,6 +91,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: 
         return _build_to(lib_path, lib_path + ".obj", verbose, extra_flags)
     if not force and up_to_date():
         return LIB_PATH
+    build_call()
     return _build_to(LIB_PATH, OBJ_DIR, verbose, extra_flags)
 
 

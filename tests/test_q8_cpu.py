@@ -147,6 +147,41 @@ def test_reference_rounds_as_torch_does():
     assert codes.tolist() == [[448, 1], [224, 0.5], [0, 0], [0, 0]]
 
 
+def test_calls_without_ctypes(lib):
+    """The compiled binding passes every argument on: the statuses of the C ABI, for each call."""
+    calls = pk._calls()
+    c = pk._PaQ8Cache(16, 16, 16, 16, 1)
+    r = pk._PaRotary(16, 16, 128, 1, 0, 1.0)
+    a, ra = ctypes.addressof(c), ctypes.addressof(r)
+    store = [16, 16, 1024, 1024, 1, a, 16, 0, 8, 128, 16, 4, None, None]
+    load = [16, 16, 1, a, 16, 0, 8, 128, 16, 4, None, None]
+    decode = [16, 16, a, 16, 1, 16, 0, 16, 8, 128, 1, 16, 4, 0.0, 0, 256, 1 << 30, None, None]
+    head = [16, 16, 16, 16, 2048, 2048, 1024, 1024, 1, 16, 0, ra]
+    tail = [16, 0, 16, 8, 128, 16, 4, None, None]
+    for name, args, bad in (
+            ("pa_store_kvcache_q8", store, {2: 1023, 3: -5, 4: 0, 7: -1, 8: 0, 9: 96, 10: 0, 11: 0}),
+            ("pa_load_kvcache_q8", load, {2: 0, 3: None, 5: -1, 6: 0, 7: 96, 8: 0, 9: -1}),
+            ("pa_decode_q8", decode, {2: None, 4: -1, 6: -1, 7: 12, 8: 0, 9: 96, 10: 0, 11: 0, 12: 0,
+                                      14: -1}),
+            ("pa_rotary_store", head + [16, 16] + tail, {4: 2047, 5: 2047, 6: 1023, 7: 1023, 8: 0,
+                                                         11: None, 15: -1, 16: 0, 17: 0, 18: 96,
+                                                         19: 0, 20: 0}),
+            ("pa_rotary_store_q8", head + [a] + tail, {4: 2047, 5: 2047, 6: 1023, 7: 1023, 8: 0,
+                                                       11: None, 12: None, 14: -1, 15: 0, 16: 0,
+                                                       17: 96, 18: 0, 19: 0})):
+        fn = getattr(calls, name)
+        assert fn(*args) == 0, name  # nothing to do
+        for i, x in bad.items():
+            assert fn(*args[:i], x, *args[i + 1:]) in (1, 2, 3), (name, i)
+        for wrong in (args[:-1], args + [0], []):
+            with pytest.raises(TypeError):
+                fn(*wrong)
+        with pytest.raises(TypeError):
+            fn("x", *args[1:])
+    with pytest.raises(TypeError):
+        calls.pa_decode_q8(*decode[:13], "x", *decode[14:])
+
+
 # ---------------------------------------------------------------- the binding
 def host_cache(nb=2, bs=16, hk=8, d=128, dtype=torch.int8):
     return pk.Q8Cache(nb, bs, hk, d, dtype, device="cpu")
