@@ -251,18 +251,23 @@ __device__ __forceinline__ void wide_rows(const RowsArgs& a) {
                                 : static_cast<const uint16_t*>(a.k) + tok * a.k_stride);
   const bool vec = a.vec != 0;
   const int64_t slot = live ? __ldg(a.slots + tok) : -1;
+  // (rotary calls: a second group without a head is not loaded, 11.0 -> 10.7 us for 4,095 tokens of
+  // 32 / 8 heads of 64; alone, the quantising store is slower for the branch)
+  const bool two = !ROT || chunk * C::R + C::HPW < heads;
   uint4 xa[U], xb[U];
-  auto load = [&](bool v) {
+  auto load = [&](bool v, int n) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
+    for (int i = 0; i < n; ++i) {
       // (not under a condition of its own, which would put each load next to its use)
       const uint16_t* row = src + min(h0 + i * C::HPW, heads - 1) * D;
       xa[i] = ld_vec8(row + p.va, v);
       xb[i] = ld_vec8(row + p.vb, v);
     }
   };
-  if (vec) load(true);
-  else load(false);
+  if (ROT) xa[1] = xb[1] = make_uint4(0u, 0u, 0u, 0u);
+  if (vec && two) load(true, U);
+  else if (vec) load(true, 1);
+  else load(false, U);
   if constexpr (ROT) {
     if (!is_v) {
       float c[8], s[8];
@@ -481,7 +486,7 @@ int launch_rows_t(RowsArgs a, const DeviceInfo& info, cudaStream_t stream) {
   const int64_t n = a.num_tokens, q_heads = ROT ? a.num_heads : 0, kv_heads = a.num_kv_heads;
   // half full items at least; queries three quarters where keys and values take flat blocks anyway
   // (32,000 tokens of 4 / 2 heads of 128: 26.1 us flat, 30.4 wide; 9 / 3: 42.8 and 50.6)
-  const bool kv_wide = 2 * kv_heads >= R;
+  const bool kv_wide = ROT ? 2 * kv_heads >= R : kv_heads % R == 0;
   const bool q_wide = kv_wide ? 2 * q_heads >= R : 4 * q_heads >= 3 * over(q_heads, R) * R;
   a.q_chunks = q_wide ? (int)over(q_heads, R) : 0;
   a.kv_chunks = kv_wide ? (int)over(kv_heads, R) : 0;
