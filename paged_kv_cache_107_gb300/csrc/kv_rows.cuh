@@ -334,7 +334,7 @@ __device__ __forceinline__ void wide_rows(const RowsArgs& a) {
 // head count: a warp's rows may be of several tokens. The angles of the block's tokens are worked
 // out once, in shared memory. For fewer heads than half a wide item's, whose lanes would have no
 // row: 32,000 tokens of 1 / 1 heads of 128 take 17.3 us, in wide items 35.4; quantised alone 6.6
-// and 27.5. (A wide item that is half full or more is up to 6 % faster.)
+// and 27.5. (The launcher has the rule.)
 template <int D, bool F16, int FMT, bool ROT, bool ADJ>
 __device__ __forceinline__ void flat_rows(const RowsArgs& a, uint32_t blk, bool is_q, bool is_v) {
   using C = RowsCfg<D>;
@@ -484,9 +484,12 @@ int launch_rows_t(RowsArgs a, const DeviceInfo& info, cudaStream_t stream) {
   constexpr int64_t R = RowsCfg<D>::R;
   auto over = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
   const int64_t n = a.num_tokens, q_heads = ROT ? a.num_heads : 0, kv_heads = a.num_kv_heads;
-  // half full items at least; queries three quarters where keys and values take flat blocks anyway
-  // (32,000 tokens of 4 / 2 heads of 128: 26.1 us flat, 30.4 wide; 9 / 3: 42.8 and 50.6)
-  const bool kv_wide = ROT ? 2 * kv_heads >= R : kv_heads % R == 0;
+  // Wide items have to be half full (of 128 dims: more than that; 20,000 tokens of 4 / 4 heads 24.7 us
+  // flat, 29.0 wide, of 6 / 6 32.4 and 31.0), queries three quarters where keys and values take
+  // flat blocks anyway (32,000 of 4 / 2 heads 26.1 and 30.4, of 9 / 3 42.8 and 50.6). Without
+  // angles only full ones are wide (20,000 of 12 heads of 64 15.8 and 18.0).
+  const bool kv_wide =
+      ROT ? (D == 128 ? 2 * kv_heads > R : 2 * kv_heads >= R) : kv_heads % R == 0;
   const bool q_wide = kv_wide ? 2 * q_heads >= R : 4 * q_heads >= 3 * over(q_heads, R) * R;
   a.q_chunks = q_wide ? (int)over(q_heads, R) : 0;
   a.kv_chunks = kv_wide ? (int)over(kv_heads, R) : 0;
