@@ -30,7 +30,9 @@
 //  * The K scale multiplies the score. The V scale is taken into the weight, which is then rounded
 //    to fp16: w_t = p_t vs_t 2^(14-E), E the exponent of the largest vs met so far by the warp
 //    (when it grows the accumulators are rescaled), so that w < 2^15 and what is rounded off
-//    lies 2^-39 below the largest scale or 2^-11 below w itself.
+//    lies 2^-39 below the largest scale or 2^-11 below w itself. That is a quarter of a bf16
+//    result's own rounding; an fp16 result's it would double in square (0.00030 of the result's
+//    size against 0.00021), so there what is rounded off goes through a second product.
 //  * bf16 queries go to fp16 with a power of two for each head (row_to_f16 below).
 //  * Rows of shared memory are 128 bytes with the 128-byte swizzle: a head of 128 dims, or two
 //    heads of 64, which lie side by side in the cache (half as many rows for the copies, 72.8 us
@@ -224,8 +226,7 @@ struct Q8Maps {
 // for elements 2^28 and more below that largest. The query sits in the four lanes of a quad.
 // Returns the factor that undoes it.
 template <int KC>
-__device__ __forceinline__ float row_to_f16(uint32_t (&qa)[KC][2], bool f16) {
-  if (f16) return 1.f;
+__device__ __forceinline__ float row_to_f16(uint32_t (&qa)[KC][2]) {
   uint32_t top = 0u;
 #pragma unroll
   for (int c = 0; c < KC; ++c)
@@ -246,7 +247,7 @@ __device__ __forceinline__ float row_to_f16(uint32_t (&qa)[KC][2], bool f16) {
   return pow2f(e - 14);
 }
 
-template <int HS, int D, int FMT>
+template <int HS, int D, int FMT, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_q8_kernel(const __grid_constant__ Q8Maps tm, const DecodeQ8Args a, const int tb) {
   using C = Q8Cfg<HS, D>;
@@ -668,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ctl.q_empty[qs]);
       ++q_n;
       // (not 0: masked scores are -inf)
-      const float c_gid = fmaxf(row_to_f16<KC>(qa, a.f16 != 0) * a.scale_log2, 1.4e-45f);
+      const float c_gid = fmaxf((F16 ? 1.f : row_to_f16<KC>(qa)) * a.scale_log2, 1.4e-45f);
       cq[0] = __shfl_sync(0xffffffffu, c_gid, 8 * tig);
       cq[1] = __shfl_sync(0xffffffffu, c_gid, 8 * tig + 4);
     }
@@ -776,7 +777,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float nu = pow2f(14 - e_run);
-      uint32_t wt[NI];  // the operand's words: head gid, tokens 8 i + 2 tig, + 1
+      // the operand's words: head gid, tokens 8 i + 2 tig, + 1; for fp16 results what they lose too
+      uint32_t wt[NI], wl[F16 ? NI : 1];
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const float p0 = fast_exp2(fmaf(sc[i >> 1][2 * (i & 1)], cq[0], -m_ref[0]));
@@ -784,7 +786,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         l_part[0] += p0;
         l_part[1] += p1;
         vf[i] *= nu;
-        wt[i] = transpose8(f2_elt2<true>(p0 * vf[i], p1 * vf[i]));
+        const float w0 = p0 * vf[i], w1 = p1 * vf[i];
+        const uint32_t hi = f2_elt2<true>(w0, w1);
+        wt[i] = transpose8(hi);
+        if constexpr (F16) {
+          const float2 held = f16x2_f2(hi);
+          wl[i] = transpose8(f2_elt2<true>(w0 - held.x, w1 - held.y));
+        }
       }
       // ---- O^T += V^T W^T: blocks of 16 tokens ----------------------------------------
 #pragma unroll
@@ -802,6 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             widen4<FMT, true>(r[2 * i], a0, a1);
             widen4<FMT, true>(r[2 * i + 1], a2, a3);
             mma_f16(o[2 * p + i], a0, a1, a2, a3, wt[2 * h], wt[2 * h + 1]);
+            if constexpr (F16) mma_f16(o[2 * p + i], a0, a1, a2, a3, wl[2 * h], wl[2 * h + 1]);
           }
         }
       }
@@ -890,8 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int n = 0; n < KC; ++n) {
               const float r0 = o[n][e] * inv, r1 = o[n][2 + e] * inv;
-              *reinterpret_cast<uint32_t*>(dst + n * 16) =
-                  a.f16 ? f2_elt2<true>(r0, r1) : f2_elt2<false>(r0, r1);
+              *reinterpret_cast<uint32_t*>(dst + n * 16) = f2_elt2<F16>(r0, r1);
             }
           } else {
             float* dst = a.part_o + (((int64_t)c * 2 + slot) * H + hg) * D + 2 * gid;
@@ -919,12 +927,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __threadfence();
             const bool first_slot = tile_begin(c_lo, nt, g) < pb;
             uint16_t* dst = static_cast<uint16_t*>(a.out) + ((int64_t)b * H + kvh * G) * D;
-            if (a.f16)
-              combine_q8<D, true>(a.part_o, a.part_lse, dst, H, kvh * G, G, (int)c_lo, nseg,
-                                  first_slot, lane);
-            else
-              combine_q8<D, false>(a.part_o, a.part_lse, dst, H, kvh * G, G, (int)c_lo, nseg,
-                                   first_slot, lane);
+            combine_q8<D, F16>(a.part_o, a.part_lse, dst, H, kvh * G, G, (int)c_lo, nseg, first_slot,
+                               lane);
             if (lane == 0) *counter = 0;  // leave the counter zero for the next call
           }
         }
@@ -940,14 +944,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int HS, int D, int FMT>
+template <int HS, int D, int FMT, bool F16>
 int launch_decode_q8_t(DecodeQ8Args a, const DeviceInfo& info, cudaStream_t stream) {
   using C = Q8Cfg<HS, D>;
   static std::atomic<bool> attr_done[64];  // zero-initialised: false
   const int dev = info.device;
   if (dev < 0 || dev >= 64) return PA_ERR_CUDA;
   if (!attr_done[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(paged_decode_q8_kernel<HS, D, FMT>,
+    if (cudaFuncSetAttribute(paged_decode_q8_kernel<HS, D, FMT, F16>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
       return PA_ERR_CUDA;
     attr_done[dev].store(true, std::memory_order_release);
@@ -968,19 +972,19 @@ int launch_decode_q8_t(DecodeQ8Args a, const DeviceInfo& info, cudaStream_t stre
   const int slabs = a.num_kv_heads / HS;
   if (a.auto_grid) a.grid_ctas = slabs < info.num_sms ? info.num_sms / slabs : 1;
   const dim3 grid((unsigned)a.grid_ctas, (unsigned)slabs);
-  if (launch_dependent(paged_decode_q8_kernel<HS, D, FMT>, grid, dim3(kThreads), C::SMEM, stream,
+  if (launch_dependent(paged_decode_q8_kernel<HS, D, FMT, F16>, grid, dim3(kThreads), C::SMEM, stream,
                        tm, a, tb) != cudaSuccess)
     return PA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool F16>
 int dispatch_slab_q8(const DecodeQ8Args& a, const DeviceInfo& info, cudaStream_t stream) {
   switch (decode_head_slab(a.num_kv_heads)) {
-    case 8: return launch_decode_q8_t<8, D, FMT>(a, info, stream);
-    case 4: return launch_decode_q8_t<4, D, FMT>(a, info, stream);
-    case 2: return launch_decode_q8_t<2, D, FMT>(a, info, stream);
-    default: return launch_decode_q8_t<1, D, FMT>(a, info, stream);
+    case 8: return launch_decode_q8_t<8, D, FMT, F16>(a, info, stream);
+    case 4: return launch_decode_q8_t<4, D, FMT, F16>(a, info, stream);
+    case 2: return launch_decode_q8_t<2, D, FMT, F16>(a, info, stream);
+    default: return launch_decode_q8_t<1, D, FMT, F16>(a, info, stream);
   }
 }
 

@@ -67,8 +67,9 @@ def dequantised(codes, scales):
 
 def decode(q, k_rows, v_rows, v_scale_top, tables, lens, bs, out_dtype, scale=None, code_max=448.0):
     """(out, tolerance) of pa_decode_q8. Beyond attention_reference's bound for the scores: each
-    weight p vs is rounded to fp16, 2^-11 relative or 2^-39 of the largest value scale, times a
-    code of at most code_max, once for each key; the output is rounded once to its type."""
+    weight p vs is rounded to fp16, 2^-11 relative (with fp16 results to two fp16 numbers, 2^-22) or
+    2^-39 of the largest value scale, times a code of at most code_max, once for each key; the
+    output is rounded once to its type."""
     q = q.double().cpu().numpy()
     out, tol = np.zeros(q.shape), np.zeros(q.shape)
     half = torch.finfo(out_dtype).eps / 2
@@ -78,7 +79,7 @@ def decode(q, k_rows, v_rows, v_scale_top, tables, lens, bs, out_dtype, scale=No
         o, A, dev = ref.attend(q[b:b + 1], k_rows[rows], v_rows[rows], [n - 1],
                                np.ones((1, n), bool), scale=scale)
         out[b] = o[0]
-        weights = 2.0 ** -11 * A + n * code_max * 2.0 ** -39 * v_scale_top
+        weights = (2.0 ** -22 if out_dtype == torch.float16 else 2.0 ** -11) * A + n * code_max * 2.0 ** -39 * v_scale_top
         tol[b] = (half * np.abs(o) + (1 + half) * (weights + np.expm1(2 * dev) * A)
                   + 2.0 ** -25)[0]
     return out, tol
