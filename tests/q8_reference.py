@@ -65,11 +65,16 @@ def dequantised(codes, scales):
     return x.reshape(-1, *x.shape[2:]).numpy()
 
 
-def decode(q, k_rows, v_rows, v_scale_top, tables, lens, bs, out_dtype, scale=None, code_max=448.0):
+def decode(q, k_rows, v_rows, v_scale_top, tables, lens, bs, out_dtype, scale=None, code_max=448.0,
+           k_scale_top=0.0):
     """(out, tolerance) of pa_decode_q8. Beyond attention_reference's bound for the scores: each
     weight p vs is rounded to fp16, 2^-11 relative (with fp16 results to two fp16 numbers, 2^-22) or
     2^-39 of the largest value scale, times a code of at most code_max, once for each key; the
-    output is rounded once to its type."""
+    output is rounded once to its type.
+
+    int8 codes x enter the scores as 1152 + x, and the sums start at -1152 sum q: the D / 16 MMAs of
+    a sum each round (or truncate) twice at most, 2^-23 of partial sums that reach
+    (1152 + 1152 + 127) sum |q|, in units of scale times the key's scale."""
     q = q.double().cpu().numpy()
     out, tol = np.zeros(q.shape), np.zeros(q.shape)
     half = torch.finfo(out_dtype).eps / 2
@@ -79,6 +84,11 @@ def decode(q, k_rows, v_rows, v_scale_top, tables, lens, bs, out_dtype, scale=No
         o, A, dev = ref.attend(q[b:b + 1], k_rows[rows], v_rows[rows], [n - 1],
                                np.ones((1, n), bool), scale=scale)
         out[b] = o[0]
+        if code_max == 127.0:
+            d = q.shape[-1]
+            factor = d ** -0.5 if scale is None else scale
+            dev = dev + (2 * (d // 16) * 2.0 ** -23 * 2431 * np.abs(q[b]).sum(-1)[None, :, None]
+                         * factor * k_scale_top)
         weights = (2.0 ** -22 if out_dtype == torch.float16 else 2.0 ** -11) * A + n * code_max * 2.0 ** -39 * v_scale_top
         tol[b] = (half * np.abs(o) + (1 + half) * (weights + np.expm1(2 * dev) * A)
                   + 2.0 ** -25)[0]

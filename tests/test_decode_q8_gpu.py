@@ -64,7 +64,7 @@ class Case:
         v = ref.dequantised(self.cache.v, self.cache.v_scale)
         top = float(self.cache.v_scale.nan_to_num(0.0).max())
         return ref.decode(self.q, k, v, top, self.tables, self.lens, self.bs, self.dtype, scale,
-                          CODE_MAX[self.fmt])
+                          CODE_MAX[self.fmt], float(self.cache.k_scale.nan_to_num(0.0).max()))
 
     def check(self, what="", **kw):
         out = self.run(**kw)

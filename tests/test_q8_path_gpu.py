@@ -57,7 +57,8 @@ class Server:
     def check_decode(self, q, out):
         k, v = self.rows()
         o, tol = ref.decode(q, k, v, float(self.cache.v_scale.max()), self.tables, self.lens,
-                            self.bs, torch.bfloat16, None, 448.0)
+                            self.bs, torch.bfloat16, None, 448.0 if self.fmt == "e4m3" else 127.0,
+                            float(self.cache.k_scale.max()))
         att.assert_within(out.double().cpu().numpy(), o, tol)
         assert self.err.item() == 0
 
