@@ -585,10 +585,9 @@ int pa_load_kvcache_q8(void* k_out, void* v_out, int dtype, const pa_q8_cache* c
  *
  * Arithmetic: codes are widened exactly; a bf16 query row is scaled by a power of two into
  * fp16's range (elements below the row's largest by a factor of 2^28 or more lose bits); fp32
- * products, softmax and accumulation; each probability times its key's value scale is rounded
- * to fp16 before the second product (2^-11 relative; with fp16 results to the sum of two fp16
- * numbers, 2^-22; either way 2^-39 of the largest value scale met so far where that is more); one
- * rounding of the output.
+ * products, softmax and accumulation; each probability times its key's value scale enters the
+ * second product as the sum of two fp16 numbers (off by 2^-22 of itself, or by 2^-39 of the
+ * largest value scale met so far where that is more); one rounding of the output.
  * Block sizes that no power of two from 8 up divides are much slower than others.
  */
 int pa_decode_q8(void* out, const void* q, const pa_q8_cache* cache, const int32_t* block_tables,

@@ -30,12 +30,14 @@
 //  * A warp takes 32 tokens of a stage (64 with heads of 64), a lane two heads' scores of four
 //    (eight) of them. The running maximum is moved only when one of these scores exceeds it (one
 //    vote): most tiles need no shuffle and no rescaling.
-//  * The K scale multiplies the score. The V scale is taken into the weight, which is then rounded
-//    to fp16: w_t = p_t vs_t 2^(14-E), E the exponent of the largest vs met so far by the warp
-//    (when it grows the accumulators are rescaled), so that w < 2^15 and what is rounded off
-//    lies 2^-39 below the largest scale or 2^-11 below w itself. That is a quarter of a bf16
-//    result's own rounding; an fp16 result's it would double in square (0.00030 of the result's
-//    size against 0.00021), so there what is rounded off goes through a second product.
+//  * The K scale multiplies the score. The V scale is taken into the weight, which then enters the
+//    product as the sum of two fp16 numbers: w_t = p_t vs_t 2^(14-E), E the exponent of the largest
+//    vs met so far by the warp (when it grows the accumulators are rescaled), so that w < 2^15 and
+//    what is rounded off lies 2^-39 below the largest scale or 2^-22 below w itself. With one
+//    fp16 number, 2^-11, an fp16 result's error grows by half (0.00030 of its size against 0.00021),
+//    and bf16 results come out a unit of the last place away from the exact one's rounding wherever
+//    that lies near a tie. The second product costs 0 to 4 %: with bf16 results 84.6 -> 84.8 us for the 256
+//    sequences, 70.1 -> 72.5 for the 200, 54.6 -> 56.9 for 256 with 32 / 4 heads of 128.
 //  * bf16 queries go to fp16 with a power of two for each head (row_to_f16 below).
 //  * Rows of shared memory are 128 bytes with the 128-byte swizzle: a head of 128 dims, or two
 //    heads of 64, which lie side by side in the cache (half as many rows for the copies, 72.8 us
@@ -795,8 +797,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float nu = pow2f(14 - e_run);
-      // the operand's words: head gid, tokens 8 i + 2 tig, + 1; for fp16 results what they lose too
-      uint32_t wt[NI], wl[F16 ? NI : 1];
+      // the operand's words, and what they lose: head gid, tokens 8 i + 2 tig, + 1
+      uint32_t wt[NI], wl[NI];
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const float p0 = fast_exp2(fmaf(sc[i >> 1][2 * (i & 1)], cq[0], -m_ref[0]));
@@ -807,10 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float w0 = p0 * vf[i], w1 = p1 * vf[i];
         const uint32_t hi = f2_elt2<true>(w0, w1);
         wt[i] = transpose8(hi);
-        if constexpr (F16) {
-          const float2 held = f16x2_f2(hi);
-          wl[i] = transpose8(f2_elt2<true>(w0 - held.x, w1 - held.y));
-        }
+        const float2 held = f16x2_f2(hi);
+        wl[i] = transpose8(f2_elt2<true>(w0 - held.x, w1 - held.y));
       }
       // ---- O^T += V^T W^T: blocks of 16 tokens ----------------------------------------
 #pragma unroll
@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             widen4<FMT, true>(r[2 * i], a0, a1);
             widen4<FMT, true>(r[2 * i + 1], a2, a3);
             mma_f16(o[2 * p + i], a0, a1, a2, a3, wt[2 * h], wt[2 * h + 1]);
-            if constexpr (F16) mma_f16(o[2 * p + i], a0, a1, a2, a3, wl[2 * h], wl[2 * h + 1]);
+            mma_f16(o[2 * p + i], a0, a1, a2, a3, wl[2 * h], wl[2 * h + 1]);
           }
         }
       }

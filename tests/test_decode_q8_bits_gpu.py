@@ -1,0 +1,63 @@
+"""pa_decode_q8 where few bits decide: bounds of each sequence and head alone, without the slack of
+test_decode_q8_gpu (whose value and key scales are the batch's largest)."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_107_gb300 as pk
+from tests import attention_reference as att
+from tests import q8_reference as ref
+from tests.test_decode_q8_gpu import CODE_MAX, DEV, Case
+
+pytestmark = pytest.mark.gpu
+
+
+def reference(case, scale=None):
+    """(out, tolerance). attention_reference's deviation of the scores (their products are exact,
+    the sums fp32); each weight is held in two fp16 numbers, 2^-22 relative or 2^-39 of the largest
+    value scale that the sequence holds for the head, times a code; the fp32 sums over the keys
+    take two MMAs for every 16 keys, and the parts of a sequence, at most 2^-23 of A each
+    (16 of them here); the output is rounded once to its type."""
+    k = ref.dequantised(case.cache.k, case.cache.k_scale)
+    v = ref.dequantised(case.cache.v, case.cache.v_scale)
+    vs = case.cache.v_scale.cpu().double().transpose(1, 2).reshape(-1, case.Hk).numpy()
+    q = case.q.double().cpu().numpy()
+    least = 2.0 ** -25 if case.dtype == torch.float16 else 2.0 ** -134  # half a subnormal's step
+    out, tol = np.zeros(q.shape), np.full(q.shape, least)
+    half = torch.finfo(case.dtype).eps / 2
+    for b, n in enumerate(case.lens):
+        if n == 0:
+            continue
+        t = np.arange(n)
+        rows = np.asarray(case.tables[b])[t // case.bs].astype(np.int64) * case.bs + t % case.bs
+        o, A, dev = att.attend(q[b:b + 1], k[rows], v[rows], [n - 1], np.ones((1, n), bool),
+                               scale=scale)
+        top = np.repeat(vs[rows].max(0), q.shape[1] // case.Hk)[None, :, None]
+        weights = (2.0 ** -22 + (n / 8 + 16) * 2.0 ** -23) * A
+        weights = weights + n * CODE_MAX[case.fmt] * 2.0 ** -39 * top
+        out[b] = o[0]
+        tol[b] += (half * np.abs(o) + (1 + half) * (weights + np.expm1(2 * dev) * A))[0]
+    return out, tol
+
+
+def check(case, scale=None):
+    out = case.run(scale=scale)
+    att.assert_within(out.double().cpu().numpy(), *reference(case, scale))
+    assert case.err.item() == 0
+    return out
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,Hk,G", [(128, 8, 2), (64, 8, 4), (64, 1, 8), (128, 3, 1)])
+def test_results_are_rounded_once(fmt, dtype, D, Hk, G):
+    """Scores near each other: nothing but the output's rounding is seen."""
+    check(Case([1 + 3 * b for b in range(20)], Hk * G, Hk, D, fmt, dtype, 16, seed=G), scale=1e-3)
+    check(Case([700, 33], Hk * G, Hk, D, fmt, dtype, 16, seed=G), scale=1e-3)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,Hk", [(128, 8), (64, 2)])
+def test_rows_of_very_different_sizes(fmt, dtype, D, Hk):
+    check(Case([300, 1, 77, 500], Hk * 4, Hk, D, fmt, dtype, 16, seed=5, spread=8), scale=1e-4)
