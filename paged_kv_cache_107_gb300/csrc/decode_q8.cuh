@@ -7,16 +7,16 @@
 // decode_kernel.cuh and decode_tc.cuh. Bound by the bytes of codes and scales: 256 sequences of
 // 100 to 2,048 positions (16 / 8 heads of 128) take 84 us, 6.7 TB/s or 0.99 of the copy rate; 8 of
 // 32k to 131k with 32 / 8 heads 217, 7.0 TB/s; 200 of up to 4,096 with 32 / 8 fp16 heads of 64 66 us
-// at block size 32 and more (6.2 TB/s) and 72 at 16, whose 8 KB runs the memory serves more slowly.
+// at block size 32 and more (6.2 TB/s) and 75.5 at 16, whose 8 KB runs the memory serves more slowly.
 // Without any products these take 83.6, 218, 63 and 67. What differs from the 16-bit kernels:
 //
 //  * A code is half as many bytes, so a stage of 64 KB holds twice the tokens, and every byte has
 //    to be widened: e4m3 by the hardware's conversion to fp16 (exact), int8 by placing the byte
 //    in an fp16 number (q8.cuh). Nothing is widened in shared memory: a register of four codes
-//    becomes two fp16 words of an MMA operand. int8 keys x stay 1152 + x as they come, and the
-//    scores' sums start at -1152 sum q instead (75.3 -> 72.1 us for the 200 sequences below);
-//    the fp32 sums pass through 2,431 sum |q| at most on the way, 2^-23 of which a score of 127
-//    sum |q| may lose. For the values' long sums that would be too much.
+//    becomes two fp16 words of an MMA operand. (int8 keys x could enter the scores as the 1152 + x
+//    that they come as, with sums that start at -1152 sum q: 72.2 us instead of 75.5 for the 200
+//    sequences. But the fp32 sums would pass through 2,431 sum |q|, where each of the D / 16
+//    MMAs rounds: scores of queries far from zero mean lose more than an fp16 result's own rounding.)
 //  * Both products are taken transposed, S^T = K Q^T and O^T = V^T W^T: 16 tokens, or 16 dims, are
 //    the 16 rows of an MMA and the up to 8 heads of a group its 8 columns, so that no row is
 //    padding (with the heads as rows half of them are: 114 us against 89 for the 256 sequences).
@@ -611,7 +611,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // of heads 2 tig, + 1: running max (log2 units), the same but 0 while it is -inf, this lane's
   // part of the sum, c over the power of two in the fp16 queries
   float m_run[2], m_ref[2], l_part[2], cq[2];
-  float bias[2] = {0.f, 0.f};     // where the sums of their scores start (kCodeBias)
   constexpr int kE0 = -112;
   int e_run = kE0;                // exponent of the largest value scale so far
   auto reset = [&]() {
@@ -676,19 +675,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++q_n;
       // (not 0: masked scores are -inf)
       const float c_gid = fmaxf((F16 ? 1.f : row_to_f16<KC>(qa)) * a.scale_log2, 1.4e-45f);
-      if constexpr (kCodeBias<FMT> != 0.f) {
-        float sum = 0.f;
-#pragma unroll
-        for (int kc = 0; kc < KC; ++kc) {
-          const float2 x = f16x2_f2(qa[kc][0]), y = f16x2_f2(qa[kc][1]);
-          sum += (x.x + x.y) + (y.x + y.y);
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum *= -kCodeBias<FMT>;
-        bias[0] = __shfl_sync(0xffffffffu, sum, 8 * tig);
-        bias[1] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4);
-      }
       cq[0] = __shfl_sync(0xffffffffu, c_gid, 8 * tig);
       cq[1] = __shfl_sync(0xffffffffu, c_gid, 8 * tig + 4);
     }
@@ -724,8 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sc[TW / 16][4];
 #pragma unroll
       for (int h = 0; h < TW / 16; ++h) {
-        sc[h][0] = sc[h][2] = bias[0];
-        sc[h][1] = sc[h][3] = bias[1];
+        sc[h][0] = sc[h][1] = sc[h][2] = sc[h][3] = 0.f;
         const int t = tw0 + 16 * h + (lane & 7) + (((lane >> 3) & 1) << 3);
         const uint32_t base = st_u + (uint32_t)row_off(t) + ((uint32_t)(hi ^ (sw & 1)) << 4);
 #pragma unroll
@@ -735,8 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t a0, a1, a2, a3;
-            widen4_biased<FMT>(r[2 * i], a0, a2);
-            widen4_biased<FMT>(r[2 * i + 1], a1, a3);
+            widen4<FMT, false>(r[2 * i], a0, a2);
+            widen4<FMT, false>(r[2 * i + 1], a1, a3);
             mma_f16(sc[h], a0, a1, a2, a3, qa[2 * p + i][0], qa[2 * p + i][1]);
           }
         }

@@ -28,21 +28,6 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
   }
 }
 
-// Four codes of a word for a product whose sum starts at kCodeBias times the other operand's sum,
-// less: int8 codes x as 1152 + x, without the subtraction.
-template <int FMT>
-__device__ __forceinline__ void widen4_biased(uint32_t w, uint32_t& a, uint32_t& b) {
-  if constexpr (FMT == PA_Q8_E4M3) {
-    widen4<FMT, false>(w, a, b);
-  } else {
-    w ^= 0x80808080u;
-    a = __byte_perm(w, 0x64646464u, 0x4140);
-    b = __byte_perm(w, 0x64646464u, 0x4342);
-  }
-}
-template <int FMT>
-constexpr float kCodeBias = FMT == PA_Q8_E4M3 ? 0.f : 1152.f;
-
 // fp16 pair to fp32, exactly.
 __device__ __forceinline__ float2 f16x2_f2(uint32_t w) {
   float2 f;

@@ -47,6 +47,21 @@ def check(case, scale=None):
     return out
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,Hk", [(128, 8), (64, 8), (64, 1), (128, 2)])
+def test_int8_scores_of_queries_with_a_mean(dtype, D, Hk):
+    """Queries far from zero mean over keys with one large element, which the query ignores, and
+    small ones: sums of code times query are a thousandth of what 128 times the query's sum is."""
+    case = Case([1 + b % 7 for b in range(48)], Hk * 2, Hk, D, "int8", dtype, 16, seed=D)
+    codes = torch.randint(-1, 2, case.cache.k.shape, generator=case.g, device=DEV)
+    codes[..., 0] = 127
+    case.cache.k.copy_(codes)
+    case.cache.k_scale.fill_(0.125)
+    case.q.copy_(8 + torch.randn(case.q.shape, generator=case.g, device=DEV))
+    case.q[..., 0] = 0.0
+    check(case, scale=0.125)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("D,Hk,G", [(128, 8, 2), (64, 8, 4), (64, 1, 8), (128, 3, 1)])
