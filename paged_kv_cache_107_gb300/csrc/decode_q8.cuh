@@ -673,8 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.q_empty[qs]);
       ++q_n;
-      // (not 0: masked scores are -inf)
-      const float c_gid = fmaxf((F16 ? 1.f : row_to_f16<KC>(qa)) * a.scale_log2, 1.4e-45f);
+      const float c_gid = (F16 ? 1.f : row_to_f16<KC>(qa)) * a.scale_log2;
       cq[0] = __shfl_sync(0xffffffffu, c_gid, 8 * tig);
       cq[1] = __shfl_sync(0xffffffffu, c_gid, 8 * tig + 4);
     }
@@ -729,8 +728,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- online softmax ---------------------------------------------------------------
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        sc[i >> 1][2 * (i & 1)] *= kf[i];
-        sc[i >> 1][2 * (i & 1) + 1] *= kf[i];
+        // (__fmul_rn is not contracted: the maximum and the difference from it take the same
+        // rounded score. Of an unrounded one the difference could be half a unit of the maximum's
+        // last place above 0, which from 2^24 on is a weight that no fp16 number holds)
+        sc[i >> 1][2 * (i & 1)] = __fmul_rn(sc[i >> 1][2 * (i & 1)] * kf[i], cq[0]);
+        sc[i >> 1][2 * (i & 1) + 1] = __fmul_rn(sc[i >> 1][2 * (i & 1) + 1] * kf[i], cq[1]);
       }
       if (tw0 + TW > count) {
 #pragma unroll
@@ -749,8 +751,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         vtop = max(vtop, max(__float_as_uint(vf[2 * h]) & 0x7fffffffu,
                              __float_as_uint(vf[2 * h + 1]) & 0x7fffffffu));
       }
-      top[0] *= cq[0];
-      top[1] *= cq[1];
       vtop = __reduce_max_sync(0xffffffffu, vtop);
       const int e_new = (int)(vtop >> 23) - 127;
       if (__any_sync(0xffffffffu, top[0] > m_run[0] || top[1] > m_run[1]) || e_new > e_run) {
@@ -786,8 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t wt[NI], wl[NI];
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const float p0 = fast_exp2(fmaf(sc[i >> 1][2 * (i & 1)], cq[0], -m_ref[0]));
-        const float p1 = fast_exp2(fmaf(sc[i >> 1][2 * (i & 1) + 1], cq[1], -m_ref[1]));
+        const float p0 = fast_exp2(sc[i >> 1][2 * (i & 1)] - m_ref[0]);
+        const float p1 = fast_exp2(sc[i >> 1][2 * (i & 1) + 1] - m_ref[1]);
         l_part[0] += p0;
         l_part[1] += p1;
         vf[i] *= nu;

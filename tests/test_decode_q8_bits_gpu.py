@@ -73,6 +73,33 @@ def test_results_are_rounded_once(fmt, dtype, D, Hk, G):
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,Hk", [(128, 8), (64, 8), (64, 1)])
+@pytest.mark.parametrize("scale", [2.0 ** 18, 2.0 ** 22 * 1.3, 2.0 ** 30, 2.0 ** 60])
+def test_scores_beyond_their_own_precision(fmt, dtype, D, Hk, scale):
+    """A sequence of equal keys weighs them equally, whatever the size of their score and however
+    coarse an fp32 number of that size is. Where CTAs share a sequence, each one's log-sum-exp
+    m + log2 l is rounded at m's size: half a unit u of the last place, so that the weights of two of
+    them move by up to 2^u against each other and the result by (2^u - 1) A, or at most from
+    one value to another."""
+    case = Case([1 + b % 40 for b in range(60)], Hk * 2, Hk, D, fmt, dtype, 16, seed=Hk)
+    case.cache.k.view(torch.uint8).copy_(torch.randint(
+        1, 100, (1, 1, Hk, D), generator=case.g, device=DEV).to(torch.uint8))
+    case.cache.k_scale.fill_(0.01)
+    out, alone = case.run(scale=scale), case.run(scale=scale, grid_ctas=1)
+    key = np.repeat(ref.dequantised(case.cache.k, case.cache.k_scale)[0], 2, axis=0)
+    m = np.abs((case.q.double().cpu().numpy() * key).sum(-1, keepdims=True)) * scale * np.log2(np.e)
+    u = np.spacing((m + 6.0).astype(np.float32)).astype(np.float64)  # log2 40 < 6
+    case.q.zero_()  # what equal weights give
+    want, tol = reference(case)
+    att.assert_within(alone.double().cpu().numpy(), want, tol)
+    v = ref.dequantised(case.cache.v, case.cache.v_scale)
+    far = 2.0 * np.nanmax(np.abs(v))
+    att.assert_within(out.double().cpu().numpy(), want,
+                      tol + np.minimum(np.exp2(np.minimum(u, 64.0)) - 1.0, 1.0) * far)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("D,Hk", [(128, 8), (64, 2)])
 def test_rows_of_very_different_sizes(fmt, dtype, D, Hk):
     check(Case([300, 1, 77, 500], Hk * 4, Hk, D, fmt, dtype, 16, seed=5, spread=8), scale=1e-4)
