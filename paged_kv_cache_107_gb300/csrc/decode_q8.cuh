@@ -730,9 +730,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < NI; ++i) {
         // (__fmul_rn is not contracted: the maximum and the difference from it take the same
         // rounded score. Of an unrounded one the difference could be half a unit of the maximum's
-        // last place above 0, which from 2^24 on is a weight that no fp16 number holds)
-        sc[i >> 1][2 * (i & 1)] = __fmul_rn(sc[i >> 1][2 * (i & 1)] * kf[i], cq[0]);
-        sc[i >> 1][2 * (i & 1) + 1] = __fmul_rn(sc[i >> 1][2 * (i & 1) + 1] * kf[i], cq[1]);
+        // last place above 0, which from 2^24 on is a weight that no fp16 number holds. The two
+        // factors first: the product of codes and queries of 2^14 times a bf16 key's scale alone
+        // could overflow)
+        sc[i >> 1][2 * (i & 1)] = __fmul_rn(sc[i >> 1][2 * (i & 1)], kf[i] * cq[0]);
+        sc[i >> 1][2 * (i & 1) + 1] = __fmul_rn(sc[i >> 1][2 * (i & 1) + 1], kf[i] * cq[1]);
       }
       if (tw0 + TW > count) {
 #pragma unroll

@@ -99,6 +99,17 @@ def test_scores_beyond_their_own_precision(fmt, dtype, D, Hk, scale):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("D,Hk", [(128, 8), (64, 1)])
+@pytest.mark.parametrize("up", [60, 100, 112])
+def test_large_keys_under_small_queries(fmt, D, Hk, up):
+    """bf16 keys 2^up times the usual size under queries as much smaller: ordinary scores."""
+    case = Case([40, 7, 300], Hk * 2, Hk, D, fmt, "bf16", 16, seed=up)
+    case.cache.k_scale.mul_(2.0 ** up)
+    case.q *= 2.0 ** -up
+    check(case, scale=0.25)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("D,Hk", [(128, 8), (64, 2)])
 def test_rows_of_very_different_sizes(fmt, dtype, D, Hk):
