@@ -950,7 +950,9 @@ def pa_decode_q8(out: torch.Tensor, q: torch.Tensor, cache: Q8Cache, block_table
     """pa_decode over an 8-bit cache: out, q [B, H, D] bf16 or fp16; the same tables, lengths and
     workspace."""
     nb, bs, hk, d2 = _q8_cache(cache)._shape
-    dt = q.dtype
+    dt, grid_ctas = q.dtype, int(grid_ctas)
+    if abs(grid_ctas) > 0x7fffffff:
+        raise PagedAttentionError(f"grid_ctas out of range: {grid_ctas}")
     if not (stream is None and dt in _ATTN_TYPES and out.dtype is dt and q.dim() == 3
             and block_tables.dtype is torch.int32 and block_tables.dim() == 2
             and context_lens.dtype is torch.int32 and context_lens.dim() == 1
@@ -974,7 +976,7 @@ def pa_decode_q8(out: torch.Tensor, q: torch.Tensor, cache: Q8Cache, block_table
                                       lambda w: w.fits(B, H, hk, D), q.device, stream)
     rc = (_call_module or _calls()).pa_decode_q8(
         out.data_ptr(), q.data_ptr(), cache._arg, block_tables.data_ptr(), block_tables.shape[1],
-        context_lens.data_ptr(), B, H, hk, D, PA_DTYPE[dt], bs, nb, _scale(scale), int(grid_ctas),
+        context_lens.data_ptr(), B, H, hk, D, PA_DTYPE[dt], bs, nb, _scale(scale), grid_ctas,
         workspace.buffer.data_ptr(), workspace.nbytes,
         None if dev_err is None else dev_err.data_ptr(), _stream_of(stream, cache._index))
     if rc:

@@ -1,0 +1,62 @@
+"""The compiled binding of the 8-bit cache's and the rotary calls: arguments of the wrong kind or
+size are exceptions, never another value. No GPU is needed."""
+import ctypes
+
+import pytest
+import torch
+
+import paged_kv_cache_107_gb300 as pk
+from paged_kv_cache_107_gb300 import build as lib_build
+
+# Calls that have nothing to do (status 0), and the C type of each argument.
+CACHE = pk._PaQ8Cache(16, 16, 16, 16, 1)
+ROTARY = pk._PaRotary(16, 16, 128, 1, 0, 1.0)
+A, R = ctypes.addressof(CACHE), ctypes.addressof(ROTARY)
+HEAD, TAIL = [16, 16, 16, 16, 2048, 2048, 1024, 1024, 1, 16, 0, R], [16, 0, 16, 8, 128, 16, 4, None, None]
+CALLS = {
+    "pa_store_kvcache_q8": ([16, 16, 1024, 1024, 1, A, 16, 0, 8, 128, 16, 4, None, None],
+                            "ppllippiiiilpp"),
+    "pa_load_kvcache_q8": ([16, 16, 1, A, 16, 0, 8, 128, 16, 4, None, None], "ppippiiiilpp"),
+    "pa_decode_q8": ([16, 16, A, 16, 1, 16, 0, 16, 8, 128, 1, 16, 4, 0.0, 0, 256, 1 << 30, None,
+                      None], "ppppipiiiiiilfipzpp"),
+    "pa_rotary_store": (HEAD + [16, 16] + TAIL, "ppppllll" "iplpppp" "iiiiilpp"),
+    "pa_rotary_store_q8": (HEAD + [A] + TAIL, "ppppllll" "iplppp" "iiiiilpp"),
+}
+
+
+@pytest.fixture(scope="module")
+def calls():
+    lib_build.build()
+    return pk._calls()
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_arguments_keep_their_kind(calls, name):
+    args, types = CALLS[name]
+    fn = getattr(calls, name)
+    assert len(args) == len(types) and fn(*args) == 0
+    for i, t in enumerate(types):
+        def call(x):
+            return fn(*args[:i], x, *args[i + 1:])
+
+        if t == "f":
+            for x in ("x", None):
+                with pytest.raises(TypeError):
+                    call(x)
+            assert call(1) == 0
+            continue
+        for x in (1.0, 0.0, "x", *(() if t == "p" else (None,))):
+            with pytest.raises(TypeError):
+                call(x)
+        for x in {"i": (1 << 31, -(1 << 31) - 1, 1 << 32, 1 << 70), "l": (1 << 63, -(1 << 63) - 1),
+                  "p": (-1, 1 << 64), "z": (-1, 1 << 64)}[t]:
+            with pytest.raises(OverflowError):
+                call(x)
+
+
+@pytest.mark.parametrize("grid", [1 << 31, 1 << 32, -(1 << 40)])
+def test_a_grid_is_not_cut_to_32_bits(grid):
+    cache = pk.Q8Cache(2, 16, 8, 128, torch.int8, device="cpu")
+    q, i = torch.zeros(2, 16, 128, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(pk.PagedAttentionError, match="grid_ctas"):
+        pk.pa_decode_q8(q, q, cache, i[:, None], i, grid_ctas=grid)
