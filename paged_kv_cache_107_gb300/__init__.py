@@ -779,7 +779,7 @@ _call_module = None
 
 
 def _calls():
-    """lib/_pa_call.so (csrc/py_call.c), bound to the loaded library."""
+    """The module of csrc/py_call.c, bound to the loaded library."""
     global _call_module
     if _call_module is None:
         lib = load_library()

@@ -2,8 +2,8 @@
 
 Every .cu file under csrc/ is compiled for sm_103a only (one -gencode), in parallel, then
 linked into one shared library with a plain C ABI (include/pa.h). No torch headers are
-involved; the CUDA runtime is linked statically. Beside it goes lib/_pa_call.so, the Python
-module of csrc/py_call.c.
+involved; the CUDA runtime is linked statically. Beside it goes the Python module of
+csrc/py_call.c, lib/_pa_call with the running interpreter's extension suffix.
 """
 from __future__ import annotations
 
@@ -20,7 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libpagedkv.so")
 CALL_SRC = os.path.join(CSRC, "py_call.c")
-CALL_PATH = os.path.join(LIB_DIR, "_pa_call.so")
+# (the suffix names the interpreter and the machine: a module of another one is not taken for it)
+CALL_PATH = os.path.join(LIB_DIR, "_pa_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 OBJ_DIR = os.path.join(LIB_DIR, "obj")
 GENCODE = "arch=compute_103a,code=sm_103a"
 
@@ -50,11 +51,15 @@ def _deps():
         os.path.join(CSRC, "*.h")) + [os.path.join(os.path.dirname(HERE), "include", "pa.h")]
 
 
-def up_to_date() -> bool:
-    if not (os.path.exists(LIB_PATH) and _call_up_to_date()):
+def _lib_up_to_date() -> bool:
+    if not os.path.exists(LIB_PATH):
         return False
     t = os.path.getmtime(LIB_PATH)
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def up_to_date() -> bool:
+    return _lib_up_to_date() and _call_up_to_date()
 
 
 def _call_up_to_date() -> bool:
@@ -66,7 +71,7 @@ def _call_up_to_date() -> bool:
 
 
 def build_call() -> str:
-    """Compile csrc/py_call.c for the running interpreter. Returns lib/_pa_call.so's path."""
+    """Compile csrc/py_call.c for the running interpreter. Returns the module's path."""
     os.makedirs(LIB_DIR, exist_ok=True)
     cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
     if not cc:
@@ -82,17 +87,19 @@ def build_call() -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: str = None) -> str:
-    """Compile csrc/*.cu for sm_103a and link lib/libpagedkv.so. Returns its path.
+    """Compile csrc/*.cu for sm_103a and link lib/libpagedkv.so, and the Python module beside it,
+    as far as they are not up to date. Returns the library's path.
 
     lib_path: build a separate library there instead (always rebuilt, objects beside it),
     for example a test build with extra preprocessor flags; the in-tree library is left
     alone."""
     if lib_path is not None:
         return _build_to(lib_path, lib_path + ".obj", verbose, extra_flags)
-    if not force and up_to_date():
-        return LIB_PATH
-    build_call()
-    return _build_to(LIB_PATH, OBJ_DIR, verbose, extra_flags)
+    if force or not _call_up_to_date():
+        build_call()
+    if force or not _lib_up_to_date():
+        _build_to(LIB_PATH, OBJ_DIR, verbose, extra_flags)
+    return LIB_PATH
 
 
 def _build_to(lib_path: str, obj_dir: str, verbose: bool, extra_flags) -> str:

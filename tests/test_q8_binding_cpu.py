@@ -1,6 +1,8 @@
 """The compiled binding of the 8-bit cache's and the rotary calls: arguments of the wrong kind or
 size are exceptions, never another value. No GPU is needed."""
 import ctypes
+import importlib.util
+import sysconfig
 
 import pytest
 import torch
@@ -60,3 +62,31 @@ def test_a_grid_is_not_cut_to_32_bits(grid):
     q, i = torch.zeros(2, 16, 128, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
     with pytest.raises(pk.PagedAttentionError, match="grid_ctas"):
         pk.pa_decode_q8(q, q, cache, i[:, None], i, grid_ctas=grid)
+
+
+def build_module_under(monkeypatch, **config):
+    """build.py as another interpreter would import it."""
+    get = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: config.get(name, get(name)))
+    spec = importlib.util.spec_from_file_location("another_build", lib_build.__file__)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+def test_a_module_of_another_interpreter_is_not_taken(calls, monkeypatch):
+    assert calls.__spec__.origin == lib_build.CALL_PATH and lib_build.up_to_date()
+    other = build_module_under(monkeypatch, EXT_SUFFIX=".cpython-399-elsewhere.so")
+    assert other.LIB_PATH == lib_build.LIB_PATH
+    assert other.CALL_PATH != lib_build.CALL_PATH and not other.up_to_date()
+
+
+def test_only_what_is_stale_is_built(calls, monkeypatch):
+    made = []
+    monkeypatch.setattr(lib_build, "build_call", lambda: made.append("module"))
+    monkeypatch.setattr(lib_build, "_build_to", lambda path, *a: made.append(path))
+    assert lib_build.build() == lib_build.LIB_PATH and made == []
+    monkeypatch.setattr(lib_build, "CALL_PATH", lib_build.CALL_PATH + ".missing")
+    assert lib_build.build() == lib_build.LIB_PATH and made == ["module"]
+    assert lib_build.build(force=True) == lib_build.LIB_PATH
+    assert sorted(made[1:]) == sorted(["module", lib_build.LIB_PATH])
