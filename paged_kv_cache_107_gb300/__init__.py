@@ -14,6 +14,7 @@ import importlib.util
 import math
 import os
 import threading
+import types
 from typing import Optional
 
 import torch
@@ -773,26 +774,35 @@ def pa_decode_shared(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
 
 
 # ---------------------------------------------------------------- 8-bit caches
-_CALLS = ("pa_store_kvcache_q8", "pa_load_kvcache_q8", "pa_decode_q8", "pa_rotary_store",
-          "pa_rotary_store_q8")
+# Their arguments' C types, as in csrc/py_call.c.
+_CALLS = {"pa_store_kvcache_q8": "ppllippiiiilpp",
+          "pa_load_kvcache_q8": "ppippiiiilpp",
+          "pa_decode_q8": "ppppipiiiiiilfipzpp",
+          "pa_rotary_store": "ppppllll" "iplpppp" "iiiiilpp",
+          "pa_rotary_store_q8": "ppppllll" "iplppp" "iiiiilpp"}
+_C_TYPES = {"p": ctypes.c_void_p, "i": ctypes.c_int, "l": ctypes.c_int64, "z": ctypes.c_size_t,
+            "f": ctypes.c_float}
 _call_module = None
 
 
 def _calls():
-    """The module of csrc/py_call.c, bound to the loaded library."""
+    """The module of csrc/py_call.c, bound to the loaded library; where it is not built, the
+    same functions through ctypes (1 to 2 us more a call)."""
     global _call_module
     if _call_module is None:
         lib = load_library()
-        with _lock:
-            if not os.path.exists(_build.CALL_PATH):
-                raise PagedAttentionError(f"{_build.CALL_PATH} not found; build it first "
-                                          "(python -m paged_kv_cache_107_gb300.build)")
-            spec = importlib.util.spec_from_file_location("_pa_call", _build.CALL_PATH)
-            module = importlib.util.module_from_spec(spec)
-            spec.loader.exec_module(module)
-            module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
-                          for name in _CALLS))
-            _call_module = module
+        if os.path.exists(_build.CALL_PATH):
+            with _lock:
+                spec = importlib.util.spec_from_file_location("_pa_call", _build.CALL_PATH)
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+                module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                              for name in _CALLS))
+        else:
+            module = types.SimpleNamespace(**{
+                name: _typed(name, [_C_TYPES[t] for t in kinds], ctypes.c_int)
+                for name, kinds in _CALLS.items()})
+        _call_module = module
     return _call_module
 
 

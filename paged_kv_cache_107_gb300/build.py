@@ -3,7 +3,8 @@
 Every .cu file under csrc/ is compiled for sm_103a only (one -gencode), in parallel, then
 linked into one shared library with a plain C ABI (include/pa.h). No torch headers are
 involved; the CUDA runtime is linked statically. Beside it goes the Python module of
-csrc/py_call.c, lib/_pa_call with the running interpreter's extension suffix.
+csrc/py_call.c, lib/_pa_call with the running interpreter's extension suffix, where a C compiler
+and Python.h are there (the binding goes through ctypes without it).
 """
 from __future__ import annotations
 
@@ -59,7 +60,7 @@ def _lib_up_to_date() -> bool:
 
 
 def up_to_date() -> bool:
-    return _lib_up_to_date() and _call_up_to_date()
+    return _lib_up_to_date() and (_call_up_to_date() or _call_tools() is None)
 
 
 def _call_up_to_date() -> bool:
@@ -70,15 +71,24 @@ def _call_up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in (CALL_SRC, header))
 
 
-def build_call() -> str:
-    """Compile csrc/py_call.c for the running interpreter. Returns the module's path."""
-    os.makedirs(LIB_DIR, exist_ok=True)
+def _call_tools():
+    """(C compiler, folder of Python.h), None where one is missing."""
     cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
-    if not cc:
-        raise RuntimeError("no C compiler: set CC")
+    include = sysconfig.get_paths()["include"]
+    return (cc, include) if cc and os.path.exists(os.path.join(include, "Python.h")) else None
+
+
+def build_call():
+    """Compile csrc/py_call.c for the running interpreter. Returns the module's path, or None
+    without a C compiler or Python.h."""
+    tools = _call_tools()
+    if tools is None:
+        sys.stderr.write("csrc/py_call.c not compiled: no C compiler (CC) or no Python.h\n")
+        return None
+    cc, include = tools
+    os.makedirs(LIB_DIR, exist_ok=True)
     tmp = CALL_PATH + f".tmp{os.getpid()}"
-    cmd = [cc, "-O2", "-std=gnu11", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
-           CALL_SRC, "-o", tmp]
+    cmd = [cc, "-O2", "-std=gnu11", "-shared", "-fPIC", "-I", include, CALL_SRC, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cc} failed for {CALL_SRC}:\n{r.stdout}\n{r.stderr}")
@@ -95,10 +105,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: 
     alone."""
     if lib_path is not None:
         return _build_to(lib_path, lib_path + ".obj", verbose, extra_flags)
-    if force or not _call_up_to_date():
-        build_call()
     if force or not _lib_up_to_date():
         _build_to(LIB_PATH, OBJ_DIR, verbose, extra_flags)
+    if force or not _call_up_to_date():
+        build_call()
     return LIB_PATH
 
 

@@ -90,3 +90,31 @@ def test_only_what_is_stale_is_built(calls, monkeypatch):
     assert lib_build.build() == lib_build.LIB_PATH and made == ["module"]
     assert lib_build.build(force=True) == lib_build.LIB_PATH
     assert sorted(made[1:]) == sorted(["module", lib_build.LIB_PATH])
+
+
+def test_the_library_is_built_without_python_headers(calls, monkeypatch, tmp_path):
+    """Only the module needs them, and the calls go through ctypes without it."""
+    made = []
+    monkeypatch.setattr(sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    monkeypatch.setattr(lib_build, "CALL_PATH", str(tmp_path / "_pa_call.so"))
+    monkeypatch.setattr(lib_build, "_build_to", lambda path, *a: made.append(path))
+    assert lib_build.up_to_date() and lib_build.build() == lib_build.LIB_PATH and not made
+    assert lib_build.build(force=True) == lib_build.LIB_PATH and made == [lib_build.LIB_PATH]
+    monkeypatch.setattr(pk, "_call_module", None)
+    other = pk._calls()
+    assert other is not calls
+    for name, (args, types) in CALLS.items():
+        fn = getattr(other, name)
+        assert fn(*args) == 0
+        # the module's statuses, with one argument at a time refused (nothing is ever to do)
+        for i, t in enumerate(types):
+            if t in "ilp":
+                bad = [*args[:i], None if t == "p" else -1, *args[i + 1:]]
+                assert fn(*bad) == getattr(calls, name)(*bad), (name, i)
+
+
+def test_a_compiler_error_is_not_passed_over(monkeypatch, tmp_path):
+    monkeypatch.setattr(lib_build, "CALL_SRC", str(tmp_path / "absent.c"))
+    monkeypatch.setattr(lib_build, "CALL_PATH", str(tmp_path / "_pa_call.so"))
+    with pytest.raises(RuntimeError, match="absent.c"):
+        lib_build.build_call()
