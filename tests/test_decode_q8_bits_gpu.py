@@ -111,6 +111,24 @@ def test_large_keys_under_small_queries(fmt, D, Hk, up):
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_a_sequence_is_not_bound_by_anothers_scales(fmt, dtype):
+    """One sequence's value scales near fp32's largest leave the others' bits as they were."""
+    case = Case([40, 70, 0, 33], 16, 8, 64, fmt, dtype, 16, seed=6)
+    clean = check(case)
+    for i, n in enumerate((16, 16, 16, 16, 6)):
+        case.cache.v_scale[case.tables[1][i], :, :n] = 2.0 ** 110
+    out = case.run()
+    assert torch.equal(out[[0, 2, 3]], clean[[0, 2, 3]])
+    if dtype == "bf16":
+        att.assert_within(out.double().cpu().numpy(), *reference(case))
+    for grid in (1, 2, 5):
+        got, want = (case.run(grid_ctas=grid), reference(case))
+        keep = [0, 2, 3]
+        att.assert_within(got[keep].double().cpu().numpy(), want[0][keep], want[1][keep])
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("D,Hk", [(128, 8), (64, 2)])
 def test_rows_of_very_different_sizes(fmt, dtype, D, Hk):
     check(Case([300, 1, 77, 500], Hk * 4, Hk, D, fmt, dtype, 16, seed=5, spread=8), scale=1e-4)
