@@ -135,6 +135,12 @@ def _one_device(*tensors, stream=None) -> None:
         raise PagedAttentionError(f"stream belongs to {stream.device}, tensors to cuda:{cur}")
 
 
+def _on(device):
+    """The device that an argument names: a device, its name or its index (0 among them); the current
+    CUDA device for None."""
+    return torch.device("cuda" if device is None else device)
+
+
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: Optional[int] = None):
     if not t.is_cuda:
         raise PagedAttentionError(f"{name} must be a CUDA tensor")
@@ -286,7 +292,7 @@ class SampleWorkspace:
     def __init__(self, num_seqs: int, device=None):
         self.nbytes = pa_sample_workspace_size(max(num_seqs, 1))
         self.num_seqs = num_seqs
-        self.buffer = torch.zeros(self.nbytes, dtype=torch.uint8, device=device or "cuda")
+        self.buffer = torch.zeros(self.nbytes, dtype=torch.uint8, device=_on(device))
 
 
 _sample_ws = {}
@@ -340,7 +346,7 @@ class DecodeWorkspace:
         if n == 0:
             raise PagedAttentionError("invalid decode workspace sizes")
         self.nbytes = n
-        self.buffer = torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+        self.buffer = torch.zeros(n, dtype=torch.uint8, device=_on(device))
         self.key = (num_seqs, num_heads, num_kv_heads, head_dim)
 
     def fits(self, num_seqs, num_heads, num_kv_heads, head_dim=128) -> bool:
@@ -722,7 +728,7 @@ class SharedDecodeWorkspace:
         if n == 0:
             raise PagedAttentionError("invalid decode workspace sizes")
         self.nbytes = n
-        self.buffer = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+        self.buffer = torch.empty(n, dtype=torch.uint8, device=_on(device))
 
     def fits(self, num_seqs, num_heads, num_kv_heads, head_dim=128) -> bool:
         return pa_decode_shared_workspace_size(num_seqs, num_heads, num_kv_heads,
@@ -821,7 +827,7 @@ class Q8Cache:
 
     def __init__(self, num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int = 128,
                  dtype: torch.dtype = torch.float8_e4m3fn, device=None):
-        shape, device = (num_blocks, block_size, num_kv_heads, head_dim), device or "cuda"
+        shape, device = (num_blocks, block_size, num_kv_heads, head_dim), _on(device)
         codes = [torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype)
                  for _ in range(2)]
         scales = [torch.zeros(num_blocks, num_kv_heads, block_size, device=device)
@@ -1049,7 +1055,7 @@ class Rotary:
             raise PagedAttentionError("at most 16 axes")
         if not math.isfinite(amplitude):
             raise PagedAttentionError("amplitude must be finite")
-        device = torch.device(device or "cuda")
+        device = _on(device)
         turns = [pa_rotary_turns(f) for f in inv_freq]
         self._tensors = (torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns],
                                       dtype=torch.int64, device=device),
