@@ -561,8 +561,9 @@ int pa_store_kvcache_q8(const void* k, const void* v, int64_t k_tok_stride, int6
 
 /*
  * pa_load_kvcache_q8 — blocks of an 8-bit cache as blocks of 16-bit elements: block i of k_out
- * and v_out receives code * scale (rounded once, to the nearest) of block blocks[i] of the
- * cache. So a prefill over a cached prefix reads the sequences' blocks back into a scratch
+ * and v_out receives code * scale of block blocks[i] of the cache, the fp32 product (exact for e4m3
+ * codes under a power of two) rounded to the nearest element.
+ * So a prefill over a cached prefix reads the sequences' blocks back into a scratch
  * cache and attends there (pa_prefill_varlen with tables that number the scratch's blocks).
  *
  *   k_out, v_out    device, [num_listed, block_size, num_kv_heads, head_dim] of type `dtype`
@@ -588,7 +589,8 @@ int pa_load_kvcache_q8(void* k_out, void* v_out, int dtype, const pa_q8_cache* c
  * products, softmax and accumulation; each probability times its key's value scale enters the
  * second product as the sum of two fp16 numbers (off by 2^-22 of itself, or by 2^-39 of the
  * largest value scale met so far where that is more); one rounding of the output.
- * Block sizes that no power of two from 8 up divides are much slower than others.
+ * Block sizes that no power of two from 8 up divides are much slower than others (745 to 824 us
+ * instead of 86 for 256 sequences of 100 to 2,048 positions, 16 / 8 heads of 128).
  */
 int pa_decode_q8(void* out, const void* q, const pa_q8_cache* cache, const int32_t* block_tables,
                  int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,

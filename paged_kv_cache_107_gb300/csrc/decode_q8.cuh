@@ -5,10 +5,14 @@
 //   x_t = c ks_t (q . kc_t),  m = max x,  l = sum 2^(x_t - m),  o = sum (2^(x_t - m) vs_t) vc_t / l
 // The work split (stream-K over key tiles), the partial results and their order are those of
 // decode_kernel.cuh and decode_tc.cuh. Bound by the bytes of codes and scales: 256 sequences of
-// 100 to 2,048 positions (16 / 8 heads of 128) take 84 us, 6.7 TB/s or 0.99 of the copy rate; 8 of
-// 32k to 131k with 32 / 8 heads 217, 7.0 TB/s; 200 of up to 4,096 with 32 / 8 fp16 heads of 64 66 us
-// at block size 32 and more (6.2 TB/s) and 75.5 at 16, whose 8 KB runs the memory serves more slowly.
-// Without any products these take 83.6, 218, 63 and 67. What differs from the 16-bit kernels:
+// 100 to 2,048 positions (16 / 8 heads of 128) take 85 us, 6.7 TB/s or 0.98 of the copy rate; 8 of
+// 32k to 131k with 32 / 8 heads 217, 7.0 TB/s; 200 of up to 4,096 with 32 / 8 fp16 heads of 64 (int8)
+// 69 us at block size 32 and more (6.0 TB/s) and 76 at 16, whose 8 KB runs the memory serves more
+// slowly. Without any products these take 83.6, 218, 63 and 67. With few KV heads the rows are short
+// (256 sequences, two queries a KV head: 28 us at 1, 37 at 2, 55 at 3, 51 at 4 KV heads, of which the
+// bytes are 10, 21, 31 and 42). Block sizes that no power of two from 8 up divides are copied by one
+// warp a token at a time: 763 us at 4, 748 at 20, 745 at 100, 824 at 1 for the 256 sequences, 86 at 16.
+// What differs from the 16-bit kernels:
 //
 //  * A code is half as many bytes, so a stage of 64 KB holds twice the tokens, and every byte has
 //    to be widened: e4m3 by the hardware's conversion to fp16 (exact), int8 by placing the byte
@@ -36,15 +40,15 @@
 //    what is rounded off lies 2^-39 below the largest scale or 2^-22 below w itself. With one
 //    fp16 number, 2^-11, an fp16 result's error grows by half (0.00030 of its size against 0.00021),
 //    and bf16 results come out a unit of the last place away from the exact one's rounding wherever
-//    that lies near a tie. The second product costs 0 to 4 %: with bf16 results 84.6 -> 84.8 us for the 256
-//    sequences, 70.1 -> 72.5 for the 200, 54.6 -> 56.9 for 256 with 32 / 4 heads of 128.
+//    that lies near a tie. The second product costs 0 to 4 %: with bf16 results 84.6 -> 84.8 us for
+//    the 256 sequences, 70.1 -> 72.5 for the 200, 54.6 -> 56.9 for 256 with 32 / 4 heads of 128.
 //  * bf16 queries go to fp16 with a power of two for each head (row_to_f16 below).
 //  * Rows of shared memory are 128 bytes with the 128-byte swizzle: a head of 128 dims, or two
-//    heads of 64, which lie side by side in the cache (half as many rows for the copies, 72.8 us
-//    against 70.9 for the 200 sequences at block size 16). A single head of 64 has 64-byte rows
+//    heads of 64, which lie side by side in the cache (half as many rows for the copies: 76.0 us for the
+//    200 sequences at block size 16, with rows of one head 77.5). A single head of 64 has 64-byte rows
 //    and the 64-byte swizzle.
 //  * Stages of 64 KB, as elsewhere: with half as many tokens of 64 dims in each the same 200
-//    sequences take 78 us (88 at block size 16).
+//    sequences take 82.5 us (92.6 at block size 16).
 //  * Scales come beside the codes, [head][token] of each box, by TMA; their slots are padded to
 //    128 bytes (a TMA destination's alignment). Fetched by the producer's lanes instead, 16 bytes
 //    at a time, the same batches take 2 to 4 % longer.
@@ -330,10 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (a.auto_grid) {
       // A tile takes a CTA 0.95 us, each segment of a sequence its combine 0.11 us for every pair
       // of heads of 128: with g CTAs NT / g of the one and g / held of the other, least at this g
-      // (one sequence of 200, 1,000, 30,000 keys 7.7, 9.1, 24.6 us; with at least four tiles for
-      // each CTA 10.5, 10.6, 32; of 1,000 with 8 heads a group 14.5, with a tile for each CTA
-      // 20.8). Rows of 64 are joined in a quarter of the time. Then as few CTAs as keep the longest
-      // share (16 of 1,000: 11.8 us, 13.9 without).
+      // (one sequence of 200, 1,000, 30,000 keys 7.5, 9.3, 26.2 us; with at least four tiles for
+      // each CTA 10.6, 10.5, 28.9; of 1,000 with 8 heads a group 14.5, with a tile for each CTA
+      // 18.5). Rows of 64 are joined in a quarter of the time (1,000, 30,000 keys of 32 / 8 heads
+      // of 64 8.9, 25.9 us; with the ratio of 128 10.4, 29.6). Then as few CTAs as keep the longest
+      // share (16 of 1,000: 12.5 us, 14.4 without).
       constexpr float kRatio = D == 128 ? 8.6f : 34.f;
       want = (int64_t)sqrtf((float)NT * (float)held * (kRatio / (float)((G + 1) / 2)));
       want = want < 1 ? 1 : want;

@@ -17,7 +17,9 @@
 //
 // Bound by bytes: 17,556 tokens of 16 / 8 heads of 128 are turned and stored in 43.4 us, 6.6 TB/s
 // or 0.98 of the copy rate; their keys and values quantised in 17.7 us (e4m3) and 18.5 (int8,
-// whose instructions take 80 % of the issue slots), 64,000 tokens in 57 and 59 (1.02, 0.99). Each
+// whose instructions take 80 % of the issue slots), 64,000 tokens in 57 and 59 (1.02, 0.99). Turned
+// and quantised in one launch the first take 43.8 us (e4m3) and 45.6 (int8; 73 % of the issue slots)
+// of which the bytes are 37.3; in two, 60.7 and 61.3. Each
 // warp has one item and the grid as many blocks as that takes: one resident wave of blocks that
 // stride over the tokens was slower (49.8 us, 24.3), and so were items of 4 (46.8, 31.3) or of one
 // (50.2, 24.0) groups.
@@ -332,9 +334,9 @@ __device__ __forceinline__ void wide_rows(const RowsArgs& a) {
 
 // Blocks of consecutive rows (token, head) of the queries, the keys or the values, whatever the
 // head count: a warp's rows may be of several tokens. The angles of the block's tokens are worked
-// out once, in shared memory. For fewer heads than half a wide item's, whose lanes would have no
-// row: 32,000 tokens of 1 / 1 heads of 128 take 17.3 us, in wide items 35.4; quantised alone 6.6
-// and 27.5. (The launcher has the rule.)
+// out once, in shared memory. For head counts that would leave too many lanes of wide items without
+// a row (launch_rows_t has the rule): 32,000 tokens of 1 / 1 heads of 128 take 17.3 us, in wide items
+// 35.4; quantised alone 6.6 and 27.5.
 template <int D, bool F16, int FMT, bool ROT, bool ADJ>
 __device__ __forceinline__ void flat_rows(const RowsArgs& a, uint32_t blk, bool is_q, bool is_v) {
   using C = RowsCfg<D>;
@@ -487,7 +489,11 @@ int launch_rows_t(RowsArgs a, const DeviceInfo& info, cudaStream_t stream) {
   // Wide items have to be half full (of 128 dims: more than that; 20,000 tokens of 4 / 4 heads 24.7 us
   // flat, 29.0 wide, of 6 / 6 32.4 and 31.0), queries three quarters where keys and values take
   // flat blocks anyway (32,000 of 4 / 2 heads 26.1 and 30.4, of 9 / 3 42.8 and 50.6). Without
-  // angles only full ones are wide (20,000 of 12 heads of 64 15.8 and 18.0).
+  // angles only full ones are wide (20,000 of 12 heads of 64 15.8 and 18.0). The 8-bit rotary form
+  // follows the 16-bit one's rule, which serves it less well: 17,556 tokens to e4m3 and int8 take, of
+  // 16 / 8 heads of 128, 43.8, 45.6 us wide and 47.5, 49.0 flat, of 4 / 4 30.1, 33.1 and 21.0, 22.3;
+  // but of 6 / 6 31.2, 34.1 and 30.2, 31.8, of 12 / 12 58.6, 63.7 and 54.3, 57.1, of 32 / 8 heads
+  // of 64 41.5, 43.9 and 38.2, 39.1.
   const bool kv_wide =
       ROT ? (D == 128 ? 2 * kv_heads > R : 2 * kv_heads >= R) : kv_heads % R == 0;
   const bool q_wide = kv_wide ? 2 * q_heads >= R : 4 * q_heads >= 3 * over(q_heads, R) * R;
