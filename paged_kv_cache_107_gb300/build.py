@@ -22,7 +22,7 @@ LIB_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libpagedkv.so")
 CALL_SRC = os.path.join(CSRC, "py_call.c")
 # (the suffix names the interpreter and the machine: a module of another one is not taken for it)
-CALL_PATH = os.path.join(LIB_DIR, "_pa_call" + sysconfig.get_config_var("EXT_SUFFIX"))
+CALL_PATH = os.path.join(LIB_DIR, "_pa_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 OBJ_DIR = os.path.join(LIB_DIR, "obj")
 GENCODE = "arch=compute_103a,code=sm_103a"
 

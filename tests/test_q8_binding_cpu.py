@@ -118,3 +118,11 @@ def test_a_compiler_error_is_not_passed_over(monkeypatch, tmp_path):
     monkeypatch.setattr(lib_build, "CALL_PATH", str(tmp_path / "_pa_call.so"))
     with pytest.raises(RuntimeError, match="absent.c"):
         lib_build.build_call()
+
+
+def test_an_interpreter_without_a_suffix(monkeypatch):
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: None)
+    spec = importlib.util.spec_from_file_location("another_build", lib_build.__file__)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    assert module.CALL_PATH.endswith("_pa_call.so")
